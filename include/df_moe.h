@@ -366,6 +366,107 @@ DF_MOE_API int df_moe_route_noalloc(const float* router, int32_t E, int32_t H,
                                     const void* x_bf16, int32_t T, int32_t k,
                                     int32_t* ids, float* weights, void* stream);
 
+/* ---- the expert path's operators, without a handle -------------------------
+ * No counterpart in the pages: the pieces of an expert-parallel MoE layer for
+ * callers with experts of their own (other weight formats, 8-bit experts,
+ * training through frozen experts), beside the layer above. A serving path is
+ * quantize -> permute (codes and scales) -> fp8_matmul -> ... -> unpermute;
+ * its backward is unpermute_grad -> quantize -> fp8_matmul on the transposed
+ * weights -> permute_grad.
+ *
+ * All of them: `device` is the CUDA device of the arrays (negative: the
+ * current one), made current for the call; `stream` belongs to it. They
+ * allocate nothing, keep nothing between calls, may run at the same time on
+ * any streams (and be captured into graphs) as long as their outputs and
+ * workspaces are apart, and give the same bits on every run. Every array is device memory,
+ * aligned to its elements; outputs do not overlap inputs. A row distance
+ * (ld..., in elements) of 0 stands for rows without gaps; elements between
+ * rows are neither read nor written. T = 0 or M = 0 is an empty call.
+ * Sums are fp32, in a fixed order, and round to the output's type once.
+ * Limits: k <= 32, E, G <= 1024, T * k < 2^31, row lengths <= 262144.
+ * Errors: EINVAL, ERANGE, ECUDA; messages from df_moe_last_error(NULL). */
+#define DF_MOE_BF16 0
+#define DF_MOE_F16 1
+#define DF_MOE_F32 2
+#define DF_MOE_E4M3 3
+
+/* Bytes of workspace that df_moe_permute needs for these sizes (0 up to
+ * 65,536 assignments; never above 4 MiB; 0 for sizes out of range). */
+DF_MOE_API size_t df_moe_permute_workspace(int64_t T, int32_t k, int32_t E);
+
+/* Tokens sorted by expert. Assignment a = t k + j (ids[t][j]) is dropped when
+ * its id lies outside [0, E); the others are sorted by expert, equal experts
+ * by a (a token may name an expert more than once):
+ *   offs  [E + 1]   first row of each expert; offs[E] = n, the rows there are
+ *   pos   [T][k]    row of each assignment, -1 if dropped
+ *   src   [T * k]   assignment of each row
+ *   rows  [T * k][H] rows[pos[a]] = x[a / k]
+ * Rows of src, rows and rows_scales from n on are left as they were.
+ *   x     [T][H] of dtype (DF_MOE_E4M3: bytes)
+ *   scales [T][n_scales], rows_scales [T * k][n_scales] fp32: a second array
+ *          moved the same way (the scales of 8-bit rows); n_scales = 0: none
+ *   workspace: df_moe_permute_workspace bytes, 4-byte aligned; not shared by
+ *          calls (or captured graphs) that may overlap */
+DF_MOE_API int df_moe_permute(int device, const int32_t* ids, int64_t T, int32_t k, int32_t E,
+                              const void* x, int32_t dtype, int64_t H, int64_t ldx,
+                              const float* scales, int32_t n_scales, int64_t ld_scales, void* rows,
+                              int64_t ldr, float* rows_scales, int64_t ld_rows_scales,
+                              int32_t* offs, int32_t* pos, int32_t* src, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Gradient of x: dx[t] = sum_j drows[pos[t][j]]. A place outside [0, n_rows)
+ * counts as dropped. dtype: DF_MOE_BF16, _F16 or _F32, of drows and dx. */
+DF_MOE_API int df_moe_permute_grad(int device, const void* drows, int32_t dtype, int64_t n_rows,
+                                   int64_t ldr, const int32_t* pos, int64_t T, int32_t k,
+                                   int64_t H, void* dx, int64_t ldx, void* stream);
+
+/* Rows back to their tokens: y[t] = sum_j weights[t][j] rows[pos[t][j]].
+ * Dropped assignments add nothing, whatever their weight; a token without any
+ * has y[t] = 0. weights [T][k] fp32. */
+DF_MOE_API int df_moe_unpermute(int device, const void* rows, int32_t dtype, int64_t n_rows,
+                                int64_t ldr, const int32_t* pos, const float* weights, int64_t T,
+                                int32_t k, int64_t H, void* y, int64_t ldy, void* stream);
+
+/* Its gradients: drows[pos[t][j]] = weights[t][j] dy[t] (rows that no
+ * assignment has are left as they were), dweights[t][j] = the dot product of
+ * dy[t] and rows[pos[t][j]] (fp32; 0 where dropped). dtype is that of dy,
+ * rows and drows. A row has at most one assignment, as permute's places do. */
+DF_MOE_API int df_moe_unpermute_grad(int device, const void* dy, int64_t lddy, const void* rows,
+                                     int32_t dtype, int64_t n_rows, int64_t ldr,
+                                     const int32_t* pos, const float* weights, int64_t T,
+                                     int32_t k, int64_t H, void* drows, int64_t lddr,
+                                     float* dweights, void* stream);
+
+/* Rows in 8 bits: per row and block of 128 columns m = the largest magnitude
+ * of the block's finite values, at least 2^-100;
+ *   scales[r][b] = m / 448,  codes[r][c] = e4m3(448 x[r][c] / m), nearest even.
+ * NaN and infinities get the code NaN. x [M][K] bf16, fp16 or fp32; codes
+ * [M][K]; scales [M][ceil(K / 128)]. */
+DF_MOE_API int df_moe_fp8_quantize(int device, const void* x, int32_t dtype, int64_t M, int64_t K,
+                                   int64_t ldx, uint8_t* codes, int64_t ldc, float* scales,
+                                   int64_t lds, void* stream);
+
+/* The product of 8-bit rows with their group's 8-bit weights:
+ *   y[r][n] = sum_b xs[r][b] ws[g][n / 128][b] sum_{k in block b} x[r][k] w[g][n][k]
+ * over blocks of 128 of K, g the group with offs[g] <= r < offs[g + 1].
+ *   x  [M][K] e4m3 codes, ldx a multiple of 16; xs [M][ceil(K / 128)] fp32
+ *   w  [G][N][K] e4m3 codes, ldw a multiple of 16, groups N * ldw apart;
+ *      ws [G][ceil(N / 128)][ceil(K / 128)] fp32, without gaps
+ *   transposed: the same product with w stored [G][K][N] (K * ldw apart) and
+ *      ws [G][ceil(K / 128)][ceil(N / 128)]: with the forward's own w and ws,
+ *      and rows of dy, this is the gradient of x
+ *   offs [G + 1] ascending from 0 (read as if clamped to [0, M]); rows outside
+ *      every group are left as they were; NULL: one group of all M rows (G = 1)
+ *   y  [M][N] of dtype
+ *   status NULL or a device word: bit 2u is set when a bounded wait inside the
+ *      kernel gave up (the call's y holds NaN there)
+ * x and w are 16-byte aligned. */
+DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, const float* xs,
+                                 int64_t ldxs, const uint8_t* w, int64_t ldw, const float* ws,
+                                 const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
+                                 int32_t transposed, void* y, int32_t dtype, int64_t ldy,
+                                 uint32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

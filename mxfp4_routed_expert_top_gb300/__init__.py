@@ -3,4 +3,6 @@
 from .binding import (MoE, DfMoeError, Config, LayerWeights, lib, span_bytes_for,  # noqa: F401
                       STACK_RMSNORM_RESIDUAL, PREFILL_MMA_SYNC, MXFP8_ACT, PLANES,
                       SYMBOLS,
-                      route_noalloc, Graph, stream_read)
+                      route_noalloc, Graph, stream_read,
+                      BF16, F16, F32, E4M3, permute_workspace, permute, permute_grad, unpermute,
+                      unpermute_grad, fp8_quantize, fp8_matmul)

@@ -17,6 +17,9 @@ PREFILL_MMA_SYNC = 4
 MXFP8_ACT = 8
 PLANES = 16
 KERNEL_KINDS = 18
+BF16, F16, F32, E4M3 = 0, 1, 2, 3
+_DTYPES = {"bf16": BF16, "f16": F16, "f32": F32, "e4m3": E4M3,
+           BF16: BF16, F16: F16, F32: F32, E4M3: E4M3}
 
 # every symbol the header declares (checked by the CPU tests)
 SYMBOLS = [
@@ -31,6 +34,8 @@ SYMBOLS = [
     "df_moe_graph_create", "df_moe_graph_launch", "df_moe_graph_launch_count",
     "df_moe_graph_destroy", "df_moe_stream_read", "df_moe_create_cached",
     "df_moe_cache_stats", "df_moe_test_drop_arrival", "df_moe_step_mxfp8",
+    "df_moe_permute_workspace", "df_moe_permute", "df_moe_permute_grad", "df_moe_unpermute",
+    "df_moe_unpermute_grad", "df_moe_fp8_quantize", "df_moe_fp8_matmul",
 ]
 
 
@@ -105,6 +110,18 @@ def lib():
                                            ctypes.POINTER(ctypes.c_void_p)]
         L.df_moe_cache_stats.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64),
                                          ctypes.POINTER(i64)]
+        ci, sz = ctypes.c_int, ctypes.c_size_t
+        L.df_moe_permute_workspace.argtypes = [i64, i32, i32]
+        L.df_moe_permute_workspace.restype = sz
+        L.df_moe_permute.argtypes = [ci, vp, i64, i32, i32, vp, i32, i64, i64, vp, i32, i64, vp, i64,
+                                     vp, i64, vp, vp, vp, vp, sz, vp]
+        L.df_moe_permute_grad.argtypes = [ci, vp, i32, i64, i64, vp, i64, i32, i64, vp, i64, vp]
+        L.df_moe_unpermute.argtypes = [ci, vp, i32, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp]
+        L.df_moe_unpermute_grad.argtypes = [ci, vp, i64, vp, i32, i64, i64, vp, vp, i64, i32, i64,
+                                            vp, i64, vp, vp]
+        L.df_moe_fp8_quantize.argtypes = [ci, vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
+        L.df_moe_fp8_matmul.argtypes = [ci, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, i64, i64,
+                                        i32, vp, i32, i64, vp, vp]
         for name in SYMBOLS:
             f = getattr(L, name)
             if f.restype is ctypes.c_int:  # default
@@ -344,3 +361,87 @@ def stream_read(buf, nbytes, sink, stream=None):
     rc = lib().df_moe_stream_read(_ptr(buf), nbytes, _ptr(sink), _stream(stream))
     if rc != OK:
         raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
+
+
+# ---- the expert path's operators (no handle) ---------------------------------
+def _dtype(d):
+    try:
+        return _DTYPES[d]
+    except (KeyError, TypeError):
+        raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,))
+
+
+def _device(*arrays):
+    """The one CUDA device that the torch tensors among the arrays lie on; -1
+    (the current device) where all of them are raw addresses."""
+    dev = -1
+    for a in arrays:
+        if a is None or isinstance(a, int):
+            continue
+        get = getattr(a, "get_device", None)
+        d = get() if get is not None else -1
+        if d < 0:
+            raise DfMoeError(EINVAL, "every array must be in device memory")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise DfMoeError(EINVAL, "arrays on different devices: %d and %d" % (dev, d))
+    return dev
+
+
+def _done(rc):
+    if rc != OK:
+        raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
+
+
+def permute_workspace(T, k, E):
+    """Bytes of workspace that permute needs (df_moe_permute_workspace)."""
+    return lib().df_moe_permute_workspace(T, k, E)
+
+
+def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, workspace_bytes=0,
+            ldx=0, ldr=0, scales=None, n_scales=0, ld_scales=0, rows_scales=None, ld_rows_scales=0,
+            stream=None):
+    """Tokens sorted by expert (df_moe_permute): rows[pos[a]] = x[a // k]."""
+    dev = _device(ids, x, rows, offs, pos, src, workspace, scales, rows_scales)
+    _done(lib().df_moe_permute(dev, _ptr(ids), T, k, E, _ptr(x), _dtype(dtype), H, ldx,
+                               _ptr(scales), n_scales, ld_scales, _ptr(rows), ldr,
+                               _ptr(rows_scales), ld_rows_scales, _ptr(offs), _ptr(pos), _ptr(src),
+                               _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=None):
+    """Gradient of permute's x (df_moe_permute_grad)."""
+    _done(lib().df_moe_permute_grad(_device(drows, pos, dx), _ptr(drows), _dtype(dtype), n_rows,
+                                    ldr, _ptr(pos), T, k, H, _ptr(dx), ldx, _stream(stream)))
+
+
+def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, stream=None):
+    """Weighted rows back to their tokens (df_moe_unpermute)."""
+    _done(lib().df_moe_unpermute(_device(rows, pos, weights, y), _ptr(rows), _dtype(dtype), n_rows,
+                                 ldr, _ptr(pos), _ptr(weights), T, k, H, _ptr(y), ldy,
+                                 _stream(stream)))
+
+
+def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweights, lddy=0, ldr=0,
+                   lddr=0, stream=None):
+    """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
+    dev = _device(dy, rows, pos, weights, drows, dweights)
+    _done(lib().df_moe_unpermute_grad(dev, _ptr(dy), lddy, _ptr(rows), _dtype(dtype), n_rows, ldr,
+                                      _ptr(pos), _ptr(weights), T, k, H, _ptr(drows), lddr,
+                                      _ptr(dweights), _stream(stream)))
+
+
+def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
+    """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
+    _done(lib().df_moe_fp8_quantize(_device(x, codes, scales), _ptr(x), _dtype(dtype), M, K, ldx,
+                                    _ptr(codes), ldc, _ptr(scales), lds, _stream(stream)))
+
+
+def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0, ldxs=0, ldw=0,
+               ldy=0, status=None, stream=None):
+    """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
+    dev = _device(x, xs, w, ws, offs, y, status)
+    _done(lib().df_moe_fp8_matmul(dev, _ptr(x), ldx, _ptr(xs), ldxs, _ptr(w), ldw, _ptr(ws),
+                                  _ptr(offs), G, M, N, K, 1 if transposed else 0, _ptr(y),
+                                  _dtype(dtype), ldy, _ptr(status), _stream(stream)))
