@@ -154,30 +154,48 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
 }
 
 // ---- product --------------------------------------------------------------------
-// The weights are the 128-row operand (A), NT rows of x the other (B), as in
-// the layer's own batch GEMMs: lane = output column n, tensor memory column =
-// row of x. A unit is (a tile of NT rows of one group) x (128 columns n), K in
+// A unit is (a tile of NT rows of x of one group) x (NN columns n), K in
 // blocks of 128, the blocks of the scales.
 //
-// Roles of a CTA: EW epilogue warps, one TMA warp, one MMA warp. The TMA warp
-// fills a ring of stages (A 16 KB, B NT x 128 bytes, both in the 128-byte
+// Roles of a CTA: EW epilogue warps and four more: copies, MMAs, and two that
+// fetch scales. The copy warp fills a ring of stages (in the 128-byte
 // swizzle), the MMA warp issues four K = 32 steps a block into the next of AS
 // accumulators, and the epilogue warps add the block, times its scales, to
-// their registers. With `split` > 1 a cluster of that many CTAs shares a unit:
-// each takes a part of K, and the sums meet in distributed shared memory, in
-// the order of the parts.
-constexpr int kFM = 128;          // rows of A (columns n of y)
-constexpr int kFK = 128;          // K a block
-constexpr int kFABytes = kFM * kFK;
+// their registers.
+//
+// The scales decide the orientation. Groups of more than 32 rows take the
+// rows of x as the 128-row operand (XA): lane = row of x, and a thread has one
+// scale for its whole part of a block. With lane = n every accumulator column
+// has its own, and fetching those from shared memory took its bandwidth from
+// the MMA's operands. Short tiles (NT = 16, 32) keep the weights as the
+// 128-row operand: they stream, and 128 rows of x would be mostly empty.
+// Measured with 16 experts of 1536 x 7168: 12 rows each 35.4 us (NT = 16)
+// against 37.8 (NT = 128); 24 rows 35.9 (32) and 37.8; 48 rows 46.8 (32) and
+// 38.7; 80 rows 46.7 and 39.8.
+//
+// split > 1 (NT <= 32): a cluster of that many CTAs shares a unit, each takes
+// a part of K, and the sums meet in distributed shared memory, in the order
+// of the parts.
+constexpr int kFK = 128;          // K a block, and the columns n of a block of w's scales
+constexpr int kFABytes = 128 * kFK;
 constexpr int kFBatch = 8;        // blocks whose scales are fetched together
 
-__host__ __device__ constexpr int fp8_ew(int NT) { return NT > 64 ? 8 : 4; }
-__host__ __device__ constexpr int fp8_stages(int NT) {
-  return NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 4 : 5;
-}
-__host__ __device__ constexpr int fp8_accs(int NT) { return NT == 256 ? 2 : 4; }
-__host__ __device__ constexpr int fp8_cols(int NT) { return NT * fp8_accs(NT); }
-__host__ __device__ constexpr int fp8_ctas_per_sm(int NT) { return NT >= 128 ? 1 : 2; }
+template <int NT>
+struct Fp8Cfg {
+  static constexpr bool XA = NT >= 128;                  // rows of x are the 128-row operand
+  static constexpr int NN = XA ? 256 : 128;              // columns n a unit
+  static constexpr int DN = XA ? NN : NT;                // accumulator columns
+  static constexpr int EW = XA ? 8 : 4;                  // epilogue warps
+  static constexpr int CW = 4 * DN / EW;                 // accumulator columns a warp holds
+  static constexpr int NTHR = (EW + 4) * 32;
+  static constexpr int BRows = DN;                       // rows of the second operand
+  static constexpr int BBytes = BRows * kFK;
+  static constexpr int NS = XA ? 4 : 5;                  // stages
+  static constexpr int AS = XA ? 2 : 4;                  // accumulators
+  static constexpr uint32_t Cols = DN * AS;
+  static constexpr int Scales = XA ? 2 * 128 : NT;       // of a block: rows (x 2 blocks of n)
+  static constexpr int CtasPerSm = XA ? 1 : 2;
+};
 
 struct Fp8Params {
   CUtensorMap w, x;
@@ -186,75 +204,198 @@ struct Fp8Params {
   void* y;
   uint32_t* status;
   int64_t M, ldxs, ldy;
-  int G, N, K, KB, NB, split;
+  int G, N, K, KB, NB, units_n, split, vec;
 };
 
 template <int NT>
 struct Fp8Smem {
-  float sc[2][kFBatch][NT];  // scales of two batches of blocks
-  uint64_t full[fp8_stages(NT)], empty[fp8_stages(NT)];
-  uint64_t acc_full[fp8_accs(NT)], acc_empty[fp8_accs(NT)];
+  using C = Fp8Cfg<NT>;
+  uint8_t out[C::EW][512];                  // what a warp rearranges of y
+  float sc[2][kFBatch][C::Scales + 4];      // scales of two batches of blocks
+  uint64_t full[C::NS], empty[C::NS];
+  uint64_t acc_full[C::AS], acc_empty[C::AS];
+  uint64_t sc_full[2], sc_empty[2];
   int warp_sums[32];
   uint32_t tmem;
   int err;
 };
 
 template <int NT>
-size_t fp8_smem_bytes(int G) {
-  return (size_t)fp8_stages(NT) * (kFABytes + NT * kFK) + sizeof(Fp8Smem<NT>) +
-         2 * (size_t)(G + 1) * sizeof(int);
+constexpr size_t fp8_smem_bytes(int G) {
+  using C = Fp8Cfg<NT>;
+  return (size_t)C::NS * (kFABytes + C::BBytes) + sizeof(Fp8Smem<NT>) + 2 * (size_t)(G + 1) * sizeof(int);
 }
 
-// e4m3 x e4m3, fp32 D; `ta`: A is M-major in shared memory.
-__device__ __forceinline__ uint32_t idesc_e4m3(int N, int ta) {
-  return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kFM >> 4) << 24);
+// e4m3 x e4m3, fp32 D; ta, tb: A is M-major, B N-major in shared memory.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int ta, int tb) {
+  return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t uni(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+// One lane of the (converged) warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+
+// Bounded wait for the barrier at shared address `bar`; the same answer in
+// every lane.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+// The shared::cluster address of `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+#define DFM_TMA(DIM, COORD)                                                                    \
+  "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %3, 0;\n\t"                                            \
+  "@e cp.async.bulk.tensor." DIM                                                               \
+  ".shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, " COORD "], [%2];\n\t}"
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                            uint32_t leader) {
+  asm volatile(DFM_TMA("2d", "{%4, %5}") ::"r"(dst), "l"(map), "r"(bar), "r"(leader), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                            uint32_t leader) {
+  asm volatile(DFM_TMA("3d", "{%4, %5, %6}") ::"r"(dst), "l"(map), "r"(bar), "r"(leader), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+#undef DFM_TMA
+
+// Four MMA steps of 32 along K into one accumulator, issued by the lane with
+// `leader`; KA and KB say how far a step moves the operands' descriptors,
+// whose low words are given. The whole warp runs this: the operands are then
+// the same in every lane as far as the compiler is concerned, and sit in
+// uniform registers (issued from a branch of one lane, a block's MMAs and
+// waits took 1000 cycles, of which the MMAs need 512).
+template <int KA, int KB>
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t ad, uint32_t bd, uint32_t idesc, uint32_t leader) {
+  // the high word of umma::smem_desc_sw128: atoms of 1024 bytes, version 1, 128-byte swizzle
+  constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 l;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+      "setp.ne.u32 e, %6, 0;\n\tsetp.ne.u32 p0, %3, %3;\n\tsetp.eq.u32 pt, %3, %3;\n\t"
+      "mov.b64 a0, {%1, %7};\n\tmov.b64 b0, {%2, %7};\n\t"
+      "add.u32 l, %1, %4;\n\tmov.b64 a1, {l, %7};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a2, {l, %7};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a3, {l, %7};\n\t"
+      "add.u32 l, %2, %5;\n\tmov.b64 b1, {l, %7};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b2, {l, %7};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b3, {l, %7};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a0, b0, %3, p0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, pt;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "n"(KA), "n"(KB), "r"(leader), "n"(hi)
+      : "memory");
+}
+// `bar` completes when the MMAs issued so far have.
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+
+// 32 lanes x 16 columns of tensor memory: thread l gets lane l's.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// 16 lanes x 8 N columns of tensor memory: thread l gets, for each group of 8
+// columns, columns 2 (l % 4) and the next of lane l / 4 (first two values)
+// and of lane l / 4 + 8. The wait names the registers, so that no use of them
+// moves above it.
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+__device__ __forceinline__ void tmem_ld(uint32_t (&r)[8], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
 }
-
-// acc += p * s, two fp32 at a time.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s) {
-  asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(p0), "r"(p1), "l"(s));
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void put_y(float* y, float v) { *y = v; }
 __device__ __forceinline__ void put_y(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put_y(__half* y, float v) { *y = __float2half_rn(v); }
 
+template <typename Y>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<float>(float, float) { return 0; }
+
+// 32 bytes of a row: 8 fp32 values or 16 of 16 bits (32-byte aligned).
+template <typename Y>
+__device__ __forceinline__ void store_sector(Y* y, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = sizeof(Y) == 4 ? __float_as_uint(v[i]) : pack16<Y>(v[2 * i % 16], v[(2 * i + 1) % 16]);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // What a unit is: `rows` rows of x from `row0`, all of group g, times columns
-// n0 .. n0 + 127.
+// from n0.
 struct Fp8Unit {
   int g, rows, n0;
   int64_t row0;
@@ -262,8 +403,8 @@ struct Fp8Unit {
 
 // tiles[g]: row tiles of the groups before g; offs[g]: first row of group g.
 template <int NT>
-__device__ __forceinline__ Fp8Unit fp8_unit(int u, int NB, int G, const int* tiles, const int* offs) {
-  const int tile = u / NB;
+__device__ __forceinline__ Fp8Unit fp8_unit(int u, int units_n, int G, const int* tiles, const int* offs) {
+  const int tile = u / units_n;
   int lo = 0, hi = G - 1;  // the last g with tiles[g] <= tile
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -275,31 +416,31 @@ __device__ __forceinline__ Fp8Unit fp8_unit(int u, int NB, int G, const int* til
   const int first = NT * (tile - tiles[lo]);
   r.row0 = (int64_t)offs[lo] + first;
   r.rows = min(NT, offs[lo + 1] - offs[lo] - first);
-  r.n0 = (u - tile * NB) * kFM;
+  r.n0 = (u - tile * units_n) * Fp8Cfg<NT>::NN;
   return r;
 }
 
+// Lane = n: where the scale of row c of a tile stands: a thread's rows of two groups of
+// eight (2 q, 2 q + 1 of each) side by side, one 16-byte load.
+__device__ __forceinline__ int scale_slot(int c) {
+  return (c & ~15) | ((c & 6) << 1) | ((c & 8) >> 2) | (c & 1);
+}
+
 template <int NT, bool TRANS, typename Y>
-__global__ void __launch_bounds__((fp8_ew(NT) + 2) * 32, fp8_ctas_per_sm(NT))
+__global__ void __launch_bounds__(Fp8Cfg<NT>::NTHR, Fp8Cfg<NT>::CtasPerSm)
 fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
-  constexpr int EW = fp8_ew(NT), NS = fp8_stages(NT), AS = fp8_accs(NT);
-  constexpr int ET = EW * 32, NTHR = ET + 64;
-  constexpr int CW = EW == 8 ? NT / 2 : NT;  // accumulator columns a warp holds
-  constexpr int kBBytes = NT * kFK;
+  using C = Fp8Cfg<NT>;
+  constexpr int EW = C::EW, NS = C::NS, AS = C::AS, CW = C::CW;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sa = smem;
   uint8_t* sb = smem + NS * kFABytes;
-  Fp8Smem<NT>* sm = reinterpret_cast<Fp8Smem<NT>*>(sb + NS * kBBytes);
+  Fp8Smem<NT>* sm = reinterpret_cast<Fp8Smem<NT>*>(sb + NS * C::BBytes);
   int* tiles = reinterpret_cast<int*>(sm + 1);
   int* offs = tiles + p.G + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == EW + 1) {
-    constexpr uint32_t cols = fp8_cols(NT);
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&sm->tmem)),
-                 "r"(cols)
-                 : "memory");
+  if (warp == EW + 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(C::Cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
@@ -311,18 +452,22 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       mbar_init(&sm->acc_full[i], 1);
       mbar_init(&sm->acc_empty[i], EW);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->sc_full[i], 2);
+      mbar_init(&sm->sc_empty[i], EW);
+    }
     sm->err = 0;
     fence_barrier_init();
   }
-  // the groups' first rows, kept inside [0, M] and in order whatever the
-  // caller's array holds, and their tiles
+  // the groups' first rows, kept inside [0, M] whatever the caller's array
+  // holds, and their tiles
   const int M = (int)p.M;
-  for (int g = tid; g <= p.G; g += NTHR)
+  for (int g = tid; g <= p.G; g += C::NTHR)
     offs[g] = p.offs ? min(max(p.offs[g], 0), M) : (g ? M : 0);
   __syncthreads();
   {
     int base = 0;
-    for (int g0 = 0; g0 < p.G; g0 += NTHR) {
+    for (int g0 = 0; g0 < p.G; g0 += C::NTHR) {
       const int g = g0 + tid;
       const int n = g < p.G ? (max(0, offs[g + 1] - offs[g]) + NT - 1) / NT : 0;
       // exclusive prefix sum over the block
@@ -335,7 +480,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       if (lane == 31) sm->warp_sums[warp] = incl;
       __syncthreads();
       int before = base, all = base;
-      for (int w = 0; w < NTHR / 32; ++w) {
+      for (int w = 0; w < C::NTHR / 32; ++w) {
         if (w < warp) before += sm->warp_sums[w];
         all += sm->warp_sums[w];
       }
@@ -349,202 +494,351 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm->tmem);
-  const int units = tiles[p.G] * p.NB;
+  const int units = tiles[p.G] * p.units_n;
   const int part = blockIdx.x % p.split;
   const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
   const int kb0 = (int)((int64_t)p.KB * part / p.split);
   const int kb1 = (int)((int64_t)p.KB * (part + 1) / p.split);
 
-  if (warp == EW) {
-    // ---- copies
-    int it = 0;
-    bool ok = true;
-    for (int u = first; u < units && ok; u += step) {
-      const Fp8Unit un = fp8_unit<NT>(u, p.NB, p.G, tiles, offs);
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % NS;
-        ok = it < NS || mbar_wait(&sm->empty[s], ((it / NS) - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          sm->err = 1;
-          break;
-        }
-        const uint32_t bar = uni(smem_u32(&sm->full[s]));
-        const uint32_t da = uni(smem_u32(sa + s * kFABytes)), db = uni(smem_u32(sb + s * kBBytes));
-        if (lane == 0) mbar_arrive_expect_tx(&sm->full[s], kFABytes + kBBytes);
-        __syncwarp();
-        if (TRANS) tma_load_3d(da, &p.w, un.n0, kb * kFK, un.g, bar);
-        else tma_load_3d(da, &p.w, kb * kFK, un.n0, un.g, bar);
-        tma_load_2d(db, &p.x, kb * kFK, (int)un.row0, bar);
-      }
-    }
-    if (!ok)  // copies in flight land before the block leaves
-      for (int i = max(0, it - NS); i < it; ++i) (void)mbar_wait(&sm->full[i % NS], (i / NS) & 1);
-  } else if (warp == EW + 1) {
-    // ---- MMAs
-    const uint32_t idesc = idesc_e4m3(NT, TRANS ? 1 : 0);
-    // K step of 32: 32 bytes along a K-major row; 32 rows of 128 bytes M-major
-    constexpr uint32_t ka = TRANS ? 32 * 128 / 16 : 2;
-    int it = 0;
-    bool ok = true;
-    for (int u = first; u < units && ok; u += step) {
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % NS, as = it % AS;
-        ok = mbar_wait(&sm->full[s], (it / NS) & 1) &&
-             (it < AS || mbar_wait(&sm->acc_empty[as], ((it / AS) - 1) & 1));
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          sm->err = 1;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t ad = umma::smem_desc_sw128(smem_u32(sa + s * kFABytes));
-        const uint64_t bd = umma::smem_desc_sw128(smem_u32(sb + s * kBBytes));
-        asm volatile(
-            "{\n\t"
-            ".reg .pred e, p0, pt;\n\t"
-            ".reg .b32 r;\n\t"
-            ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-            "elect.sync r|e, 0xffffffff;\n\t"
-            "setp.ne.u32 p0, %3, %3;\n\t"
-            "setp.eq.u32 pt, %3, %3;\n\t"
-            "add.u64 a1, %1, %6;\n\tadd.u64 a2, a1, %6;\n\tadd.u64 a3, a2, %6;\n\t"
-            "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, pt;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, pt;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, pt;\n\t"
-            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
-            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
-            "}" ::"r"(uni(tmem + (uint32_t)(as * NT))),
-            "l"(ad), "l"(bd), "r"(idesc), "r"(uni(smem_u32(&sm->empty[s]))),
-            "r"(uni(smem_u32(&sm->acc_full[as]))), "n"(ka)
-            : "memory");
-      }
-    }
-    // the MMAs issued must land before the tensor memory is released
-    if (it > 0) (void)mbar_wait(&sm->empty[(it - 1) % NS], ((it - 1) / NS) & 1);
-  } else {
-    // ---- sums: warp w reads tensor memory lanes 32 (w % 4) .. + 31
-    const int c0 = (warp >> 2) * CW;
-    const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c0;
-    const int nl = 32 * (warp & 3) + lane;
-    constexpr int PER = NT * kFBatch / ET;  // scales a thread fetches of a batch
-    // a wait that runs out ends every later wait of its warp, but no warp
-    // leaves: all of them meet at the named barriers to the end
-    int it = 0;
-    bool ok = true;
-    for (int u = first; u < units; u += step) {
-      const Fp8Unit un = fp8_unit<NT>(u, p.NB, p.G, tiles, offs);
-      uint64_t acc[CW / 2];
+  if (warp >= EW) {
+    if (C::XA) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == EW) {
+      // ---- copies, issued by one lane
+      const uint32_t leader = elect_one(), a0 = uni(smem_u32(sa)), b0 = uni(smem_u32(sb));
+      const uint32_t empty = uni(smem_u32(sm->empty)), full = uni(smem_u32(sm->full));
+      int s = 0;
+      uint32_t phase = 1;  // the first round finds every stage free
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
+        const int n0 = (int)uni(un.n0), r0 = (int)uni((uint32_t)un.row0);
+        const int g = (int)uni(un.g);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = bar_wait(empty + 8 * s, phase);
+          if (!ok) break;
+          const uint32_t bar = full + 8 * s, da = a0 + s * kFABytes, db = b0 + s * C::BBytes;
+          expect_tx(bar, kFABytes + C::BBytes, leader);
+          // the weights' box is 128 x 128 where it is N-major (TRANS)
+          const uint32_t dw = C::XA ? db : da;
+          if (TRANS) {
 #pragma unroll
-      for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
-      const float* ws = p.ws + (int64_t)un.g * p.NB * p.KB;
-      const int nb = un.n0 / kFM;
-      float fetched[PER];
-      // the scales of blocks kb .. kb + 7: value i belongs to block i % 8, row i / 8
-      auto fetch = [&](int kb) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int v = tid + i * ET, b = kb + (v & (kFBatch - 1)), r = v / kFBatch;
-          fetched[i] = 0.f;
-          if (b < kb1 && r < un.rows)
-            fetched[i] = p.xs[(un.row0 + r) * p.ldxs + b] *
-                         (TRANS ? ws[(int64_t)b * p.NB + nb] : ws[(int64_t)nb * p.KB + b]);
-        }
-      };
-      auto store = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int v = tid + i * ET;
-          sm->sc[buf][v & (kFBatch - 1)][v / kFBatch] = fetched[i];
-        }
-      };
-      fetch(kb0);
-      named_barrier_sync(1, ET);  // the last unit's scales have been read
-      store(0);
-      named_barrier_sync(1, ET);
-      int buf = 0;
-      for (int kb = kb0; kb < kb1; kb += kFBatch) {
-        const bool more = kb + kFBatch < kb1;
-        if (more) fetch(kb + kFBatch);
-        const int blocks = min(kFBatch, kb1 - kb);
-        for (int b = 0; b < blocks; ++b, ++it) {
-          const int as = it % AS;
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm->acc_full[as], (it / AS) & 1));
-          if (!ok) {
-            sm->err = 1;
-            continue;
+            for (int n = 0; n < (C::XA ? C::BRows : 128); n += 128)
+              tma_load_3d(dw + n * kFK, &p.w, n0 + n, kb * kFK, g, bar, leader);
+          } else {
+            tma_load_3d(dw, &p.w, kb * kFK, n0, g, bar, leader);
           }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const float* sc = &sm->sc[buf][b][c0];
+          tma_load_2d(C::XA ? da : db, &p.x, kb * kFK, r0, bar, leader);
+          if (++s == NS) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        sm->err = 1;
+        // copies in flight land before the block leaves: of a stage's last
+        // round, or (waiting for nothing) of the round before
+        for (int i = 0; i < NS; ++i) (void)bar_wait(full + 8 * i, i < s ? phase ^ 1 : phase);
+      }
+    } else if (warp == EW + 1) {
+      // ---- MMAs, issued by one lane
+      // transposed weights are M- or N-major: a K step of 32 is 32 rows of
+      // 128 bytes, against 32 bytes along a K-major row. An N-major operand
+      // is one box of 128 wide: 256 columns n in one CTA are two MMAs.
+      constexpr int KA = TRANS && !C::XA ? 32 * 128 / 16 : 2, KB = TRANS && C::XA ? 32 * 128 / 16 : 2;
+      constexpr int PARTS = TRANS && C::XA ? C::BRows / 128 : 1;
+      const uint32_t idesc = idesc_e4m3(128, C::DN / PARTS, TRANS && !C::XA, TRANS && C::XA);
+      const uint32_t leader = elect_one(), tm = uni(tmem);
+      const uint32_t a0 = uni((uint32_t)umma::smem_desc_sw128(smem_u32(sa)));
+      const uint32_t b0 = uni((uint32_t)umma::smem_desc_sw128(smem_u32(sb)));
+      const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
+      const uint32_t acc_full = uni(smem_u32(sm->acc_full)), acc_empty = uni(smem_u32(sm->acc_empty));
+      const int total = first < units ? ((units - first + step - 1) / step) * (kb1 - kb0) : 0;
+      int s = 0, as = 0;
+      uint32_t phase = 0, acc_phase = 1;  // the first round finds every accumulator free
+      int it = 0;
+      bool ok = true;
+      for (; it < total; ++it) {
+        ok = bar_wait(full + 8 * s, phase) && bar_wait(acc_empty + 8 * as, acc_phase);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-          for (int c = 0; c < CW; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(r, tbase + (uint32_t)(as * NT + c));
-            tmem_ld_wait();
+        for (int h = 0; h < PARTS; ++h)
+          mma_block<KA, KB>(tm + (uint32_t)(as * C::DN + h * (C::DN / PARTS)), a0 + (uint32_t)(s * (kFABytes >> 4)),
+                                b0 + (uint32_t)((s * C::BBytes + h * (128 * kFK)) >> 4), idesc, leader);
+        mma_commit(acc_full + 8 * as, leader);
+        mma_commit(empty + 8 * s, leader);
+        if (++s == NS) {
+          s = 0;
+          phase ^= 1;
+        }
+        if (++as == AS) {
+          as = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) sm->err = 1;
+      // the MMAs issued must land before the tensor memory is released
+      if (it > 0) (void)bar_wait(empty + 8 * (s ? s - 1 : NS - 1), s ? phase : phase ^ 1);
+    } else {
+      // ---- scales: xs ws of eight blocks at a time, one value a thread and
+      // step: block i % 8, row i / 8
+      const int st = tid - (EW + 2) * 32;
+      int batch = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
+        const int nb = un.n0 / kFK;
+        const float* ws = p.ws + (int64_t)un.g * p.NB * p.KB;
+                for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
+          const int buf = batch & 1;
+          ok = batch < 2 || mbar_wait(&sm->sc_empty[buf], ((batch >> 1) - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            sm->err = 1;
+            break;
+          }
+          const int b = kb + (st & (kFBatch - 1));
+          float wv[2] = {0.f, 0.f};  // XA: of the two blocks of n
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sc + c + i);
-              fma2(acc[(c + i) / 2], r[i], r[i + 1], s.x);
-              fma2(acc[(c + i) / 2 + 1], r[i + 2], r[i + 3], s.y);
+          for (int h = 0; h < (C::XA ? 2 : 1); ++h)
+            if (b < kb1 && nb + h < p.NB)
+              wv[h] = TRANS ? ws[(int64_t)b * p.NB + nb + h] : ws[(int64_t)(nb + h) * p.KB + b];
+          const float* xs = p.xs + un.row0 * p.ldxs + b;
+          constexpr int PER = (C::XA ? 128 : NT) * kFBatch / 64, U = PER < 8 ? PER : 8;
+          for (int i0 = 0; i0 < PER; i0 += U) {
+            float v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int r = (st >> 3) + 8 * (i0 + i);
+              v[i] = b < kb1 && r < un.rows ? xs[r * p.ldxs] : 0.f;
+            }
+            float* sc = sm->sc[buf][st & (kFBatch - 1)];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int r = (st >> 3) + 8 * (i0 + i);
+              if (C::XA) {
+                sc[r] = v[i] * wv[0];
+                sc[128 + r] = v[i] * wv[1];
+              } else {
+                sc[scale_slot(r)] = v[i] * wv[0];
+              }
             }
           }
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
-        }
-        if (more) {
-          store(buf ^ 1);
-          named_barrier_sync(1, ET);
-          buf ^= 1;
+          if (lane == 0) mbar_arrive(&sm->sc_full[buf]);
         }
       }
-      float out[CW];
+    }
+  } else {
+    // ---- sums. A wait that runs out ends every later wait of its warp and
+    // leaves NaN in the rows it still writes.
+    int it = 0, batch = 0;
+    bool ok = true;
+    if constexpr (C::XA) {
+      // warp w: tensor memory lanes 32 (w % 4) .. + 31, a row of x each, and
+      // columns 128 (w / 4) .. + 127, one block of n
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      static_assert(128 % CW == 0, "a warp's columns lie in one block of w's scales");
+      const int c0 = (warp >> 2) * CW, l0 = 32 * (warp & 3);
+      const uint32_t tbase = tmem + ((uint32_t)l0 << 16) + (uint32_t)c0;
+      for (int u = first; u < units; u += step) {
+        const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
+        float acc[CW];
 #pragma unroll
-      for (int i = 0; i < CW / 2; ++i) {
-        out[2 * i] = __uint_as_float((uint32_t)acc[i]);
-        out[2 * i + 1] = __uint_as_float((uint32_t)(acc[i] >> 32));
-      }
-      // a wait that ran out leaves NaN, never a wrong number
-      if (!ok) {
+        for (int i = 0; i < CW; ++i) acc[i] = 0.f;
+        for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
+          const int buf = batch & 1;
+          ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1);
+          const int blocks = min(kFBatch, kb1 - kb);
+          for (int b = 0; b < blocks; ++b, ++it) {
+            const int as = it % AS;
+            const float s = sm->sc[buf][b][(c0 & 128) + l0 + lane];
+            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1);
+            if (!ok) continue;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t ta = tbase + (uint32_t)(as * C::DN);
+            constexpr int L = 16;  // columns a load
+            uint32_t r[2][L];      // the next load runs while this one is added
+            tmem_ld_rows(r[0], ta);
 #pragma unroll
-        for (int i = 0; i < CW; ++i) out[i] = __uint_as_float(0x7fffffffu);
-      }
-      if (p.split == 1) {
-        const int n = un.n0 + nl;
-        if (n < p.N) {
-          Y* y = static_cast<Y*>(p.y) + (un.row0 + c0) * p.ldy + n;
+            for (int i = 0; i < CW / L; ++i) {
+              tmem_wait(r[i & 1]);
+              if (i + 1 < CW / L) {
+                tmem_ld_rows(r[(i + 1) & 1], ta + L * (i + 1));
+              } else {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
+              }
 #pragma unroll
-          for (int c = 0; c < CW; ++c)
-            if (c0 + c < un.rows) put_y(y + c * p.ldy, out[c]);
+              for (int c = 0; c < L; ++c) acc[L * i + c] = fmaf(__uint_as_float(r[i & 1][c]), s, acc[L * i + c]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->sc_empty[buf]);
         }
-      } else {
-        // the stages are idle: this part's sums go there, [row][128]
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        float* red = reinterpret_cast<float*>(smem);
+        if (!ok) {
+          sm->err = 1;
 #pragma unroll
-        for (int c = 0; c < CW; ++c) red[(c0 + c) * kFM + nl] = out[c];
+          for (int i = 0; i < CW; ++i) acc[i] = __uint_as_float(0x7fffffffu);
+        }
+        const int n0 = un.n0 + c0, row = l0 + lane;
+        Y* y = static_cast<Y*>(p.y) + (un.row0 + row) * p.ldy + n0;
+        if (p.vec && n0 + CW <= p.N) {
+          // a lane's own row, 32 bytes (a sector) a store
+          if (row < un.rows) {
+#pragma unroll
+            for (int i = 0; i < CW; i += 32 / (int)sizeof(Y)) store_sector(y + i, &acc[i]);
+          }
+        } else {
+          // four columns at a time through shared memory, so that a store
+          // covers eight rows of four
+          float* stage = reinterpret_cast<float*>(sm->out[warp]);
+          const int rows = un.rows - l0;
+          Y* base = static_cast<Y*>(p.y) + (un.row0 + l0) * p.ldy + n0;
+#pragma unroll
+          for (int i = 0; i < CW; i += 4) {
+            *reinterpret_cast<float4*>(stage + 4 * lane) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int r = 8 * q + (lane >> 2), c = lane & 3;
+              if (r < rows && n0 + i + c < p.N) put_y(base + r * p.ldy + i + c, stage[32 * q + lane]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    } else {
+      // warp w: lanes (columns n) 32 (w % 4) .. + 31, all columns (rows of x)
+      constexpr int LDN = CW >= 32 ? 4 : 2, LC = 8 * LDN, CH = CW / LC;  // CH loads of LC columns a half
+      const int l0 = 32 * warp;
+      const uint32_t tbase = tmem + ((uint32_t)l0 << 16);
+      const int nq = lane >> 2, tq = 2 * (lane & 3);
+      uint8_t* stage = sm->out[warp];
+      for (int u = first; u < units; u += step) {
+        const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
+        // acc[c / 8][h][j][i]: column 8 (c / 8) + tq + i of lane 16 h + 8 j + nq
+        float acc[CW / 8][2][2][2];
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i) acc[i >> 2][(i >> 1) & 1][i & 1][0] = acc[i >> 2][(i >> 1) & 1][i & 1][1] = 0.f;
+        for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
+          const int buf = batch & 1;
+          ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1);
+          const int blocks = min(kFBatch, kb1 - kb);
+          for (int b = 0; b < blocks; ++b, ++it) {
+            const int as = it % AS;
+            const float* sc = &sm->sc[buf][b][2 * tq];
+            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1);
+            if (!ok) continue;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t ta = tbase + (uint32_t)(as * C::DN);
+            // load i: columns LC (i / 2) .., lanes 16 (i % 2) ..; the next
+            // runs while this one is added
+            uint32_t r[2][4 * LDN];
+            tmem_ld(r[0], ta);
+#pragma unroll
+            for (int i = 0; i < 2 * CH; ++i) {
+              tmem_wait(r[i & 1]);
+              if (i + 1 < 2 * CH) {
+                tmem_ld(r[(i + 1) & 1], ta + ((uint32_t)(16 * ((i + 1) & 1)) << 16) + (uint32_t)(LC * ((i + 1) / 2)));
+              } else {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
+              }
+#pragma unroll
+              for (int g = 0; g < LDN; g += 2) {
+                const int gc = LDN * (i / 2) + g, h = i & 1;
+                const uint32_t* v = &r[i & 1][4 * g];
+                const float4 s = *reinterpret_cast<const float4*>(sc + 8 * gc);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float* lo = acc[gc][h][j];
+                  float* hi = acc[gc + 1][h][j];
+                  lo[0] = fmaf(__uint_as_float(v[2 * j]), s.x, lo[0]);
+                  lo[1] = fmaf(__uint_as_float(v[2 * j + 1]), s.y, lo[1]);
+                  hi[0] = fmaf(__uint_as_float(v[2 * j + 4]), s.z, hi[0]);
+                  hi[1] = fmaf(__uint_as_float(v[2 * j + 5]), s.w, hi[1]);
+                }
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->sc_empty[buf]);
+        }
+        if (!ok) {
+          sm->err = 1;
+#pragma unroll
+          for (int i = 0; i < CW / 2; ++i)
+            acc[i >> 2][(i >> 1) & 1][i & 1][0] = acc[i >> 2][(i >> 1) & 1][i & 1][1] = __uint_as_float(0x7fffffffu);
+        }
+        if (p.split > 1) {
+          // the stages are idle: this part's sums go there, [row][128]
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int i = 0; i < CW / 8; ++i)
+#pragma unroll
+            for (int hj = 0; hj < 4; ++hj) {
+              const int n = l0 + 8 * hj + nq, c = 8 * i + tq;
+              red[c * 128 + n] = acc[i][hj >> 1][hj & 1][0];
+              red[(c + 1) * 128 + n] = acc[i][hj >> 1][hj & 1][1];
+            }
+        } else if (sizeof(Y) == 2 && p.vec && un.n0 + l0 + 32 <= p.N) {
+          // eight rows at a time through the warp's staging: four 8 x 8
+          // matrices transposed, then 64 bytes a row in 16-byte stores; piece q
+          // of row r stands at q ^ (r / 2) % 4
+          const int r = lane >> 2, q = lane & 3, mr = lane & 7, mi = lane >> 3;
+          const uint32_t put = smem_u32(stage + 64 * mr + 16 * (mi ^ ((mr >> 1) & 3)));
+          const uint8_t* get = stage + 64 * r + 16 * (q ^ ((r >> 1) & 3));
+          Y* y = static_cast<Y*>(p.y) + (un.row0 + r) * p.ldy + un.n0 + l0 + 8 * q;
+#pragma unroll
+          for (int i = 0; i < CW / 8; ++i) {
+            if (8 * i >= un.rows) break;
+            uint32_t v[4];
+#pragma unroll
+            for (int hj = 0; hj < 4; ++hj)
+              v[hj] = pack16<Y>(acc[i][hj >> 1][hj & 1][0], acc[i][hj >> 1][hj & 1][1]);
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(put), "r"(v[0]),
+                         "r"(v[1]), "r"(v[2]), "r"(v[3])
+                         : "memory");
+            __syncwarp();
+            const uint4 row = *reinterpret_cast<const uint4*>(get);
+            if (8 * i + r < un.rows) *reinterpret_cast<uint4*>(y + (int64_t)(8 * i) * p.ldy) = row;
+            __syncwarp();
+          }
+        } else {
+          // a warp's store covers 8 columns n of 4 rows
+          Y* y = static_cast<Y*>(p.y) + (un.row0 + tq) * p.ldy + un.n0 + l0 + nq;
+          const int left = un.rows - tq, nleft = p.N - (un.n0 + l0 + nq);
+#pragma unroll
+          for (int i = 0; i < CW / 8; ++i)
+#pragma unroll
+            for (int hj = 0; hj < 4; ++hj) {
+              if (8 * hj < nleft) {
+                if (8 * i < left) put_y(y + (int64_t)(8 * i) * p.ldy + 8 * hj, acc[i][hj >> 1][hj & 1][0]);
+                if (8 * i + 1 < left) put_y(y + (int64_t)(8 * i + 1) * p.ldy + 8 * hj, acc[i][hj >> 1][hj & 1][1]);
+              }
+            }
+        }
       }
     }
   }
-  if (p.split > 1 && first < units) {
+  __syncwarp();
+  if (!C::XA && p.split > 1 && first < units) {
     // one unit a cluster: part q sums the rows r = q, q + split, ... over the
     // parts in their order
-    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const Fp8Unit un = fp8_unit<NT>(first, p.NB, p.G, tiles, offs);
+    const Fp8Unit un = fp8_unit<NT>(first, p.units_n, p.G, tiles, offs);
     const uint32_t red = smem_u32(smem);
-    for (int i = tid; i < kFM * un.rows; i += NTHR) {
-      const int r = i / kFM, n = i % kFM;
+    for (int i = tid; i < 128 * un.rows; i += C::NTHR) {
+      const int r = i / 128, n = i % 128;
       if (r % p.split != part || un.n0 + n >= p.N) continue;
       float sum = 0.f;
       for (int q = 0; q < p.split; ++q) {
-        uint32_t remote;
         float v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(red + 4 * (r * kFM + n)), "r"(q));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_cta(red + 4 * (r * 128 + n), q)) : "memory");
         sum += v;
       }
       put_y(static_cast<Y*>(p.y) + (un.row0 + r) * p.ldy + un.n0 + n, sum);
@@ -557,10 +851,8 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (tid == 0 && *(volatile int*)&sm->err && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
-  if (warp == EW + 1) {
-    constexpr uint32_t cols = fp8_cols(NT);
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
-                 : "memory");
+  if (warp == EW + 2) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::Cols) : "memory");
   }
 }
 
@@ -596,15 +888,16 @@ bool map_u8(CUtensorMap* out, const void* base, int64_t cols, int64_t rows, int6
 
 template <int NT, bool TRANS, typename Y>
 const char* fp8_launch(const Fp8MatmulArgs& a, int sms, cudaStream_t s) {
-  static_assert(fp8_ctas_per_sm(NT) * (fp8_stages(NT) * (kFABytes + NT * kFK) + sizeof(Fp8Smem<NT>) +
-                                       (kOpsMaxExperts + 1) * 8 + 1024) <= 228 * 1024,
-                "shared memory");
+  using C = Fp8Cfg<NT>;
+  static_assert(C::CtasPerSm * (fp8_smem_bytes<NT>(kOpsMaxExperts) + 1024) <= 228 * 1024, "shared memory");
+  static_assert(C::CtasPerSm * C::Cols <= 512, "tensor memory");
   Fp8Params p{};
-  p.NB = (a.N + kFM - 1) / kFM;
+  p.NB = (a.N + kFK - 1) / kFK;
   p.KB = (a.K + kFK - 1) / kFK;
+  p.units_n = (a.N + C::NN - 1) / C::NN;
   const bool maps =
-      (a.transposed ? map_u8(&p.w, a.w, a.N, a.K, a.G, a.ldw, kFK) : map_u8(&p.w, a.w, a.K, a.N, a.G, a.ldw, kFM)) &&
-      map_u8(&p.x, a.x, a.K, a.M, 0, a.ldx, NT);
+      (a.transposed ? map_u8(&p.w, a.w, a.N, a.K, a.G, a.ldw, kFK) : map_u8(&p.w, a.w, a.K, a.N, a.G, a.ldw, C::XA ? C::BRows : 128)) &&
+      map_u8(&p.x, a.x, a.K, a.M, 0, a.ldx, C::XA ? 128 : NT);
   if (!maps) return "tensor map encoding failed";
   p.xs = a.xs;
   p.ws = a.ws;
@@ -617,21 +910,32 @@ const char* fp8_launch(const Fp8MatmulArgs& a, int sms, cudaStream_t s) {
   p.G = a.G;
   p.N = a.N;
   p.K = a.K;
+  // XA stores whole sectors, else 16 bytes
+  p.vec = !(((uintptr_t)a.y | (uint64_t)(a.ldy * (int64_t)sizeof(Y))) & (C::XA ? 31 : 15));
   // at most this many row tiles: every group's last one may be short
   const int64_t tiles = a.M / NT + (a.M < a.G ? a.M : a.G);
-  const int64_t units = tiles * p.NB;
+  const int64_t units = tiles * p.units_n;
   if (units > 0x3fffffff) return "too many tiles";
-  const int slots = sms * fp8_ctas_per_sm(NT);
   p.split = 1;
-  while (p.split < 8 && 2 * p.split * units <= slots && 2 * p.split <= p.KB) p.split *= 2;
-  const int64_t grid = p.split > 1 ? units * p.split : units < slots ? units : slots;
+  int64_t grid;
+  const int slots = sms * C::CtasPerSm;
+  while (!C::XA && p.split < 8 && 2 * p.split * units <= slots && 2 * p.split <= p.KB) p.split *= 2;
+  grid = p.split > 1 ? units * p.split : units < slots ? units : slots;
   const size_t smem = fp8_smem_bytes<NT>(a.G);
   auto kernel = fp8_matmul_kernel<NT, TRANS, Y>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return cudaGetErrorString(cudaGetLastError());
+  // once a device: what the largest G needs
+  static std::atomic<uint64_t> configured{0};
+  int device = 0;
+  (void)cudaGetDevice(&device);
+  if (device >= 64 || !(configured.load() >> device & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)fp8_smem_bytes<NT>(kOpsMaxExperts)) != cudaSuccess)
+      return cudaGetErrorString(cudaGetLastError());
+    if (device < 64) configured.fetch_or(1ull << device);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((fp8_ew(NT) + 2) * 32);
+  cfg.blockDim = dim3(C::NTHR);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -640,7 +944,7 @@ const char* fp8_launch(const Fp8MatmulArgs& a, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
@@ -669,9 +973,7 @@ const char* launch_fp8_matmul(const Fp8MatmulArgs& a, int dtype, int sms, cudaSt
   const int64_t mean = (a.M + groups - 1) / groups;
   if (mean <= 16) return fp8_nt<16>(a, dtype, sms, s);
   if (mean <= 32) return fp8_nt<32>(a, dtype, sms, s);
-  if (mean <= 64) return fp8_nt<64>(a, dtype, sms, s);
-  if (mean <= 128) return fp8_nt<128>(a, dtype, sms, s);
-  return fp8_nt<256>(a, dtype, sms, s);
+  return fp8_nt<128>(a, dtype, sms, s);
 }
 
 }  // namespace dfm
