@@ -18,6 +18,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
+
 #include "internal.h"
 #include "ops.h"
 
@@ -348,9 +350,27 @@ struct alignas(sizeof(T) * N) Pack {
   T v[N];
 };
 
+// A row is read once: its lines are not kept in L1.
+template <typename P>
+__device__ __forceinline__ P load_once(const void* p) {
+  P r;
+  if constexpr (sizeof(P) == 16) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    memcpy(&r, &v, 16);
+  } else {
+    r = *static_cast<const P*>(p);
+  }
+  return r;
+}
+
 // y[t] = sum_j w_j rows[pos_j]: a thread per N columns of a token; the loads
-// of eight rows are in flight together. Sums in fp32 in the order of j, one
-// rounding at the end.
+// of four rows are in flight together. Sums in fp32 in the order of j, one
+// rounding at the end. HBM bounds it: 4096 tokens x 16 rows of 7168 bf16 (999
+// MB) take 153 us with four rows in flight, 184 with eight (fewer threads an
+// SM), 165 with two; with the rows in L1 it is 158.
 template <typename T, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(128)
 unpermute_kernel(const UnpermuteArgs p, int nv) {
@@ -364,7 +384,7 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
   float acc[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] = 0.f;
-  constexpr int U = 8;
+  constexpr int U = 4;
   for (int j0 = 0; j0 < p.k; j0 += U) {
     Pack<T, N> r[U];
     float wt[U];
@@ -375,7 +395,7 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
       const int32_t q = j < p.k ? at[j] : -1;
       there[u] = q >= 0 && q < p.n_rows;
       wt[u] = WEIGHTED && there[u] ? w[j] : 1.f;
-      if (there[u]) r[u] = *reinterpret_cast<const Pack<T, N>*>(rows + q * p.ldr + c);
+      if (there[u]) r[u] = load_once<Pack<T, N>>(rows + q * p.ldr + c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -406,7 +426,7 @@ cudaError_t unpermute_n(const UnpermuteArgs& p, cudaStream_t s) {
 // A block per token and group of J of its assignments: dy is read once a
 // group, each row read once and its gradient written beside it; the J dot
 // products are summed over the block in a fixed order.
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 128;
 template <typename T, int N, int J>
 __global__ void __launch_bounds__(kGradThreads)
 unpermute_grad_kernel(const UnpermuteGradArgs p, int groups) {
@@ -430,7 +450,7 @@ unpermute_grad_kernel(const UnpermuteGradArgs p, int groups) {
     Pack<T, N> r[J];
 #pragma unroll
     for (int u = 0; u < J; ++u)
-      if (q[u] >= 0) r[u] = *reinterpret_cast<const Pack<T, N>*>(rows + q[u] * p.ldr + c);
+      if (q[u] >= 0) r[u] = load_once<Pack<T, N>>(rows + q[u] * p.ldr + c);
 #pragma unroll
     for (int u = 0; u < J; ++u)
       if (q[u] >= 0) {
@@ -470,9 +490,13 @@ cudaError_t unpermute_grad_j(const UnpermuteGradArgs& p, cudaStream_t s) {
 
 template <typename T, int N>
 cudaError_t unpermute_grad_n(const UnpermuteGradArgs& p, int sms, cudaStream_t s) {
-  // few tokens: one assignment a block, so that more SMs share the rows
-  if ((int64_t)p.T * p.k <= 4 * sms) return unpermute_grad_j<T, N, 1>(p, s);
-  return unpermute_grad_j<T, N, 4>(p, s);
+  // few tokens: one assignment a block, so that more SMs share the rows; else
+  // groups of at most four, as even as they come
+  const int groups = (p.k + 3) / 4, each = (p.k + groups - 1) / groups;
+  if ((int64_t)p.T * p.k <= 4 * sms || each == 1) return unpermute_grad_j<T, N, 1>(p, s);
+  return each == 2   ? unpermute_grad_j<T, N, 2>(p, s)
+         : each == 3 ? unpermute_grad_j<T, N, 3>(p, s)
+                     : unpermute_grad_j<T, N, 4>(p, s);
 }
 
 // The widest vector of at most 16 bytes that every address and distance allows.
