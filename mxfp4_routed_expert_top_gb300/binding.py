@@ -364,6 +364,20 @@ def stream_read(buf, nbytes, sink, stream=None):
 
 
 # ---- the expert path's operators (no handle) ---------------------------------
+# A decode step makes several of these calls with microseconds of work each, so
+# the marshalling is kept short: one pass over the arrays, the C functions
+# looked up once.
+_ops = None
+
+
+def _op(name):
+    global _ops
+    if _ops is None:
+        L = lib()
+        _ops = {n: getattr(L, n) for n in SYMBOLS}
+    return _ops[name]
+
+
 def _dtype(d):
     try:
         return _DTYPES[d]
@@ -371,77 +385,94 @@ def _dtype(d):
         raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,))
 
 
-def _device(*arrays):
-    """The one CUDA device that the torch tensors among the arrays lie on; -1
-    (the current device) where all of them are raw addresses."""
-    dev = -1
+def _place(*arrays):
+    """[device, address, address, ...]: the one CUDA device that the torch
+    tensors among the arrays lie on (-1, the current one, where there are only
+    raw addresses), and the arrays' addresses."""
+    dev, out = -1, [-1]
     for a in arrays:
-        if a is None or isinstance(a, int):
+        if a is None or a.__class__ is int:
+            out.append(a)
             continue
-        get = getattr(a, "get_device", None)
-        d = get() if get is not None else -1
-        if d < 0:
-            raise DfMoeError(EINVAL, "every array must be in device memory")
-        if dev < 0:
+        try:
+            d, p = a.get_device(), a.data_ptr()
+        except AttributeError:
+            raise DfMoeError(EINVAL, "every array must be in device memory") from None
+        if d != dev:
+            if d < 0:
+                raise DfMoeError(EINVAL, "every array must be in device memory")
+            if dev >= 0:
+                raise DfMoeError(EINVAL, "arrays on different devices: %d and %d" % (dev, d))
             dev = d
-        elif d != dev:
-            raise DfMoeError(EINVAL, "arrays on different devices: %d and %d" % (dev, d))
-    return dev
+        elif d < 0:
+            raise DfMoeError(EINVAL, "every array must be in device memory")
+        out.append(p)
+    out[0] = dev
+    return out
 
 
-def _done(rc):
-    if rc != OK:
-        raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
+def _failed(rc):
+    raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
 
 
 def permute_workspace(T, k, E):
     """Bytes of workspace that permute needs (df_moe_permute_workspace)."""
-    return lib().df_moe_permute_workspace(T, k, E)
+    return _op("df_moe_permute_workspace")(T, k, E)
 
 
 def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, workspace_bytes=0,
             ldx=0, ldr=0, scales=None, n_scales=0, ld_scales=0, rows_scales=None, ld_rows_scales=0,
             stream=None):
     """Tokens sorted by expert (df_moe_permute): rows[pos[a]] = x[a // k]."""
-    dev = _device(ids, x, rows, offs, pos, src, workspace, scales, rows_scales)
-    _done(lib().df_moe_permute(dev, _ptr(ids), T, k, E, _ptr(x), _dtype(dtype), H, ldx,
-                               _ptr(scales), n_scales, ld_scales, _ptr(rows), ldr,
-                               _ptr(rows_scales), ld_rows_scales, _ptr(offs), _ptr(pos), _ptr(src),
-                               _ptr(workspace), workspace_bytes, _stream(stream)))
+    dev, i, x, r, o, q, s, w, xs, rs = _place(ids, x, rows, offs, pos, src, workspace, scales,
+                                              rows_scales)
+    rc = _op("df_moe_permute")(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
+                               ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream(stream))
+    if rc:
+        _failed(rc)
 
 
 def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=None):
     """Gradient of permute's x (df_moe_permute_grad)."""
-    _done(lib().df_moe_permute_grad(_device(drows, pos, dx), _ptr(drows), _dtype(dtype), n_rows,
-                                    ldr, _ptr(pos), T, k, H, _ptr(dx), ldx, _stream(stream)))
+    dev, r, q, y = _place(drows, pos, dx)
+    rc = _op("df_moe_permute_grad")(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
+                                    _stream(stream))
+    if rc:
+        _failed(rc)
 
 
 def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, stream=None):
     """Weighted rows back to their tokens (df_moe_unpermute)."""
-    _done(lib().df_moe_unpermute(_device(rows, pos, weights, y), _ptr(rows), _dtype(dtype), n_rows,
-                                 ldr, _ptr(pos), _ptr(weights), T, k, H, _ptr(y), ldy,
-                                 _stream(stream)))
+    dev, r, q, w, y = _place(rows, pos, weights, y)
+    rc = _op("df_moe_unpermute")(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
+                                 _stream(stream))
+    if rc:
+        _failed(rc)
 
 
 def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweights, lddy=0, ldr=0,
                    lddr=0, stream=None):
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
-    dev = _device(dy, rows, pos, weights, drows, dweights)
-    _done(lib().df_moe_unpermute_grad(dev, _ptr(dy), lddy, _ptr(rows), _dtype(dtype), n_rows, ldr,
-                                      _ptr(pos), _ptr(weights), T, k, H, _ptr(drows), lddr,
-                                      _ptr(dweights), _stream(stream)))
+    dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
+    rc = _op("df_moe_unpermute_grad")(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
+                                      lddr, dw, _stream(stream))
+    if rc:
+        _failed(rc)
 
 
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
-    _done(lib().df_moe_fp8_quantize(_device(x, codes, scales), _ptr(x), _dtype(dtype), M, K, ldx,
-                                    _ptr(codes), ldc, _ptr(scales), lds, _stream(stream)))
+    dev, x, c, s = _place(x, codes, scales)
+    rc = _op("df_moe_fp8_quantize")(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream(stream))
+    if rc:
+        _failed(rc)
 
 
 def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0, ldxs=0, ldw=0,
                ldy=0, status=None, stream=None):
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
-    dev = _device(x, xs, w, ws, offs, y, status)
-    _done(lib().df_moe_fp8_matmul(dev, _ptr(x), ldx, _ptr(xs), ldxs, _ptr(w), ldw, _ptr(ws),
-                                  _ptr(offs), G, M, N, K, 1 if transposed else 0, _ptr(y),
-                                  _dtype(dtype), ldy, _ptr(status), _stream(stream)))
+    dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
+    rc = _op("df_moe_fp8_matmul")(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
+                                  1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream(stream))
+    if rc:
+        _failed(rc)

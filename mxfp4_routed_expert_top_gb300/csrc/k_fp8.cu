@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cstring>
 
 #include "internal.h"
 #include "ops.h"
@@ -38,10 +39,6 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 template <>
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
-__device__ __forceinline__ bool finite_f32(float v) {
-  return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
-}
-
 // Two e4m3 codes, nearest even, saturating; NaN gives 0x7f.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -49,107 +46,181 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N <= 16 ? sizeof(T) * N : 16) PackQ {
-  T v[N];
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) < INFINITY; }
+
+// n / nb for n < 2^31: with 2^(shift - 1) < nb <= 2^shift and mul =
+// ceil(2^(31 + shift) / nb), the error n (mul nb - 2^(31 + shift)) stays below
+// 2^(31 + shift).
+struct FastDiv {
+  uint32_t mul, shift;
+  explicit FastDiv(uint32_t nb) : mul(0), shift(0) {
+    while ((1ull << shift) < nb) ++shift;
+    mul = (uint32_t)(((1ull << (31 + shift)) + nb - 1) / nb);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> (31 + shift));
+  }
 };
 
-// Half a warp a block of 128: eight values a lane. The quotient 448 x / m is
+// The scale and the codes of a block whose values lie N a lane in groups of
+// 32 >> SHIFT lanes; lanes without a value hold 0. The quotient 448 x / m is
 // taken as (0.875 x) / (m / 512), so that neither side overflows, by
 // Markstein's division (IBM J. R&D 34, 1990): with y the rounded reciprocal of
 // d, q0 = n y, q = q0 + (n - q0 d) y is the rounded quotient. Ties of bf16
 // and fp16 inputs therefore stay ties, and the codes are those of the exact
-// quotient. HBM bounds it: 128 (s + 1) + 4 bytes a block of s-byte values.
+// quotient. Blocks with NaN or infinities take a branch of their own.
+template <int N, int SHIFT>
+__device__ __forceinline__ float quantize_block(float (&v)[N], uint32_t (&code)[N / 2]) {
+  float m = 0x1p-100f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) m = max_abs_nan(m, v[n]);
+#pragma unroll
+  for (int o = 16 >> SHIFT; o; o >>= 1) m = max_abs_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool odd = !finite_f32(m);
+  if (__any_sync(0xffffffffu, odd)) {
+    if (odd) {  // the same in all of the block's lanes
+      m = 0x1p-100f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) m = fmaxf(m, finite_f32(v[n]) ? fabsf(v[n]) : 0.f);
+    }
+#pragma unroll
+    for (int o = 16 >> SHIFT; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (!finite_f32(v[n])) v[n] = __uint_as_float(0x7fffffffu);
+  }
+  const float d = m * 0x1p-9f, y = __frcp_rn(d);
+#pragma unroll
+  for (int n = 0; n < N; n += 2) {
+    float q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float num = v[n + i] * 0.875f, q0 = num * y;
+      q[i] = fmaf(fmaf(-q0, d, num), y, q0);
+    }
+    code[n / 2] = e4m3x2(q[0], q[1]);
+  }
+  return __fdiv_rn(m, 448.f);
+}
+
+// Rows of whole 32-byte pieces: eight lanes a block, sixteen values a lane,
+// two blocks in flight. HBM should bound it (128 (s + 1) + 4 bytes a block of
+// s-byte values); issue slots did as long as a value cost 24 instructions
+// (index division, tests for finiteness, 16 lanes a block): 65536 x 1536 bf16
+// 94 us, now 56 (305 MB).
 constexpr int kQThreads = 256, kQUnroll = 2;
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantizeArgs p, int nb, uint32_t total) {
-  const int hl = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const FastDiv by_nb) {
+  constexpr int R = sizeof(T) / 2;  // 32-byte loads a lane
+  const int l = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3;
+  const uint32_t warps = gridDim.x * (kQThreads / 32);
+  const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const T* x = static_cast<const T*>(p.x);
+  for (uint64_t w0 = warp; 4 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
+    uint32_t raw[kQUnroll][R][8], row[kQUnroll], blk[kQUnroll];
+    bool there[kQUnroll], mine[kQUnroll];
+#pragma unroll
+    for (int u = 0; u < kQUnroll; ++u) {  // lane l: columns 16 l .. 16 l + 15
+      const uint64_t g = 4 * (w0 + (uint64_t)u * warps) + sub;
+      there[u] = g < total;
+      row[u] = by_nb(there[u] ? (uint32_t)g : 0);
+      blk[u] = (there[u] ? (uint32_t)g : 0) - row[u] * nb;
+      mine[u] = there[u] && (int)(128 * blk[u]) + 16 * l < p.K;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) raw[u][i][n] = 0;
+      if (mine[u]) {
+        const char* q = reinterpret_cast<const char*>(x + (int64_t)row[u] * p.ldx + 128 * blk[u] + 16 * l);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(raw[u][i][0]), "=r"(raw[u][i][1]), "=r"(raw[u][i][2]), "=r"(raw[u][i][3]),
+                         "=r"(raw[u][i][4]), "=r"(raw[u][i][5]), "=r"(raw[u][i][6]), "=r"(raw[u][i][7])
+                       : "l"(q + 32 * i));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kQUnroll; ++u) {
+      T e[16];
+      memcpy(e, raw[u], sizeof e);
+      float v[16];
+#pragma unroll
+      for (int n = 0; n < 16; ++n) v[n] = to_f32<T>(e[n]);
+      uint32_t code[8];
+      const float scale = quantize_block<16, 2>(v, code);
+      if (mine[u])
+        *reinterpret_cast<uint4*>(p.codes + (int64_t)row[u] * p.ldc + 128 * blk[u] + 16 * l) =
+            make_uint4(code[0] | code[1] << 16, code[2] | code[3] << 16, code[4] | code[5] << 16,
+                       code[6] | code[7] << 16);
+      if (there[u] && l == 0) p.scales[(int64_t)row[u] * p.lds + blk[u]] = scale;
+    }
+  }
+}
+
+// Any other rows: half a warp a block, value by value, two blocks in flight
+// (14001 x 7167 bf16: 109 us; a whole warp a block, twice the exchanges a
+// value, 148; eight lanes, 16-byte pieces a load, 126).
+template <typename T>
+__global__ void __launch_bounds__(kQThreads)
+fp8_quantize_odd_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const FastDiv by_nb) {
+  const int l = threadIdx.x & 15, sub = (threadIdx.x >> 4) & 1;
   const uint32_t warps = gridDim.x * (kQThreads / 32);
   const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const T* x = static_cast<const T*>(p.x);
   for (uint64_t w0 = warp; 2 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
     float v[kQUnroll][8];
-    uint32_t row[kQUnroll];
-    int col[kQUnroll];
+    uint32_t row[kQUnroll], blk[kQUnroll];
     bool there[kQUnroll];
 #pragma unroll
     for (int u = 0; u < kQUnroll; ++u) {
-      const uint64_t g = 2 * (w0 + (uint64_t)u * warps) + half;
+      const uint64_t g = 2 * (w0 + (uint64_t)u * warps) + sub;
       there[u] = g < total;
-      row[u] = there[u] ? (uint32_t)g / (uint32_t)nb : 0;
-      col[u] = there[u] ? ((uint32_t)g - row[u] * nb) * 128 : 0;
-      const T* src = x + (int64_t)row[u] * p.ldx + col[u];
-      if (VEC) {  // lane hl: columns 8 hl .. 8 hl + 7 (K is a multiple of 8)
-        if (there[u] && col[u] + 8 * hl < p.K) {
-          const PackQ<T, 16 / sizeof(T)>* q = reinterpret_cast<const PackQ<T, 16 / sizeof(T)>*>(src + 8 * hl);
-          constexpr int L = 16 / sizeof(T);
+      row[u] = by_nb(there[u] ? (uint32_t)g : 0);
+      blk[u] = (there[u] ? (uint32_t)g : 0) - row[u] * nb;
+      const T* src = x + (int64_t)row[u] * p.ldx + 128 * blk[u];
 #pragma unroll
-          for (int i = 0; i < 8 / L; ++i) {
-            const PackQ<T, L> r = q[i];
-#pragma unroll
-            for (int n = 0; n < L; ++n) v[u][i * L + n] = to_f32<T>(r.v[n]);
-          }
-        } else {
-#pragma unroll
-          for (int n = 0; n < 8; ++n) v[u][n] = 0.f;
-        }
-      } else {  // lane hl: columns hl, hl + 16, ...
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int c = hl + 16 * n;
-          v[u][n] = there[u] && col[u] + c < p.K ? to_f32<T>(src[c]) : 0.f;
-        }
+      for (int n = 0; n < 8; ++n) {
+        const int c = l + 16 * n;
+        v[u][n] = there[u] && (int)(128 * blk[u]) + c < p.K ? to_f32<T>(src[c]) : 0.f;
       }
     }
 #pragma unroll
     for (int u = 0; u < kQUnroll; ++u) {
-      float m = 0x1p-100f;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) m = fmaxf(m, finite_f32(v[u][n]) ? fabsf(v[u][n]) : 0.f);
-#pragma unroll
-      for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float d = m * 0x1p-9f, y = __frcp_rn(d);
       uint32_t code[4];
-#pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        float q[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float num = v[u][n + i] * 0.875f, q0 = num * y;
-          q[i] = fmaf(fmaf(-q0, d, num), y, q0);
-          if (!finite_f32(v[u][n + i])) q[i] = __uint_as_float(0x7fffffffu);
-        }
-        code[n / 2] = e4m3x2(q[0], q[1]);
-      }
+      const float scale = quantize_block<8, 1>(v[u], code);
       if (!there[u]) continue;
-      uint8_t* dst = p.codes + (int64_t)row[u] * p.ldc + col[u];
-      if (VEC) {
-        if (col[u] + 8 * hl < p.K)
-          *reinterpret_cast<uint2*>(dst + 8 * hl) =
-              make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-      } else {
+      uint8_t* dst = p.codes + (int64_t)row[u] * p.ldc + 128 * blk[u];
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-          if (col[u] + hl + 16 * n < p.K) dst[hl + 16 * n] = (uint8_t)(code[n / 2] >> (8 * (n & 1)));
-      }
-      if (hl == 0) p.scales[(int64_t)row[u] * p.lds + col[u] / 128] = __fdiv_rn(m, 448.f);
+      for (int n = 0; n < 8; ++n)
+        if ((int)(128 * blk[u]) + l + 16 * n < p.K) dst[l + 16 * n] = (uint8_t)(code[n / 2] >> (8 * (n & 1)));
+      if (l == 0) p.scales[(int64_t)row[u] * p.lds + blk[u]] = scale;
     }
   }
 }
 
 template <typename T>
 cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
-  const int nb = (p.K + 127) / 128;
+  const uint32_t nb = (uint32_t)((p.K + 127) / 128);
   const uint64_t total = (uint64_t)p.M * nb;
-  const uint64_t blocks = (total + 2 * (kQThreads / 32) - 1) / (2 * (kQThreads / 32));
-  const uint64_t most = (uint64_t)sms * 8 * 4;
+  const uint64_t blocks = (total + 4 * (kQThreads / 32) - 1) / (4 * (kQThreads / 32));
+  const uint64_t most = (uint64_t)sms * 24;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-  const bool vec = !(((uintptr_t)p.x | (uint64_t)(p.ldx * (int64_t)sizeof(T))) & 15) &&
-                   !(((uintptr_t)p.codes | (uint64_t)p.ldc) & 7) && p.K % 8 == 0;
+  const bool vec = !(((uintptr_t)p.x | (uint64_t)(p.ldx * (int64_t)sizeof(T))) & 31) &&
+                   !(((uintptr_t)p.codes | (uint64_t)p.ldc) & 15) && p.K % 16 == 0;
+  const FastDiv by_nb(nb);
   if (vec)
-    fp8_quantize_kernel<T, true><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total);
+    fp8_quantize_kernel<T><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total, by_nb);
   else
-    fp8_quantize_kernel<T, false><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total);
+    fp8_quantize_odd_kernel<T><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total, by_nb);
   return cudaGetLastError();
 }
 
