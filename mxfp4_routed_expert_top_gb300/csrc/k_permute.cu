@@ -89,12 +89,18 @@ __device__ __forceinline__ void copy_scales(const PermuteArgs& p, int t0, int t1
 // One launch for up to kSelfCount assignments: every block counts all of them
 // itself (before its own and from its own on), so no block waits for another
 // and nothing goes through global memory. Block (b, c) then ranks its own
-// tokens' assignments and copies column range c of their rows.
+// tokens' assignments and copies column range c of their rows. A block of
+// 1024 threads an SM halves what an SM counts against two of 512; clusters
+// of eight that shared the counting through distributed shared memory were
+// slower (4096 tokens x 16 rows of 256 bf16: 17.5 us, two blocks 21, clusters
+// 31). Writes bound the large calls: with rows of 7168 (999 MB, 940 of them
+// written) take 189 us, of which bulk copies through shared memory saved nothing.
+constexpr int kSelfThreads = 1024;
 constexpr int kSelfCount = 65536;
 constexpr int kSelfChunk = 1024;  // assignments a block may own
 
 template <typename V>
-__global__ void __launch_bounds__(kPermThreads)
+__global__ void __launch_bounds__(kSelfThreads)
 permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per_block) {
   __shared__ int before[kOpsMaxExperts], rest[kOpsMaxExperts];
   __shared__ int own_id[kSelfChunk], own_pos[kSelfChunk];
@@ -102,12 +108,12 @@ permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * tokens_per_block, t1 = min(p.T, t0 + tokens_per_block);
   const int A = p.T * p.k, a0 = t0 * p.k, a1 = t1 * p.k;
-  for (int e = tid; e < p.E; e += kPermThreads) before[e] = rest[e] = 0;
+  for (int e = tid; e < p.E; e += kSelfThreads) before[e] = rest[e] = 0;
   __syncthreads();
   if (((uintptr_t)p.ids & 15) == 0) {
     const int4* ids4 = reinterpret_cast<const int4*>(p.ids);
 #pragma unroll 4
-    for (int i = tid; i < A / 4; i += kPermThreads) {
+    for (int i = tid; i < A / 4; i += kSelfThreads) {
       const int4 e = ids4[i];
       const int ev[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
@@ -115,38 +121,34 @@ permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per
         if ((unsigned)ev[u] < (unsigned)p.E)
           atomicAdd(4 * i + u < a0 ? &before[ev[u]] : &rest[ev[u]], 1);
     }
-    for (int a = (A & ~3) + tid; a < A; a += kPermThreads) {
+    for (int a = (A & ~3) + tid; a < A; a += kSelfThreads) {
       const int e = p.ids[a];
       if ((unsigned)e < (unsigned)p.E) atomicAdd(a < a0 ? &before[e] : &rest[e], 1);
     }
   } else {
 #pragma unroll 4
-    for (int a = tid; a < A; a += kPermThreads) {
+    for (int a = tid; a < A; a += kSelfThreads) {
       const int e = p.ids[a];
       if ((unsigned)e < (unsigned)p.E) atomicAdd(a < a0 ? &before[e] : &rest[e], 1);
     }
   }
-  for (int i = tid; i < a1 - a0; i += kPermThreads) {
+  for (int i = tid; i < a1 - a0; i += kSelfThreads) {
     const int e = p.ids[a0 + i];
     own_id[i] = (unsigned)e < (unsigned)p.E ? e : -1;
   }
   __syncthreads();
   // before[e] becomes the row of this block's first assignment to expert e
-  static_assert(2 * kPermThreads == kOpsMaxExperts, "two experts a thread");
-  const int e0 = 2 * tid, e1 = e0 + 1;
-  const int c0 = e0 < p.E ? before[e0] + rest[e0] : 0, c1 = e1 < p.E ? before[e1] + rest[e1] : 0;
-  const int o0 = block_scan(c0 + c1, warp_sums), o1 = o0 + c0;
+  static_assert(kSelfThreads == kOpsMaxExperts, "one expert a thread");
+  const int count = tid < p.E ? before[tid] + rest[tid] : 0;
+  const int start = block_scan(count, warp_sums);
   const bool writer = blockIdx.y == 0;
-  if (e0 < p.E) before[e0] += o0;
-  if (e1 < p.E) before[e1] += o1;
+  if (tid < p.E) before[tid] += start;
   if (writer && blockIdx.x == 0) {
-    if (e0 < p.E) p.offs[e0] = o0;
-    if (e1 < p.E) p.offs[e1] = o1;
-    if (e0 == p.E - 1) p.offs[p.E] = o0 + c0;
-    if (e1 == p.E - 1) p.offs[p.E] = o1 + c1;
+    if (tid < p.E) p.offs[tid] = start;
+    if (tid == p.E - 1) p.offs[p.E] = start + count;
   }
   __syncthreads();
-  for (int i = tid; i < a1 - a0; i += kPermThreads) {
+  for (int i = tid; i < a1 - a0; i += kSelfThreads) {
     const int e = own_id[i];
     int q = -1;
     if (e >= 0) {
@@ -297,17 +299,16 @@ template <typename V>
 cudaError_t permute_v(const PermuteArgs& p, void* workspace, int sms, cudaStream_t s) {
   const int64_t A = (int64_t)p.T * p.k;
   const int vecs = (int)(p.bytes / (int64_t)sizeof(V));
-  const int want = 2 * sms;
   if (A <= kSelfCount) {
-    int tpb = (p.T + want - 1) / want;
+    int tpb = (p.T + sms - 1) / sms;
     if (tpb * p.k > kSelfChunk) tpb = kSelfChunk / p.k;
     const int gx = (p.T + tpb - 1) / tpb;
     // few tokens: their columns are split too, at least 64 values a block
-    int gy = want / gx;
+    int gy = sms / gx;
     if (gy > (vecs + 63) / 64) gy = (vecs + 63) / 64;
     if (gy < 1) gy = 1;
     const int vpb = (vecs + gy - 1) / gy;
-    permute_kernel<V><<<dim3(gx, gy), kPermThreads, 0, s>>>(p, tpb, vecs, vpb);
+    permute_kernel<V><<<dim3(gx, gy), kSelfThreads, 0, s>>>(p, tpb, vecs, vpb);
     return cudaGetLastError();
   }
   const int chunks = (int)permute_chunks(A);
@@ -371,7 +372,7 @@ __device__ __forceinline__ P load_once(const void* p) {
 // rounding at the end. HBM bounds it: 4096 tokens x 16 rows of 7168 bf16 (999
 // MB) take 153 us with four rows in flight, 184 with eight (fewer threads an
 // SM), 165 with two; with the rows in L1 it is 158.
-template <typename T, int N, bool WEIGHTED>
+template <typename T, int N, int U, bool WEIGHTED>
 __global__ void __launch_bounds__(128)
 unpermute_kernel(const UnpermuteArgs p, int nv) {
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
@@ -384,7 +385,6 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
   float acc[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] = 0.f;
-  constexpr int U = 4;
   for (int j0 = 0; j0 < p.k; j0 += U) {
     Pack<T, N> r[U];
     float wt[U];
@@ -412,15 +412,23 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
   *reinterpret_cast<Pack<T, N>*>(static_cast<T*>(p.y) + (int64_t)t * p.ldy + c) = out;
 }
 
+template <typename T, int N, int U>
+cudaError_t unpermute_u(const UnpermuteArgs& p, unsigned blocks, int nv, cudaStream_t s) {
+  if (p.weights)
+    unpermute_kernel<T, N, U, true><<<blocks, 128, 0, s>>>(p, nv);
+  else
+    unpermute_kernel<T, N, U, false><<<blocks, 128, 0, s>>>(p, nv);
+  return cudaGetLastError();
+}
+
 template <typename T, int N>
-cudaError_t unpermute_n(const UnpermuteArgs& p, cudaStream_t s) {
+cudaError_t unpermute_n(const UnpermuteArgs& p, int sms, cudaStream_t s) {
   const int nv = p.H / N;
   const int64_t blocks = ((int64_t)p.T * nv + 127) / 128;
-  if (p.weights)
-    unpermute_kernel<T, N, true><<<(unsigned)blocks, 128, 0, s>>>(p, nv);
-  else
-    unpermute_kernel<T, N, false><<<(unsigned)blocks, 128, 0, s>>>(p, nv);
-  return cudaGetLastError();
+  // at most two blocks an SM: sixteen rows in flight, as latency is all there
+  // is (one token x 16 rows of 7168: 5.0 us a call against 5.75)
+  if (blocks <= 2 * sms && p.k > 4) return unpermute_u<T, N, 16>(p, (unsigned)blocks, nv, s);
+  return unpermute_u<T, N, 4>(p, (unsigned)blocks, nv, s);
 }
 
 // A block per token and group of J of its assignments: dy is read once a
@@ -507,14 +515,14 @@ int vector_bytes(uint64_t bits, int most) {
 }
 
 template <typename T>
-cudaError_t unpermute_t(const UnpermuteArgs& p, cudaStream_t s) {
+cudaError_t unpermute_t(const UnpermuteArgs& p, int sms, cudaStream_t s) {
   constexpr int B = sizeof(T);
   const uint64_t bits = (uint64_t)p.rows | (uint64_t)p.y | (uint64_t)(p.ldr * B) |
                         (uint64_t)(p.ldy * B) | (uint64_t)((int64_t)p.H * B);
   const int n = vector_bytes(bits, 16) / B;
-  if (n >= 16 / B) return unpermute_n<T, 16 / B>(p, s);
-  if (n >= 8 / B) return unpermute_n<T, 8 / B>(p, s);
-  return unpermute_n<T, 1>(p, s);
+  if (n >= 16 / B) return unpermute_n<T, 16 / B>(p, sms, s);
+  if (n >= 8 / B) return unpermute_n<T, 8 / B>(p, sms, s);
+  return unpermute_n<T, 1>(p, sms, s);
 }
 
 template <typename T>
@@ -548,10 +556,10 @@ cudaError_t launch_permute(const PermuteArgs& p, void* workspace, int sms, cudaS
   }
 }
 
-cudaError_t launch_unpermute(const UnpermuteArgs& p, int dtype, cudaStream_t s) {
-  return dtype == 0   ? unpermute_t<__nv_bfloat16>(p, s)
-         : dtype == 1 ? unpermute_t<__half>(p, s)
-                      : unpermute_t<float>(p, s);
+cudaError_t launch_unpermute(const UnpermuteArgs& p, int dtype, int sms, cudaStream_t s) {
+  return dtype == 0   ? unpermute_t<__nv_bfloat16>(p, sms, s)
+         : dtype == 1 ? unpermute_t<__half>(p, sms, s)
+                      : unpermute_t<float>(p, sms, s);
 }
 
 cudaError_t launch_unpermute_grad(const UnpermuteGradArgs& p, int dtype, int sms,

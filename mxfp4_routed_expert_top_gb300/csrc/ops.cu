@@ -112,7 +112,7 @@ int unpermute(int device, const void* rows, int dtype, int64_t n_rows, int64_t l
   OnDevice on(device);
   if (on.rc()) return on.rc();
   const dfm::UnpermuteArgs a{rows, pos, weights, y, (int)T, k, (int)H, n_rows, ldr, ldy};
-  return launched("unpermute launch", dfm::launch_unpermute(a, dtype, (cudaStream_t)stream));
+  return launched("unpermute launch", dfm::launch_unpermute(a, dtype, on.sms(), (cudaStream_t)stream));
 }
 
 }  // namespace

@@ -38,7 +38,7 @@ struct UnpermuteArgs {
   int T, k, H;
   int64_t n_rows, ldr, ldy;  // in elements
 };
-cudaError_t launch_unpermute(const UnpermuteArgs& p, int dtype, cudaStream_t s);
+cudaError_t launch_unpermute(const UnpermuteArgs& p, int dtype, int sms, cudaStream_t s);
 
 struct UnpermuteGradArgs {
   const void* dy;
