@@ -264,7 +264,7 @@ struct Fp8Cfg {
   static constexpr int NS = XA ? 4 : 5;                  // stages
   static constexpr int AS = XA ? 2 : 4;                  // accumulators
   static constexpr uint32_t Cols = DN * AS;
-  static constexpr int Scales = XA ? 2 * 128 : NT;       // of a block: rows (x 2 blocks of n)
+  static constexpr int Scales = XA ? 128 : NT;           // a block's scales of x
   static constexpr int CtasPerSm = XA ? 1 : 2;
 };
 
@@ -281,8 +281,9 @@ struct Fp8Params {
 template <int NT>
 struct Fp8Smem {
   using C = Fp8Cfg<NT>;
-  uint8_t out[C::EW][512];                  // what a warp rearranges of y
-  float sc[2][kFBatch][C::Scales + 4];      // scales of two batches of blocks
+  uint8_t out[C::EW][C::XA ? 2048 : 512];   // what a warp rearranges of y
+  float sc[2][kFBatch][C::Scales + 4];      // scales of two batches of blocks: xs (times ws unless XA)
+  float scw[2][kFBatch][2];                 // XA: ws of the unit's two blocks of n
   uint64_t full[C::NS], empty[C::NS];
   uint64_t acc_full[C::AS], acc_empty[C::AS];
   uint64_t sc_full[2], sc_empty[2];
@@ -652,8 +653,8 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       // the MMAs issued must land before the tensor memory is released
       if (it > 0) (void)bar_wait(empty + 8 * (s ? s - 1 : NS - 1), s ? phase : phase ^ 1);
     } else {
-      // ---- scales: xs ws of eight blocks at a time, one value a thread and
-      // step: block i % 8, row i / 8
+      // ---- scales: xs ws of kFBatch blocks at a time, one value a thread
+      // and step: block i % kFBatch, row i / kFBatch
       const int st = tid - (EW + 2) * 32;
       int batch = 0;
       bool ok = true;
@@ -661,7 +662,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
         const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
         const int nb = un.n0 / kFK;
         const float* ws = p.ws + (int64_t)un.g * p.NB * p.KB;
-                for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
+        for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
           const int buf = batch & 1;
           ok = batch < 2 || mbar_wait(&sm->sc_empty[buf], ((batch >> 1) - 1) & 1);
           if (!__all_sync(0xffffffffu, ok)) {
@@ -675,25 +676,24 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           for (int h = 0; h < (C::XA ? 2 : 1); ++h)
             if (b < kb1 && nb + h < p.NB)
               wv[h] = TRANS ? ws[(int64_t)b * p.NB + nb + h] : ws[(int64_t)(nb + h) * p.KB + b];
+          if (C::XA && st < kFBatch) {
+            sm->scw[buf][st][0] = wv[0];
+            sm->scw[buf][st][1] = wv[1];
+          }
           const float* xs = p.xs + un.row0 * p.ldxs + b;
           constexpr int PER = (C::XA ? 128 : NT) * kFBatch / 64, U = PER < 8 ? PER : 8;
           for (int i0 = 0; i0 < PER; i0 += U) {
             float v[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-              const int r = (st >> 3) + 8 * (i0 + i);
+              const int r = st / kFBatch + 64 / kFBatch * (i0 + i);
               v[i] = b < kb1 && r < un.rows ? xs[r * p.ldxs] : 0.f;
             }
             float* sc = sm->sc[buf][st & (kFBatch - 1)];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-              const int r = (st >> 3) + 8 * (i0 + i);
-              if (C::XA) {
-                sc[r] = v[i] * wv[0];
-                sc[128 + r] = v[i] * wv[1];
-              } else {
-                sc[scale_slot(r)] = v[i] * wv[0];
-              }
+              const int r = st / kFBatch + 64 / kFBatch * (i0 + i);
+              sc[C::XA ? r : scale_slot(r)] = C::XA ? v[i] : v[i] * wv[0];
             }
           }
           __syncwarp();
@@ -724,7 +724,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           const int blocks = min(kFBatch, kb1 - kb);
           for (int b = 0; b < blocks; ++b, ++it) {
             const int as = it % AS;
-            const float s = sm->sc[buf][b][(c0 & 128) + l0 + lane];
+            const float s = sm->sc[buf][b][l0 + lane] * sm->scw[buf][b][c0 >> 7];
             ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1);
             if (!ok) continue;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -762,19 +762,31 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
             for (int i = 0; i < CW; i += 32 / (int)sizeof(Y)) store_sector(y + i, &acc[i]);
           }
         } else {
-          // four columns at a time through shared memory, so that a store
-          // covers eight rows of four
-          float* stage = reinterpret_cast<float*>(sm->out[warp]);
+          // 64 bytes of each row at a time through shared memory, so that a
+          // store covers one or two rows (32 rows each, value by value, it
+          // took 54 us where this takes 25: 3006 x 2050 x 1111, fp32);
+          // piece q of row r stands at q ^ (r / 2) % 4
+          uint8_t* stage = sm->out[warp];
           const int rows = un.rows - l0;
           Y* base = static_cast<Y*>(p.y) + (un.row0 + l0) * p.ldy + n0;
+          constexpr int CC = 64 / (int)sizeof(Y), RR = 32 / CC > 0 ? 32 / CC : 1;  // columns a piece, rows a store
 #pragma unroll
-          for (int i = 0; i < CW; i += 4) {
-            *reinterpret_cast<float4*>(stage + 4 * lane) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-            __syncwarp();
+          for (int i = 0; i < CW; i += CC) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int r = 8 * q + (lane >> 2), c = lane & 3;
-              if (r < rows && n0 + i + c < p.N) put_y(base + r * p.ldy + i + c, stage[32 * q + lane]);
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = sizeof(Y) == 4 ? __float_as_uint(acc[i + (4 * q + e) % CC])
+                                      : pack16<Y>(acc[i + (8 * q + 2 * e) % CC], acc[i + (8 * q + 2 * e + 1) % CC]);
+              *reinterpret_cast<uint4*>(stage + 64 * lane + 16 * (q ^ ((lane >> 1) & 3))) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            const int c = lane % CC, at = c * (int)sizeof(Y);
+            if (n0 + i + c < p.N) {
+#pragma unroll 8
+              for (int r = lane / CC; r < min(rows, 32); r += RR)
+                base[r * p.ldy + i + c] = *reinterpret_cast<const Y*>(stage + 64 * r + 16 * ((at >> 4) ^ ((r >> 1) & 3)) + (at & 15));
             }
             __syncwarp();
           }
