@@ -124,6 +124,7 @@ fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const Fas
   const uint32_t warps = gridDim.x * (kQThreads / 32);
   const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const T* x = static_cast<const T*>(p.x);
+  pdl_wait();
   for (uint64_t w0 = warp; 4 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
     uint32_t raw[kQUnroll][R][8], row[kQUnroll], blk[kQUnroll];
     bool there[kQUnroll], mine[kQUnroll];
@@ -142,7 +143,7 @@ fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const Fas
         const char* q = reinterpret_cast<const char*>(x + (int64_t)row[u] * p.ldx + 128 * blk[u] + 16 * l);
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                        : "=r"(raw[u][i][0]), "=r"(raw[u][i][1]), "=r"(raw[u][i][2]), "=r"(raw[u][i][3]),
                          "=r"(raw[u][i][4]), "=r"(raw[u][i][5]), "=r"(raw[u][i][6]), "=r"(raw[u][i][7])
                        : "l"(q + 32 * i));
@@ -176,6 +177,7 @@ fp8_quantize_odd_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const
   const uint32_t warps = gridDim.x * (kQThreads / 32);
   const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const T* x = static_cast<const T*>(p.x);
+  pdl_wait();
   for (uint64_t w0 = warp; 2 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
     float v[kQUnroll][8];
     uint32_t row[kQUnroll], blk[kQUnroll];
@@ -217,11 +219,10 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
   const bool vec = !(((uintptr_t)p.x | (uint64_t)(p.ldx * (int64_t)sizeof(T))) & 31) &&
                    !(((uintptr_t)p.codes | (uint64_t)p.ldc) & 15) && p.K % 16 == 0;
   const FastDiv by_nb(nb);
-  if (vec)
-    fp8_quantize_kernel<T><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total, by_nb);
-  else
-    fp8_quantize_odd_kernel<T><<<grid, kQThreads, 0, s>>>(p, nb, (uint32_t)total, by_nb);
-  return cudaGetLastError();
+  return vec ? launch_after_previous(fp8_quantize_kernel<T>, dim3(grid), dim3(kQThreads), 0, s, p, nb, (uint32_t)total,
+                                     by_nb)
+             : launch_after_previous(fp8_quantize_odd_kernel<T>, dim3(grid), dim3(kQThreads), 0, s, p, nb,
+                                     (uint32_t)total, by_nb);
 }
 
 // ---- product --------------------------------------------------------------------
@@ -511,6 +512,10 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   int* offs = tiles + p.G + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.w) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.x) : "memory");
+  }
   if (warp == EW + 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(C::Cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -531,6 +536,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     sm->err = 0;
     fence_barrier_init();
   }
+  pdl_wait();  // the kernel before this one is complete
   // the groups' first rows, kept inside [0, M] whatever the caller's array
   // holds, and their tiles
   const int M = (int)p.M;
@@ -1021,13 +1027,15 @@ const char* fp8_launch(const Fp8MatmulArgs& a, int sms, cudaStream_t s) {
   cfg.blockDim = dim3(C::NTHR);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }

@@ -15,6 +15,13 @@
 // T + n rows once each (n valid assignments), so HBM bounds them at large T
 // and the launch at small T. Every place is counted, never taken by an atomic
 // whose order could show, and every sum has a fixed order.
+//
+// Every kernel here and in k_fp8.cu is launched as a programmatic dependent of
+// the one before it: its blocks may start while that one's memory is flushed,
+// and wait (griddepcontrol.wait) before they touch global memory. Their loads
+// are ordinary ones (not .nc): the lines may have been in L1 since before the
+// wait. None of them lets its own dependents start early: a kernel of the
+// layer that reads its input without waiting relies on that.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -22,6 +29,7 @@
 
 #include "internal.h"
 #include "ops.h"
+#include "pipeline.cuh"
 
 namespace dfm {
 namespace {
@@ -109,6 +117,7 @@ permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per
   const int t0 = blockIdx.x * tokens_per_block, t1 = min(p.T, t0 + tokens_per_block);
   const int A = p.T * p.k, a0 = t0 * p.k, a1 = t1 * p.k;
   for (int e = tid; e < p.E; e += kSelfThreads) before[e] = rest[e] = 0;
+  pdl_wait();
   __syncthreads();
   if (((uintptr_t)p.ids & 15) == 0) {
     const int4* ids4 = reinterpret_cast<const int4*>(p.ids);
@@ -170,10 +179,11 @@ permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per
 // ---- more assignments: counted per chunk, summed over the chunks, placed ----
 // counts [chunks][E]: how many of chunk c go to expert e.
 __global__ void __launch_bounds__(kPermThreads)
-permute_count_kernel(const int32_t* __restrict__ ids, int64_t A, int E, int64_t chunk,
-                     int32_t* __restrict__ counts) {
+permute_count_kernel(const int32_t* ids, int64_t A, int E, int64_t chunk,
+                     int32_t* counts) {
   __shared__ int cnt[kOpsMaxExperts];
   for (int e = threadIdx.x; e < E; e += kPermThreads) cnt[e] = 0;
+  pdl_wait();
   __syncthreads();
   const int64_t a0 = blockIdx.x * chunk, a1 = a0 + chunk < A ? a0 + chunk : A;
 #pragma unroll 4
@@ -189,13 +199,14 @@ permute_count_kernel(const int32_t* __restrict__ ids, int64_t A, int E, int64_t 
 // row behind the last chunk the totals. A block holds 32 experts, one a lane,
 // and each of its 32 warps a range of chunks.
 __global__ void __launch_bounds__(1024)
-permute_scan_kernel(int32_t* __restrict__ counts, int E, int chunks) {
+permute_scan_kernel(int32_t* counts, int E, int chunks) {
   __shared__ int part[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + lane;
   const int per = (chunks + 31) / 32;
   const int c0 = min(warp * per, chunks), c1 = min(c0 + per, chunks);
   int sum = 0;
+  pdl_wait();
   if (e < E) {
 #pragma unroll 4
     for (int c = c0; c < c1; ++c) sum += counts[(int64_t)c * E + e];
@@ -220,9 +231,9 @@ permute_scan_kernel(int32_t* __restrict__ counts, int E, int chunks) {
 // at a time, ranking equal experts within the 32 by lane.
 constexpr int kPlaceWarps = kPermThreads / 32;
 __global__ void __launch_bounds__(kPermThreads)
-permute_place_kernel(const int32_t* __restrict__ ids, int64_t A, int E, int64_t chunk, int chunks,
-                     const int32_t* __restrict__ counts, int32_t* __restrict__ offs,
-                     int32_t* __restrict__ pos, int32_t* __restrict__ src) {
+permute_place_kernel(const int32_t* ids, int64_t A, int E, int64_t chunk, int chunks,
+                     const int32_t* counts, int32_t* offs,
+                     int32_t* pos, int32_t* src) {
   extern __shared__ int part[];  // [kPlaceWarps][E]
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -232,6 +243,7 @@ permute_place_kernel(const int32_t* __restrict__ ids, int64_t A, int E, int64_t 
   const int64_t w1 = w0 + per < a1 ? w0 + per : a1;
   int* const mine = part + warp * E;
   for (int i = tid; i < kPlaceWarps * E; i += kPermThreads) part[i] = 0;
+  pdl_wait();
   __syncthreads();
   for (int64_t a = w0; a < w1; a += 32) {
     const int e = a + lane < w1 ? ids[a + lane] : -1;
@@ -283,6 +295,7 @@ permute_place_kernel(const int32_t* __restrict__ ids, int64_t A, int E, int64_t 
 template <typename V>
 __global__ void __launch_bounds__(kPermThreads)
 permute_copy_kernel(const PermuteArgs p, int vecs) {
+  pdl_wait();
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     const int32_t* at = p.pos + (int64_t)t * p.k;
     copy_rows<V>(p, t, t + 1, at, 0, vecs);
@@ -308,23 +321,27 @@ cudaError_t permute_v(const PermuteArgs& p, void* workspace, int sms, cudaStream
     if (gy > (vecs + 63) / 64) gy = (vecs + 63) / 64;
     if (gy < 1) gy = 1;
     const int vpb = (vecs + gy - 1) / gy;
-    permute_kernel<V><<<dim3(gx, gy), kSelfThreads, 0, s>>>(p, tpb, vecs, vpb);
-    return cudaGetLastError();
+    return launch_after_previous(permute_kernel<V>, dim3(gx, gy), dim3(kSelfThreads), 0, s, p, tpb, vecs, vpb);
   }
   const int chunks = (int)permute_chunks(A);
   int64_t chunk = (A + chunks - 1) / chunks;
   int32_t* counts = static_cast<int32_t*>(workspace);
-  permute_count_kernel<<<chunks, kPermThreads, 0, s>>>(p.ids, A, p.E, chunk, counts);
-  permute_scan_kernel<<<(p.E + 31) / 32, 1024, 0, s>>>(counts, p.E, chunks);
   const size_t smem = (size_t)kPlaceWarps * p.E * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(permute_place_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kPlaceWarps * kOpsMaxExperts * (int)sizeof(int));
-  if (e != cudaSuccess) return e;
-  permute_place_kernel<<<chunks, kPermThreads, smem, s>>>(p.ids, A, p.E, chunk, chunks, counts,
-                                                          p.offs, p.pos, p.src);
-  permute_copy_kernel<V><<<4 * sms < p.T ? 4 * sms : p.T, kPermThreads, 0, s>>>(p, vecs);
-  return cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_after_previous(permute_count_kernel, dim3(chunks), dim3(kPermThreads), 0, s, p.ids, A, p.E, chunk,
+                              counts);
+  if (e == cudaSuccess)
+    e = launch_after_previous(permute_scan_kernel, dim3((p.E + 31) / 32), dim3(1024), 0, s, counts, p.E, chunks);
+  if (e == cudaSuccess)
+    e = launch_after_previous(permute_place_kernel, dim3(chunks), dim3(kPermThreads), smem, s, p.ids, A, p.E, chunk,
+                              chunks, counts, p.offs, p.pos, p.src);
+  if (e == cudaSuccess)
+    e = launch_after_previous(permute_copy_kernel<V>, dim3(4 * sms < p.T ? 4 * sms : p.T), dim3(kPermThreads), 0, s,
+                              p, vecs);
+  return e;
 }
 
 // ---- rows of a type as fp32 vectors -------------------------------------------
@@ -357,7 +374,7 @@ __device__ __forceinline__ P load_once(const void* p) {
   P r;
   if constexpr (sizeof(P) == 16) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     memcpy(&r, &v, 16);
@@ -375,6 +392,7 @@ __device__ __forceinline__ P load_once(const void* p) {
 template <typename T, int N, int U, bool WEIGHTED>
 __global__ void __launch_bounds__(128)
 unpermute_kernel(const UnpermuteArgs p, int nv) {
+  pdl_wait();
   const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   const int t = (int)(i / nv);
   if (t >= p.T) return;
@@ -414,11 +432,8 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
 
 template <typename T, int N, int U>
 cudaError_t unpermute_u(const UnpermuteArgs& p, unsigned blocks, int nv, cudaStream_t s) {
-  if (p.weights)
-    unpermute_kernel<T, N, U, true><<<blocks, 128, 0, s>>>(p, nv);
-  else
-    unpermute_kernel<T, N, U, false><<<blocks, 128, 0, s>>>(p, nv);
-  return cudaGetLastError();
+  return p.weights ? launch_after_previous(unpermute_kernel<T, N, U, true>, dim3(blocks), dim3(128), 0, s, p, nv)
+                   : launch_after_previous(unpermute_kernel<T, N, U, false>, dim3(blocks), dim3(128), 0, s, p, nv);
 }
 
 template <typename T, int N>
@@ -439,6 +454,7 @@ template <typename T, int N, int J>
 __global__ void __launch_bounds__(kGradThreads)
 unpermute_grad_kernel(const UnpermuteGradArgs p, int groups) {
   __shared__ float part[kGradThreads / 32][J];
+  pdl_wait();
   const int t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * J;
   const T* dy = static_cast<const T*>(p.dy) + (int64_t)t * p.lddy;
   const T* rows = static_cast<const T*>(p.rows);
@@ -491,9 +507,8 @@ unpermute_grad_kernel(const UnpermuteGradArgs p, int groups) {
 template <typename T, int N, int J>
 cudaError_t unpermute_grad_j(const UnpermuteGradArgs& p, cudaStream_t s) {
   const int groups = (p.k + J - 1) / J;
-  unpermute_grad_kernel<T, N, J>
-      <<<(unsigned)((int64_t)p.T * groups), kGradThreads, 0, s>>>(p, groups);
-  return cudaGetLastError();
+  return launch_after_previous(unpermute_grad_kernel<T, N, J>, dim3((unsigned)((int64_t)p.T * groups)),
+                               dim3(kGradThreads), 0, s, p, groups);
 }
 
 template <typename T, int N>
