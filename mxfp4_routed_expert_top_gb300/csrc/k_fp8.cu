@@ -55,20 +55,6 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
 
 __device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) < INFINITY; }
 
-// n / nb for n < 2^31: with 2^(shift - 1) < nb <= 2^shift and mul =
-// ceil(2^(31 + shift) / nb), the error n (mul nb - 2^(31 + shift)) stays below
-// 2^(31 + shift).
-struct FastDiv {
-  uint32_t mul, shift;
-  explicit FastDiv(uint32_t nb) : mul(0), shift(0) {
-    while ((1ull << shift) < nb) ++shift;
-    mul = (uint32_t)(((1ull << (31 + shift)) + nb - 1) / nb);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-    return (uint32_t)(((uint64_t)n * mul) >> (31 + shift));
-  }
-};
-
 // The scale and the codes of a block whose values lie N a lane in groups of
 // 32 >> SHIFT lanes; lanes without a value hold 0. The quotient 448 x / m is
 // taken as (0.875 x) / (m / 512), so that neither side overflows, by

@@ -80,6 +80,43 @@ __device__ __forceinline__ void copy_rows(const PermuteArgs& p, int t0, int t1, 
   }
 }
 
+// The same for rows that are not aligned to 4 bytes, in words w of [w0, w1):
+// word w of a row holds the bytes c .. c + 3 with c = 4 (w - 1) + a, where a
+// is what the row lacks to a 4-byte boundary, so that its store is aligned;
+// each value comes from three aligned words of x by a funnel shift (words
+// without a byte of the row are not read). The first and last words of a row
+// are stored byte by byte.
+__device__ __forceinline__ void copy_rows_odd(const PermuteArgs& p, int t0, int t1, const int32_t* pos, int w0,
+                                              int w1) {
+  const int nw = w1 - w0, items = (t1 - t0) * nw, bytes = (int)p.bytes;
+  for (int i = threadIdx.x; i < items; i += blockDim.x) {
+    const int dt = i / nw, from = 4 * (w0 + i - dt * nw - 1);
+    const char* x = p.x + (int64_t)(t0 + dt) * p.ldx;
+    const int m = (int)((uintptr_t)(x + from) & 3);
+    uint32_t word[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const int c = from - m + 4 * n;  // bytes c .. c + 3 of the row
+      word[n] = c + 3 >= 0 && c < bytes ? *reinterpret_cast<const uint32_t*>(x + c) : 0;
+    }
+    const int32_t* at = pos + dt * p.k;
+    for (int j = 0; j < p.k; ++j) {
+      const int32_t q = at[j];
+      if (q < 0) continue;
+      char* row = p.rows + q * p.ldr;
+      const int a = (int)(-(uintptr_t)row & 3), c = from + a, s = m + a;
+      const uint32_t v = s < 4 ? __funnelshift_r(word[0], word[1], 8 * s) : __funnelshift_r(word[1], word[2], 8 * (s - 4));
+      if (c >= 0 && c + 4 <= bytes) {
+        *reinterpret_cast<uint32_t*>(row + c) = v;
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (c + b >= 0 && c + b < bytes) row[c + b] = (char)(v >> (8 * b));
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void copy_scales(const PermuteArgs& p, int t0, int t1,
                                             const int32_t* pos) {
   const int S = p.n_scales, items = (t1 - t0) * S;
@@ -172,7 +209,8 @@ permute_kernel(const PermuteArgs p, int tokens_per_block, int vecs, int vecs_per
   }
   __syncthreads();
   const int v0 = blockIdx.y * vecs_per_block;
-  copy_rows<V>(p, t0, t1, own_pos, v0, min(vecs, v0 + vecs_per_block));
+  if constexpr (sizeof(V) < 4) copy_rows_odd(p, t0, t1, own_pos, v0, min(vecs, v0 + vecs_per_block));
+  else copy_rows<V>(p, t0, t1, own_pos, v0, min(vecs, v0 + vecs_per_block));
   if (p.n_scales && writer) copy_scales(p, t0, t1, own_pos);
 }
 
@@ -298,7 +336,8 @@ permute_copy_kernel(const PermuteArgs p, int vecs) {
   pdl_wait();
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     const int32_t* at = p.pos + (int64_t)t * p.k;
-    copy_rows<V>(p, t, t + 1, at, 0, vecs);
+    if constexpr (sizeof(V) < 4) copy_rows_odd(p, t, t + 1, at, 0, vecs);
+    else copy_rows<V>(p, t, t + 1, at, 0, vecs);
     if (p.n_scales) copy_scales(p, t, t + 1, at);
   }
 }
@@ -311,7 +350,7 @@ int64_t permute_chunks(int64_t A) {
 template <typename V>
 cudaError_t permute_v(const PermuteArgs& p, void* workspace, int sms, cudaStream_t s) {
   const int64_t A = (int64_t)p.T * p.k;
-  const int vecs = (int)(p.bytes / (int64_t)sizeof(V));
+  const int vecs = sizeof(V) < 4 ? (int)((p.bytes + 3) / 4 + 1) : (int)(p.bytes / (int64_t)sizeof(V));
   if (A <= kSelfCount) {
     int tpb = (p.T + sms - 1) / sms;
     if (tpb * p.k > kSelfChunk) tpb = kSelfChunk / p.k;
@@ -391,12 +430,14 @@ __device__ __forceinline__ P load_once(const void* p) {
 // SM), 165 with two; with the rows in L1 it is 158.
 template <typename T, int N, int U, bool WEIGHTED>
 __global__ void __launch_bounds__(128)
-unpermute_kernel(const UnpermuteArgs p, int nv) {
+unpermute_kernel(const UnpermuteArgs p, int nv, uint64_t by_nv) {
   pdl_wait();
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int t = (int)(i / nv);
-  if (t >= p.T) return;
-  const int c = (int)(i - (int64_t)t * nv) * N;
+  // i / nv: by_nv = ceil(2^64 / nv) (0 for 1) is exact as long as i nv < 2^64
+  const uint64_t i = blockIdx.x * (uint64_t)blockDim.x + threadIdx.x;
+  const int64_t token = by_nv ? (int64_t)__umul64hi(i, by_nv) : (int64_t)i;
+  if (token >= p.T) return;
+  const int t = (int)token;
+  const int c = (int)(i - (uint64_t)t * nv) * N;
   const T* rows = static_cast<const T*>(p.rows);
   const int32_t* at = p.pos + (int64_t)t * p.k;
   const float* w = p.weights + (int64_t)t * p.k;
@@ -430,10 +471,68 @@ unpermute_kernel(const UnpermuteArgs p, int nv) {
   *reinterpret_cast<Pack<T, N>*>(static_cast<T*>(p.y) + (int64_t)t * p.ldy + c) = out;
 }
 
+// Rows that no 8-byte vector fits: a warp per token and 256 columns, eight a
+// lane, value by value; two rows in flight.
+template <typename T, bool WEIGHTED>
+__global__ void __launch_bounds__(128)
+unpermute_odd_kernel(const UnpermuteArgs p, uint32_t segments, FastDiv by_segments) {
+  pdl_wait();
+  constexpr int C = 8, U = 2;
+  const int lane = threadIdx.x & 31;
+  const uint32_t i = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const uint32_t t = by_segments(i);
+  if (t >= (uint32_t)p.T) return;
+  const int c0 = (int)(i - t * segments) * 32 * C + lane;
+  const T* rows = static_cast<const T*>(p.rows);
+  const int32_t* at = p.pos + (int64_t)t * p.k;
+  const float* w = p.weights + (int64_t)t * p.k;
+  float acc[C];
+#pragma unroll
+  for (int n = 0; n < C; ++n) acc[n] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += U) {
+    T r[U][C];
+    float wt[U];
+    bool there[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t q = j0 + u < p.k ? at[j0 + u] : -1;
+      there[u] = q >= 0 && q < p.n_rows;
+      wt[u] = WEIGHTED && there[u] ? w[j0 + u] : 1.f;
+      const T* row = rows + q * p.ldr + c0;
+#pragma unroll
+      for (int n = 0; n < C; ++n)
+        if (there[u] && c0 + 32 * n < p.H) r[u][n] = row[32 * n];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (there[u]) {
+#pragma unroll
+        for (int n = 0; n < C; ++n)
+          acc[n] = WEIGHTED ? fmaf(wt[u], Elem<T>::get(r[u][n]), acc[n]) : acc[n] + Elem<T>::get(r[u][n]);
+      }
+  }
+  T* y = static_cast<T*>(p.y) + (int64_t)t * p.ldy + c0;
+#pragma unroll
+  for (int n = 0; n < C; ++n)
+    if (c0 + 32 * n < p.H) y[32 * n] = Elem<T>::put(acc[n]);
+}
+
+template <typename T>
+cudaError_t unpermute_odd(const UnpermuteArgs& p, cudaStream_t s) {
+  const uint32_t segments = (uint32_t)((p.H + 255) / 256);
+  const uint64_t warps = (uint64_t)p.T * segments;  // below 2^31
+  const dim3 blocks((unsigned)((warps + 3) / 4));
+  return p.weights ? launch_after_previous(unpermute_odd_kernel<T, true>, blocks, dim3(128), 0, s, p, segments,
+                                           FastDiv(segments))
+                   : launch_after_previous(unpermute_odd_kernel<T, false>, blocks, dim3(128), 0, s, p, segments,
+                                           FastDiv(segments));
+}
+
 template <typename T, int N, int U>
 cudaError_t unpermute_u(const UnpermuteArgs& p, unsigned blocks, int nv, cudaStream_t s) {
-  return p.weights ? launch_after_previous(unpermute_kernel<T, N, U, true>, dim3(blocks), dim3(128), 0, s, p, nv)
-                   : launch_after_previous(unpermute_kernel<T, N, U, false>, dim3(blocks), dim3(128), 0, s, p, nv);
+  const uint64_t by_nv = nv == 1 ? 0 : ~0ull / (uint64_t)nv + 1;
+  return p.weights ? launch_after_previous(unpermute_kernel<T, N, U, true>, dim3(blocks), dim3(128), 0, s, p, nv, by_nv)
+                   : launch_after_previous(unpermute_kernel<T, N, U, false>, dim3(blocks), dim3(128), 0, s, p, nv, by_nv);
 }
 
 template <typename T, int N>
@@ -448,7 +547,9 @@ cudaError_t unpermute_n(const UnpermuteArgs& p, int sms, cudaStream_t s) {
 
 // A block per token and group of J of its assignments: dy is read once a
 // group, each row read once and its gradient written beside it; the J dot
-// products are summed over the block in a fixed order.
+// products are summed over the block in a fixed order. Column steps are not
+// unrolled: registers cost blocks an SM (1023 x 6 rows of 2049 fp32, 104 MB:
+// 22 us, 29 unrolled; 2048 x 8 of 7168 bf16, 499 MB: 77).
 constexpr int kGradThreads = 128;
 template <typename T, int N, int J>
 __global__ void __launch_bounds__(kGradThreads)
@@ -469,6 +570,7 @@ unpermute_grad_kernel(const UnpermuteGradArgs p, int groups) {
     w[u] = q[u] >= 0 ? p.weights[(int64_t)t * p.k + j] : 0.f;
     dot[u] = 0.f;
   }
+#pragma unroll 1
   for (int c = threadIdx.x * N; c < p.H; c += kGradThreads * N) {
     const Pack<T, N> d = *reinterpret_cast<const Pack<T, N>*>(dy + c);
     Pack<T, N> r[J];
@@ -537,7 +639,7 @@ cudaError_t unpermute_t(const UnpermuteArgs& p, int sms, cudaStream_t s) {
   const int n = vector_bytes(bits, 16) / B;
   if (n >= 16 / B) return unpermute_n<T, 16 / B>(p, sms, s);
   if (n >= 8 / B) return unpermute_n<T, 8 / B>(p, sms, s);
-  return unpermute_n<T, 1>(p, sms, s);
+  return unpermute_odd<T>(p, s);
 }
 
 template <typename T>
@@ -566,8 +668,7 @@ cudaError_t launch_permute(const PermuteArgs& p, void* workspace, int sms, cudaS
     case 16: return permute_v<uint4>(p, workspace, sms, s);
     case 8: return permute_v<uint2>(p, workspace, sms, s);
     case 4: return permute_v<uint32_t>(p, workspace, sms, s);
-    case 2: return permute_v<uint16_t>(p, workspace, sms, s);
-    default: return permute_v<uint8_t>(p, workspace, sms, s);
+    default: return permute_v<uint8_t>(p, workspace, sms, s);  // by words, shifted
   }
 }
 

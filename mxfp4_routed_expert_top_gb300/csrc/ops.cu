@@ -108,7 +108,7 @@ int unpermute(int device, const void* rows, int dtype, int64_t n_rows, int64_t l
   const int size = dfm::dtype_bytes(dtype);
   if (off(rows, size) || off(y, size) || off(pos, 4) || off(weights, 4))
     return fail(DF_MOE_EINVAL, "an array is not aligned to its elements");
-  if (T * H / 128 >= kMaxRows) return fail(DF_MOE_ERANGE, "T * H is too large");
+  if (T > kMaxRows / ((H + 127) / 128)) return fail(DF_MOE_ERANGE, "T * H is too large");
   OnDevice on(device);
   if (on.rc()) return on.rc();
   const dfm::UnpermuteArgs a{rows, pos, weights, y, (int)T, k, (int)H, n_rows, ldr, ldy};

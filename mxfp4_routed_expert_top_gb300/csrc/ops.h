@@ -14,6 +14,20 @@ inline int dtype_bytes(int dtype) {  // DF_MOE_BF16, _F16, _F32, _E4M3
   return dtype == 2 ? 4 : dtype == 3 ? 1 : 2;
 }
 
+// n / nb for n < 2^31: with 2^(shift - 1) < nb <= 2^shift and mul =
+// ceil(2^(31 + shift) / nb), the error n (mul nb - 2^(31 + shift)) stays below
+// 2^(31 + shift).
+struct FastDiv {
+  uint32_t mul, shift;
+  explicit FastDiv(uint32_t nb) : mul(0), shift(0) {
+    while ((1ull << shift) < nb) ++shift;
+    mul = (uint32_t)(((1ull << (31 + shift)) + nb - 1) / nb);
+  }
+  __device__ uint32_t operator()(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> (31 + shift));
+  }
+};
+
 // Rows of `bytes` bytes and the distances of consecutive rows, in bytes.
 struct PermuteArgs {
   const int32_t* ids;  // [T][k]

@@ -145,6 +145,21 @@ def test_permute_strides_and_odd_addresses(dfm):
         check_permuted(Permuted(dfm, ids, E, x, "bf16", H, pad=3), ids, E, x, H)
 
 
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 7, 8, 9, 31, 130])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_permute_rows_off_word_boundaries(dfm, H, dtype, shift):
+    """Rows whose every alignment and length modulo a word occurs: no byte
+    beside them changes."""
+    g = gen(H + shift)
+    T, k, E = 23, 3, 4
+    ids = random_ids(T, k, E, g, 0.2)
+    wide = randn(T, H + 5, g=g, dtype=dtype)
+    x = wide.view(torch.uint8 if dtype == "e4m3" else torch.bfloat16)[:, shift:].view(DT[dtype])
+    for pad in (0, 1, 2, 3):
+        check_permuted(Permuted(dfm, ids, E, x, dtype, H, pad=pad), ids, E, x, H)
+
+
 def test_permute_empty(dfm):
     offs = torch.full((6,), 9, dtype=torch.int32, device="cuda")
     dfm.permute(None, 0, 2, 5, None, "bf16", 8, None, offs, None, None)
@@ -176,7 +191,7 @@ def test_rows_past_32_bits(dfm):
 UNPERMUTE_CASES = [
     (1, 1, 1, "f32", 0), (1, 16, 7168, "bf16", 0), (3, 2, 33, "f16", 0.5), (8, 16, 7168, "bf16", 0.2),
     (301, 7, 130, "bf16", 0.1), (129, 32, 2049, "f32", 0.1), (64, 9, 36, "f16", 0), (1200, 3, 64, "f32", 0.9),
-    (2, 5, 12, "bf16", 0),
+    (2, 5, 12, "bf16", 0), (40, 3, 257, "f16", 0.2), (5, 4, 1, "f32", 0), (70, 6, 511, "bf16", 0.1), (33, 2, 20, "f32", 0),
 ]
 
 
