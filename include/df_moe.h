@@ -455,11 +455,12 @@ DF_MOE_API int df_moe_fp8_quantize(int device, const void* x, int32_t dtype, int
  *   transposed: the same product with w stored [G][K][N] (K * ldw apart) and
  *      ws [G][ceil(K / 128)][ceil(N / 128)]: with the forward's own w and ws,
  *      and rows of dy, this is the gradient of x
- *   offs [G + 1] ascending from 0 (read as if clamped to [0, M]); rows outside
- *      every group are left as they were; NULL: one group of all M rows (G = 1)
+ *   offs [G + 1] ascending, read as if clamped to [0, M]; rows outside every
+ *      group are left as they were, and all of y where offs descends; NULL: one
+ *      group of all M rows (G = 1)
  *   y  [M][N] of dtype
- *   status NULL or a device word: bit 2u is set when a bounded wait inside the
- *      kernel gave up (the call's y holds NaN there)
+ *   status NULL or a device word: bit 1u is set when offs descends, bit 2u
+ *      when a bounded wait inside the kernel gave up (y holds NaN there)
  * x and w are 16-byte aligned. */
 DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, const float* xs,
                                  int64_t ldxs, const uint8_t* w, int64_t ldw, const float* ws,

@@ -524,7 +524,8 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   }
   pdl_wait();  // the kernel before this one is complete
   // the groups' first rows, kept inside [0, M] whatever the caller's array
-  // holds, and their tiles
+  // holds, and their tiles; groups that are not in order have no units
+  bool bad = false;
   const int M = (int)p.M;
   for (int g = tid; g <= p.G; g += C::NTHR)
     offs[g] = p.offs ? min(max(p.offs[g], 0), M) : (g ? M : 0);
@@ -534,6 +535,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     for (int g0 = 0; g0 < p.G; g0 += C::NTHR) {
       const int g = g0 + tid;
       const int n = g < p.G ? (max(0, offs[g + 1] - offs[g]) + NT - 1) / NT : 0;
+      bad = bad || (g < p.G && offs[g + 1] < offs[g]);
       // exclusive prefix sum over the block
       int incl = n;
 #pragma unroll
@@ -555,10 +557,11 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     if (tid == 0) tiles[p.G] = base;
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  bad = __syncthreads_or(bad) != 0;
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm->tmem);
-  const int units = tiles[p.G] * p.units_n;
+  if (bad && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, DEV_ERR_RANGE);
+  const int units = bad ? 0 : tiles[p.G] * p.units_n;
   const int part = blockIdx.x % p.split;
   const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
   const int kb0 = (int)((int64_t)p.KB * part / p.split);

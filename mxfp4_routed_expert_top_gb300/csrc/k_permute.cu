@@ -334,8 +334,9 @@ template <typename V>
 __global__ void __launch_bounds__(kPermThreads)
 permute_copy_kernel(const PermuteArgs p, int vecs) {
   pdl_wait();
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const int32_t* at = p.pos + (int64_t)t * p.k;
+  for (int64_t i = blockIdx.x; i < p.T; i += gridDim.x) {
+    const int t = (int)i;
+    const int32_t* at = p.pos + i * p.k;
     if constexpr (sizeof(V) < 4) copy_rows_odd(p, t, t + 1, at, 0, vecs);
     else copy_rows<V>(p, t, t + 1, at, 0, vecs);
     if (p.n_scales) copy_scales(p, t, t + 1, at);

@@ -444,6 +444,18 @@ def test_product_offsets_are_clamped(dfm):
     within(y, want, 132 * 2.0 ** -23 * size, "f32")
 
 
+@pytest.mark.parametrize("rows", [40, 4000])
+def test_product_descending_offsets_write_nothing(dfm, rows):
+    g = gen(6)
+    G, N, K = 3, 128, 128
+    x, xs, w, ws = product_inputs(G, rows, N, K, False, g)
+    y = torch.full((rows, N), 7.0, device="cuda")
+    offs = torch.tensor([0, 30, 10, 40], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dfm.fp8_matmul(x, xs, w, ws, offs, G, rows, N, K, y, "f32", status=status)
+    assert status.item() == 1 and bool((y == 7).all())
+
+
 def test_product_nan_stays_in_its_row(dfm):
     g = gen(7)
     G, M, N, K = 2, 40, 256, 384
