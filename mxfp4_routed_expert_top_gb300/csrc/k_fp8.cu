@@ -96,12 +96,12 @@ __device__ __forceinline__ float quantize_block(float (&v)[N], uint32_t (&code)[
   return __fdiv_rn(m, 448.f);
 }
 
-// Rows of whole 32-byte pieces: eight lanes a block, sixteen values a lane,
-// two blocks in flight. HBM should bound it (128 (s + 1) + 4 bytes a block of
-// s-byte values); issue slots did as long as a value cost 24 instructions
-// (index division, tests for finiteness, 16 lanes a block): 65536 x 1536 bf16
-// 94 us, now 56 (305 MB).
-constexpr int kQThreads = 256, kQUnroll = 2;
+// Rows of whole 32-byte pieces: eight lanes a block, sixteen values a lane.
+// HBM bounds it (128 (s + 1) + 4 bytes a block of s-byte values): 65536 x 1536
+// bf16 (305 MB) take 51 us, 54 with two blocks in flight a warp (registers
+// cost warps an SM), and took 94 when a value cost 24 instructions (index
+// division, tests for finiteness, 16 lanes a block).
+constexpr int kQThreads = 256, kQUnroll = 1;
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
 fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const FastDiv by_nb) {
@@ -153,44 +153,68 @@ fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const Fas
   }
 }
 
-// Any other rows: half a warp a block, value by value, two blocks in flight
-// (14001 x 7167 bf16: 109 us; a whole warp a block, twice the exchanges a
-// value, 148; eight lanes, 16-byte pieces a load, 126).
+// Any other rows: eight lanes a block, in words of four values that are
+// aligned in memory (word w holds the block's values 4 w - m .. 4 w - m + 3, m
+// what lies between the word boundary and the block), so that a block has 33
+// of them and a lane up to five; words without a value of the block are not
+// read. Where codes lie like x (the same distance of rows modulo 4) their
+// words are aligned too. 14001 x 7167 bf16: 92 us; value by value 109.
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
 fp8_quantize_odd_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const FastDiv by_nb) {
-  const int l = threadIdx.x & 15, sub = (threadIdx.x >> 4) & 1;
+  constexpr int R = 5;
+  struct alignas(4 * sizeof(T)) Word {
+    T v[4];
+  };
+  const int l = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3;
   const uint32_t warps = gridDim.x * (kQThreads / 32);
   const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const T* x = static_cast<const T*>(p.x);
   pdl_wait();
-  for (uint64_t w0 = warp; 2 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
-    float v[kQUnroll][8];
+  for (uint64_t w0 = warp; 4 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
+    Word word[kQUnroll][R];
     uint32_t row[kQUnroll], blk[kQUnroll];
-    bool there[kQUnroll];
+    int len[kQUnroll], first[kQUnroll];
 #pragma unroll
     for (int u = 0; u < kQUnroll; ++u) {
-      const uint64_t g = 2 * (w0 + (uint64_t)u * warps) + sub;
-      there[u] = g < total;
-      row[u] = by_nb(there[u] ? (uint32_t)g : 0);
-      blk[u] = (there[u] ? (uint32_t)g : 0) - row[u] * nb;
+      const uint64_t g = 4 * (w0 + (uint64_t)u * warps) + sub;
+      const bool there = g < total;
+      row[u] = by_nb(there ? (uint32_t)g : 0);
+      blk[u] = (there ? (uint32_t)g : 0) - row[u] * nb;
+      len[u] = there ? min(128, p.K - (int)(128 * blk[u])) : 0;
       const T* src = x + (int64_t)row[u] * p.ldx + 128 * blk[u];
+      const int m = (int)((uintptr_t)src / sizeof(T)) & 3;
+      first[u] = 4 * l - m;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int c = l + 16 * n;
-        v[u][n] = there[u] && (int)(128 * blk[u]) + c < p.K ? to_f32<T>(src[c]) : 0.f;
+      for (int r = 0; r < R; ++r) {
+        const int e = first[u] + 32 * r;  // the word's first value
+        if (e < len[u] && e + 3 >= 0) word[u][r] = *reinterpret_cast<const Word*>(src + e);
       }
     }
 #pragma unroll
     for (int u = 0; u < kQUnroll; ++u) {
-      uint32_t code[4];
-      const float scale = quantize_block<8, 1>(v[u], code);
-      if (!there[u]) continue;
-      uint8_t* dst = p.codes + (int64_t)row[u] * p.ldc + 128 * blk[u];
+      float v[4 * R];
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if ((int)(128 * blk[u]) + l + 16 * n < p.K) dst[l + 16 * n] = (uint8_t)(code[n / 2] >> (8 * (n & 1)));
-      if (l == 0) p.scales[(int64_t)row[u] * p.lds + blk[u]] = scale;
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[4 * r + i] = (unsigned)(first[u] + 32 * r + i) < (unsigned)len[u] ? to_f32<T>(word[u][r].v[i]) : 0.f;
+      uint32_t code[2 * R];
+      const float scale = quantize_block<4 * R, 2>(v, code);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int e = first[u] + 32 * r;
+        uint8_t* dst = p.codes + (int64_t)row[u] * p.ldc + 128 * blk[u] + e;
+        const uint32_t four = code[2 * r] | code[2 * r + 1] << 16;
+        if (e >= 0 && e + 3 < len[u] && ((uintptr_t)dst & 3) == 0) {
+          *reinterpret_cast<uint32_t*>(dst) = four;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((unsigned)(e + i) < (unsigned)len[u]) dst[i] = (uint8_t)(four >> (8 * i));
+        }
+      }
+      if (len[u] > 0 && l == 0) p.scales[(int64_t)row[u] * p.lds + blk[u]] = scale;
     }
   }
 }

@@ -331,6 +331,33 @@ def test_quantize(dfm, M, K, dtype, pad):
     assert bool((codes[:, K:] == 0x55).all()) and bool((scales[:, nb] == 7).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K, shift, pad", [(1, 0, 0), (2, 1, 1), (3, 3, 2), (5, 2, 0), (127, 1, 3), (128, 3, 1), (129, 2, 2),
+                                           (131, 0, 0), (257, 3, 5), (1001, 1, 0)])
+def test_quantize_rows_off_vector_boundaries(dfm, K, shift, pad, dtype):
+    """Every alignment of rows of x and codes against each other; NaN beside
+    the rows does not enter, and nothing beside the codes is written."""
+    g = gen(K + shift)
+    M = 13
+    wide = torch.randn(M, K + pad + 4, generator=g, device="cuda").to(DT[dtype])
+    wide[:, :shift] = float("nan")
+    wide[:, shift + K:] = float("nan")
+    x = wide[:, shift:shift + K]
+    codes = torch.full((M, K + 3), 0x55, dtype=torch.uint8, device="cuda")
+    nb = -(-K // 128)
+    scales = torch.zeros(M, nb, device="cuda")
+    dfm.fp8_quantize(x, dtype, M, K, codes[:, 1:], scales, ldx=wide.shape[1], ldc=K + 3)
+    want, s, ratio = quantized(x)
+    got = codes[:, 1:K + 1].contiguous().view(torch.float8_e4m3fn).double()
+    if dtype == "f32":  # as above: a code may differ next to a middle
+        lower, upper = e4m3_nearest(ratio * (1 - 2.0 ** -22)), e4m3_nearest(ratio * (1 + 2.0 ** -22))
+        assert bool(((got == want) | (got == lower) | (got == upper)).all())
+    else:
+        assert torch.equal(got, want)
+    assert torch.equal(scales.double(), s.float().double())
+    assert bool((codes[:, 0] == 0x55).all()) and bool((codes[:, K + 1:] == 0x55).all())
+
+
 def test_quantize_infinities_nan_and_extremes(dfm):
     x = torch.zeros(5, 256, device="cuda")
     x[0, 3], x[0, 4], x[0, 130] = float("inf"), 2.0, -float("inf")
