@@ -255,6 +255,17 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
 // against 37.8 (NT = 128); 24 rows 35.9 (32) and 37.8; 48 rows 46.8 (32) and
 // 38.7; 80 rows 46.7 and 39.8.
 //
+// What bounds it. Long groups: a block of 128 x 256 x 128 takes about 830
+// cycles, of which its MMAs take 512 (the tensor pipe is 62% busy). Two
+// accumulators fill the tensor memory, and each is taken for the MMAs, the
+// signal (about 150 cycles), the epilogue's loads and FMAs (440: issue slots,
+// two warps a scheduler) and the way back: 8192 x 7168 x 7168 take 300 us, 2.8
+// PFLOP/s. Not faster there: a pair of CTAs on 256 x 256 (cta_group::2, 291 to
+// 306 us by shape), sixteen epilogue warps (325), packed fp32 FMAs (308), two
+// accumulators of 128 columns in place of one (343), two MMA warps (298),
+// longer tensor memory loads (324). Short groups stream weights at 85% of the
+// copy rate (16 experts of 1536 x 7168, one token: 31 us).
+//
 // split > 1 (NT <= 32): a cluster of that many CTAs shares a unit, each takes
 // a part of K, and the sums meet in distributed shared memory, in the order
 // of the parts.
