@@ -138,8 +138,9 @@ __device__ __forceinline__ void copy_scales(const PermuteArgs& p, int t0, int t1
 // 1024 threads an SM halves what an SM counts against two of 512; clusters
 // of eight that shared the counting through distributed shared memory were
 // slower (4096 tokens x 16 rows of 256 bf16: 17.5 us, two blocks 21, clusters
-// 31). Writes bound the large calls: with rows of 7168 (999 MB, 940 of them
-// written) take 189 us, of which bulk copies through shared memory saved nothing.
+// 31). Writes bound the large calls: 4096 x 16 rows of 7168 (999 MB, 940 of
+// them written) take 181 us, of which bulk copies through shared memory saved
+// nothing.
 constexpr int kSelfThreads = 1024;
 constexpr int kSelfCount = 65536;
 constexpr int kSelfChunk = 1024;  // assignments a block may own

@@ -244,9 +244,9 @@ def test_unpermute_grad(dfm, T, k, H, dtype, drop):
     want = (weights.double()[:, :, None] * dy.double()[:, None, :]).masked_fill(gone[:, :, None], 0)
     within(got, want, 2.0 ** -24 * want.abs(), dtype)
     terms = (rows[place].double() * dy.double()[:, None, :]).masked_fill(gone[:, :, None], 0)
-    # a thread's own chain (8 columns at a time over 256 threads), 5 steps in
-    # the warp and 8 over the warps
-    chain = -(-H // 256) + 8 + 5 + 8
+    # a thread's own chain (up to 8 columns at a time over 128 threads: at most
+    # H / 128 + 8 terms), 5 steps in the warp and 4 over the warps
+    chain = -(-H // 128) + 8 + 5 + 4
     within(dw, terms.sum(2), chain * 2.0 ** -24 * terms.abs().sum(2), "f32")
     assert bool((dw[gone] == 0).all())
 
