@@ -255,16 +255,20 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
 // against 37.8 (NT = 128); 24 rows 35.9 (32) and 37.8; 48 rows 46.8 (32) and
 // 38.7; 80 rows 46.7 and 39.8.
 //
-// What bounds it. Long groups: a block of 128 x 256 x 128 takes about 830
-// cycles, of which its MMAs take 512 (the tensor pipe is 62% busy). Two
-// accumulators fill the tensor memory, and each is taken for the MMAs, the
-// signal (about 150 cycles), the epilogue's loads and FMAs (440: issue slots,
-// two warps a scheduler) and the way back: 8192 x 7168 x 7168 take 300 us, 2.8
-// PFLOP/s. Not faster there: a pair of CTAs on 256 x 256 (cta_group::2, 291 to
-// 306 us by shape), sixteen epilogue warps (325), packed fp32 FMAs (308), two
-// accumulators of 128 columns in place of one (343), two MMA warps (298),
-// longer tensor memory loads (324). Short groups stream weights at 85% of the
-// copy rate (16 experts of 1536 x 7168, one token: 31 us).
+// What bounds it. Long groups: a block of 128 x 256 x 128 takes about 790
+// cycles, of which its MMAs take 512. Two accumulators fill the tensor memory,
+// and each is taken for the MMAs, the signal (about 150 cycles), the
+// epilogue's loads and FMAs (440: issue slots, two warps a scheduler) and the
+// way back, where every instruction between two blocks counts (toggled
+// indexes in place of computed ones and no code for failures inside the loop:
+// 302 to 285 us on 8192 x 7168 x 7168, 2.95 PFLOP/s). Not faster, against
+// what the kernel took when each was tried: a pair of CTAs on 256 x 256
+// (cta_group::2: 306 for 294), sixteen epilogue warps (325 for 291), packed
+// fp32 FMAs (308 for 308), two accumulators of 128 columns in place of one (343
+// for 299), two MMA warps (298 for 300), longer tensor memory loads (324 for
+// 291), the next block's scale or barrier read early (292 for 285). Short
+// groups stream weights at 85% of the copy rate (16 experts of 1536 x 7168, one
+// token: 31 us).
 //
 // split > 1 (NT <= 32): a cluster of that many CTAs shares a unit, each takes
 // a part of K, and the sums meet in distributed shared memory, in the order
@@ -337,6 +341,7 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait for the barrier at shared address `bar`; the same answer in
 // every lane.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     uint32_t ok;
     asm volatile(
@@ -348,6 +353,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, ok)) return true;
   }
   return false;
+}
+// The lane with `leader` arrives.
+__device__ __forceinline__ void arrive_if(uint32_t bar, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(leader) : "memory");
 }
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes, uint32_t leader) {
   asm volatile(
@@ -743,20 +752,26 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       static_assert(128 % CW == 0, "a warp's columns lie in one block of w's scales");
       const int c0 = (warp >> 2) * CW, l0 = 32 * (warp & 3);
       const uint32_t tbase = tmem + ((uint32_t)l0 << 16) + (uint32_t)c0;
+      static_assert(AS == 2, "the accumulator alternates");
+      const uint32_t sc_full = smem_u32(sm->sc_full), sc_empty = smem_u32(sm->sc_empty);
+      const uint32_t acc_full = smem_u32(sm->acc_full), acc_empty = smem_u32(sm->acc_empty), leader = lane == 0;
+      uint32_t buf = 0, sc_phase = 0, as = 0, acc_phase = 0;
       for (int u = first; u < units; u += step) {
         const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
         float acc[CW];
 #pragma unroll
         for (int i = 0; i < CW; ++i) acc[i] = 0.f;
-        for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
-          const int buf = batch & 1;
-          ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1);
+        for (int kb = kb0; kb < kb1 && ok; kb += kFBatch) {
+          ok = bar_wait(sc_full + 8 * buf, sc_phase);
+          if (!ok) break;
           const int blocks = min(kFBatch, kb1 - kb);
-          for (int b = 0; b < blocks; ++b, ++it) {
-            const int as = it % AS;
-            const float s = sm->sc[buf][b][l0 + lane] * sm->scw[buf][b][c0 >> 7];
-            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1);
-            if (!ok) continue;
+          const float* sc = &sm->sc[buf][0][l0 + lane];
+          const float* scw = &sm->scw[buf][0][c0 >> 7];
+#pragma unroll 1
+          for (int b = 0; b < blocks; ++b) {
+            const float s = sc[b * (C::Scales + 4)] * scw[2 * b];
+            ok = bar_wait(acc_full + 8 * as, acc_phase);
+            if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t ta = tbase + (uint32_t)(as * C::DN);
             constexpr int L = 16;  // columns a load
@@ -769,14 +784,18 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
                 tmem_ld_rows(r[(i + 1) & 1], ta + L * (i + 1));
               } else {
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
+                arrive_if(acc_empty + 8 * as, leader);
               }
 #pragma unroll
               for (int c = 0; c < L; ++c) acc[L * i + c] = fmaf(__uint_as_float(r[i & 1][c]), s, acc[L * i + c]);
             }
+            as ^= 1;
+            acc_phase ^= as ^ 1;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->sc_empty[buf]);
+          arrive_if(sc_empty + 8 * buf, leader);
+          buf ^= 1;
+          sc_phase ^= buf ^ 1;
         }
         if (!ok) {
           sm->err = 1;
