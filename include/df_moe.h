@@ -375,7 +375,9 @@ DF_MOE_API int df_moe_route_noalloc(const float* router, int32_t E, int32_t H,
  * weights -> permute_grad.
  *
  * All of them: `device` is the CUDA device of the arrays (negative: the
- * current one), made current for the call; `stream` belongs to it. They
+ * current one), made current for the call; `stream` belongs to it (NULL: the
+ * legacy default stream; the Python binding passes torch's current stream
+ * where the caller names none). They
  * allocate nothing, keep nothing between calls, may run at the same time on
  * any streams (and be captured into graphs) as long as their outputs and
  * workspaces are apart, and give the same bits on every run. Every array is device memory,

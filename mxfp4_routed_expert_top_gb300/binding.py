@@ -366,8 +366,12 @@ def stream_read(buf, nbytes, sink, stream=None):
 # ---- the expert path's operators (no handle) ---------------------------------
 # A decode step makes several of these calls with microseconds of work each, so
 # the marshalling is kept short: one pass over the arrays, the C functions
-# looked up once.
+# looked up once. A call runs on `stream`, or without one on the stream that
+# torch has current on the arrays' device (between other work of the same
+# program, and inside a capture); where all arrays are raw addresses, that is
+# the legacy default stream.
 _ops = None
+_torch_stream = None
 
 
 def _op(name):
@@ -411,6 +415,19 @@ def _place(*arrays):
     return out
 
 
+def _stream_on(dev, stream):
+    """The raw stream of a call on arrays of device `dev` (as _place gives it)."""
+    global _torch_stream
+    if stream is not None:
+        return _stream(stream)
+    if dev < 0:
+        return None
+    if _torch_stream is None:  # the arrays are torch's, so torch is loaded
+        import torch
+        _torch_stream = torch._C._cuda_getCurrentRawStream
+    return _torch_stream(dev)
+
+
 def _failed(rc):
     raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
 
@@ -427,7 +444,7 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
     dev, i, x, r, o, q, s, w, xs, rs = _place(ids, x, rows, offs, pos, src, workspace, scales,
                                               rows_scales)
     rc = _op("df_moe_permute")(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
-                               ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream(stream))
+                               ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -436,7 +453,7 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
     """Gradient of permute's x (df_moe_permute_grad)."""
     dev, r, q, y = _place(drows, pos, dx)
     rc = _op("df_moe_permute_grad")(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
-                                    _stream(stream))
+                                    _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -445,7 +462,7 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
     """Weighted rows back to their tokens (df_moe_unpermute)."""
     dev, r, q, w, y = _place(rows, pos, weights, y)
     rc = _op("df_moe_unpermute")(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
-                                 _stream(stream))
+                                 _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -455,7 +472,7 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
     dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
     rc = _op("df_moe_unpermute_grad")(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
-                                      lddr, dw, _stream(stream))
+                                      lddr, dw, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -463,7 +480,7 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
     dev, x, c, s = _place(x, codes, scales)
-    rc = _op("df_moe_fp8_quantize")(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream(stream))
+    rc = _op("df_moe_fp8_quantize")(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -473,6 +490,6 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
     dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
     rc = _op("df_moe_fp8_matmul")(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
-                                  1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream(stream))
+                                  1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))
     if rc:
         _failed(rc)

@@ -139,3 +139,37 @@ def test_empty_calls_need_no_device(dfm):
     dfm.unpermute(None, "bf16", 0, None, None, 0, 2, 64, None)
     dfm.permute_grad(None, "bf16", 0, None, 0, 2, 64, None)
     dfm.unpermute_grad(None, None, "bf16", 0, None, None, 0, 2, 64, None, None)
+
+
+class OnDevice0:
+    """Stands for a torch tensor on device 0: an address, never followed."""
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return A
+
+
+EVERY_CALL = [
+    ("permute", PERMUTE), ("permute_grad", dict(drows=A, dtype="f32", n_rows=8, pos=A, T=4, k=2, H=64, dx=A)),
+    ("unpermute", UNPERMUTE), ("unpermute_grad", GRAD), ("fp8_quantize", QUANT), ("fp8_matmul", MATMUL),
+]
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL)
+def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name, kw):
+    """Tensors: the stream that torch has current on their device. Raw
+    addresses only: the default stream. A stream that is given is taken."""
+    import torch
+    binding, seen = dfm.binding, []
+    monkeypatch.setattr(binding, "_op", lambda n: lambda *a: seen.append(a[-1]) or 0)
+    monkeypatch.setattr(binding, "_torch_stream", None, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000 + dev)
+    call = getattr(dfm, name)
+    tensors = {key: OnDevice0() if v == A else v for key, v in kw.items()}
+    call(**tensors)
+    call(**kw)
+    call(**dict(tensors, stream=0x77))
+    call(**dict(tensors, stream=0))
+    assert seen == [0x5000, None, 0x77, 0]

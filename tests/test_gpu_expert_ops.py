@@ -657,3 +657,48 @@ def test_places_match_the_layers_grouping(dfm):
         m.sync()
     assert torch.equal(offs[:E + 1], r.offs)
     assert torch.equal(tok * k + slot, r.src)
+
+
+@pytest.mark.parametrize("T, k, E, H, I", [(300, 3, 7, 384, 256)])
+def test_calls_without_a_stream_follow_the_current_one(dfm, T, k, E, H, I):
+    """Inside torch.cuda.stream(s), calls that name no stream come after s's own
+    work before them and before its work after them. The inputs are zeros until
+    that work has written them, so a call that ran early would show."""
+    m = Experts8(dfm, T, k, E, H, I, 40)
+    m.forward()
+    m.backward()
+    torch.cuda.synchronize()
+    want = m.outputs()
+    inputs = [(t, t.clone()) for t in (m.x, m.ids, m.weights, m.dy)]
+    for t, _ in inputs:
+        t.zero_()
+    for t in (m.y, m.dw, m.dx):
+        t.fill_(7)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for t, value in inputs:
+            t.copy_(value)
+        m.forward()
+        m.backward()
+        got = m.outputs()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_without_a_stream_are_captured(dfm):
+    m = Experts8(dfm, 100, 3, 7, 384, 256, 41)
+    m.forward()
+    m.backward()
+    torch.cuda.synchronize()
+    want = m.outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward()
+        m.backward()
+    for t in (m.y, m.dw, m.dx, m.h, m.drows, m.rows, m.dh):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(m.outputs(), want))
