@@ -470,6 +470,14 @@ DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, cons
                                  int32_t transposed, void* y, int32_t dtype, int64_t ldy,
                                  uint32_t* status, void* stream);
 
+/* Test hook for that status bit (no GPU fault involved): in the next
+ * df_moe_fp8_matmul of the calling thread one role of the kernel's block 0
+ * gives up before its first wait (1 the copies, 2 the MMAs, 3 the scales, 4
+ * the sums; 0 takes the request back) and the block's other waits use a short
+ * limit (2^12 polls), so that they run out and the call ends, with the status
+ * bit and NaN in that block's part of y. One-shot. Errors: EINVAL. */
+DF_MOE_API int df_moe_test_fp8_give_up(int32_t role);
+
 #ifdef __cplusplus
 }
 #endif

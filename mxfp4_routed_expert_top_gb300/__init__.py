@@ -5,4 +5,4 @@ from .binding import (MoE, DfMoeError, Config, LayerWeights, lib, span_bytes_for
                       SYMBOLS,
                       route_noalloc, Graph, stream_read,
                       BF16, F16, F32, E4M3, permute_workspace, permute, permute_grad, unpermute,
-                      unpermute_grad, fp8_quantize, fp8_matmul)
+                      unpermute_grad, fp8_quantize, fp8_matmul, test_fp8_give_up)

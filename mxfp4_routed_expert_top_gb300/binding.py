@@ -35,7 +35,7 @@ SYMBOLS = [
     "df_moe_graph_destroy", "df_moe_stream_read", "df_moe_create_cached",
     "df_moe_cache_stats", "df_moe_test_drop_arrival", "df_moe_step_mxfp8",
     "df_moe_permute_workspace", "df_moe_permute", "df_moe_permute_grad", "df_moe_unpermute",
-    "df_moe_unpermute_grad", "df_moe_fp8_quantize", "df_moe_fp8_matmul",
+    "df_moe_unpermute_grad", "df_moe_fp8_quantize", "df_moe_fp8_matmul", "df_moe_test_fp8_give_up",
 ]
 
 
@@ -122,6 +122,7 @@ def lib():
         L.df_moe_fp8_quantize.argtypes = [ci, vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
         L.df_moe_fp8_matmul.argtypes = [ci, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, i64, i64,
                                         i32, vp, i32, i64, vp, vp]
+        L.df_moe_test_fp8_give_up.argtypes = [i32]
         for name in SYMBOLS:
             f = getattr(L, name)
             if f.restype is ctypes.c_int:  # default
@@ -491,5 +492,12 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
     rc = _op("df_moe_fp8_matmul")(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
                                   1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))
+    if rc:
+        _failed(rc)
+
+
+def test_fp8_give_up(role):
+    """Test hook: one role of the next fp8_matmul gives up (df_moe_test_fp8_give_up)."""
+    rc = _op("df_moe_test_fp8_give_up")(role)
     if rc:
         _failed(rc)

@@ -302,7 +302,10 @@ struct Fp8Params {
   uint32_t* status;
   int64_t M, ldxs, ldy;
   int G, N, K, KB, NB, units_n, split, vec;
+  int give_up;  // test hook: the role of block 0 (Role) that gives up before its first wait
 };
+
+enum Role { kNone = 0, kCopies, kMmas, kScales, kSums };
 
 template <int NT>
 struct Fp8Smem {
@@ -340,9 +343,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // Bounded wait for the barrier at shared address `bar`; the same answer in
 // every lane.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -610,6 +613,9 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
   const int kb0 = (int)((int64_t)p.KB * part / p.split);
   const int kb1 = (int)((int64_t)p.KB * (part + 1) / p.split);
+  // A wait that runs out sets err; every role then stops at its next wait.
+  const int gives_up = blockIdx.x == 0 ? p.give_up : kNone;
+  const uint32_t limit = gives_up ? kTestWaitLimit : kWaitLimit;
 
   if (warp >= EW) {
     if (C::XA) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -619,13 +625,13 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       const uint32_t empty = uni(smem_u32(sm->empty)), full = uni(smem_u32(sm->full));
       int s = 0;
       uint32_t phase = 1;  // the first round finds every stage free
-      bool ok = true;
+      bool ok = gives_up != kCopies;
       for (int u = first; u < units && ok; u += step) {
         const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
         const int n0 = (int)uni(un.n0), r0 = (int)uni((uint32_t)un.row0);
         const int g = (int)uni(un.g);
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = bar_wait(empty + 8 * s, phase);
+          ok = bar_wait(empty + 8 * s, phase, limit);
           if (!ok) break;
           const uint32_t bar = full + 8 * s, da = a0 + s * kFABytes, db = b0 + s * C::BBytes;
           expect_tx(bar, kFABytes + C::BBytes, leader);
@@ -645,12 +651,11 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           }
         }
       }
-      if (!ok) {
-        sm->err = 1;
-        // copies in flight land before the block leaves: of a stage's last
-        // round, or (waiting for nothing) of the round before
-        for (int i = 0; i < NS; ++i) (void)bar_wait(full + 8 * i, i < s ? phase ^ 1 : phase);
-      }
+      if (!ok) sm->err = 1;
+      // copies in flight land before the block leaves, also where the MMA warp
+      // gave up and waits for none of them: of a stage's last round, or
+      // (waiting for nothing) of the round before
+      for (int i = 0; i < NS; ++i) (void)bar_wait(full + 8 * i, i < s ? phase ^ 1 : phase, kWaitLimit);
     } else if (warp == EW + 1) {
       // ---- MMAs, issued by one lane
       // transposed weights are M- or N-major: a K step of 32 is 32 rows of
@@ -664,13 +669,13 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
       const uint32_t b0 = uni((uint32_t)umma::smem_desc_sw128(smem_u32(sb)));
       const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
       const uint32_t acc_full = uni(smem_u32(sm->acc_full)), acc_empty = uni(smem_u32(sm->acc_empty));
-      const int total = first < units ? ((units - first + step - 1) / step) * (kb1 - kb0) : 0;
+      bool ok = gives_up != kMmas;
+      const int total = ok && first < units ? ((units - first + step - 1) / step) * (kb1 - kb0) : 0;
       int s = 0, as = 0;
       uint32_t phase = 0, acc_phase = 1;  // the first round finds every accumulator free
       int it = 0;
-      bool ok = true;
       for (; it < total; ++it) {
-        ok = bar_wait(full + 8 * s, phase) && bar_wait(acc_empty + 8 * as, acc_phase);
+        ok = bar_wait(full + 8 * s, phase, limit) && bar_wait(acc_empty + 8 * as, acc_phase, limit);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
@@ -689,21 +694,26 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
         }
       }
       if (!ok) sm->err = 1;
-      // the MMAs issued must land before the tensor memory is released
-      if (it > 0) (void)bar_wait(empty + 8 * (s ? s - 1 : NS - 1), s ? phase : phase ^ 1);
+      // the MMAs issued, and their arrivals, must land before the tensor
+      // memory is released and the block leaves
+      if (it > 0) {
+        (void)bar_wait(empty + 8 * (s ? s - 1 : NS - 1), s ? phase : phase ^ 1, kWaitLimit);
+        (void)bar_wait(acc_full + 8 * (as ? as - 1 : AS - 1), as ? acc_phase ^ 1 : acc_phase, kWaitLimit);
+      }
     } else {
       // ---- scales: xs ws of kFBatch blocks at a time, one value a thread
       // and step: block i % kFBatch, row i / kFBatch
       const int st = tid - (EW + 2) * 32;
       int batch = 0;
-      bool ok = true;
+      bool ok = gives_up != kScales;
+      if (!ok) sm->err = 1;
       for (int u = first; u < units && ok; u += step) {
         const Fp8Unit un = fp8_unit<NT>(u, p.units_n, p.G, tiles, offs);
         const int nb = un.n0 / kFK;
         const float* ws = p.ws + (int64_t)un.g * p.NB * p.KB;
         for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
           const int buf = batch & 1;
-          ok = batch < 2 || mbar_wait(&sm->sc_empty[buf], ((batch >> 1) - 1) & 1);
+          ok = batch < 2 || mbar_wait(&sm->sc_empty[buf], ((batch >> 1) - 1) & 1, limit);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             sm->err = 1;
@@ -744,7 +754,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     // ---- sums. A wait that runs out ends every later wait of its warp and
     // leaves NaN in the rows it still writes.
     int it = 0, batch = 0;
-    bool ok = true;
+    bool ok = gives_up != kSums;
     if constexpr (C::XA) {
       // warp w: tensor memory lanes 32 (w % 4) .. + 31, a row of x each, and
       // columns 128 (w / 4) .. + 127, one block of n
@@ -762,7 +772,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
 #pragma unroll
         for (int i = 0; i < CW; ++i) acc[i] = 0.f;
         for (int kb = kb0; kb < kb1 && ok; kb += kFBatch) {
-          ok = bar_wait(sc_full + 8 * buf, sc_phase);
+          ok = bar_wait(sc_full + 8 * buf, sc_phase, limit);
           if (!ok) break;
           const int blocks = min(kFBatch, kb1 - kb);
           const float* sc = &sm->sc[buf][0][l0 + lane];
@@ -770,7 +780,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
 #pragma unroll 1
           for (int b = 0; b < blocks; ++b) {
             const float s = sc[b * (C::Scales + 4)] * scw[2 * b];
-            ok = bar_wait(acc_full + 8 * as, acc_phase);
+            ok = bar_wait(acc_full + 8 * as, acc_phase, limit);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t ta = tbase + (uint32_t)(as * C::DN);
@@ -856,12 +866,12 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
         for (int i = 0; i < CW / 2; ++i) acc[i >> 2][(i >> 1) & 1][i & 1][0] = acc[i >> 2][(i >> 1) & 1][i & 1][1] = 0.f;
         for (int kb = kb0; kb < kb1; kb += kFBatch, ++batch) {
           const int buf = batch & 1;
-          ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1);
+          ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1, limit);
           const int blocks = min(kFBatch, kb1 - kb);
           for (int b = 0; b < blocks; ++b, ++it) {
             const int as = it % AS;
             const float* sc = &sm->sc[buf][b][2 * tq];
-            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1);
+            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1, limit);
             if (!ok) continue;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t ta = tbase + (uint32_t)(as * C::DN);
@@ -1042,6 +1052,7 @@ const char* fp8_launch(const Fp8MatmulArgs& a, int sms, cudaStream_t s) {
   p.G = a.G;
   p.N = a.N;
   p.K = a.K;
+  p.give_up = a.give_up;
   // XA stores whole sectors, else 16 bytes
   p.vec = !(((uintptr_t)a.y | (uint64_t)(a.ldy * (int64_t)sizeof(Y))) & (C::XA ? 31 : 15));
   // at most this many row tiles: every group's last one may be short

@@ -1,6 +1,6 @@
 // ops.cu — C entry points of the expert-path operators (no handle): argument
 // checks, the device, the launch. They keep nothing between calls but the
-// SM count of each device.
+// SM count of each device (and what the test hook asks of the next product).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -59,6 +59,8 @@ class OnDevice {
  private:
   int before_ = 0, now_ = 0, rc_ = DF_MOE_OK;
 };
+
+thread_local int give_up_next = 0;
 
 constexpr int64_t kMaxRows = 0x7fffffff;
 constexpr int kMaxHidden = 1 << 18;
@@ -244,6 +246,12 @@ DF_MOE_API int df_moe_fp8_quantize(int device, const void* x, int32_t dtype, int
                   dfm::launch_fp8_quantize(a, dtype, on.sms(), (cudaStream_t)stream));
 }
 
+DF_MOE_API int df_moe_test_fp8_give_up(int32_t role) {
+  if (role < 0 || role > 4) return fail(DF_MOE_EINVAL, "role must be in [0, 4]");
+  give_up_next = role;
+  return DF_MOE_OK;
+}
+
 DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, const float* xs,
                                  int64_t ldxs, const uint8_t* w, int64_t ldw, const float* ws,
                                  const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K,
@@ -291,6 +299,8 @@ DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, cons
   a.ldw = ldw;
   a.ldy = ldy;
   a.status = status;
+  a.give_up = give_up_next;
+  give_up_next = 0;
   const char* err = dfm::launch_fp8_matmul(a, dtype, on.sms(), (cudaStream_t)stream);
   if (err) {
     (void)cudaGetLastError();

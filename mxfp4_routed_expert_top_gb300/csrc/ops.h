@@ -86,6 +86,7 @@ struct Fp8MatmulArgs {
   int G, N, K, transposed;
   int64_t M, ldx, ldxs, ldw, ldy;  // in elements
   uint32_t* status;
+  int give_up;  // test hook: 0, or the role (1 to 4) of block 0 that gives up
 };
 // What it could not do, as text, or null.
 const char* launch_fp8_matmul(const Fp8MatmulArgs& p, int dtype, int sms, cudaStream_t s);

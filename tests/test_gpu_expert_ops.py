@@ -702,3 +702,63 @@ def test_calls_without_a_stream_are_captured(dfm):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(m.outputs(), want))
+
+
+# ---- waits that run out -------------------------------------------------------------
+def given_up(dfm, role, counts, N, K, trans, seed):
+    """(clean y, y, status) of the product where `role` of block 0 gives up."""
+    g = gen(seed)
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    M, G = int(offs[-1]), len(counts)
+    x, xs, w, ws = product_inputs(G, M, N, K, trans, g)
+    o = torch.from_numpy(offs.astype(np.int32)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = [torch.full((M, N), 7.0, device="cuda") for _ in range(3)]
+
+    def call(out):
+        dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, out, "f32", transposed=trans, ldx=x.shape[1], ldw=w.shape[2],
+                       status=status)
+        torch.cuda.synchronize()
+        return status.item()
+
+    assert call(y[0]) == 0
+    dfm.test_fp8_give_up(role)
+    found = call(y[1])
+    status.zero_()
+    assert call(y[2]) == 0 and torch.equal(y[2], y[0])  # the request was for one call
+    return y[0], y[1], found
+
+
+GIVE_UP = [  # the 128-row form, few blocks of K and many; more units than SMs; short tiles
+    ([300, 200], 300, 200, False), ([300, 200], 300, 1500, True), ([40000], 256, 700, False),
+    ([1] * 16, 257, 100, False), ([16] * 340, 120, 1024, True),
+]
+
+
+@pytest.mark.parametrize("role", [1, 2, 3, 4])
+@pytest.mark.parametrize("counts, N, K, trans", GIVE_UP)
+def test_product_reports_a_wait_that_gave_up(dfm, counts, N, K, trans, role):
+    """Status bit 2, NaN in what block 0 computes, every other value as ever."""
+    clean, got, status = given_up(dfm, role, counts, N, K, trans, 50)
+    assert status == 2
+    gone = got.isnan()
+    assert bool(gone[0, 0]) and torch.equal(got[~gone], clean[~gone])
+    # whole units of at most 128 rows x 256 columns, three of them at most
+    assert int(gone.sum()) <= 3 * 128 * 256
+
+
+@pytest.mark.parametrize("role", [1, 2, 3, 4])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts, N, K", [([3], 128, 1024), ([30], 300, 2000), ([1] * 4, 256, 500)])
+def test_product_reports_a_wait_that_gave_up_in_a_part_of_k(dfm, counts, N, K, trans, role):
+    """Calls whose units are shared by the CTAs of a cluster: what the other
+    clusters compute is as ever."""
+    clean, got, status = given_up(dfm, role, counts, N, K, trans, 51)
+    assert status == 2
+    assert torch.equal(got[:, 128:], clean[:, 128:]) and torch.equal(got[counts[0]:], clean[counts[0]:])
+
+
+def test_product_give_up_is_checked(dfm):
+    for role in (-1, 5):
+        with pytest.raises(dfm.DfMoeError):
+            dfm.test_fp8_give_up(role)
