@@ -969,7 +969,12 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   __syncwarp();
   if (!C::XA && p.split > 1 && first < units) {
     // one unit a cluster: part q sums the rows r = q, q + split, ... over the
-    // parts in their order
+    // parts in their order. A part whose waits ran out is NaN: its sums were
+    // written while copies could still land in the stages, which are drained
+    // by now.
+    __syncthreads();
+    if (*(volatile int*)&sm->err)
+      for (int i = tid; i < 128 * NT; i += C::NTHR) reinterpret_cast<float*>(smem)[i] = __uint_as_float(0x7fffffffu);
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const Fp8Unit un = fp8_unit<NT>(first, p.units_n, p.G, tiles, offs);

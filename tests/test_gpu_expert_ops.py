@@ -756,6 +756,8 @@ def test_product_reports_a_wait_that_gave_up_in_a_part_of_k(dfm, counts, N, K, t
     clean, got, status = given_up(dfm, role, counts, N, K, trans, 51)
     assert status == 2
     assert torch.equal(got[:, 128:], clean[:, 128:]) and torch.equal(got[counts[0]:], clean[counts[0]:])
+    # the sum over the parts is NaN if one of them is
+    assert bool(got[:counts[0], :128].isnan().all())
 
 
 def test_product_give_up_is_checked(dfm):
