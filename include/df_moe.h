@@ -457,6 +457,8 @@ DF_MOE_API int df_moe_fp8_quantize(int device, const void* x, int32_t dtype, int
  *   transposed: the same product with w stored [G][K][N] (K * ldw apart) and
  *      ws [G][ceil(K / 128)][ceil(N / 128)]: with the forward's own w and ws,
  *      and rows of dy, this is the gradient of x
+ *   (scales may have any size: xs ws need not be a normal number where the
+ *      sums are)
  *   offs [G + 1] ascending, read as if clamped to [0, M]; rows outside every
  *      group are left as they were, and all of y where offs descends; NULL: one
  *      group of all M rows (G = 1)

@@ -20,6 +20,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "ops.h"
@@ -311,8 +312,9 @@ template <int NT>
 struct Fp8Smem {
   using C = Fp8Cfg<NT>;
   uint8_t out[C::EW][C::XA ? 2048 : 512];   // what a warp rearranges of y
-  float sc[2][kFBatch][C::Scales + 4];      // scales of two batches of blocks: xs (times ws unless XA)
-  float scw[2][kFBatch][2];                 // XA: ws of the unit's two blocks of n
+  float sc[2][kFBatch][C::Scales + 4];      // scales of two batches of blocks: xs (times ws unless XA or wide)
+  float scw[2][kFBatch][2];                 // ws of the unit's blocks of n
+  int wide[2][2];                           // a scale warp's rows have a product xs ws out of range
   uint64_t full[C::NS], empty[C::NS];
   uint64_t acc_full[C::AS], acc_empty[C::AS];
   uint64_t sc_full[2], sc_empty[2];
@@ -532,6 +534,33 @@ __device__ __forceinline__ int scale_slot(int c) {
   return (c & ~15) | ((c & 6) << 1) | ((c & 8) >> 2) | (c & 1);
 }
 
+// Scales of any size: xs ws may leave fp32's normal range where xs ws P does
+// not (rows of zeros have scales of 2^-109). The scale warps look at the
+// products of each batch of blocks; one that holds such a product (wide) is
+// added with two factors a value, P times the first times the second, at 1.3
+// times the usual time (2048 x 16 rows of 32 experts, 1536 x 7168, every
+// product wide: 371 us, 272 otherwise); rows whose products are normal get
+// the same bits in either.
+//
+// The two factors: P times the first, times the second, has neither
+// overflow nor underflow on the way that the result has not. 1 and xs ws,
+// unless that product is not a normal number: then the larger scale first
+// where it is too small (the smaller is at least 2^-149, so the larger is below
+// 2^23, and |P| below 2^25), the smaller first where it is too large.
+__device__ __forceinline__ bool out_of_range(float xs, float ws) {
+  const float s = fabsf(xs * ws);
+  return !(s >= 0x1p-126f && s < INFINITY) && xs != 0.f && ws != 0.f;
+}
+// The same for several xs, of which the smallest but zero (its bits less one;
+// all ones where there is none) and the largest magnitude are given.
+__device__ __forceinline__ bool out_of_range(uint32_t least, float most, float ws) {
+  return least != 0xffffffffu && (out_of_range(__uint_as_float(least + 1), ws) || out_of_range(most, ws));
+}
+__device__ __forceinline__ float2 scale_factors(float xs, float ws) {
+  if (!out_of_range(xs, ws)) return make_float2(1.f, xs * ws);
+  return (fabsf(xs * ws) < 1.f) == (fabsf(xs) > fabsf(ws)) ? make_float2(xs, ws) : make_float2(ws, xs);
+}
+
 template <int NT, bool TRANS, typename Y>
 __global__ void __launch_bounds__(Fp8Cfg<NT>::NTHR, Fp8Cfg<NT>::CtasPerSm)
 fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
@@ -725,11 +754,14 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           for (int h = 0; h < (C::XA ? 2 : 1); ++h)
             if (b < kb1 && nb + h < p.NB)
               wv[h] = TRANS ? ws[(int64_t)b * p.NB + nb + h] : ws[(int64_t)(nb + h) * p.KB + b];
-          if (C::XA && st < kFBatch) {
+          if (st < kFBatch) {
             sm->scw[buf][st][0] = wv[0];
             sm->scw[buf][st][1] = wv[1];
           }
           const float* xs = p.xs + un.row0 * p.ldxs + b;
+          bool wide = false;
+          uint32_t least = 0xffffffffu;  // the smallest |xs| but zero, its bits less one, and the largest
+          float most = 0.f;
           constexpr int PER = (C::XA ? 128 : NT) * kFBatch / 64, U = PER < 8 ? PER : 8;
           for (int i0 = 0; i0 < PER; i0 += U) {
             float v[U];
@@ -738,13 +770,22 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
               const int r = st / kFBatch + 64 / kFBatch * (i0 + i);
               v[i] = b < kb1 && r < un.rows ? xs[r * p.ldxs] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              least = min(least, __float_as_uint(fabsf(v[i])) - 1);  // zero: the largest
+              most = fmaxf(most, fabsf(v[i]));
+            }
+            static_assert(C::XA || PER == U, "all of a warp's rows are known before the first is stored");
+            if (!C::XA) wide = __any_sync(0xffffffffu, out_of_range(least, most, wv[0]));
             float* sc = sm->sc[buf][st & (kFBatch - 1)];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
               const int r = st / kFBatch + 64 / kFBatch * (i0 + i);
-              sc[C::XA ? r : scale_slot(r)] = C::XA ? v[i] : v[i] * wv[0];
+              sc[C::XA ? r : scale_slot(r)] = C::XA || wide ? v[i] : v[i] * wv[0];
             }
           }
+          if (C::XA) wide = __any_sync(0xffffffffu, out_of_range(least, most, wv[0]) || out_of_range(least, most, wv[1]));
+          if (lane == 0) sm->wide[buf][st >> 5] = wide;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->sc_full[buf]);
         }
@@ -777,31 +818,43 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           const int blocks = min(kFBatch, kb1 - kb);
           const float* sc = &sm->sc[buf][0][l0 + lane];
           const float* scw = &sm->scw[buf][0][c0 >> 7];
+          const auto add_blocks = [&](auto is_wide) {
+            constexpr bool WIDE = decltype(is_wide)::value;
 #pragma unroll 1
-          for (int b = 0; b < blocks; ++b) {
-            const float s = sc[b * (C::Scales + 4)] * scw[2 * b];
-            ok = bar_wait(acc_full + 8 * as, acc_phase, limit);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t ta = tbase + (uint32_t)(as * C::DN);
-            constexpr int L = 16;  // columns a load
-            uint32_t r[2][L];      // the next load runs while this one is added
-            tmem_ld_rows(r[0], ta);
+            for (int b = 0; b < blocks; ++b) {
+              const float xs = sc[b * (C::Scales + 4)], ws = scw[2 * b];
+              const float2 f = WIDE ? scale_factors(xs, ws) : make_float2(1.f, xs * ws);
+              ok = bar_wait(acc_full + 8 * as, acc_phase, limit);
+              if (!ok) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint32_t ta = tbase + (uint32_t)(as * C::DN);
+              constexpr int L = 16;           // columns a load
+              constexpr int A = WIDE ? 0 : 1;  // the next load runs while this one is added (WIDE: no registers left)
+              uint32_t r[1 + A][L];
+              tmem_ld_rows(r[0], ta);
 #pragma unroll
-            for (int i = 0; i < CW / L; ++i) {
-              tmem_wait(r[i & 1]);
-              if (i + 1 < CW / L) {
-                tmem_ld_rows(r[(i + 1) & 1], ta + L * (i + 1));
-              } else {
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                arrive_if(acc_empty + 8 * as, leader);
+              for (int i = 0; i < CW / L; ++i) {
+                if (WIDE && i) tmem_ld_rows(r[0], ta + L * i);
+                tmem_wait(r[i & A]);
+                if (i + 1 < CW / L) {
+                  if (!WIDE) tmem_ld_rows(r[(i + 1) & A], ta + L * (i + 1));
+                } else {
+                  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                  arrive_if(acc_empty + 8 * as, leader);
+                }
+#pragma unroll
+                for (int c = 0; c < L; ++c) {
+                  const float v = __uint_as_float(r[i & A][c]);
+                  acc[L * i + c] = fmaf(WIDE ? v * f.x : v, f.y, acc[L * i + c]);
+                }
               }
-#pragma unroll
-              for (int c = 0; c < L; ++c) acc[L * i + c] = fmaf(__uint_as_float(r[i & 1][c]), s, acc[L * i + c]);
+              as ^= 1;
+              acc_phase ^= as ^ 1;
             }
-            as ^= 1;
-            acc_phase ^= as ^ 1;
-          }
+          };
+          const int2 wide = *reinterpret_cast<const int2*>(sm->wide[buf]);
+          if (wide.x | wide.y) add_blocks(std::true_type());
+          else add_blocks(std::false_type());
           __syncwarp();
           arrive_if(sc_empty + 8 * buf, leader);
           buf ^= 1;
@@ -810,7 +863,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
         if (!ok) {
           sm->err = 1;
 #pragma unroll
-          for (int i = 0; i < CW; ++i) acc[i] = __uint_as_float(0x7fffffffu);
+          for (int i = 0; i < CW; ++i) acc[i] = fmaf(acc[i], __uint_as_float(0x7fffffffu), acc[i]);  // (a move costs spills)
         }
         const int n0 = un.n0 + c0, row = l0 + lane;
         Y* y = static_cast<Y*>(p.y) + (un.row0 + row) * p.ldy + n0;
@@ -868,43 +921,59 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
           const int buf = batch & 1;
           ok = ok && bar_wait(smem_u32(&sm->sc_full[buf]), (batch >> 1) & 1, limit);
           const int blocks = min(kFBatch, kb1 - kb);
-          for (int b = 0; b < blocks; ++b, ++it) {
-            const int as = it % AS;
-            const float* sc = &sm->sc[buf][b][2 * tq];
-            ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1, limit);
-            if (!ok) continue;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t ta = tbase + (uint32_t)(as * C::DN);
-            // load i: columns LC (i / 2) .., lanes 16 (i % 2) ..; the next
-            // runs while this one is added
-            uint32_t r[2][4 * LDN];
-            tmem_ld(r[0], ta);
+          // a thread's rows are all of one scale warp
+          const bool raw = sm->wide[buf][tq >> 2], wide = sm->wide[buf][0] | sm->wide[buf][1];
+          const auto add_blocks = [&](auto is_wide) {
+            constexpr bool WIDE = decltype(is_wide)::value;
+            for (int b = 0; b < blocks; ++b, ++it) {
+              const int as = it % AS;
+              const float* sc = &sm->sc[buf][b][2 * tq];
+              const float ws = WIDE ? sm->scw[buf][b][0] : 0.f;
+              ok = ok && bar_wait(smem_u32(&sm->acc_full[as]), (it / AS) & 1, limit);
+              if (!ok) continue;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint32_t ta = tbase + (uint32_t)(as * C::DN);
+              // load i: columns LC (i / 2) .., lanes 16 (i % 2) ..; the next
+              // runs while this one is added
+              uint32_t r[2][4 * LDN];
+              tmem_ld(r[0], ta);
 #pragma unroll
-            for (int i = 0; i < 2 * CH; ++i) {
-              tmem_wait(r[i & 1]);
-              if (i + 1 < 2 * CH) {
-                tmem_ld(r[(i + 1) & 1], ta + ((uint32_t)(16 * ((i + 1) & 1)) << 16) + (uint32_t)(LC * ((i + 1) / 2)));
-              } else {
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
-              }
+              for (int i = 0; i < 2 * CH; ++i) {
+                tmem_wait(r[i & 1]);
+                if (i + 1 < 2 * CH) {
+                  tmem_ld(r[(i + 1) & 1], ta + ((uint32_t)(16 * ((i + 1) & 1)) << 16) + (uint32_t)(LC * ((i + 1) / 2)));
+                } else {
+                  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                  if (lane == 0) mbar_arrive(&sm->acc_empty[as]);
+                }
 #pragma unroll
-              for (int g = 0; g < LDN; g += 2) {
-                const int gc = LDN * (i / 2) + g, h = i & 1;
-                const uint32_t* v = &r[i & 1][4 * g];
-                const float4 s = *reinterpret_cast<const float4*>(sc + 8 * gc);
+                for (int g = 0; g < LDN; g += 2) {
+                  const int gc = LDN * (i / 2) + g, h = i & 1;
+                  const uint32_t* v = &r[i & 1][4 * g];
+                  float4 s = *reinterpret_cast<const float4*>(sc + 8 * gc), f;
+                  if (WIDE) {
+                    const float2 q[4] = {raw ? scale_factors(s.x, ws) : make_float2(1.f, s.x),
+                                         raw ? scale_factors(s.y, ws) : make_float2(1.f, s.y),
+                                         raw ? scale_factors(s.z, ws) : make_float2(1.f, s.z),
+                                         raw ? scale_factors(s.w, ws) : make_float2(1.f, s.w)};
+                    f = make_float4(q[0].x, q[1].x, q[2].x, q[3].x);
+                    s = make_float4(q[0].y, q[1].y, q[2].y, q[3].y);
+                  }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float* lo = acc[gc][h][j];
-                  float* hi = acc[gc + 1][h][j];
-                  lo[0] = fmaf(__uint_as_float(v[2 * j]), s.x, lo[0]);
-                  lo[1] = fmaf(__uint_as_float(v[2 * j + 1]), s.y, lo[1]);
-                  hi[0] = fmaf(__uint_as_float(v[2 * j + 4]), s.z, hi[0]);
-                  hi[1] = fmaf(__uint_as_float(v[2 * j + 5]), s.w, hi[1]);
+                  for (int j = 0; j < 2; ++j) {
+                    float* lo = acc[gc][h][j];
+                    float* hi = acc[gc + 1][h][j];
+                    lo[0] = fmaf(WIDE ? __uint_as_float(v[2 * j]) * f.x : __uint_as_float(v[2 * j]), s.x, lo[0]);
+                    lo[1] = fmaf(WIDE ? __uint_as_float(v[2 * j + 1]) * f.y : __uint_as_float(v[2 * j + 1]), s.y, lo[1]);
+                    hi[0] = fmaf(WIDE ? __uint_as_float(v[2 * j + 4]) * f.z : __uint_as_float(v[2 * j + 4]), s.z, hi[0]);
+                    hi[1] = fmaf(WIDE ? __uint_as_float(v[2 * j + 5]) * f.w : __uint_as_float(v[2 * j + 5]), s.w, hi[1]);
+                  }
                 }
               }
             }
-          }
+          };
+          if (wide) add_blocks(std::true_type());
+          else add_blocks(std::false_type());
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->sc_empty[buf]);
         }

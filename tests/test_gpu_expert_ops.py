@@ -764,3 +764,63 @@ def test_product_give_up_is_checked(dfm):
     for role in (-1, 5):
         with pytest.raises(dfm.DfMoeError):
             dfm.test_fp8_give_up(role)
+
+
+# ---- scales whose product is no normal number -----------------------------------------
+WIDE = [[5, 0, 9], [25, 30], [300, 90], [2] * 300]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", WIDE)
+def test_product_scales_below_the_normal_range(dfm, counts, trans):
+    """xs of three sizes (1e-24, quantize's for a row of zeros, ordinary) times
+    ws of two: products that are subnormal or below the smallest, whose sums
+    are not. Each block of K adds at most half the smallest subnormal to the
+    bound; the ordinary rows have the bits that they have alone."""
+    g = gen(60)
+    M, G, N, K = sum(counts), len(counts), 390, 1200
+    x, xs, w, ws = product_inputs(G, M, N, K, trans, g)
+    odd = torch.arange(ws.shape[2 if trans else 1], device="cuda") % 2 == 1
+    size = torch.where(odd, 2.0 ** -42, 1e-20)
+    ws = (0.5 + torch.rand(ws.shape, generator=g, device="cuda")) * (size if trans else size[:, None])
+    o = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+
+    def call(scales):
+        y = torch.full((M, N), 7.0, device="cuda")
+        dfm.fp8_matmul(x, scales, w, ws, o, G, M, N, K, y, "f32", transposed=trans, ldx=x.shape[1], ldw=w.shape[2])
+        return y
+
+    ordinary = call(xs)
+    xs[0::3] *= 1e-22  # from about 1e-2
+    xs[1::3] = 2.0 ** -100 / 448
+    y = call(xs)
+    assert torch.equal(y[2::3], ordinary[2::3])
+    want, total = product_definition(x, xs, w, ws, o.tolist(), N, K, trans)
+    kb = -(-K // 128)
+    within(y, want, (128 + kb + 3) * 2.0 ** -23 * total + kb * 2.0 ** -150, "f32")
+    assert bool((y[1, 128:256] != 0).any())
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", WIDE)
+def test_product_scales_above_the_normal_range(dfm, counts, trans):
+    """xs ws = 2^130 in one block of K: columns whose weights are 0 there get
+    nothing from it, and those with x w = 2^-18 get 128 2^-18 2^130 = 2^119."""
+    g = gen(61)
+    M, G, N, K = sum(counts), len(counts), 300, 640
+    x, xs, w, ws = product_inputs(G, M, N, K, trans, g)
+    x[:, 128:256] = 1  # the code of 2^-9
+    block = (slice(None), slice(128, 256), slice(None)) if trans else (slice(None), slice(None), slice(128, 256))
+    w[block] = 0
+    w[(slice(None), slice(128, 256), slice(128, N)) if trans else (slice(None), slice(128, N), slice(128, 256))] = 1
+    xs[:, 1] = 2.0 ** 70
+    if trans:
+        ws[:, 1] = 2.0 ** 60
+    else:
+        ws[:, :, 1] = 2.0 ** 60
+    o = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+    y = torch.full((M, N), 7.0, device="cuda")
+    dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, y, "f32", transposed=trans, ldx=x.shape[1], ldw=w.shape[2])
+    want, total = product_definition(x, xs, w, ws, o.tolist(), N, K, trans)
+    within(y, want, (128 + 5 + 3) * 2.0 ** -23 * total, "f32")
+    assert bool((y[:, 128:] == 2.0 ** 119).all())
