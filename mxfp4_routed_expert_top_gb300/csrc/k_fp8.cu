@@ -578,10 +578,6 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.w) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&p.x) : "memory");
   }
-  if (warp == EW + 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(C::Cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sm->full[i], 1);
@@ -599,6 +595,12 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
     fence_barrier_init();
   }
   pdl_wait();  // the kernel before this one is complete
+  // Tensor memory only from here on: a kernel that lets its dependents start
+  // and takes its own later would wait for this block, which waits for it.
+  if (warp == EW + 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(C::Cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   // the groups' first rows, kept inside [0, M] whatever the caller's array
   // holds, and their tiles; groups that are not in order have no units
   bool bad = false;

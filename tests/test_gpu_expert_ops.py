@@ -824,3 +824,61 @@ def test_product_scales_above_the_normal_range(dfm, counts, trans):
     want, total = product_definition(x, xs, w, ws, o.tolist(), N, K, trans)
     within(y, want, (128 + 5 + 3) * 2.0 ** -23 * total, "f32")
     assert bool((y[:, 128:] == 2.0 ** 119).all())
+
+
+# ---- behind a kernel that lets its dependents start early ------------------------------
+EARLY_KERNEL = r"""
+#include <cuda_runtime.h>
+#include <stdint.h>
+// One warp a block: lets the next kernel's blocks start, waits about 50 us,
+// takes all of its SM's tensor memory, gives it back and leaves a mark.
+__global__ void early(int* mark) {
+  __shared__ uint32_t at;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = 0; i < 50; ++i) __nanosleep(1000);
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"((uint32_t)__cvta_generic_to_shared(&at)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  __syncwarp();
+  const uint32_t columns = *(volatile uint32_t*)&at;
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(columns) : "memory");
+  if (threadIdx.x == 0) mark[blockIdx.x] = 1;
+}
+extern "C" __attribute__((visibility("default"))) int launch_early(int* mark, int blocks, void* stream) {
+  early<<<blocks, 32, 0, (cudaStream_t)stream>>>(mark);
+  return (int)cudaGetLastError();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def early_kernel(dfm, tmp_path_factory):
+    import ctypes
+    import subprocess
+    d = tmp_path_factory.mktemp("early")
+    (d / "early.cu").write_text(EARLY_KERNEL)
+    subprocess.run(["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-Xcompiler", "-fPIC", "-o",
+                    str(d / "early.so"), str(d / "early.cu")], check=True)
+    f = ctypes.CDLL(str(d / "early.so")).launch_early
+    f.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
+    return f
+
+
+@pytest.mark.parametrize("counts, N, K", [([1], 1536, 1024), ([5] * 16, 512, 700), ([30] * 9, 512, 700), ([400], 256, 512)])
+def test_product_behind_a_kernel_that_takes_tensor_memory_late(dfm, early_kernel, counts, N, K):
+    """The product's blocks may start beside that kernel's, one an SM; they
+    take no tensor memory before it has ended."""
+    g = gen(70)
+    M, G = sum(counts), len(counts)
+    x, xs, w, ws = product_inputs(G, M, N, K, False, g)
+    o = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    mark = torch.zeros(sms, dtype=torch.int32, device="cuda")
+    y = [torch.full((M, N), 7.0, device="cuda") for _ in range(2)]
+    kw = dict(ldx=x.shape[1], ldw=w.shape[2])
+    dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, y[0], "f32", **kw)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        assert early_kernel(mark.data_ptr(), sms, None) == 0
+        dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, y[1], "f32", stream=0, **kw)
+    torch.cuda.synchronize()
+    assert bool((mark == 1).all()) and torch.equal(y[0], y[1])
