@@ -30,6 +30,7 @@
 #include "internal.h"
 #include "ops.h"
 #include "pipeline.cuh"
+#include "rowword.h"
 
 namespace dfm {
 namespace {
@@ -85,36 +86,53 @@ __device__ __forceinline__ void copy_rows(const PermuteArgs& p, int t0, int t1, 
 // is what the row lacks to a 4-byte boundary, so that its store is aligned;
 // each value comes from three aligned words of x by a funnel shift (words
 // without a byte of the row are not read). The first and last words of a row
-// are stored byte by byte.
-__device__ __forceinline__ void copy_rows_odd(const PermuteArgs& p, int t0, int t1, const int32_t* pos, int w0,
-                                              int w1) {
-  const int nw = w1 - w0, items = (t1 - t0) * nw, bytes = (int)p.bytes;
-  for (int i = threadIdx.x; i < items; i += blockDim.x) {
-    const int dt = i / nw, from = 4 * (w0 + i - dt * nw - 1);
-    const char* x = p.x + (int64_t)(t0 + dt) * p.ldx;
-    const int m = (int)((uintptr_t)(x + from) & 3);
-    uint32_t word[3];
+// are stored byte by byte. ENDS: words of x may reach over the array's ends,
+// and are then read byte by byte.
+template <bool ENDS>
+__device__ __forceinline__ void copy_word_odd(const PermuteArgs& p, int t0, const int32_t* pos, int w0, int nw, int i) {
+  const int dt = i / nw, from = 4 * (w0 + i - dt * nw - 1), bytes = (int)p.bytes;
+  const char* x = p.x + (int64_t)(t0 + dt) * p.ldx;
+  const int m = (int)((uintptr_t)(x + from) & 3);
+  uint32_t word[3];
 #pragma unroll
-    for (int n = 0; n < 3; ++n) {
-      const int c = from - m + 4 * n;  // bytes c .. c + 3 of the row
+  for (int n = 0; n < 3; ++n) {
+    const int c = from - m + 4 * n;  // bytes c .. c + 3 of the row
+    if (ENDS) {
+      const Four<char> four = array_four<char>(ArrayOf<char>{p.x}, x + c - p.x, (int64_t)(p.T - 1) * p.ldx + bytes);
+      memcpy(&word[n], &four, 4);
+    } else {
       word[n] = c + 3 >= 0 && c < bytes ? *reinterpret_cast<const uint32_t*>(x + c) : 0;
     }
-    const int32_t* at = pos + dt * p.k;
-    for (int j = 0; j < p.k; ++j) {
-      const int32_t q = at[j];
-      if (q < 0) continue;
-      char* row = p.rows + q * p.ldr;
-      const int a = (int)(-(uintptr_t)row & 3), c = from + a, s = m + a;
-      const uint32_t v = s < 4 ? __funnelshift_r(word[0], word[1], 8 * s) : __funnelshift_r(word[1], word[2], 8 * (s - 4));
-      if (c >= 0 && c + 4 <= bytes) {
-        *reinterpret_cast<uint32_t*>(row + c) = v;
-      } else {
+  }
+  const int32_t* at = pos + dt * p.k;
+  for (int j = 0; j < p.k; ++j) {
+    const int32_t q = at[j];
+    if (q < 0) continue;
+    char* row = p.rows + q * p.ldr;
+    const int a = (int)(-(uintptr_t)row & 3), c = from + a, s = m + a;
+    const uint32_t v = s < 4 ? __funnelshift_r(word[0], word[1], 8 * s) : __funnelshift_r(word[1], word[2], 8 * (s - 4));
+    if (c >= 0 && c + 4 <= bytes) {
+      *reinterpret_cast<uint32_t*>(row + c) = v;
+    } else {
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (c + b >= 0 && c + b < bytes) row[c + b] = (char)(v >> (8 * b));
-      }
+      for (int b = 0; b < 4; ++b)
+        if (c + b >= 0 && c + b < bytes) row[c + b] = (char)(v >> (8 * b));
     }
   }
+}
+
+// Reads reach at most 3 bytes over a row: over the array's start in the first
+// two words of token 0, over its end in the last three of the last token (in
+// any where rows are nearer than that). The block's last threads take those:
+// a test in every word cost 7%, and first threads 1 us a call of short rows.
+__device__ __forceinline__ void copy_rows_odd(const PermuteArgs& p, int t0, int t1, const int32_t* pos, int w0,
+                                              int w1) {
+  const int nw = w1 - w0, items = (t1 - t0) * nw, last = (int)((p.bytes + 3) / 4) + 1 - 3;
+  const int head = p.ldx < 3 ? items : t0 == 0 ? max(0, min(2 - w0, nw)) : 0;
+  const int tail = t1 == p.T ? max(0, min(min(w1 - last, nw), items - head)) : 0;
+  for (int i = blockDim.x - 1 - threadIdx.x; i < head + tail; i += blockDim.x)
+    copy_word_odd<true>(p, t0, pos, w0, nw, i < head ? i : items - tail + i - head);
+  for (int i = head + threadIdx.x; i < items - tail; i += blockDim.x) copy_word_odd<false>(p, t0, pos, w0, nw, i);
 }
 
 __device__ __forceinline__ void copy_scales(const PermuteArgs& p, int t0, int t1,

@@ -173,3 +173,46 @@ def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name,
     call(**dict(tensors, stream=0x77))
     call(**dict(tensors, stream=0))
     assert seen == [0x5000, None, 0x77, 0]
+
+
+ROW_WORD_TEST = r"""
+#include <cstdint>
+#include <cstdio>
+#include "rowword.h"
+// Every read of an array, checked: n values, the first of them at address `at`
+// (in values), where words of four start at multiples of four.
+struct Checked {
+  int at, n;
+  void seen(int64_t i) const { if (i < 0 || i >= n) { std::printf("read of value %d of %d\n", (int)i, n); throw 1; } }
+  dfm::Four<uint16_t> four(int64_t i) const {
+    dfm::Four<uint16_t> r;
+    if ((at + i) & 3) { std::printf("word %d not aligned\n", (int)(at + i)); throw 1; }
+    for (int u = 0; u < 4; ++u) { seen(i + u); r.v[u] = (uint16_t)(100 + i + u); }
+    return r;
+  }
+  uint16_t one(int64_t i) const { seen(i); return (uint16_t)(100 + i); }
+};
+int main() {
+  for (int at = 8; at < 12; ++at)
+    for (int n = 1; n < 40; ++n)
+      for (int w = 0; w < 60; w += 4) {
+        const dfm::Four<uint16_t> r = dfm::array_four<uint16_t>(Checked{at, n}, w - at, n);
+        for (int u = 0; u < 4; ++u) {
+          const int i = w - at + u;
+          if (r.v[u] != (i >= 0 && i < n ? 100 + i : 0)) { std::printf("value %d of %d\n", i, n); return 1; }
+        }
+      }
+  return 0;
+}
+"""
+
+
+def test_words_of_unaligned_rows_read_nothing_beside_the_array(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    (tmp_path / "t.cpp").write_text(ROW_WORD_TEST)
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(root, "mxfp4_routed_expert_top_gb300", "csrc"), "-o",
+                    str(tmp_path / "t"), str(tmp_path / "t.cpp")], check=True)
+    r = subprocess.run([str(tmp_path / "t")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
