@@ -25,6 +25,7 @@
 #include "internal.h"
 #include "ops.h"
 #include "pipeline.cuh"
+#include "rowword.h"
 #include "umma.cuh"
 
 namespace dfm {
@@ -159,64 +160,72 @@ fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const Fas
 // what lies between the word boundary and the block), so that a block has 33
 // of them and a lane up to five; words without a value of the block are not
 // read. Where codes lie like x (the same distance of rows modulo 4) their
-// words are aligned too. 14001 x 7167 bf16: 92 us; value by value 109.
-template <typename T>
+// words are aligned too. 14001 x 7167 bf16: 89 us; value by value 109.
+template <typename T, bool ENDS>
+__device__ __forceinline__ void quantize_odd(const QuantizeArgs& p, uint32_t nb, const FastDiv& by_nb, uint32_t g,
+                                             bool there) {
+  constexpr int R = 5;
+  const int l = threadIdx.x & 7;
+  const T* x = static_cast<const T*>(p.x);
+  const uint32_t row = by_nb(there ? g : 0), blk = (there ? g : 0) - row * nb;
+  const int len = there ? min(128, p.K - (int)(128 * blk)) : 0;
+  const T* src = x + (int64_t)row * p.ldx + 128 * blk;
+  const int first = 4 * l - ((int)((uintptr_t)src / sizeof(T)) & 3);
+  Four<T> word[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = first + 32 * r;  // the word's first value
+    if (e < len && e + 3 >= 0) {
+      if (ENDS) word[r] = array_four<T>(ArrayOf<T>{x}, src - x + e, (p.M - 1) * p.ldx + p.K);
+      else word[r] = *reinterpret_cast<const Four<T>*>(src + e);
+    }
+  }
+  float v[4 * R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[4 * r + i] = (unsigned)(first + 32 * r + i) < (unsigned)len ? to_f32<T>(word[r].v[i]) : 0.f;
+  uint32_t code[2 * R];
+  const float scale = quantize_block<4 * R, 2>(v, code);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = first + 32 * r;
+    uint8_t* dst = p.codes + (int64_t)row * p.ldc + 128 * blk + e;
+    const uint32_t four = code[2 * r] | code[2 * r + 1] << 16;
+    if (e >= 0 && e + 3 < len && ((uintptr_t)dst & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(dst) = four;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((unsigned)(e + i) < (unsigned)len) dst[i] = (uint8_t)(four >> (8 * i));
+    }
+  }
+  if (len > 0 && l == 0) p.scales[(int64_t)row * p.lds + blk] = scale;
+}
+
+// Words may reach (at most three values) over an end of x in the first block,
+// the last, and the one before it, behind which K may have one value: CTA 0
+// takes those, and reads no such word. (A test in every block cost 3%.) Where
+// rows are nearer than three values, ALL_ENDS, every block is read like that.
+template <typename T, bool ALL_ENDS>
 __global__ void __launch_bounds__(kQThreads)
 fp8_quantize_odd_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const FastDiv by_nb) {
-  constexpr int R = 5;
-  struct alignas(4 * sizeof(T)) Word {
-    T v[4];
-  };
-  const int l = threadIdx.x & 7, sub = (threadIdx.x >> 3) & 3;
-  const uint32_t warps = gridDim.x * (kQThreads / 32);
-  const uint32_t warp = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
-  const T* x = static_cast<const T*>(p.x);
+  const int sub = (threadIdx.x >> 3) & 3, ends = ALL_ENDS ? 0 : 1;
+  const uint32_t near_end = total < 3 ? 1 : total - 2;
   pdl_wait();
-  for (uint64_t w0 = warp; 4 * w0 < total; w0 += (uint64_t)warps * kQUnroll) {
-    Word word[kQUnroll][R];
-    uint32_t row[kQUnroll], blk[kQUnroll];
-    int len[kQUnroll], first[kQUnroll];
-#pragma unroll
-    for (int u = 0; u < kQUnroll; ++u) {
-      const uint64_t g = 4 * (w0 + (uint64_t)u * warps) + sub;
-      const bool there = g < total;
-      row[u] = by_nb(there ? (uint32_t)g : 0);
-      blk[u] = (there ? (uint32_t)g : 0) - row[u] * nb;
-      len[u] = there ? min(128, p.K - (int)(128 * blk[u])) : 0;
-      const T* src = x + (int64_t)row[u] * p.ldx + 128 * blk[u];
-      const int m = (int)((uintptr_t)src / sizeof(T)) & 3;
-      first[u] = 4 * l - m;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int e = first[u] + 32 * r;  // the word's first value
-        if (e < len[u] && e + 3 >= 0) word[u][r] = *reinterpret_cast<const Word*>(src + e);
-      }
+  if (!ALL_ENDS && blockIdx.x == 0) {
+    if (threadIdx.x < 32) {
+      const uint32_t g = sub ? near_end + sub - 1 : 0;
+      quantize_odd<T, true>(p, nb, by_nb, g, g < total);
     }
-#pragma unroll
-    for (int u = 0; u < kQUnroll; ++u) {
-      float v[4 * R];
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[4 * r + i] = (unsigned)(first[u] + 32 * r + i) < (unsigned)len[u] ? to_f32<T>(word[u][r].v[i]) : 0.f;
-      uint32_t code[2 * R];
-      const float scale = quantize_block<4 * R, 2>(v, code);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int e = first[u] + 32 * r;
-        uint8_t* dst = p.codes + (int64_t)row[u] * p.ldc + 128 * blk[u] + e;
-        const uint32_t four = code[2 * r] | code[2 * r + 1] << 16;
-        if (e >= 0 && e + 3 < len[u] && ((uintptr_t)dst & 3) == 0) {
-          *reinterpret_cast<uint32_t*>(dst) = four;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((unsigned)(e + i) < (unsigned)len[u]) dst[i] = (uint8_t)(four >> (8 * i));
-        }
-      }
-      if (len[u] > 0 && l == 0) p.scales[(int64_t)row[u] * p.lds + blk[u]] = scale;
-    }
+    return;
+  }
+  const uint32_t warps = (gridDim.x - ends) * (kQThreads / 32);
+  const uint32_t warp = (blockIdx.x - ends) * (kQThreads / 32) + (threadIdx.x >> 5);
+  for (uint64_t w0 = warp; 4 * w0 < total; w0 += warps) {
+    const uint64_t g = 4 * w0 + sub;
+    quantize_odd<T, ALL_ENDS>(p, nb, by_nb, (uint32_t)g, ALL_ENDS ? g < total : g >= 1 && g < near_end);
   }
 }
 
@@ -230,10 +239,12 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
   const bool vec = !(((uintptr_t)p.x | (uint64_t)(p.ldx * (int64_t)sizeof(T))) & 31) &&
                    !(((uintptr_t)p.codes | (uint64_t)p.ldc) & 15) && p.K % 16 == 0;
   const FastDiv by_nb(nb);
-  return vec ? launch_after_previous(fp8_quantize_kernel<T>, dim3(grid), dim3(kQThreads), 0, s, p, nb, (uint32_t)total,
-                                     by_nb)
-             : launch_after_previous(fp8_quantize_odd_kernel<T>, dim3(grid), dim3(kQThreads), 0, s, p, nb,
-                                     (uint32_t)total, by_nb);
+  if (vec)
+    return launch_after_previous(fp8_quantize_kernel<T>, dim3(grid), dim3(kQThreads), 0, s, p, nb, (uint32_t)total, by_nb);
+  return p.ldx < 3 ? launch_after_previous(fp8_quantize_odd_kernel<T, true>, dim3(grid), dim3(kQThreads), 0, s, p, nb,
+                                           (uint32_t)total, by_nb)
+                   : launch_after_previous(fp8_quantize_odd_kernel<T, false>, dim3(grid + 1), dim3(kQThreads), 0, s, p,
+                                           nb, (uint32_t)total, by_nb);
 }
 
 // ---- product --------------------------------------------------------------------

@@ -882,3 +882,44 @@ def test_product_behind_a_kernel_that_takes_tensor_memory_late(dfm, early_kernel
         dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, y[1], "f32", stream=0, **kw)
     torch.cuda.synchronize()
     assert bool((mark == 1).all()) and torch.equal(y[0], y[1])
+
+
+# ---- arrays of unaligned rows, to their ends -------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 129, 257])
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 40])
+def test_quantize_rows_without_gaps_at_odd_addresses(dfm, M, K, dtype):
+    """The first and last blocks, whose words of four would reach over x."""
+    base = randn(M * K + 8, g=gen(M + K), dtype=dtype)
+    for shift in (1, 2, 3):
+        x = base[shift:shift + M * K].view(M, K)
+        codes = torch.full((M, K), 0x55, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(M, -(-K // 128), device="cuda")
+        dfm.fp8_quantize(x, dtype, M, K, codes, scales)
+        want, s, ratio = quantized(x)
+        got = codes.view(torch.float8_e4m3fn).double()
+        lower, upper = e4m3_nearest(ratio * (1 - 2.0 ** -22)), e4m3_nearest(ratio * (1 + 2.0 ** -22))
+        assert bool(((got == want) | ((dtype == "f32") & ((got == lower) | (got == upper)))).all())
+        assert torch.equal(scales.double(), s.float().double())
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 9, 4097])
+@pytest.mark.parametrize("T", [1, 2, 700])
+def test_permute_rows_without_gaps_at_odd_addresses(dfm, T, H):
+    g = gen(T + H)
+    k, E = 2, 5
+    ids = random_ids(T, k, E, g, 0.1)
+    base = torch.randint(0, 255, (T * H + 8,), generator=g, device="cuda", dtype=torch.uint8).view(DT["e4m3"])
+    for shift in (0, 1, 2, 3):
+        x = base[shift:shift + T * H].view(T, H)
+        check_permuted(Permuted(dfm, ids, E, x, "e4m3", H), ids, E, x, H)
+
+
+@pytest.mark.parametrize("H", [1, 2, 9])
+def test_permute_rows_without_gaps_above_one_blocks_counting(dfm, H):
+    g = gen(H)
+    T, k, E = 33000, 2, 5
+    ids = random_ids(T, k, E, g, 0.1)
+    base = torch.randint(0, 255, (T * H + 8,), generator=g, device="cuda", dtype=torch.uint8).view(DT["e4m3"])
+    x = base[3:3 + T * H].view(T, H)
+    check_permuted(Permuted(dfm, ids, E, x, "e4m3", H), ids, E, x, H)
