@@ -442,7 +442,10 @@ DF_MOE_API int df_moe_unpermute_grad(int device, const void* dy, int64_t lddy, c
 /* Rows in 8 bits: per row and block of 128 columns m = the largest magnitude
  * of the block's finite values, at least 2^-100;
  *   scales[r][b] = m / 448,  codes[r][c] = e4m3(448 x[r][c] / m), nearest even.
- * NaN and infinities get the code NaN. x [M][K] bf16, fp16 or fp32; codes
+ * bf16 and fp16: the code nearest to the exact quotient. fp32: the quotient
+ * goes through fp32 (0.875 x, then divided by m / 512, each rounded), so that a
+ * code may be the neighbour where 448 x / m lies within 2^-23 of its value from
+ * the middle of two. NaN and infinities get the code NaN. x [M][K] bf16, fp16 or fp32; codes
  * [M][K]; scales [M][ceil(K / 128)]. */
 DF_MOE_API int df_moe_fp8_quantize(int device, const void* x, int32_t dtype, int64_t M, int64_t K,
                                    int64_t ldx, uint8_t* codes, int64_t ldc, float* scales,

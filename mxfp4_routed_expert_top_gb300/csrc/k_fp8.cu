@@ -61,9 +61,10 @@ __device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) < INFINITY
 // 32 >> SHIFT lanes; lanes without a value hold 0. The quotient 448 x / m is
 // taken as (0.875 x) / (m / 512), so that neither side overflows, by
 // Markstein's division (IBM J. R&D 34, 1990): with y the rounded reciprocal of
-// d, q0 = n y, q = q0 + (n - q0 d) y is the rounded quotient. Ties of bf16
-// and fp16 inputs therefore stay ties, and the codes are those of the exact
-// quotient. Blocks with NaN or infinities take a branch of their own.
+// d, q0 = n y, q = q0 + (n - q0 d) y is the rounded quotient. For bf16 and
+// fp16, where 0.875 x is exact, ties therefore stay ties, and the codes are
+// those of the exact quotient; for fp32 0.875 x is rounded too, and a quotient
+// within 2^-23 of its value from the middle of two codes may get either. Blocks with NaN or infinities take a branch of their own.
 template <int N, int SHIFT>
 __device__ __forceinline__ float quantize_block(float (&v)[N], uint32_t (&code)[N / 2]) {
   float m = 0x1p-100f;

@@ -923,3 +923,33 @@ def test_permute_rows_without_gaps_above_one_blocks_counting(dfm, H):
     base = torch.randint(0, 255, (T * H + 8,), generator=g, device="cuda", dtype=torch.uint8).view(DT["e4m3"])
     x = base[3:3 + T * H].view(T, H)
     check_permuted(Permuted(dfm, ids, E, x, "e4m3", H), ids, E, x, H)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quantize_next_to_the_middle_of_two_codes(dfm, dtype):
+    """Quotients at and next to the middles. bf16 and fp16: the nearest code to
+    the exact quotient, ties to even. fp32: also its neighbour, where the
+    quotient lies within 2^-23 of its value from the middle."""
+    values = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
+    middle = (values[1:] + values[:-1]) / 2
+    g = gen(80)
+    m = (1 + torch.rand(64, generator=g, device="cuda")).to(DT[dtype])
+    m[:8] = 1.75  # the scale is 2^-8: middles are reached exactly
+    x = torch.zeros(64, 3, 128, device="cuda", dtype=DT[dtype])
+    near = (middle[None] * m.double()[:, None] / 448).to(DT[dtype])
+    ulp = torch.finfo(DT[dtype]).eps
+    for i, step in enumerate((0.0, ulp, -ulp)):
+        x[:, i, :126] = (near.double() * (1 + step)).to(DT[dtype])
+    x[:, :, 127] = m[:, None]
+    x = x.view(192, 128)
+    codes = torch.empty(192, 128, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty(192, 1, device="cuda")
+    dfm.fp8_quantize(x, dtype, 192, 128, codes, scales)
+    want, s, ratio = quantized(x)
+    got = codes.double()
+    if dtype == "f32":
+        lower, upper = e4m3_nearest(ratio * (1 - 2.0 ** -23)), e4m3_nearest(ratio * (1 + 2.0 ** -23))
+        assert bool(((got == want) | (got == lower) | (got == upper)).all())
+    else:
+        assert torch.equal(got, want)
+    assert torch.equal(scales.double(), s.float().double())
