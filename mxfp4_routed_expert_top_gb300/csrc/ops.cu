@@ -278,7 +278,7 @@ DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, cons
   if (off(x, 16) || off(w, 16)) return fail(DF_MOE_EINVAL, "x and w must be 16-byte aligned");
   if (off(xs, 4) || off(ws, 4) || off(offs, 4) || off(status, 4) || off(y, dfm::dtype_bytes(dtype)))
     return fail(DF_MOE_EINVAL, "an array is not aligned to its elements");
-  if (ldx >= (1ll << 39) || ldw * (transposed ? K : N) >= (1ll << 39))
+  if (ldx >= (1ll << 39) || ldw >= (1ll << 39) || ldw * (transposed ? K : N) >= (1ll << 39))
     return fail(DF_MOE_ERANGE, "a row distance or a group's weights are too large");
   OnDevice on(device);
   if (on.rc()) return on.rc();

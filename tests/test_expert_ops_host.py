@@ -216,3 +216,8 @@ def test_words_of_unaligned_rows_read_nothing_beside_the_array(tmp_path):
                     str(tmp_path / "t"), str(tmp_path / "t.cpp")], check=True)
     r = subprocess.run([str(tmp_path / "t")], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_matmul_refuses_a_row_distance_whose_product_overflows(dfm):
+    refused(dfm, dfm.fp8_matmul, -5, "too large", **dict(MATMUL, ldw=1 << 62))
+    refused(dfm, dfm.fp8_matmul, -5, "too large", **dict(MATMUL, N=256, ldw=1 << 56))
