@@ -373,6 +373,7 @@ def stream_read(buf, nbytes, sink, stream=None):
 # the legacy default stream.
 _ops = None
 _torch_stream = None
+_INT32 = 0x7fffffff  # larger: cut by the C call's 32-bit arguments, so refused here
 
 
 def _op(name):
@@ -429,12 +430,21 @@ def _stream_on(dev, stream):
     return _torch_stream(dev)
 
 
+def _int32(**sizes):
+    """Refuses what a 32-bit argument would cut."""
+    for name, v in sizes.items():
+        if v > _INT32:
+            raise DfMoeError(EINVAL, "%s = %d does not fit 32 bits" % (name, v))
+
+
 def _failed(rc):
     raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
 
 
 def permute_workspace(T, k, E):
     """Bytes of workspace that permute needs (df_moe_permute_workspace)."""
+    if (k | E) > _INT32:
+        return 0
     return _op("df_moe_permute_workspace")(T, k, E)
 
 
@@ -442,6 +452,10 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
             ldx=0, ldr=0, scales=None, n_scales=0, ld_scales=0, rows_scales=None, ld_rows_scales=0,
             stream=None):
     """Tokens sorted by expert (df_moe_permute): rows[pos[a]] = x[a // k]."""
+    if (k | E | n_scales) > _INT32:
+        _int32(k=k, E=E, n_scales=n_scales)
+    if workspace_bytes < 0:
+        raise DfMoeError(EINVAL, "workspace_bytes is negative")
     dev, i, x, r, o, q, s, w, xs, rs = _place(ids, x, rows, offs, pos, src, workspace, scales,
                                               rows_scales)
     rc = _op("df_moe_permute")(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
@@ -452,6 +466,8 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
 
 def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=None):
     """Gradient of permute's x (df_moe_permute_grad)."""
+    if k > _INT32:
+        _int32(k=k)
     dev, r, q, y = _place(drows, pos, dx)
     rc = _op("df_moe_permute_grad")(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
                                     _stream_on(dev, stream))
@@ -461,6 +477,8 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
 
 def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, stream=None):
     """Weighted rows back to their tokens (df_moe_unpermute)."""
+    if k > _INT32:
+        _int32(k=k)
     dev, r, q, w, y = _place(rows, pos, weights, y)
     rc = _op("df_moe_unpermute")(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
                                  _stream_on(dev, stream))
@@ -471,6 +489,8 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
 def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweights, lddy=0, ldr=0,
                    lddr=0, stream=None):
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
+    if k > _INT32:
+        _int32(k=k)
     dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
     rc = _op("df_moe_unpermute_grad")(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
                                       lddr, dw, _stream_on(dev, stream))
@@ -489,6 +509,8 @@ def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None
 def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0, ldxs=0, ldw=0,
                ldy=0, status=None, stream=None):
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
+    if G > _INT32:
+        _int32(G=G)
     dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
     rc = _op("df_moe_fp8_matmul")(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
                                   1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))

@@ -221,3 +221,17 @@ def test_words_of_unaligned_rows_read_nothing_beside_the_array(tmp_path):
 def test_matmul_refuses_a_row_distance_whose_product_overflows(dfm):
     refused(dfm, dfm.fp8_matmul, -5, "too large", **dict(MATMUL, ldw=1 << 62))
     refused(dfm, dfm.fp8_matmul, -5, "too large", **dict(MATMUL, N=256, ldw=1 << 56))
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL[:4] + EVERY_CALL[5:])
+def test_sizes_that_32_bits_would_cut_are_refused(dfm, name, kw):
+    """2^32 + 2 is not 2."""
+    for size in ("k", "E", "n_scales", "G"):
+        if size in kw or (size == "n_scales" and name == "permute"):
+            for v in (1 << 31, (1 << 32) + 2, (1 << 64) + 2):
+                refused(dfm, getattr(dfm, name), -1, "32 bits", **dict(kw, **{size: v}))
+    assert dfm.permute_workspace(70000, (1 << 32) + 2, 8) == dfm.permute_workspace(70000, 2, (1 << 32) + 8) == 0
+
+
+def test_permute_refuses_a_negative_workspace_size(dfm):
+    refused(dfm, dfm.permute, -1, "workspace_bytes", **dict(PERMUTE, T=65537, k=1, workspace=A, workspace_bytes=-1))
