@@ -953,3 +953,152 @@ def test_quantize_next_to_the_middle_of_two_codes(dfm, dtype):
     else:
         assert torch.equal(got, want)
     assert torch.equal(scales.double(), s.float().double())
+
+
+# ---- the 128-row form's stores, many units, and what reaches no other value --------------
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("counts, N, K", [([128], 256, 128), ([33, 0, 200], 384, 512), ([300, 129], 1024, 300),
+                                          ([65, 190, 1], 640, 1000)])
+def test_product_whole_sectors(dfm, counts, N, K, dtype, trans):
+    """More than 32 rows a group, rows of y of whole sectors, and columns left
+    over behind the last 256."""
+    check_product(dfm, counts, N, K, trans, dtype, seed=sum(counts) + K)
+    check_product(dfm, counts, N, K, trans, dtype, seed=sum(counts) + K, ldy_pad=16, before=2, after=5)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("counts, N, K", [([700] * 30, 1024, 300), ([257, 0, 1200, 31] * 8, 1300, 1200), ([4000], 2900, 130)])
+def test_product_more_units_than_sms(dfm, counts, N, K, dtype, trans):
+    """Stages, accumulators and scale buffers carried from unit to unit: 384 to
+    720 units of the 128-row form, with 2, 3 and 10 blocks of K."""
+    check_product(dfm, counts, N, K, trans, dtype, seed=N + K)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M, offs, read", [(40, [-5, 10, 1000, 2 ** 31 - 1], [0, 10, 40, 40]),
+                                           (90, [-5, 60, 1000, 2 ** 31 - 1], [0, 60, 90, 90]),
+                                           (700, [-2 ** 31, -1, 650, 701], [0, 0, 650, 700])])
+def test_product_offsets_are_clamped_in_every_form(dfm, M, offs, read, trans):
+    g = gen(6)
+    G, N, K = 3, 200, 300
+    x, xs, w, ws = product_inputs(G, M, N, K, trans, g)
+    y = torch.full((M, N), 7.0, device="cuda")
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, y, "f32", transposed=trans, ldx=x.shape[1], ldw=w.shape[2])
+    want, size = product_definition(x, xs, w, ws, read, N, K, trans)
+    within(y, want, (128 + 3 + 3) * 2.0 ** -23 * size, "f32")
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("counts", [[9, 7], [21, 19], [200, 150]])
+def test_product_nan_stays_in_its_row_in_every_form(dfm, counts, trans):
+    g = gen(7)
+    G, M, N, K = 2, sum(counts), 256, 384
+    x, xs, w, ws = product_inputs(G, M, N, K, trans, g)
+    o = torch.tensor([0, counts[0], M], dtype=torch.int32, device="cuda")
+    clean, dirty = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    kw = dict(transposed=trans, ldx=x.shape[1], ldw=w.shape[2])
+    dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, clean, "f32", **kw)
+    x[counts[0] - 1, 200] = 0x7F
+    xs[3, 1] = float("nan")
+    if trans:
+        w[1, 5, 130] = 0xFF
+    else:
+        w[1, 130, 5] = 0xFF
+    dfm.fp8_matmul(x, xs, w, ws, o, G, M, N, K, dirty, "f32", **kw)
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[3], bad[counts[0] - 1], bad[counts[0]:, 130] = True, True, True
+    assert bool(dirty[bad].isnan().all()) and torch.equal(dirty[~bad], clean[~bad])
+
+
+# ---- more than one call at once, with nothing left from a call before ---------------------
+def chain_outputs(m):
+    return (m.xq, m.xscale, m.rows, m.rscale, m.offs, m.pos, m.src, m.h, m.y, m.dh, m.dw, m.dhq, m.dhscale, m.drows, m.dx)
+
+
+def test_two_chains_at_once_every_round_from_nothing(dfm):
+    """Every round starts from wiped buffers and is compared."""
+    sets = [Experts8(dfm, 200 + 90 * i, 3, 7, 384, 256, 90 + i) for i in range(2)]
+    alone = []
+    for m in sets:
+        m.forward()
+        m.backward()
+        torch.cuda.synchronize()
+        alone.append(m.outputs())
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for i, (m, s) in enumerate(zip(sets, streams)):
+            with torch.cuda.stream(s):
+                for t in chain_outputs(m):
+                    t.zero_()
+                m.forward(s)
+                m.backward(s)
+                got[i].append(m.outputs())
+    torch.cuda.synchronize()
+    for rounds, want in zip(got, alone):
+        for outputs in rounds:
+            assert all(torch.equal(a, b) for a, b in zip(outputs, want))
+
+
+class LargePermute:
+    """A permute call above one block's counting, with its own workspace."""
+
+    def __init__(self, dfm, T, seed):
+        self.dfm, self.T, self.k, self.E, self.H = dfm, T, 8, 200, 24
+        g = gen(seed)
+        self.ids = random_ids(T, self.k, self.E, g, 0.1)
+        self.x = randn(T, self.H, g=g, dtype="bf16")
+        A = T * self.k
+        self.rows = torch.zeros(A, self.H, dtype=torch.bfloat16, device="cuda")
+        self.offs = torch.zeros(self.E + 1, dtype=torch.int32, device="cuda")
+        self.pos, self.src = (torch.zeros(A, dtype=torch.int32, device="cuda") for _ in range(2))
+        self.need = dfm.permute_workspace(T, self.k, self.E)
+        assert self.need > 0
+        self.workspace = torch.zeros(self.need, dtype=torch.uint8, device="cuda")
+
+    def wipe(self):
+        for t in (self.rows, self.offs, self.pos, self.src, self.workspace):
+            t.zero_()
+
+    def run(self):
+        self.dfm.permute(self.ids, self.T, self.k, self.E, self.x, "bf16", self.H, self.rows, self.offs, self.pos,
+                         self.src, self.workspace, self.need)
+
+    def right(self):
+        offs, pos, src = sorted_places(self.ids, self.E)
+        n = src.size
+        token = torch.from_numpy(src // self.k).cuda()
+        return (np.array_equal(self.offs.cpu().numpy(), offs) and np.array_equal(self.pos.cpu().numpy(), pos)
+                and np.array_equal(self.src.cpu().numpy()[:n], src) and torch.equal(self.rows[:n], self.x[token])
+                and bool((self.rows[n:] == 0).all()))
+
+
+def test_permute_with_a_workspace_on_streams_and_from_graphs(dfm):
+    """Two calls with workspaces of their own at once; then two captured graphs
+    replayed at once."""
+    calls = [LargePermute(dfm, 9001, 91), LargePermute(dfm, 20000, 92)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                c.wipe()
+                c.run()
+        torch.cuda.synchronize()
+        assert all(c.right() for c in calls)
+    graphs = []
+    for c, s in zip(calls, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            c.run()
+    for _ in range(2):
+        for c in calls:
+            c.wipe()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(c.right() for c in calls)
