@@ -371,17 +371,29 @@ def stream_read(buf, nbytes, sink, stream=None):
 # torch has current on the arrays' device (between other work of the same
 # program, and inside a capture); where all arrays are raw addresses, that is
 # the legacy default stream.
-_ops = None
-_torch_stream = None
 _INT32 = 0x7fffffff  # larger: cut by the C call's 32-bit arguments, so refused here
 
 
-def _op(name):
-    global _ops
-    if _ops is None:
-        L = lib()
-        _ops = {n: getattr(L, n) for n in SYMBOLS}
-    return _ops[name]
+class _Calls:
+    """The C functions, each looked up at its first call."""
+
+    def __getattr__(self, name):
+        f = getattr(lib(), name)
+        setattr(self, name, f)
+        return f
+
+
+_c = _Calls()
+
+
+def _find_torch_stream(dev):
+    global _torch_stream
+    import torch  # the arrays are torch's, so torch is loaded
+    _torch_stream = torch._C._cuda_getCurrentRawStream
+    return _torch_stream(dev)
+
+
+_torch_stream = _find_torch_stream  # from the first call on, torch's own
 
 
 def _dtype(d):
@@ -419,15 +431,9 @@ def _place(*arrays):
 
 def _stream_on(dev, stream):
     """The raw stream of a call on arrays of device `dev` (as _place gives it)."""
-    global _torch_stream
-    if stream is not None:
-        return _stream(stream)
-    if dev < 0:
-        return None
-    if _torch_stream is None:  # the arrays are torch's, so torch is loaded
-        import torch
-        _torch_stream = torch._C._cuda_getCurrentRawStream
-    return _torch_stream(dev)
+    if stream is None:
+        return _torch_stream(dev) if dev >= 0 else None
+    return _stream(stream)
 
 
 def _int32(**sizes):
@@ -445,7 +451,7 @@ def permute_workspace(T, k, E):
     """Bytes of workspace that permute needs (df_moe_permute_workspace)."""
     if (k | E) > _INT32:
         return 0
-    return _op("df_moe_permute_workspace")(T, k, E)
+    return _c.df_moe_permute_workspace(T, k, E)
 
 
 def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, workspace_bytes=0,
@@ -458,8 +464,8 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
     dev, i, x, r, o, q, s, w, xs, rs = _place(ids, x, rows, offs, pos, src, workspace, scales,
                                               rows_scales)
-    rc = _op("df_moe_permute")(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
-                               ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream_on(dev, stream))
+    rc = _c.df_moe_permute(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
+                           ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -469,8 +475,8 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
     if k > _INT32:
         _int32(k=k)
     dev, r, q, y = _place(drows, pos, dx)
-    rc = _op("df_moe_permute_grad")(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
-                                    _stream_on(dev, stream))
+    rc = _c.df_moe_permute_grad(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
+                                _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -480,8 +486,8 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
     if k > _INT32:
         _int32(k=k)
     dev, r, q, w, y = _place(rows, pos, weights, y)
-    rc = _op("df_moe_unpermute")(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
-                                 _stream_on(dev, stream))
+    rc = _c.df_moe_unpermute(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
+                             _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -492,8 +498,8 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
     if k > _INT32:
         _int32(k=k)
     dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
-    rc = _op("df_moe_unpermute_grad")(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
-                                      lddr, dw, _stream_on(dev, stream))
+    rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
+                                  lddr, dw, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -501,7 +507,7 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
     dev, x, c, s = _place(x, codes, scales)
-    rc = _op("df_moe_fp8_quantize")(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream_on(dev, stream))
+    rc = _c.df_moe_fp8_quantize(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
@@ -512,14 +518,14 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     if G > _INT32:
         _int32(G=G)
     dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
-    rc = _op("df_moe_fp8_matmul")(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
-                                  1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))
+    rc = _c.df_moe_fp8_matmul(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
+                              1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))
     if rc:
         _failed(rc)
 
 
 def test_fp8_give_up(role):
     """Test hook: one role of the next fp8_matmul gives up (df_moe_test_fp8_give_up)."""
-    rc = _op("df_moe_test_fp8_give_up")(role)
+    rc = _c.df_moe_test_fp8_give_up(role)
     if rc:
         _failed(rc)

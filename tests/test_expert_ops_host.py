@@ -163,8 +163,8 @@ def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name,
     addresses only: the default stream. A stream that is given is taken."""
     import torch
     binding, seen = dfm.binding, []
-    monkeypatch.setattr(binding, "_op", lambda n: lambda *a: seen.append(a[-1]) or 0)
-    monkeypatch.setattr(binding, "_torch_stream", None, raising=False)
+    monkeypatch.setattr(binding._c, "df_moe_" + name, lambda *a: seen.append(a[-1]) or 0)
+    monkeypatch.setattr(binding, "_torch_stream", binding._find_torch_stream)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000 + dev)
     call = getattr(dfm, name)
     tensors = {key: OnDevice0() if v == A else v for key, v in kw.items()}
