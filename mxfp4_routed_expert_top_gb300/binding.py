@@ -407,6 +407,21 @@ def _place(*arrays):
     """[device, address, address, ...]: the one CUDA device that the torch
     tensors among the arrays lie on (-1, the current one, where there are only
     raw addresses), and the arrays' addresses."""
+    try:  # all of them tensors on one device
+        out = [a.data_ptr() for a in arrays]
+        dev = arrays[0].get_device()
+        if dev >= 0:
+            for a in arrays:
+                if a.get_device() != dev:
+                    break
+            else:
+                return [dev, *out]
+    except AttributeError:
+        pass
+    return _place_any(arrays)
+
+
+def _place_any(arrays):
     dev, out = -1, [-1]
     for a in arrays:
         if a is None or a.__class__ is int:
@@ -427,13 +442,6 @@ def _place(*arrays):
         out.append(p)
     out[0] = dev
     return out
-
-
-def _stream_on(dev, stream):
-    """The raw stream of a call on arrays of device `dev` (as _place gives it)."""
-    if stream is None:
-        return _torch_stream(dev) if dev >= 0 else None
-    return _stream(stream)
 
 
 def _int32(**sizes):
@@ -462,10 +470,14 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
         _int32(k=k, E=E, n_scales=n_scales)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    dev, i, x, r, o, q, s, w, xs, rs = _place(ids, x, rows, offs, pos, src, workspace, scales,
-                                              rows_scales)
+    if workspace is None and scales is None and rows_scales is None:
+        dev, i, x, r, o, q, s = _place(ids, x, rows, offs, pos, src)
+        w = xs = rs = None
+    else:
+        dev, i, x, r, o, q, s, w, xs, rs = _place_any((ids, x, rows, offs, pos, src, workspace, scales,
+                                                       rows_scales))
     rc = _c.df_moe_permute(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
-                           ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _stream_on(dev, stream))
+                           ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -476,7 +488,7 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
         _int32(k=k)
     dev, r, q, y = _place(drows, pos, dx)
     rc = _c.df_moe_permute_grad(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
-                                _stream_on(dev, stream))
+                                _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -487,7 +499,7 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
         _int32(k=k)
     dev, r, q, w, y = _place(rows, pos, weights, y)
     rc = _c.df_moe_unpermute(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
-                             _stream_on(dev, stream))
+                             _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -499,7 +511,7 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
         _int32(k=k)
     dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
     rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
-                                  lddr, dw, _stream_on(dev, stream))
+                                  lddr, dw, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -507,7 +519,7 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
     dev, x, c, s = _place(x, codes, scales)
-    rc = _c.df_moe_fp8_quantize(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _stream_on(dev, stream))
+    rc = _c.df_moe_fp8_quantize(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -519,7 +531,7 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
         _int32(G=G)
     dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
     rc = _c.df_moe_fp8_matmul(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
-                              1 if transposed else 0, y, _dtype(dtype), ldy, st, _stream_on(dev, stream))
+                              1 if transposed else 0, y, _dtype(dtype), ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
