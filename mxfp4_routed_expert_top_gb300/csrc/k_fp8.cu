@@ -64,7 +64,8 @@ __device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) < INFINITY
 // d, q0 = n y, q = q0 + (n - q0 d) y is the rounded quotient. For bf16 and
 // fp16, where 0.875 x is exact, ties therefore stay ties, and the codes are
 // those of the exact quotient; for fp32 0.875 x is rounded too, and a quotient
-// within 2^-23 of its value from the middle of two codes may get either. Blocks with NaN or infinities take a branch of their own.
+// within 2^-23 of its value from the middle of two codes may get either.
+// Blocks with NaN or infinities take a branch of their own.
 template <int N, int SHIFT>
 __device__ __forceinline__ float quantize_block(float (&v)[N], uint32_t (&code)[N / 2]) {
   float m = 0x1p-100f;
@@ -101,7 +102,7 @@ __device__ __forceinline__ float quantize_block(float (&v)[N], uint32_t (&code)[
 
 // Rows of whole 32-byte pieces: eight lanes a block, sixteen values a lane.
 // HBM bounds it (128 (s + 1) + 4 bytes a block of s-byte values): 65536 x 1536
-// bf16 (305 MB) take 51 us, 54 with two blocks in flight a warp (registers
+// bf16 (305 MB) take 50 us, 54 with two blocks in flight a warp (registers
 // cost warps an SM), and took 94 when a value cost 24 instructions (index
 // division, tests for finiteness, 16 lanes a block).
 constexpr int kQThreads = 256, kQUnroll = 1;
@@ -161,7 +162,8 @@ fp8_quantize_kernel(const QuantizeArgs p, uint32_t nb, uint32_t total, const Fas
 // what lies between the word boundary and the block), so that a block has 33
 // of them and a lane up to five; words without a value of the block are not
 // read. Where codes lie like x (the same distance of rows modulo 4) their
-// words are aligned too. 14001 x 7167 bf16: 89 us; value by value 109.
+// words are aligned too. 14001 x 7167 bf16 (304 MB, 45 us at the copy rate): 89 us, issue slots 70%
+// busy; value by value 109.
 template <typename T, bool ENDS>
 __device__ __forceinline__ void quantize_odd(const QuantizeArgs& p, uint32_t nb, const FastDiv& by_nb, uint32_t g,
                                              bool there) {
@@ -258,30 +260,40 @@ cudaError_t quantize_t(const QuantizeArgs& p, int sms, cudaStream_t s) {
 // accumulators, and the epilogue warps add the block, times its scales, to
 // their registers.
 //
-// The scales decide the orientation. Groups of more than 32 rows take the
-// rows of x as the 128-row operand (XA): lane = row of x, and a thread has one
+// The scales decide the orientation. With more than 32 rows a group the rows of
+// x are the 128-row operand (XA): lane = row of x, and a thread has one
 // scale for its whole part of a block. With lane = n every accumulator column
 // has its own, and fetching those from shared memory took its bandwidth from
 // the MMA's operands. Short tiles (NT = 16, 32) keep the weights as the
 // 128-row operand: they stream, and 128 rows of x would be mostly empty.
-// Measured with 16 experts of 1536 x 7168: 12 rows each 35.4 us (NT = 16)
-// against 37.8 (NT = 128); 24 rows 35.9 (32) and 37.8; 48 rows 46.8 (32) and
-// 38.7; 80 rows 46.7 and 39.8.
+// Measured with 16 experts of 1536 x 7168 when the forms were chosen: 12 rows
+// each 35.4 us (NT = 16) against 37.8 (NT = 128); 24 rows 35.9 (32) and 37.8; 48
+// rows 46.8 (32) and 38.7; 80 rows 46.7 and 39.8.
+// The host chooses by the mean, rows / min(rows, groups): it does not know the
+// groups. Uneven ones are right but pay for it: 4096 rows of 1536 x 7168 take
+// 51 us in 8 groups of 8, and 166 in 8 of 256 (mean 16: tiles of 16 rows, each
+// of which fetches its expert's weights through L2); 1024 rows in one group 25
+// us, in one of 64 groups 48.
 //
-// What bounds it. Long groups: a block of 128 x 256 x 128 takes about 790
-// cycles, of which its MMAs take 512. Two accumulators fill the tensor memory,
-// and each is taken for the MMAs, the signal (about 150 cycles), the
-// epilogue's loads and FMAs (440: issue slots, two warps a scheduler) and the
-// way back, where every instruction between two blocks counts (toggled
+// What bounds it. Long groups: a block of 128 x 256 x 128 takes 773 cycles, of
+// which its MMAs take 512. From clock stamps of one CTA: an epilogue warp takes
+// 356 from seeing a block's accumulator to releasing it, and then about 390
+// until it looks at the next (the rest of its FMAs, the loop, the barrier),
+// which is the period. An accumulator's turn is two periods: 718 from the MMAs'
+// issue until the first warp sees it, up to 290 more until the last one does, 356,
+// about 135 back to the MMA warp and 95 to issue. Copies are not part of it
+// (773 without any). So every instruction between two blocks counts (toggled
 // indexes in place of computed ones and no code for failures inside the loop:
-// 302 to 285 us on 8192 x 7168 x 7168, 2.95 PFLOP/s). Not faster, against
+// 302 to 285 us on 8192 x 7168 x 7168). Not faster, against
 // what the kernel took when each was tried: a pair of CTAs on 256 x 256
 // (cta_group::2: 306 for 294), sixteen epilogue warps (325 for 291), packed
 // fp32 FMAs (308 for 308), two accumulators of 128 columns in place of one (343
 // for 299), two MMA warps (298 for 300), longer tensor memory loads (324 for
-// 291), the next block's scale or barrier read early (292 for 285). Short
-// groups stream weights at 85% of the copy rate (16 experts of 1536 x 7168, one
-// token: 31 us).
+// 291), the next block's scale or barrier read early (292 for 285). All of
+// these are runs of 3 to 10 ms; longer ones lower the clock: 2048 x 16 rows of
+// 32 experts, 1536 x 7168, take 270 to 287 us in a short run (2.6 PFLOP/s) and
+// 326 among other work (2.2); 8192 x 7168 x 7168 285 to 325. Short groups stream
+// weights at 85% of the copy rate (16 experts of 1536 x 7168, one token: 31 us).
 //
 // split > 1 (NT <= 32): a cluster of that many CTAs shares a unit, each takes
 // a part of K, and the sums meet in distributed shared memory, in the order
@@ -877,7 +889,7 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
         if (!ok) {
           sm->err = 1;
 #pragma unroll
-          for (int i = 0; i < CW; ++i) acc[i] = fmaf(acc[i], __uint_as_float(0x7fffffffu), acc[i]);  // (a move costs spills)
+          for (int i = 0; i < CW; ++i) acc[i] = fmaf(acc[i], __uint_as_float(0x7fffffffu), acc[i]);  // NaN (moves: spills)
         }
         const int n0 = un.n0 + c0, row = l0 + lane;
         Y* y = static_cast<Y*>(p.y) + (un.row0 + row) * p.ldy + n0;

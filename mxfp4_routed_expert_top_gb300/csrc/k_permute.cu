@@ -125,6 +125,8 @@ __device__ __forceinline__ void copy_word_odd(const PermuteArgs& p, int t0, cons
 // two words of token 0, over its end in the last three of the last token (in
 // any where rows are nearer than that). The block's last threads take those:
 // a test in every word cost 7%, and first threads 1 us a call of short rows.
+// 2000 x 8 rows of 3001 bytes (54 MB, 8 us at the copy rate) take 24 us, of 3001
+// bf16 39: issue slots (73% busy), mostly the stores of eight rows a word.
 __device__ __forceinline__ void copy_rows_odd(const PermuteArgs& p, int t0, int t1, const int32_t* pos, int w0,
                                               int w1) {
   const int nw = w1 - w0, items = (t1 - t0) * nw, last = (int)((p.bytes + 3) / 4) + 1 - 3;
@@ -157,8 +159,16 @@ __device__ __forceinline__ void copy_scales(const PermuteArgs& p, int t0, int t1
 // of eight that shared the counting through distributed shared memory were
 // slower (4096 tokens x 16 rows of 256 bf16: 17.5 us, two blocks 21, clusters
 // 31). Writes bound the large calls: 4096 x 16 rows of 7168 (999 MB, 940 of
-// them written) take 181 us, of which bulk copies through shared memory saved
+// them written) take 183 us, of which bulk copies through shared memory saved
 // nothing.
+//
+// kSelfCount: where the two ways cross, more or less. This one against counts
+// by chunks (four launches), 896 experts, rows of 64 / 256 / 7168 bf16, in a
+// graph: 8192 assignments 4.0 / 4.0 / 25 us against 11 / 11 / 33; 32768 6.9 / 8.7 / 93
+// against 15 / 16 / 96; 65536 11.8 / 16.9 / 182 against 20 / 26 / 180; 131072 24 / 35 /
+// 362 against 31 / 38 / 349. Above it, every block would count and rank ever more
+// for the same SMs; the chunks' way has a block's 512 threads for the columns of
+// one token, of which short rows use few.
 constexpr int kSelfThreads = 1024;
 constexpr int kSelfCount = 65536;
 constexpr int kSelfChunk = 1024;  // assignments a block may own
@@ -492,7 +502,8 @@ unpermute_kernel(const UnpermuteArgs p, int nv, uint64_t by_nv) {
 }
 
 // Rows that no 8-byte vector fits: a warp per token and 256 columns, eight a
-// lane, value by value; two rows in flight.
+// lane, value by value; two rows in flight. 2000 x 8 rows of 3001 bf16 (108 MB,
+// 16 us at the copy rate) take 26 us, of fp32 (216 MB, 32) 36.
 template <typename T, bool WEIGHTED>
 __global__ void __launch_bounds__(128)
 unpermute_odd_kernel(const UnpermuteArgs p, uint32_t segments, FastDiv by_segments) {
@@ -569,7 +580,9 @@ cudaError_t unpermute_n(const UnpermuteArgs& p, int sms, cudaStream_t s) {
 // group, each row read once and its gradient written beside it; the J dot
 // products are summed over the block in a fixed order. Column steps are not
 // unrolled: registers cost blocks an SM (1023 x 6 rows of 2049 fp32, 104 MB:
-// 22 us, 29 unrolled; 2048 x 8 of 7168 bf16, 499 MB: 77).
+// 21.4 us, 29 unrolled; 2048 x 8 of 7168 bf16, 499 MB: 77). Rows that no vector
+// fits go value by value: the same 1023 x 6 rows in bf16 (52 MB, 7.7 us at the
+// copy rate) take 16.3.
 constexpr int kGradThreads = 128;
 template <typename T, int N, int J>
 __global__ void __launch_bounds__(kGradThreads)
