@@ -383,7 +383,8 @@ DF_MOE_API int df_moe_route_noalloc(const float* router, int32_t E, int32_t H,
  * workspaces are apart, and give the same bits on every run. Every array is device memory,
  * aligned to its elements; outputs do not overlap inputs. A row distance
  * (ld..., in elements) of 0 stands for rows without gaps; what lies between
- * rows is not written and does not matter. T = 0 or M = 0 is an empty call.
+ * rows may be read, is not written and does not matter; nothing before the
+ * first or behind the last row is touched. T = 0 or M = 0 is an empty call.
  * Sums are fp32, in a fixed order, and round to the output's type once.
  * Limits: k <= 32, E, G <= 1024, T * k < 2^31, row lengths <= 262144.
  * Errors: EINVAL, ERANGE, ECUDA; messages from df_moe_last_error(NULL). */
