@@ -484,6 +484,159 @@ DF_MOE_API int df_moe_fp8_matmul(int device, const uint8_t* x, int64_t ldx, cons
  * bit and NaN in that block's part of y. One-shot. Errors: EINVAL. */
 DF_MOE_API int df_moe_test_fp8_give_up(int32_t role);
 
+/* ---- around the routed experts, without a handle ---------------------------
+ * The rest of a block for the same callers: the 16-bit product of a shared
+ * expert or a dense layer, the norms between blocks, the router's balance loss,
+ * each with its gradients. What is said above of all operators holds here too
+ * (device, stream, nothing allocated or kept, row distances in elements, empty
+ * calls, the same bits on every run). An array that is marked optional may be
+ * NULL. Gradients are written, not added to; sums over no rows are zero. */
+#define DF_MOE_ACT_NONE 0
+#define DF_MOE_ACT_RELU 1   /* max(z, 0), slope 0 at 0 */
+#define DF_MOE_ACT_SILU 2   /* z / (1 + exp(-z)) */
+#define DF_MOE_ACT_GELU 3   /* z Phi(z), Phi the normal distribution function */
+#define DF_MOE_ACT_SWIGLU 4 /* silu(z[n]) z[N + n]: w, bias and pre are 2 N wide */
+
+/* The product of 16-bit matrices with bias, activation and residual:
+ *   z = x w' + bias,   y = residual + act(z)
+ *   x  [M][K], w [N][K] (swiglu: [2 N][K], the gate's rows first) of dtype
+ *      (DF_MOE_BF16 or _F16), 16-byte aligned, ldx and ldw multiples of 8 (0:
+ *      K, where that is one)
+ *   bias optional, [N] (swiglu: [2 N]) of dtype
+ *   residual optional, [M][N] of out_dtype; it may be y itself, with ldr = ldy
+ *   pre optional output: z [M][N] (swiglu: [M][2 N]) rounded to dtype, what the
+ *      gradient takes; y is computed from z as it was summed
+ *   y  [M][N] of out_dtype: dtype or DF_MOE_F32
+ *   status optional device word: bit 2u is set when a bounded wait inside the
+ *      kernel gave up (y holds NaN there)
+ * N, K <= 262144, M < 2^31 - 256. */
+DF_MOE_API int df_moe_matmul(int device, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                             int32_t dtype, int64_t M, int64_t N, int64_t K, const void* bias,
+                             int32_t act, const void* residual, int64_t ldr, void* pre, int64_t ldp,
+                             void* y, int32_t out_dtype, int64_t ldy, uint32_t* status, void* stream);
+
+/* Its gradients, W = N (swiglu: 2 N) columns of z:
+ *   dz = act'(z) dy,  dx = dz w,  dw = dz' x,  dbias = column sums of dz
+ * (the residual's is dy). Each of dx, dw and dbias is optional, one at least
+ * is wanted (or dz alone).
+ *   dy  [M][N] of dtype; without an activation it is an operand: 16-byte
+ *       aligned, lddy a multiple of 8 where dx or dw is wanted
+ *   x, w as in df_moe_matmul; x only for dw, w only for dx
+ *   pre [M][W] z of dtype, and dz [M][W] of dtype (output, rounded: the products
+ *       take it in 16 bits; 16-byte aligned, lddz a multiple of 8 where dx or dw
+ *       is wanted): required with an activation, not touched without
+ *   dx  [M][K] of dtype;  dw [W][K] and dbias [W] of grad_dtype: dtype or
+ *       DF_MOE_F32. dbias sums dz before it is rounded. */
+DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                  const void* w, int64_t ldw, int32_t dtype, int64_t M, int64_t N,
+                                  int64_t K, int32_t act, const void* pre, int64_t ldp, void* dz,
+                                  int64_t lddz, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                                  void* dbias, int32_t grad_dtype, uint32_t* status, void* stream);
+
+/* Test hook for df_moe_matmul's status bit (no GPU fault involved): in the next
+ * product of the calling thread one role of the kernel's block 0 gives up
+ * before its first wait (1 the copies, 2 the MMAs, 3 the sums; 0 takes the
+ * request back), and the block's other waits use a short limit. One-shot. */
+DF_MOE_API int df_moe_test_matmul_give_up(int32_t role);
+
+#define DF_MOE_GATE_NONE 0
+#define DF_MOE_GATE_CHANNEL 1 /* [H], of weight_dtype */
+#define DF_MOE_GATE_TOKEN 2   /* [T], fp32 */
+#define DF_MOE_GATE_FULL 3    /* [T][H], of dtype */
+
+/* The norms after and before a block. With rms(v) = 1 / sqrt(mean(v^2) + eps):
+ *   a = post ? u rms(u) post_w : u                the block's output
+ *   h = residual_scale residual + gate a          the residual stream
+ *   n = h rms(h) pre_w                            the next block's input
+ *   u, residual: optional, one of them is there   [T][H] of dtype (DF_MOE_BF16,
+ *      _F16 or _F32); without u h is residual_scale residual, and neither post
+ *      nor a gate is allowed; without residual h is gate a
+ *   post_w, pre_w optional (1), [H] of weight_dtype: dtype or DF_MOE_F32
+ *   gate by gate_kind; ldg for DF_MOE_GATE_FULL
+ *   h, n outputs, each optional, one of them is there; n is computed from h
+ *      before h is rounded. h may be residual or u itself, and n may be u
+ *      or residual itself, with the same row distance.
+ * A row whose squares overflow fp32 is summed at a smaller scale; one that
+ * holds an infinity or NaN is not finite in n. H <= 32768, 1e-30 <= eps <= 3e38. */
+DF_MOE_API int df_moe_block_norm(int device, const void* u, int64_t ldu, int32_t post,
+                                 const void* post_w, int32_t gate_kind, const void* gate, int64_t ldg,
+                                 const void* residual, int64_t ldr, float residual_scale,
+                                 const void* pre_w, float eps, int64_t T, int64_t H, int32_t dtype,
+                                 int32_t weight_dtype, void* h, int64_t ldh, void* n, int64_t ldn,
+                                 void* stream);
+
+/* Bytes of workspace for df_moe_block_norm_grad (0 for sizes out of range). */
+DF_MOE_API size_t df_moe_block_norm_grad_workspace(int64_t T, int64_t H);
+
+/* Its gradients. dh [T][H]: what reaches h from behind (optional), dn [T][H]:
+ * what reaches n (optional, with h as df_moe_block_norm stored it, or for an n
+ * of the residual alone the residual); one of the two is there. With G their
+ * sum at h:
+ *   dresidual = residual_scale G, du through gate and norm  [T][H] of dtype
+ *   dpost_w, dpre_w  [H] fp32;  dgate: [H] fp32, [T] fp32 or [T][H] of dtype
+ * each optional. workspace: df_moe_block_norm_grad_workspace bytes, 16-byte
+ * aligned, for dpost_w, dpre_w and a channel's dgate (else NULL); not shared
+ * by calls (or captured graphs) that may overlap. dresidual may be dh itself
+ * or dn itself, with the same row distance, and du the other. */
+DF_MOE_API int df_moe_block_norm_grad(int device, const void* dh, int64_t lddh, const void* dn,
+                                      int64_t lddn, const void* u, int64_t ldu, const void* h,
+                                      int64_t ldh, int32_t post, const void* post_w,
+                                      int32_t gate_kind, const void* gate, int64_t ldg,
+                                      float residual_scale, const void* pre_w, float eps, int64_t T,
+                                      int64_t H, int32_t dtype, int32_t weight_dtype, void* du,
+                                      int64_t lddu, void* dresidual, int64_t lddr, float* dpost_w,
+                                      void* dgate, int64_t lddg, float* dpre_w, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+#define DF_MOE_SCORE_SOFTMAX 0
+#define DF_MOE_SCORE_SIGMOID 1
+
+/* Bytes of workspace for df_moe_balance_loss (0 for sizes out of range). */
+DF_MOE_API size_t df_moe_balance_loss_workspace(int64_t T, int32_t E, int64_t S);
+
+/* The router's balance loss and the counts of every expert, for each of S
+ * sequences: the rows offs[s] <= t < offs[s + 1] whose mask is not zero, n of
+ * them.
+ *   p_t = softmax(z_t), or sigmoid(z_t) / its sum;  l_t = logsumexp(z_t)
+ *   counts[s][e] = #{(t, j): ids[t][j] = e}, tokens[s] = n, probs[s] = mean of p_t
+ *   loss[s] = coef sum_e (E counts[s][e] / (k n)) probs[s][e] + z_coef mean l_t^2
+ *   logits [T][E] of dtype (DF_MOE_BF16, _F16 or _F32); -inf: an expert that
+ *          is not allowed, p = 0; a row of those alone has p = 0 and l = 0
+ *   ids    [T][k] int32; ids outside [0, E) are not counted
+ *   offs   optional (S = 1: all T rows), [S + 1] ascending, read as if clamped
+ *          to [0, T]. A sequence without a counted row has zeros everywhere.
+ *   mask   optional, [T] bytes; what a row with mask 0 holds does not matter
+ *   loss [S], probs [S][E] (optional) fp32; counts [S][E], tokens [S] int32
+ *   workspace: df_moe_balance_loss_workspace bytes, 16-byte aligned; not shared
+ *          by calls (or captured graphs) that may overlap
+ *   status optional device word: bit 1u is set where offs descends or leaves
+ *          [0, T] (the values of sequences that it names twice are then not
+ *          specified)
+ * E <= 1024, k <= 32, S <= 2^20. */
+DF_MOE_API int df_moe_balance_loss(int device, const void* logits, int32_t dtype, int64_t ldl,
+                                   const int32_t* ids, int64_t T, int32_t E, int32_t k,
+                                   const int32_t* offs, int64_t S, const uint8_t* mask, int32_t score,
+                                   float coef, float z_coef, float* loss, int32_t* counts,
+                                   int32_t* tokens, float* probs, void* workspace,
+                                   size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* The gradient of the logits, dlogits [T][E] of dtype: that of
+ * sum_s dloss[s] loss[s] (counts do not move with the logits), and where
+ * weights and dweights [T][k] fp32 are given that of the routing weights too:
+ * weights[t] are the scores (exp(z), or sigmoid(z)) of ids[t] over their sum,
+ * dweights their gradient (df_moe_unpermute_grad's). counts and tokens are
+ * the loss's, of the same logits, mask and offs. Rows with mask 0 get zeros;
+ * rows outside every sequence are left as they were. ids only with weights;
+ * ids outside [0, E) have no weight, and an expert that a token names
+ * twice gets both terms. dlogits may be logits itself, with lddl = ldl. */
+DF_MOE_API int df_moe_balance_loss_grad(int device, const float* dloss, const void* logits,
+                                        int32_t dtype, int64_t ldl, const int32_t* ids, int64_t T,
+                                        int32_t E, int32_t k, const int32_t* offs, int64_t S,
+                                        const uint8_t* mask, int32_t score, float coef, float z_coef,
+                                        const int32_t* counts, const int32_t* tokens,
+                                        const float* weights, const float* dweights, void* dlogits,
+                                        int64_t lddl, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

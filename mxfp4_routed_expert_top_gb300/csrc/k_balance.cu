@@ -1,0 +1,477 @@
+// k_balance.cu — the router's balance loss with the counts of every expert, and
+// the gradient of the logits. For each sequence (rows offs[s] <= t < offs[s + 1]
+// whose mask is not zero, n of them)
+//
+//   p_t = softmax(z_t), or sigmoid(z_t) / sum sigmoid(z_t);  l_t = logsumexp(z_t)
+//   count_e = #{(t, j): ids[t][j] = e},  f_e = E count_e / (k n),  P_e = mean p_te
+//   loss = coef sum_e f_e P_e + z_coef mean l_t^2
+//   dz_te = dloss (coef / n p_te m_te (f_e - sum_j f_j p_tj) + 2 z_coef / n l_t softmax(z_t)_e)
+//           + m_te sum_{j: ids[t][j] = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+//
+// with m = 1 for the softmax and 1 - sigmoid(z) for the sigmoid; the last term
+// is the gradient of the routing weights w, the kept scores over their sum.
+// sigmoid(z) / sum sigmoid(z) is the softmax of log sigmoid(z), so that scores
+// that are all tiny keep their ratios. The logits are read once in either call
+// (a row stays in a warp's registers), and HBM bounds the large ones.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstring>
+
+#include "internal.h"
+#include "ops.h"
+#include "pipeline.cuh"
+
+namespace dfm {
+namespace {
+
+constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
+constexpr int kBalBlocks = 456;  // chunks of rows at most: three blocks an SM
+
+template <typename T>
+__device__ __forceinline__ float f32_of(T v);
+template <>
+__device__ __forceinline__ float f32_of(float v) { return v; }
+template <>
+__device__ __forceinline__ float f32_of(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float f32_of(__half v) { return __half2float(v); }
+
+// A row of E values over a warp: VEC: four side by side, 128 apart; else one by
+// one, 32 apart. Element i of lane l is column `col(i)`.
+template <bool VEC, int NV>
+struct Lanes {
+  int lane, E;
+  __device__ __forceinline__ int col(int i) const { return VEC ? 4 * (lane + 32 * (i / 4)) + i % 4 : lane + 32 * i; }
+  template <typename T>
+  __device__ __forceinline__ void load(float (&v)[4 * NV], const T* p, float behind) const {
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = 4 * (lane + 32 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * i + j] = behind;
+        if (c < E) {
+          T e[4];
+          if (sizeof(T) == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + c);
+            memcpy(e, &w, sizeof e);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + c);
+            memcpy(e, &w, sizeof e);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * i + j] = f32_of<T>(e[j]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i) v[i] = lane + 32 * i < E ? f32_of<T>(p[lane + 32 * i]) : behind;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, const float (&v)[4 * NV]) const {
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = 4 * (lane + 32 * i);
+        T e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = T(v[4 * i + j]);
+        if (c < E) {
+          if (sizeof(T) == 4) {
+            uint4 w;
+            memcpy(&w, e, sizeof w);
+            *reinterpret_cast<uint4*>(p + c) = w;
+          } else {
+            uint2 w;
+            memcpy(&w, e, sizeof w);
+            *reinterpret_cast<uint2*>(p + c) = w;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i)
+        if (lane + 32 * i < E) p[lane + 32 * i] = T(v[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// v becomes softmax(v); what it returns is logsumexp(v). A row of -inf alone
+// (nothing allowed) has neither: zeros, and 0. fmaxf drops a NaN, the sum
+// keeps it.
+template <int N>
+__device__ __forceinline__ float softmax_row(float (&v)[N]) {
+  float most = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) most = fmaxf(most, v[i]);
+  most = warp_max(most);
+  const float base = most == -INFINITY ? 0.f : most;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = expf(v[i] - base);
+    sum += v[i];
+  }
+  sum = warp_sum(sum);
+  if (sum == 0.f) return 0.f;
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] *= inv;
+  return base + logf(sum);
+}
+// log(1 / (1 + exp(-z))) without overflow; -inf stays.
+__device__ __forceinline__ float log_sigmoid(float z) { return fminf(z, 0.f) - log1pf(expf(-fabsf(z))); }
+
+struct Span {
+  int64_t begin, end;
+};
+// Rows of sequence s, kept inside [0, T] whatever the caller's array holds.
+__device__ __forceinline__ Span sequence(const int32_t* offs, int s, int64_t T) {
+  if (!offs) return {0, T};
+  return {min(max((int64_t)offs[s], (int64_t)0), T), min(max((int64_t)offs[s + 1], (int64_t)0), T)};
+}
+// The last sequence that begins at or before `row` (-1: none).
+__device__ __forceinline__ int sequence_of(const int32_t* offs, int S, int64_t row) {
+  if (!offs) return 0;
+  int lo = -1, hi = S - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (offs[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A block has the rows of one chunk and leaves one entry for every sequence it
+// meets. Entry chunk + s: along the rows either number only grows and one of
+// them does from entry to entry, so no two have the same, and chunks + S are
+// enough.
+struct Entries {
+  float* probs;    // [entries][E]
+  int32_t* count;  // [entries][E]
+  float2* sums;    // [entries]: rows counted, sum of l^2
+};
+
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const BalanceArgs p, const Entries out, int chunk_rows) {
+  extern __shared__ float shared[];  // [warps][E], then counts [E]
+  __shared__ float2 warp_sums[kBalWarps];
+  int* count = reinterpret_cast<int*>(shared + kBalWarps * p.E);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Lanes<VEC, NV> at{lane, p.E};
+  const int64_t first = (int64_t)blockIdx.x * chunk_rows, last = min(first + chunk_rows, p.T);
+  pdl_wait();
+  for (int s = max(0, sequence_of(p.offs, p.S, first)); s < p.S; ++s) {
+    Span span = sequence(p.offs, s, p.T);
+    if (span.begin >= last) break;
+    span.begin = max(span.begin, first);
+    span.end = min(span.end, last);
+    if (span.begin >= span.end) continue;
+    for (int e = threadIdx.x; e < p.E; e += kBalThreads) count[e] = 0;
+    __syncthreads();
+    float sum[4 * NV], rows = 0.f, zz = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) sum[i] = 0.f;
+    for (int64_t t = span.begin + warp; t < span.end; t += kBalWarps) {
+      if (p.mask && !p.mask[t]) continue;
+      float z[4 * NV];
+      at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
+      if (lane < p.k) {
+        const int e = p.ids[t * p.k + lane];
+        if ((unsigned)e < (unsigned)p.E) atomicAdd(&count[e], 1);
+      }
+      rows += 1.f;
+      if (p.sigmoid) {
+        if (p.z_coef != 0.f) {
+          float w[4 * NV];
+#pragma unroll
+          for (int i = 0; i < 4 * NV; ++i) w[i] = z[i];
+          const float l = softmax_row(w);
+          zz = fmaf(l, l, zz);
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) z[i] = log_sigmoid(z[i]);
+        softmax_row(z);
+      } else {
+        const float l = softmax_row(z);
+        if (p.z_coef != 0.f) zz = fmaf(l, l, zz);
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i) sum[i] += z[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i)
+      if (at.col(i) < p.E) shared[warp * p.E + at.col(i)] = sum[i];
+    if (lane == 0) warp_sums[warp] = make_float2(rows, zz);
+    __syncthreads();
+    const int64_t entry = (int64_t)blockIdx.x + s;
+    for (int e = threadIdx.x; e < p.E; e += kBalThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kBalWarps; ++w) v += shared[w * p.E + e];
+      out.probs[entry * p.E + e] = v;
+      out.count[entry * p.E + e] = count[e];
+    }
+    if (threadIdx.x == 0) {
+      float2 v = make_float2(0.f, 0.f);
+      for (int w = 0; w < kBalWarps; ++w) v.x += warp_sums[w].x, v.y += warp_sums[w].y;
+      out.sums[entry] = v;
+    }
+    __syncthreads();
+  }
+}
+
+// One cluster a sequence, 128 experts a CTA: the entries' sums in their order
+// (of eight interleaved parts), and the loss.
+constexpr int kBalJoin = 1024;
+__global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArgs p, const Entries in, int chunk_rows, int parts) {
+  __shared__ float probs[8][128];
+  __shared__ int count[8][128];
+  __shared__ float2 sums[32];
+  __shared__ float loss;
+  const int e = threadIdx.x & 127, row = threadIdx.x >> 7;
+  const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, expert = 128 * part + e;
+  pdl_wait();
+  const Span span = sequence(p.offs, s, p.T);
+  const bool some = span.begin < span.end;
+  const int64_t first = some ? span.begin / chunk_rows + s : 0, last = some ? (span.end - 1) / chunk_rows + s : -1;
+  if (p.status && p.offs && threadIdx.x == 0 && part == 0 &&
+      (p.offs[s + 1] < p.offs[s] || p.offs[s] < 0 || p.offs[s + 1] > p.T))
+    atomicOr(p.status, DEV_ERR_RANGE);
+  float v = 0.f;
+  int n = 0;
+  if (expert < p.E) {
+#pragma unroll 4
+    for (int64_t i = first + row; i <= last; i += 8) {
+      v += in.probs[i * p.E + expert];
+      n += in.count[i * p.E + expert];
+    }
+  }
+  probs[row][e] = v;
+  count[row][e] = n;
+  // rows counted and l^2: every thread has some entries
+  float2 t = make_float2(0.f, 0.f);
+  for (int64_t i = first + threadIdx.x; i <= last; i += kBalJoin) t.x += in.sums[i].x, t.y += in.sums[i].y;
+  t.x = warp_sum(t.x), t.y = warp_sum(t.y);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    t = sums[threadIdx.x & 31];
+    t.x = warp_sum(t.x), t.y = warp_sum(t.y);
+    const float each = t.x > 0.f ? 1.f / t.x : 0.f;
+    v = 0.f, n = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v += probs[r][e], n += count[r][e];
+    const float mean = t.x > 0.f ? v / t.x : 0.f;
+    float term = 0.f;
+    if (expert < p.E) {
+      p.counts[(int64_t)s * p.E + expert] = n;
+      if (p.probs) p.probs[(int64_t)s * p.E + expert] = mean;
+      term = (float)n * ((float)p.E / (float)p.k) * each * mean;
+    }
+    term = warp_sum(term);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) probs[threadIdx.x >> 5][0] = term;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (threadIdx.x == 0) {
+      loss = p.coef * (probs[0][0] + probs[1][0] + probs[2][0] + probs[3][0]) + (part == 0 ? p.z_coef * t.y * each : 0.f);
+      if (part == 0) p.tokens[s] = (int)t.x;
+    }
+  }
+  __syncthreads();
+  if (parts > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (part == 0 && threadIdx.x == 0) {
+    float all = 0.f;
+    for (int q = 0; q < parts; ++q) {
+      uint32_t at;
+      float x;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&loss)), "r"(q));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+      all += x;
+    }
+    p.loss[s] = all;
+  }
+  if (parts > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// A warp a row, rows side by side in a chunk of its own, so that f stays in
+// registers over a sequence's rows.
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
+  constexpr int N = 4 * NV;
+  const int lane = threadIdx.x & 31;
+  const Lanes<VEC, NV> at{lane, p.E};
+  const int64_t warp = (int64_t)blockIdx.x * kBalWarps + (threadIdx.x >> 5);
+  const int64_t first = warp * warp_rows, last = min(first + warp_rows, p.T);
+  pdl_wait();
+  if (first >= last) return;
+  int s = sequence_of(p.offs, p.S, first);
+  Span span{0, 0};
+  float f[N], aux = 0.f, zc = 0.f;
+  bool fresh = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = 0.f;
+  for (int64_t t = first; t < last; ++t) {
+    while (s + 1 < p.S && p.offs && p.offs[s + 1] <= t) ++s, fresh = true;
+    if (s < 0) continue;
+    if (fresh) {
+      fresh = false;
+      span = sequence(p.offs, s, p.T);
+      const float n = (float)p.tokens[s], each = n > 0.f ? 1.f / n : 0.f, g = p.dloss[s];
+      aux = g * p.coef * each;
+      zc = 2.f * g * p.z_coef * each;
+      const float unit = (float)p.E / (float)p.k * each;
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = at.col(i) < p.E ? (float)p.counts[(int64_t)s * p.E + at.col(i)] * unit : 0.f;
+    }
+    if (t < span.begin || t >= span.end) continue;  // behind every sequence: left as it was
+    T* out = static_cast<T*>(p.dlogits) + t * p.lddl;
+    float z[N], m[N];
+    if (p.mask && !p.mask[t]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = 0.f;
+      at.store(out, z);
+      continue;
+    }
+    at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
+    float d[N];
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x = z[i];
+        m[i] = 1.f / (1.f + expf(x));  // 1 - sigmoid
+        d[i] = log_sigmoid(x);
+      }
+      softmax_row(d);
+    }
+    const float l = !p.sigmoid || zc != 0.f ? softmax_row(z) : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) dot = fmaf(f[i], p.sigmoid ? d[i] : z[i], dot);
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float share = p.sigmoid ? d[i] * m[i] : z[i];
+      d[i] = aux * share * (f[i] - dot);
+      if (zc != 0.f) d[i] = fmaf(zc * l, z[i], d[i]);
+    }
+    if (p.weights) {
+      const float w = lane < p.k ? p.weights[t * p.k + lane] : 0.f, dw = lane < p.k ? p.dweights[t * p.k + lane] : 0.f;
+      const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+      const bool kept = (unsigned)id < (unsigned)p.E;
+      const float mean = warp_sum(kept ? w * dw : 0.f), mine = kept ? w * (dw - mean) : 0.f;
+      for (int j = 0; j < p.k; ++j) {
+        const int e = __shfl_sync(0xffffffffu, id, j);
+        const float x = __shfl_sync(0xffffffffu, mine, j);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (at.col(i) == e) d[i] += p.sigmoid ? x * m[i] : x;
+      }
+    }
+    at.store(out, d);
+  }
+}
+
+int64_t chunk_rows_of(int64_t T) {
+  const int64_t rows = (T + kBalBlocks - 1) / kBalBlocks;
+  return (rows + kBalWarps - 1) / kBalWarps * kBalWarps;
+}
+int64_t entries_of(int64_t T, int64_t S) {
+  const int64_t rows = chunk_rows_of(T);
+  return (T + rows - 1) / rows + S;
+}
+
+bool vec_rows(const void* p, int64_t ld, int E, int size) {
+  return E % 4 == 0 && !(((uintptr_t)p | (uint64_t)(ld * size)) & (uint64_t)(4 * size - 1));
+}
+
+template <typename T, bool VEC>
+cudaError_t rows_nv(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
+  const size_t smem = (size_t)(kBalWarps + 1) * p.E * sizeof(float);  // 36 KB at most
+  const dim3 g((unsigned)blocks), b(kBalThreads);
+  const int c = (int)chunk;
+  if (p.E <= 128) return launch_after_previous(balance_rows_kernel<T, VEC, 1>, g, b, smem, s, p, out, c);
+  if (p.E <= 256) return launch_after_previous(balance_rows_kernel<T, VEC, 2>, g, b, smem, s, p, out, c);
+  if (p.E <= 512) return launch_after_previous(balance_rows_kernel<T, VEC, 4>, g, b, smem, s, p, out, c);
+  return launch_after_previous(balance_rows_kernel<T, VEC, 8>, g, b, smem, s, p, out, c);
+}
+template <typename T>
+cudaError_t rows_t(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
+  return vec_rows(p.logits, p.ldl, p.E, sizeof(T)) ? rows_nv<T, true>(p, out, chunk, blocks, s)
+                                                   : rows_nv<T, false>(p, out, chunk, blocks, s);
+}
+template <typename T, bool VEC>
+cudaError_t grad_nv(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
+  const dim3 g((unsigned)blocks), b(kBalThreads);
+  if (p.E <= 128) return launch_after_previous(balance_grad_kernel<T, VEC, 1>, g, b, 0, s, p, rows);
+  if (p.E <= 256) return launch_after_previous(balance_grad_kernel<T, VEC, 2>, g, b, 0, s, p, rows);
+  if (p.E <= 512) return launch_after_previous(balance_grad_kernel<T, VEC, 4>, g, b, 0, s, p, rows);
+  return launch_after_previous(balance_grad_kernel<T, VEC, 8>, g, b, 0, s, p, rows);
+}
+template <typename T>
+cudaError_t grad_t(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
+  return vec_rows(p.logits, p.ldl, p.E, sizeof(T)) && vec_rows(p.dlogits, p.lddl, p.E, sizeof(T)) ? grad_nv<T, true>(p, rows, blocks, s)
+                                                                                               : grad_nv<T, false>(p, rows, blocks, s);
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int64_t T, int E, int64_t S) { return (size_t)entries_of(T, S) * (8 * (size_t)E + 8); }
+
+cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace, cudaStream_t s) {
+  const int64_t chunk = chunk_rows_of(p.T), blocks = (p.T + chunk - 1) / chunk, entries = blocks + p.S;
+  Entries out;
+  out.sums = static_cast<float2*>(workspace);
+  out.probs = reinterpret_cast<float*>(out.sums + entries);
+  out.count = reinterpret_cast<int32_t*>(out.probs + entries * p.E);
+  cudaError_t e = dtype == 0   ? rows_t<__nv_bfloat16>(p, out, chunk, blocks, s)
+                  : dtype == 1 ? rows_t<__half>(p, out, chunk, blocks, s)
+                               : rows_t<float>(p, out, chunk, blocks, s);
+  if (e != cudaSuccess) return e;
+  const int parts = (p.E + 127) / 128;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.S * parts));
+  cfg.blockDim = dim3(kBalJoin);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = parts;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, p, out, (int)chunk, parts);
+}
+
+cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
+  // about as many warps as fit the GPU at once
+  const int64_t warps = (int64_t)sms * 3 * kBalWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t blocks = ((p.T + rows - 1) / rows + kBalWarps - 1) / kBalWarps;
+  return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
+         : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)
+                      : grad_t<float>(p, rows, blocks, s);
+}
+
+}  // namespace dfm

@@ -26,6 +26,7 @@
 #include "ops.h"
 #include "pipeline.cuh"
 #include "rowword.h"
+#include "tcgen.cuh"
 #include "umma.cuh"
 
 namespace dfm {
@@ -358,66 +359,6 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int ta, int tb) {
   return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t uni(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// One lane of the (converged) warp, the same every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-// Bounded wait for the barrier at shared address `bar`; the same answer in
-// every lane.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < limit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (__all_sync(0xffffffffu, ok)) return true;
-  }
-  return false;
-}
-// The lane with `leader` arrives.
-__device__ __forceinline__ void arrive_if(uint32_t bar, uint32_t leader) {
-  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(leader) : "memory");
-}
-__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes, uint32_t leader) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(bytes), "r"(leader)
-      : "memory");
-}
-
-// The shared::cluster address of `addr` in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
-#define DFM_TMA(DIM, COORD)                                                                    \
-  "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %3, 0;\n\t"                                            \
-  "@e cp.async.bulk.tensor." DIM                                                               \
-  ".shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, " COORD "], [%2];\n\t}"
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                            uint32_t leader) {
-  asm volatile(DFM_TMA("2d", "{%4, %5}") ::"r"(dst), "l"(map), "r"(bar), "r"(leader), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
-                                            uint32_t leader) {
-  asm volatile(DFM_TMA("3d", "{%4, %5, %6}") ::"r"(dst), "l"(map), "r"(bar), "r"(leader), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-#undef DFM_TMA
-
 // Four MMA steps of 32 along K into one accumulator, issued by the lane with
 // `leader`; KA and KB say how far a step moves the operands' descriptors,
 // whose low words are given. The whole warp runs this: the operands are then
@@ -445,23 +386,6 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t ad, uint32_t bd, 
       "r"(ad), "r"(bd), "r"(idesc), "n"(KA), "n"(KB), "r"(leader), "n"(hi)
       : "memory");
 }
-// `bar` completes when the MMAs issued so far have.
-__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(leader)
-      : "memory");
-}
-
-// 32 lanes x 16 columns of tensor memory: thread l gets lane l's.
-__device__ __forceinline__ void tmem_ld_rows(uint32_t (&r)[16], uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
 // 16 lanes x 8 N columns of tensor memory: thread l gets, for each group of 8
 // columns, columns 2 (l % 4) and the next of lane l / 4 (first two values)
 // and of lane l / 4 + 8. The wait names the registers, so that no use of them
@@ -480,39 +404,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t (&r)[8], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-               :
-               : "memory");
-}
-
 __device__ __forceinline__ void put_y(float* y, float v) { *y = v; }
 __device__ __forceinline__ void put_y(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put_y(__half* y, float v) { *y = __float2half_rn(v); }
-
-template <typename Y>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <>
-__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack16<float>(float, float) { return 0; }
 
 // 32 bytes of a row: 8 fp32 values or 16 of 16 bits (32-byte aligned).
 template <typename Y>
@@ -1098,25 +992,11 @@ fp8_matmul_kernel(const __grid_constant__ Fp8Params p) {
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 fp8_encoder() {
-  static std::atomic<void*> encode{nullptr};
-  void* fn = encode.load();
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return nullptr;
-    encode.store(fn);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-}
-
 // 8-bit [planes][rows][cols], `ld` bytes a row, boxes of 128 columns x
 // box_rows rows in the 128-byte swizzle; what lies outside reads as zero.
 bool map_u8(CUtensorMap* out, const void* base, int64_t cols, int64_t rows, int64_t planes,
             int64_t ld, int box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = fp8_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(ld * rows)};

@@ -1,0 +1,653 @@
+// k_matmul.cu — the product of 16-bit matrices with bias, activation and
+// residual in its epilogue, and its gradients.
+//
+//   z = x w' + b             x [M][K], w [N][K] (gated: [2N][K], gate rows first)
+//   y = residual + act(z)    gated: act(z) = silu(z_gate) z_up
+//   dz = act'(z) dy,  dx = dz w,  dw = dz' x,  db = the column sums of dz
+//
+// One product serves all three: out[r][c] = sum_k Q[r][k] P[c][k], where
+// either operand lies with its k side by side in memory ("K-major": x, w, dz
+// in dx) or with its rows side by side ("MN-major": w in dx, dz and x in dw).
+// Both kinds of tile are 64 k deep in the 128-byte swizzle; the tensor core's
+// descriptors say which it is, so nothing is transposed in memory. Products
+// of 16-bit values are exact in fp32 and the sums are fp32 (tensor memory);
+// bias, activation and residual are fp32 too, and each output is rounded once.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "internal.h"
+#include "ops.h"
+#include "pipeline.cuh"
+#include "tcgen.cuh"
+#include "umma.cuh"
+
+namespace dfm {
+namespace {
+
+constexpr int kMK = 64;  // k of a stage: 128 bytes, the swizzle's row
+
+// ---- elements of a type known at run time (0 bf16, 1 fp16, 2 fp32) ------------
+__device__ __forceinline__ float half_bits(uint32_t v, int type) {
+  return type == 0 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((unsigned short)v));
+}
+__device__ __forceinline__ uint32_t pack_bits(float lo, float hi, int type) {
+  return type == 0 ? pack16<__nv_bfloat16>(lo, hi) : pack16<__half>(lo, hi);
+}
+
+// Columns c, c + step, ... of a row: n (0 to 4) of four. VEC: all four, side by
+// side and aligned to four.
+template <bool VEC>
+__device__ __forceinline__ void load4(float (&v)[4], const void* p, int64_t i, int step, int n, int type) {
+  if (VEC) {
+    if (type == 2) {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      v[0] = half_bits(w.x & 0xffffu, type), v[1] = half_bits(w.x >> 16, type);
+      v[2] = half_bits(w.y & 0xffffu, type), v[3] = half_bits(w.y >> 16, type);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = j >= n ? 0.f : type == 2 ? static_cast<const float*>(p)[i + j * step]
+                                    : half_bits(static_cast<const uint16_t*>(p)[i + j * step], type);
+}
+template <bool VEC>
+__device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t i, int step, int n, int type) {
+  if (VEC) {
+    if (type == 2)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+          make_uint2(pack_bits(v[0], v[1], type), pack_bits(v[2], v[3], type));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= n) continue;
+    if (type == 2) static_cast<float*>(p)[i + j * step] = v[j];
+    else static_cast<uint16_t*>(p)[i + j * step] = (uint16_t)(pack_bits(v[j], 0.f, type) & 0xffffu);
+  }
+}
+
+// ---- activations --------------------------------------------------------------
+// expf and normcdff keep the fp32 outputs' last bits; the quotient is within 2
+// units of the last place.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+__device__ __forceinline__ float act_f(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays
+    case kActSilu: return z * sigmoid_f(z);
+    case kActGelu: return z * normcdff(z);
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? 1.f : z != z ? z : 0.f;
+    case kActSilu:
+    case kActSwiglu: {
+      const float s = sigmoid_f(z);
+      return s * fmaf(z, 1.f - s, 1.f);
+    }
+    case kActGelu: return fmaf(z * 0.3989422804f, expf(-0.5f * z * z), normcdff(z));
+    default: return 1.f;
+  }
+}
+
+// ---- product ------------------------------------------------------------------
+struct GemmParams {
+  CUtensorMap c, r;  // the operands whose rows are the output's columns and rows
+  const void *bias, *residual;
+  void *pre, *y;
+  uint32_t* status;
+  int64_t R, ldr, ldp, ldy;
+  int C, KB;             // output columns (of y), stages of k
+  int in, out;           // types of the operands, bias and pre; of y and residual
+  int act, c_mn, r_mn;   // the activation; operands that are MN-major
+  int units_r, split, vec;
+  int give_up;           // test hook: the role of block 0 that gives up before its first wait
+};
+enum GemmRole { kGemmNone = 0, kGemmCopies, kGemmMmas, kGemmSums };
+
+// Instruction descriptor of kind::f16 (fp32 D, both operands of one type):
+// type 0 bf16, 1 fp16; ta, tb: A is M-major, B N-major in shared memory.
+__device__ __forceinline__ uint32_t gemm_idesc(int type, int M, int N, int ta, int tb) {
+  return (type == 0 ? umma::idesc_bf16_f32(M, N) : umma::idesc_f16_f32(M, N)) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16);
+}
+// Low word of a tile's descriptor, and how far 16 of k move it. K-major: rows
+// of 128 bytes, a step of 32 bytes along them. MN-major: rows of k hold 64
+// values of MN (128 bytes), the next 64 lie 64 rows (8192 bytes) further, and
+// a step is 16 rows. Either has atoms of 8 rows (1024 bytes), the high word.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, int mn) {
+  return ((saddr >> 4) & 0x3FFFu) | (mn ? (8192u >> 4) << 16 : 1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_step(int mn) { return mn ? 16 * 128 / 16 : 2; }
+
+// The four steps of 16 of a stage; acc: added to what D holds. Issued by the
+// lane with `leader`.
+__device__ __forceinline__ void gemm_stage(uint32_t d, uint32_t ad, uint32_t as, uint32_t bd, uint32_t bs, uint32_t idesc,
+                                           uint32_t acc, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 l;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+      "setp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p0, %6, 0;\n\tsetp.eq.u32 pt, %3, %3;\n\t"
+      "mov.b64 a0, {%1, %8};\n\tmov.b64 b0, {%2, %8};\n\t"
+      "add.u32 l, %1, %4;\n\tmov.b64 a1, {l, %8};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a2, {l, %8};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a3, {l, %8};\n\t"
+      "add.u32 l, %2, %5;\n\tmov.b64 b1, {l, %8};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b2, {l, %8};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b3, {l, %8};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, p0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, pt;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "r"(as), "r"(bs), "r"(acc), "r"(leader), "n"(kDescHi)
+      : "memory");
+}
+
+// Four columns (c, c + step, ...) of output row `row`: z (and, gated, up) come
+// without the bias.
+template <bool VEC>
+__device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, int c, int step, float (&z)[4], float (&up)[4]) {
+  const int n = c >= p.C ? 0 : min(4, (p.C - c + step - 1) / step);
+  if (n <= 0) return;
+  const bool gated = p.act == kActSwiglu;
+  float v[4];
+  if (p.bias) {
+    load4<VEC>(v, p.bias, c, step, n, p.in);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] += v[j];
+    if (gated) {
+      load4<VEC>(v, p.bias, (int64_t)p.C + c, step, n, p.in);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) up[j] += v[j];
+    }
+  }
+  if (p.pre) {
+    store4<VEC>(z, p.pre, row * p.ldp + c, step, n, p.in);
+    if (gated) store4<VEC>(up, p.pre, row * p.ldp + p.C + c, step, n, p.in);
+  }
+  if (gated) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], p.act);
+  }
+  if (p.residual) {
+    load4<VEC>(v, p.residual, row * p.ldr + c, step, n, p.out);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] += v[j];
+  }
+  store4<VEC>(z, p.y, row * p.ldy + c, step, n, p.out);
+}
+
+// A unit: 128 columns of the output (gated: 64, with the gate's and the up
+// product's rows of w) as the tensor core's 128 rows, times NT rows of it.
+// A cluster of `split` CTAs shares it, each with a part of k; the sums meet in
+// distributed shared memory in the order of the parts, where the epilogue
+// reads them along the rows. The 128-row operand is the one with the output's
+// columns because with few rows it is the weights, which stream.
+template <int NT>
+struct GemmCfg {
+  static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;  // stages
+  static constexpr int CBytes = 128 * kMK * 2, RBytes = NT * kMK * 2;
+  static constexpr uint32_t Cols = NT < 32 ? 32 : NT;
+  static constexpr int NTHR = 256;
+  static_assert(NS * (CBytes + RBytes) >= 128 * NT * 4, "the sums fit the stages");
+};
+struct GemmSmem {
+  uint64_t full[8], empty[8], acc;
+  uint32_t tmem;
+  int err;
+};
+template <int NT>
+constexpr size_t gemm_smem_bytes() {
+  return (size_t)GemmCfg<NT>::NS * (GemmCfg<NT>::CBytes + GemmCfg<NT>::RBytes) + sizeof(GemmSmem);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(GemmCfg<NT>::NTHR, 2)
+gemm_split_kernel(const __grid_constant__ GemmParams p) {
+  using G = GemmCfg<NT>;
+  constexpr int NS = G::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sc = smem;
+  uint8_t* sr = smem + NS * G::CBytes;
+  GemmSmem* sm = reinterpret_cast<GemmSmem*>(sr + NS * G::RBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)uni(tid >> 5);
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.c) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.r) : "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm->full[i], 1);
+      mbar_init(&sm->empty[i], 1);
+    }
+    mbar_init(&sm->acc, 1);
+    sm->err = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();  // the kernel before this one is complete; tensor memory only from here on
+  if (warp == 6) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(G::Cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm->tmem);
+  const bool gated = p.act == kActSwiglu;
+  const int width = gated ? 64 : 128;
+  const int part = blockIdx.x % p.split, unit = blockIdx.x / p.split;
+  const int tile_c = unit / p.units_r, tile_r = unit - tile_c * p.units_r;
+  const int c0 = tile_c * width;
+  const int64_t r0 = (int64_t)tile_r * NT;
+  const int kb0 = (int)((int64_t)p.KB * part / p.split), kb1 = (int)((int64_t)p.KB * (part + 1) / p.split);
+  const int gives_up = blockIdx.x == 0 ? p.give_up : kGemmNone;
+  const uint32_t limit = gives_up ? kTestWaitLimit : kWaitLimit;
+  float* red = reinterpret_cast<float*>(smem);  // the sums, [NT][128], where the stages were
+
+  if (warp == 4) {
+    // ---- copies, issued by one lane
+    const uint32_t leader = elect_one(), sc0 = uni(smem_u32(sc)), sr0 = uni(smem_u32(sr));
+    const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
+    const int cc = (int)uni(c0), rr = (int)uni((uint32_t)r0);
+    int s = 0, kb = kb0;
+    uint32_t phase = 1;  // the first round finds every stage free
+    bool ok = gives_up != kGemmCopies;
+    for (; kb < kb1 && ok; ++kb) {
+      ok = bar_wait(empty + 8 * s, phase, limit);
+      if (!ok) break;
+      const uint32_t bar = full + 8 * s, dc = sc0 + s * G::CBytes, dr = sr0 + s * G::RBytes;
+      expect_tx(bar, G::CBytes + G::RBytes, leader);
+      const int k = kb * kMK;
+      if (p.c_mn) {
+        tma_load_2d(dc, &p.c, cc, k, bar, leader);
+        tma_load_2d(dc + 8192, &p.c, cc + 64, k, bar, leader);
+      } else {  // boxes of 64 rows
+        tma_load_2d(dc, &p.c, k, cc, bar, leader);
+        tma_load_2d(dc + 8192, &p.c, k, gated ? p.C + cc : cc + 64, bar, leader);
+      }
+      if (p.r_mn) {
+#pragma unroll
+        for (int i = 0; i < NT; i += 64) tma_load_2d(dr + 128 * i, &p.r, rr + i, k, bar, leader);
+      } else {
+        tma_load_2d(dr, &p.r, k, rr, bar, leader);
+      }
+      if (++s == NS) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) sm->err = 1;
+    // copies in flight land before the block goes on
+    const int issued = kb - kb0;
+    for (int i = 0; i < NS && i < issued; ++i) (void)bar_wait(full + 8 * i, ((issued - 1 - i) / NS) & 1, kWaitLimit);
+  } else if (warp == 5) {
+    // ---- MMAs, issued by one lane
+    const uint32_t leader = elect_one(), tm = uni(tmem);
+    const uint32_t a0 = uni(desc_lo(smem_u32(sc), p.c_mn)), b0 = uni(desc_lo(smem_u32(sr), p.r_mn));
+    const uint32_t as = uni(desc_step(p.c_mn)), bs = uni(desc_step(p.r_mn));
+    const uint32_t idesc = uni(gemm_idesc(p.in, 128, NT, p.c_mn, p.r_mn));
+    const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty)), acc = uni(smem_u32(&sm->acc));
+    bool ok = gives_up != kGemmMmas;
+    int s = 0, kb = kb0;
+    uint32_t phase = 0;
+    for (; kb < kb1 && ok; ++kb) {
+      ok = bar_wait(full + 8 * s, phase, limit);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      gemm_stage(tm, a0 + (uint32_t)(s * (G::CBytes >> 4)), as, b0 + (uint32_t)(s * (G::RBytes >> 4)), bs, idesc, kb > kb0, leader);
+      mma_commit(empty + 8 * s, leader);
+      if (++s == NS) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) sm->err = 1;
+    // MMAs issued, and their arrivals, land before tensor memory is released
+    mma_commit(acc, leader);
+    const int issued = kb - kb0;
+    for (int i = 0; i < NS && i < issued; ++i) (void)bar_wait(empty + 8 * i, ((issued - 1 - i) / NS) & 1, kWaitLimit);
+    (void)bar_wait(acc, 0, kWaitLimit);
+  } else if (warp < 4) {
+    // ---- sums to shared memory: lane = column
+    bool ok = gives_up != kGemmSums;
+    ok = ok && bar_wait(smem_u32(&sm->acc), 0, limit);
+    if (!ok) sm->err = 1;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < NT / 16; ++i) {
+        uint32_t v[16];
+        tmem_ld_rows(v, tmem + ((uint32_t)(32 * warp) << 16) + 16 * i);
+        tmem_wait(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) red[(16 * i + j) * 128 + 32 * warp + lane] = __uint_as_float(v[j]);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (*(volatile int*)&sm->err) {  // a wait ran out: NaN
+    for (int i = tid; i < 128 * NT; i += G::NTHR) red[i] = __uint_as_float(0x7fffffffu);
+    if (tid == 0 && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+    __syncthreads();
+  }
+  if (warp == 6)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::Cols) : "memory");
+  if (p.split > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  // ---- epilogue: four columns of a row a thread, 32 such items a warp and
+  // step, the cluster's CTAs in turn
+  const int rows = (int)min((int64_t)NT, p.R - r0), quads = width / 4;
+  const uint32_t red0 = smem_u32(red);
+  const auto sums = [&](float (&v)[4], int i, int step) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = 0.f;
+    for (int q = 0; q < p.split; ++q) {
+      float w[4];
+      const uint32_t at = map_cta(red0 + 4 * i, q);
+      if (step == 1) {
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(at) : "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w[j]) : "r"(at + 4 * j * step) : "memory");
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += w[j];
+    }
+  };
+  for (int g = part * (G::NTHR / 32) + warp; 32 * g < rows * quads; g += p.split * (G::NTHR / 32)) {
+    const int item = 32 * g + lane, q = item / quads, l = item - q * quads;
+    if (q >= rows) continue;
+    const int step = p.vec ? 1 : quads, c = p.vec ? 4 * l : l;
+    float z[4], up[4] = {0.f, 0.f, 0.f, 0.f};
+    sums(z, q * 128 + c, step);
+    if (gated) sums(up, q * 128 + 64 + c, step);
+    if (p.vec) gemm_finish<true>(p, r0 + q, c0 + c, 1, z, up);
+    else gemm_finish<false>(p, r0 + q, c0 + c, step, z, up);
+  }
+  if (p.split > 1) {  // nobody leaves while its sums are read
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// 16-bit rows, `ld` elements apart: a K-major operand has `rows` rows of k
+// (boxes of box_rows x 64), an MN-major one k rows of `rows` (64 x 64).
+bool map_16(CUtensorMap* out, const GemmOperand& o, int64_t rows, int64_t k, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)(o.mn ? rows : k), (cuuint64_t)(o.mn ? k : rows)};
+  const cuuint64_t strides[1] = {(cuuint64_t)(o.ld * 2)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(o.mn ? 64 : box_rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(o.p), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Once a device: the kernel's dynamic shared memory.
+cudaError_t configure(const void* kernel, size_t smem, std::atomic<uint64_t>& configured) {
+  int device = 0;
+  (void)cudaGetDevice(&device);
+  if (device < 64 && configured.load() >> device & 1) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && device < 64) configured.fetch_or(1ull << device);
+  return e;
+}
+
+// A launch as a programmatic dependent, in clusters of `cluster` blocks.
+template <typename P>
+cudaError_t launch_cluster(void (*kernel)(P), int64_t grid, int threads, size_t smem, int cluster, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+bool aligned(const void* p, int64_t ld, int bytes, int size) {
+  return !(((uintptr_t)p | (uint64_t)(ld * size)) & (uint64_t)(bytes - 1));
+}
+
+// Whether every array of the epilogue is aligned to four of its elements.
+int vec4(const GemmArgs& a) {
+  const int so = dtype_bytes(a.out);
+  return a.C % 4 == 0 && aligned(a.y, a.ldy, 4 * so, so) && aligned(a.residual, a.residual ? a.ldr : 0, 4 * so, so) &&
+         aligned(a.pre, a.pre ? a.ldp : 0, 8, 2) && aligned(a.bias, 0, 8, 2);
+}
+
+GemmParams params_of(const GemmArgs& a) {
+  GemmParams p{};
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.pre = a.pre;
+  p.y = a.y;
+  p.status = a.status;
+  p.R = a.R;
+  p.ldr = a.ldr;
+  p.ldp = a.ldp;
+  p.ldy = a.ldy;
+  p.C = a.C;
+  p.KB = (int)((a.K + kMK - 1) / kMK);
+  p.in = a.in;
+  p.out = a.out;
+  p.act = a.act;
+  p.c_mn = a.col.mn;
+  p.r_mn = a.row.mn;
+  p.give_up = a.give_up;
+  p.vec = vec4(a);
+  return p;
+}
+
+template <int NT>
+const char* gemm_split(const GemmArgs& a, int sms, cudaStream_t s) {
+  using G = GemmCfg<NT>;
+  static_assert(2 * (gemm_smem_bytes<NT>() + 1024) <= 228 * 1024, "two blocks an SM");
+  GemmParams p = params_of(a);
+  const bool gated = a.act == kActSwiglu;
+  if (!map_16(&p.c, a.col, gated ? 2 * (int64_t)a.C : a.C, a.K, 64) || !map_16(&p.r, a.row, a.R, a.K, NT))
+    return "tensor map encoding failed";
+  const int64_t units_c = (a.C + (gated ? 63 : 127)) / (gated ? 64 : 128), units_r = (a.R + NT - 1) / NT;
+  const int64_t units = units_c * units_r;
+  if (units > 0x3fffffff) return "too many tiles";
+  p.units_r = (int)units_r;
+  p.split = 1;
+  while (p.split < 8 && 2 * p.split * units <= 2 * sms && 2 * p.split <= p.KB) p.split *= 2;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = configure((const void*)gemm_split_kernel<NT>, gemm_smem_bytes<NT>(), configured);
+  if (e == cudaSuccess) e = launch_cluster(gemm_split_kernel<NT>, units * p.split, G::NTHR, gemm_smem_bytes<NT>(), p.split, s, p);
+  return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
+}
+
+// ---- gradient of the activation, and the bias's ---------------------------------
+// dz = act'(z) dy (gated: [dy u silu'(g) | dy silu(g)]) and its column sums.
+// A block has 64 columns and every parts-th 32 rows; the column sums of the
+// parts meet in the cluster's shared memory, in their order.
+struct ActGradParams {
+  const void *dy, *pre;
+  void *dz, *dbias;
+  int64_t M, lddy, ldp, lddz;
+  int N, act, grad, vec, parts;
+};
+constexpr int kAgThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float value(T v);
+template <>
+__device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float value(__half v) { return __half2float(v); }
+
+// Columns c, c + step, ...: n of eight; VEC: all eight side by side, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(T (&v)[8], const T* p, int step, int n, bool vec) {
+  if (vec) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    memcpy(v, &w, 16);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j * step] : T(0.f);
+}
+template <typename T>
+__device__ __forceinline__ void store8(const float (&v)[8], T* p, int step, int n, bool vec) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack16<T>(v[0], v[1]), pack16<T>(v[2], v[3]), pack16<T>(v[4], v[5]), pack16<T>(v[6], v[7]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) p[j * step] = T(v[j]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParams p) {
+  __shared__ float sums[kAgThreads / 32][2][64];
+  __shared__ float total[2][64];
+  const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+  const int strip = blockIdx.x / p.parts, part = blockIdx.x - strip * p.parts;
+  const int step = p.vec ? 1 : 8, c = 64 * strip + (p.vec ? 8 * tx : tx);
+  const int n = c >= p.N ? 0 : p.vec ? 8 : min(8, (p.N - c + 7) / 8);
+  const bool gated = p.act == kActSwiglu;
+  float s0[8], s1[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.f;
+  pdl_wait();
+  const T* dy = static_cast<const T*>(p.dy) + c;
+  const T* pre = static_cast<const T*>(p.pre) + c;
+  T* dz = static_cast<T*>(p.dz) + c;
+  if (n > 0) {
+    for (int64_t r = 32 * (int64_t)part + ty; r < p.M; r += 32 * p.parts) {
+      T d[8], z[8], u[8];
+      load8(d, dy + r * p.lddy, step, n, p.vec);
+      if (p.act != kActNone) load8(z, pre + r * p.ldp, step, n, p.vec);
+      if (gated) load8(u, pre + r * p.ldp + p.N, step, n, p.vec);
+      float a[8], b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[j] = value(d[j]);
+        if (gated) {
+          const float g = value(z[j]), sg = sigmoid_f(g);
+          b[j] = a[j] * (g * sg);
+          a[j] = a[j] * value(u[j]) * (sg * fmaf(g, 1.f - sg, 1.f));
+          s1[j] += b[j];
+        } else if (p.act != kActNone) {
+          a[j] *= act_slope(value(z[j]), p.act);
+        }
+        s0[j] += a[j];
+      }
+      if (p.act != kActNone) {
+        store8(a, dz + r * p.lddz, step, n, p.vec);
+        if (gated) store8(b, dz + r * p.lddz + p.N, step, n, p.vec);
+      }
+    }
+  }
+  if (!p.dbias) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      s0[j] += __shfl_xor_sync(0xffffffffu, s0[j], o);
+      s1[j] += __shfl_xor_sync(0xffffffffu, s1[j], o);
+    }
+    if ((tid & 31) < 8) {
+      const int at = p.vec ? 8 * tx + j : tx + 8 * j;
+      sums[tid >> 5][0][at] = s0[j];
+      sums[tid >> 5][1][at] = s1[j];
+    }
+  }
+  __syncthreads();
+  if (tid < 128) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAgThreads / 32; ++w) s += sums[w][tid >> 6][tid & 63];
+    total[tid >> 6][tid & 63] = s;
+  }
+  __syncthreads();
+  if (p.parts > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  const int col = 64 * strip + (tid & 63);
+  if (part == 0 && tid < (gated ? 128 : 64) && col < p.N) {
+    float s = 0.f;
+    for (int q = 0; q < p.parts; ++q) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_cta(smem_u32(&total[tid >> 6][tid & 63]), q)) : "memory");
+      s += v;
+    }
+    const int at = (tid >> 6) * p.N + col;
+    if (p.grad == 2) static_cast<float*>(p.dbias)[at] = s;
+    else static_cast<T*>(p.dbias)[at] = T(s);
+  }
+  if (p.parts > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+}  // namespace
+
+const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
+  // boxes of an MN-major operand are 64 wide
+  if (a.R <= 16 && !a.row.mn) return gemm_split<16>(a, sms, s);
+  if (a.R <= 32 && !a.row.mn) return gemm_split<32>(a, sms, s);
+  if (a.R <= 64) return gemm_split<64>(a, sms, s);
+  return gemm_split<128>(a, sms, s);
+}
+
+const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s) {
+  ActGradParams p{};
+  p.dy = a.dy;
+  p.pre = a.pre;
+  p.dz = a.dz;
+  p.dbias = a.dbias;
+  p.M = a.M;
+  p.lddy = a.lddy;
+  p.ldp = a.ldp;
+  p.lddz = a.lddz;
+  p.N = a.N;
+  p.act = a.act;
+  p.grad = a.grad;
+  const bool some = a.act != kActNone;
+  p.vec = a.N % 8 == 0 && aligned(a.dy, a.lddy, 16, 2) && (!some || (aligned(a.pre, a.ldp, 16, 2) && aligned(a.dz, a.lddz, 16, 2)));
+  const int64_t strips = (a.N + 63) / 64, most = a.dbias ? 8 : 1 << 20;
+  int64_t parts = 1;
+  while (2 * parts <= most && 64 * parts < a.M && strips * parts < 8 * sms) parts *= 2;
+  p.parts = (int)parts;
+  const int cluster = a.dbias ? p.parts : 1;
+  const cudaError_t e = a.in == 0 ? launch_cluster(act_grad_kernel<__nv_bfloat16>, strips * parts, kAgThreads, 0, cluster, s, p)
+                                  : launch_cluster(act_grad_kernel<__half>, strips * parts, kAgThreads, 0, cluster, s, p);
+  return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
+}
+
+}  // namespace dfm

@@ -91,4 +91,87 @@ struct Fp8MatmulArgs {
 // What it could not do, as text, or null.
 const char* launch_fp8_matmul(const Fp8MatmulArgs& p, int dtype, int sms, cudaStream_t s);
 
+enum Activation { kActNone = 0, kActRelu, kActSilu, kActGelu, kActSwiglu };  // DF_MOE_ACT_*
+
+// 16-bit matrix, `ld` elements a row; mn: stored with the product's k along
+// its rows' distance (k rows of R or C values), else R or C rows of k.
+struct GemmOperand {
+  const void* p;
+  int64_t ld;
+  bool mn;
+};
+// y[r][c] = residual[r][c] + act(sum_k row[r][k] col[c][k] + bias[c]); gated:
+// col has 2 C rows and act(z)[c] = silu(z[c]) z[C + c].
+struct GemmArgs {
+  GemmOperand row, col;
+  int64_t R, K;
+  int C, in, out, act;  // in: 0 bf16, 1 fp16 (operands, bias, pre); out: of y and residual
+  const void *bias, *residual;
+  void *pre, *y;
+  int64_t ldr, ldp, ldy;
+  uint32_t* status;
+  int give_up;
+};
+const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s);
+
+struct ActGradArgs {
+  const void *dy, *pre;
+  void *dz, *dbias;  // dbias or null
+  int64_t M, lddy, ldp, lddz;
+  int N, in, grad, act;  // grad: type of dbias
+};
+const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s);
+
+enum GateKind { kGateNone = 0, kGateChannel, kGateToken, kGateFull };  // DF_MOE_GATE_*
+
+constexpr int kNormMaxHidden = 32768;
+// Arrays of dtype but: post_w, pre_w and a channel's gate of the weights' type,
+// a token's gate and the gradients of weights and of those gates fp32.
+struct BlockNormArgs {
+  const void *u, *post_w, *gate, *residual, *pre_w;
+  void *h, *n;
+  int64_t T, ldu, ldg, ldr, ldh, ldn;  // in elements
+  int H, post, gate_kind;
+  float scale, eps;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& p, int dtype, int wtype, cudaStream_t s);
+
+struct BlockNormGradArgs {
+  const void *dh, *dn, *u, *h, *post_w, *gate, *pre_w;
+  void *du, *dresidual, *dgate;
+  float *dpost_w, *dpre_w;
+  int64_t T, lddh, lddn, ldu, ldh, ldg, lddu, lddr, lddg;  // in elements
+  int H, post, gate_kind;
+  float scale, eps;
+};
+size_t block_norm_grad_workspace_bytes(int64_t T, int H);
+cudaError_t launch_block_norm_grad(const BlockNormGradArgs& p, int dtype, int wtype, void* workspace, int sms, cudaStream_t s);
+
+struct BalanceArgs {
+  const void* logits;
+  const int32_t *ids, *offs;  // offs or null (S = 1)
+  const uint8_t* mask;        // or null
+  float *loss, *probs;        // probs or null
+  int32_t *counts, *tokens;
+  uint32_t* status;  // or null
+  int64_t T, ldl;
+  int E, k, S, sigmoid;
+  float coef, z_coef;
+};
+size_t balance_workspace_bytes(int64_t T, int E, int64_t S);
+cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace, cudaStream_t s);
+
+struct BalanceGradArgs {
+  const float* dloss;
+  const void* logits;
+  const int32_t *ids, *offs, *counts, *tokens;
+  const uint8_t* mask;
+  const float *weights, *dweights;  // both or neither
+  void* dlogits;
+  int64_t T, ldl, lddl;
+  int E, k, S, sigmoid;
+  float coef, z_coef;
+};
+cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s);
+
 }  // namespace dfm

@@ -1,0 +1,208 @@
+"""Refusals of the operators around the routed experts (no GPU needed): every bad
+argument is an error code and a message before a device is touched. Addresses
+are made up and never followed."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def dfm():
+    import __graft_entry__
+    __graft_entry__.build()
+    import mxfp4_routed_expert_top_gb300 as m
+    return m
+
+
+A = 1 << 20  # an aligned address
+
+
+def refused(dfm, f, code, word, **kw):
+    with pytest.raises(dfm.DfMoeError) as ei:
+        f(**kw)
+    assert ei.value.code == code, str(ei.value)
+    assert word in str(ei.value), str(ei.value)
+
+
+MATMUL = dict(x=A, w=A, dtype="bf16", M=64, N=128, K=256, y=A, out_dtype="f32")
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(M=-1), -1, "negative"), (dict(M=(1 << 31) - 256), -5, "M must"), (dict(N=0), -1, "N must"), (dict(K=0), -1, "K must"),
+    (dict(N=262145), -1, "N must"), (dict(K=262145), -1, "K must"), (dict(dtype="f32"), -1, "dtype"),
+    (dict(dtype="e4m3"), -1, "dtype"), (dict(dtype="f64"), -1, "dtype"), (dict(out_dtype="f16"), -1, "out_dtype"),
+    (dict(dtype="f16", out_dtype="bf16"), -1, "out_dtype"), (dict(act="tanh"), -1, "act"), (dict(act=None), -1, "act"),
+    (dict(K=250), -1, "multiple of 8"), (dict(ldx=264, K=265), -1, "multiple of 8"), (dict(ldx=248), -1, "multiple of 8"),
+    (dict(ldw=260), -1, "multiple of 8"), (dict(ldw=248), -1, "multiple of 8"), (dict(ldy=127), -1, "ldy"),
+    (dict(residual=A, ldr=127), -1, "residual"), (dict(pre=A, ldp=127), -1, "pre"),
+    (dict(pre=A, ldp=255, act="swiglu"), -1, "pre"), (dict(x=None), -1, "required"), (dict(w=None), -1, "required"),
+    (dict(y=None), -1, "required"), (dict(x=A + 8), -1, "16-byte"), (dict(w=A + 2), -1, "16-byte"),
+    (dict(y=A + 2), -1, "aligned"), (dict(residual=A + 2), -1, "aligned"), (dict(pre=A + 1), -1, "aligned"),
+    (dict(bias=A + 1), -1, "aligned"), (dict(status=A + 2), -1, "aligned"), (dict(ldx=1 << 39), -5, "too large"),
+    (dict(ldw=1 << 62), -5, "too large"), (dict(M=1 << 64), -1, "64 bits"), (dict(ldx=(1 << 64) + 256), -1, "64 bits"),
+])
+def test_matmul_refusals(dfm, change, code, word):
+    refused(dfm, dfm.matmul, code, word, **dict(MATMUL, **change))
+
+
+GRAD = dict(dy=A, x=A, w=A, dtype="bf16", M=64, N=128, K=256, dx=A, dw=A, dbias=A, act="swiglu", pre=A, dz=A)
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(M=-1), -1, "negative"), (dict(M=1 << 31), -5, "M must"), (dict(N=0), -1, "N must"), (dict(K=1 << 20), -1, "K must"),
+    (dict(dtype="f32"), -1, "dtype"), (dict(grad_dtype="f16"), -1, "grad_dtype"), (dict(grad_dtype="e4m3"), -1, "grad_dtype"),
+    (dict(act="relu6"), -1, "act"), (dict(dx=None, dw=None, dbias=None, act="none"), -1, "none of"),
+    (dict(pre=None), -1, "pre and dz"), (dict(dz=None), -1, "pre and dz"), (dict(ldp=255), -1, "pre"),
+    (dict(lddz=255), -1, "dz"), (dict(lddz=260), -1, "multiple of 8"), (dict(dz=A + 2), -1, "16-byte"),
+    (dict(N=127, lddz=255), -1, "multiple of 8"), (dict(N=127), -1, "multiple of 8"),
+    (dict(lddy=127), -1, "dy"), (dict(act="none", lddy=132), -1, "multiple of 8"), (dict(act="none", dy=A + 2), -1, "16-byte"),
+    (dict(act="none", dx=None, dw=None, lddy=127), -1, "dy"), (dict(dy=None), -1, "required"), (dict(x=None), -1, "required"),
+    (dict(w=None), -1, "required"), (dict(x=A + 8), -1, "16-byte"), (dict(w=A + 8), -1, "16-byte"),
+    (dict(K=250), -1, "multiple of 8"), (dict(lddx=255), -1, "dx"), (dict(lddw=255), -1, "dw"), (dict(dx=A + 1), -1, "dx"),
+    (dict(dw=A + 2), -1, "dw"), (dict(dbias=A + 2), -1, "aligned"), (dict(status=A + 1), -1, "aligned"),
+    (dict(lddz=1 << 39), -5, "too large"), (dict(lddw=1 << 64), -1, "64 bits"),
+])
+def test_matmul_grad_refusals(dfm, change, code, word):
+    refused(dfm, dfm.matmul_grad, code, word, **dict(GRAD, **change))
+
+
+NORM = dict(u=A, residual=A, dtype="bf16", T=4, H=64, h=A, n=A, post=True, post_weight=A, gate=A, gate_kind="channel",
+            pre_weight=A)
+NORM_GRAD = dict(dh=A, dn=A, u=A, h=A, dtype="bf16", T=4, H=64, du=A, dresidual=A, post=True, post_weight=A, dpost_weight=A,
+                 gate=A, gate_kind="channel", dgate=A, pre_weight=A, dpre_weight=A, workspace=A, workspace_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(T=-1), -1, "negative"), (dict(T=1 << 31), -5, "T must"), (dict(H=0), -1, "H must"), (dict(H=32769), -1, "H must"),
+    (dict(dtype="e4m3"), -1, "dtype"), (dict(weight_dtype="f16"), -1, "weight_dtype"), (dict(eps=0.0), -1, "eps"),
+    (dict(eps=-1e-6), -1, "eps"), (dict(eps=float("nan")), -1, "eps"), (dict(eps=float("inf")), -1, "eps"),
+    (dict(gate_kind="row"), -1, "gate_kind"), (dict(gate=None), -1, "gate"), (dict(gate=A + 2), -1, "aligned"),
+    (dict(gate_kind="token", gate=A + 2), -1, "aligned"), (dict(gate_kind="full", gate=A + 1), -1, "gate"),
+    (dict(gate_kind="full", ldg=63), -1, "gate"), (dict(post_weight=A + 2), -1, "aligned"),
+    (dict(pre_weight=A + 2), -1, "aligned"), (dict(T=1 << 64), -1, "64 bits"),
+])
+def test_norm_refusals(dfm, change, code, word):
+    refused(dfm, dfm.block_norm, code, word, **dict(NORM, **change))
+    refused(dfm, dfm.block_norm_grad, code, word, **dict(NORM_GRAD, **change))
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(ldu=63), -1, "u"), (dict(ldr=63), -1, "residual"), (dict(ldh=1), -1, "h"), (dict(ldn=-1), -1, "n"),
+    (dict(u=A + 1), -1, "u"), (dict(residual=A + 1), -1, "residual"), (dict(h=A + 1), -1, "h"), (dict(n=A + 1), -1, "n"),
+    (dict(u=None, residual=None), -1, "required"), (dict(h=None, n=None), -1, "required"), (dict(u=None), -1, "u"),
+    (dict(u=None, gate_kind="none", gate=None), -1, "needs u"), (dict(post=False), -1, "post"),
+])
+def test_block_norm_refusals(dfm, change, code, word):
+    refused(dfm, dfm.block_norm, code, word, **dict(NORM, **change))
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(lddh=63), -1, "dh"), (dict(lddn=63), -1, "dn"), (dict(ldu=63), -1, "u"), (dict(ldh=63), -1, "h"),
+    (dict(lddu=63), -1, "du"), (dict(lddr=63), -1, "dresidual"), (dict(gate_kind="full", lddg=63), -1, "dgate"),
+    (dict(dh=None, dn=None), -1, "required"), (dict(h=None), -1, "needs h"), (dict(u=None), -1, "need u"),
+    (dict(dn=None), -1, "need dn"), (dict(dn=None, pre_weight=None), -1, "need dn"),
+    (dict(du=None, dresidual=None, dpost_weight=None, dgate=None, dpre_weight=None), -1, "no gradient"),
+    (dict(post=False), -1, "post"), (dict(post=False, post_weight=None), -1, "post"),
+    (dict(gate_kind="none"), -1, "dgate"), (dict(workspace=None), -1, "workspace"), (dict(workspace_bytes=64), -1, "workspace"),
+    (dict(workspace=A + 4), -1, "workspace"), (dict(workspace_bytes=-1), -1, "workspace"), (dict(dpost_weight=A + 2), -1, "aligned"),
+    (dict(dgate=A + 2), -1, "aligned"), (dict(dpre_weight=A + 1), -1, "aligned"),
+])
+def test_block_norm_grad_refusals(dfm, change, code, word):
+    refused(dfm, dfm.block_norm_grad, code, word, **dict(NORM_GRAD, **change))
+
+
+def test_norm_workspace_sizes(dfm):
+    small = dfm.block_norm_grad_workspace(1, 64)
+    assert 0 < small <= dfm.block_norm_grad_workspace(1 << 20, 64)
+    assert dfm.block_norm_grad_workspace(1 << 31 - 1, 32768) > 0
+    for bad in ((0, 64), (-1, 64), (1, 0), (1, 32769), (1 << 31, 64), (1 << 65, 64)):
+        assert dfm.block_norm_grad_workspace(*bad) == 0
+
+
+BALANCE = dict(logits=A, dtype="f32", T=8, E=16, ids=A, k=2, loss=A, counts=A, tokens=A, workspace=A, workspace_bytes=1 << 30)
+BALANCE_GRAD = dict(dloss=A, logits=A, dtype="f32", T=8, E=16, ids=A, k=2, counts=A, tokens=A, dlogits=A, weights=A, dweights=A)
+
+
+@pytest.mark.parametrize("change, code, word", [
+    (dict(T=-1), -1, "negative"), (dict(T=1 << 31), -5, "T * k"), (dict(E=0), -1, "E must"), (dict(E=1025), -1, "E must"),
+    (dict(k=0), -1, "k must"), (dict(k=33), -1, "k must"), (dict(S=0), -1, "S must"), (dict(S=(1 << 20) + 1, offs=A), -5, "S must"),
+    (dict(S=2), -1, "offs"), (dict(score="tanh"), -1, "score"), (dict(dtype="e4m3"), -1, "dtype"),
+    (dict(coef=float("inf")), -1, "finite"), (dict(z_coef=float("nan")), -1, "finite"), (dict(ldl=15), -1, "ldl"),
+    (dict(logits=None), -1, "required"), (dict(logits=A + 2), -1, "aligned"), (dict(counts=A + 2), -1, "aligned"),
+    (dict(tokens=A + 1), -1, "aligned"), (dict(ids=A + 2), -1, "aligned"), (dict(offs=A + 2), -1, "aligned"),
+    (dict(counts=None), -1, "required"), (dict(tokens=None), -1, "required"), (dict(E=(1 << 32) + 2), -1, "32 bits"),
+    (dict(k=(1 << 32) + 2), -1, "32 bits"), (dict(T=1 << 64), -1, "64 bits"),
+])
+def test_balance_refusals(dfm, change, code, word):
+    refused(dfm, dfm.balance_loss, code, word, **dict(BALANCE, **change))
+    refused(dfm, dfm.balance_loss_grad, code, word, **dict(BALANCE_GRAD, **change))
+
+
+@pytest.mark.parametrize("name, change, code, word", [
+    ("balance_loss", dict(loss=None), -1, "required"), ("balance_loss", dict(ids=None), -1, "required"),
+    ("balance_loss", dict(workspace=None), -1, "workspace"), ("balance_loss", dict(workspace_bytes=32), -1, "workspace"),
+    ("balance_loss", dict(workspace=A + 8), -1, "workspace"), ("balance_loss", dict(probs=A + 2), -1, "aligned"),
+    ("balance_loss", dict(status=A + 2), -1, "aligned"), ("balance_loss", dict(workspace_bytes=-5), -1, "workspace"),
+    ("balance_loss_grad", dict(dloss=None), -1, "required"), ("balance_loss_grad", dict(dlogits=None), -1, "required"),
+    ("balance_loss_grad", dict(lddl=15), -1, "lddl"), ("balance_loss_grad", dict(weights=None), -1, "together"),
+    ("balance_loss_grad", dict(dweights=None), -1, "together"), ("balance_loss_grad", dict(ids=None), -1, "together"),
+    ("balance_loss_grad", dict(dlogits=A + 2), -1, "aligned"), ("balance_loss_grad", dict(weights=A + 2), -1, "aligned"),
+])
+def test_balance_refusals_of_one(dfm, name, change, code, word):
+    refused(dfm, getattr(dfm, name), code, word, **dict(BALANCE if name == "balance_loss" else BALANCE_GRAD, **change))
+
+
+def test_balance_workspace_sizes(dfm):
+    assert 0 < dfm.balance_loss_workspace(1, 8) <= dfm.balance_loss_workspace(1, 8, 5)
+    for bad in ((0, 8), (1, 0), (1, 1025), (1, 8, 0), (1 << 31, 8), (1, 8, (1 << 20) + 1), (1, 1 << 40), (1 << 65, 8)):
+        assert dfm.balance_loss_workspace(*bad) == 0
+
+
+def test_give_up_hook_refuses_unknown_roles(dfm):
+    for role in (-1, 4):
+        refused(dfm, dfm.test_matmul_give_up, -1, "role", role=role)
+
+
+def test_empty_calls_need_no_device(dfm):
+    dfm.matmul(None, None, "bf16", 0, 128, 128, None, "bf16")
+    dfm.matmul_grad(None, None, None, "bf16", 0, 128, 128, dx=A)
+    dfm.block_norm(None, None, "bf16", 0, 64)
+    dfm.block_norm_grad(None, None, None, None, "bf16", 0, 64, du=A)
+    dfm.balance_loss_grad(None, None, "f32", 0, 8, None, 2, None, None, None)
+
+
+EVERY_CALL = [("matmul", MATMUL), ("matmul_grad", GRAD), ("block_norm", NORM), ("block_norm_grad", NORM_GRAD),
+              ("balance_loss", BALANCE), ("balance_loss_grad", BALANCE_GRAD)]
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL)
+def test_host_arrays_and_missing_devices_are_refused(dfm, name, kw):
+    import torch
+    for key, v in kw.items():
+        if v == A:
+            refused(dfm, getattr(dfm, name), -1, "device memory", **dict(kw, **{key: torch.zeros(8)}))
+    if not torch.cuda.is_available():
+        refused(dfm, getattr(dfm, name), -3, "no CUDA device", **kw)
+
+
+class OnDevice0:
+    """Stands for a torch tensor on device 0: an address, never followed."""
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL)
+def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name, kw):
+    import torch
+    binding, seen = dfm.binding, []
+    monkeypatch.setattr(binding._c, "df_moe_" + name, lambda *a: seen.append(a[-1]) or 0)
+    monkeypatch.setattr(binding, "_torch_stream", binding._find_torch_stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000 + dev)
+    call = getattr(dfm, name)
+    tensors = {key: OnDevice0() if v == A else v for key, v in kw.items()}
+    call(**tensors)
+    call(**kw)
+    call(**dict(tensors, stream=0x77))
+    assert seen == [0x5000, None, 0x77]
