@@ -39,41 +39,83 @@ __device__ __forceinline__ uint32_t pack_bits(float lo, float hi, int type) {
   return type == 0 ? pack16<__nv_bfloat16>(lo, hi) : pack16<__half>(lo, hi);
 }
 
-// Columns c, c + step, ... of a row: n (0 to 4) of four. VEC: all four, side by
-// side and aligned to four.
-template <bool VEC>
-__device__ __forceinline__ void load4(float (&v)[4], const void* p, int64_t i, int step, int n, int type) {
-  if (VEC) {
+// Columns i, i + step, ... of a row: n of V. VEC: all V, side by side and
+// aligned to them (32 bytes at most).
+template <bool VEC, int V>
+__device__ __forceinline__ void load_columns(float (&v)[V], const void* p, int64_t i, int step, int n, int type) {
+  if constexpr (VEC) {
+    static_assert(V == 4 || V == 16, "");
     if (type == 2) {
-      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      const float* f = static_cast<const float*>(p) + i;
+      if constexpr (V == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(f);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+      } else {
+#pragma unroll
+        for (int h = 0; h < V; h += 8)
+          asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=f"(v[h]), "=f"(v[h + 1]), "=f"(v[h + 2]), "=f"(v[h + 3]), "=f"(v[h + 4]), "=f"(v[h + 5]),
+                         "=f"(v[h + 6]), "=f"(v[h + 7])
+                       : "l"(f + h));
+      }
     } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      v[0] = half_bits(w.x & 0xffffu, type), v[1] = half_bits(w.x >> 16, type);
-      v[2] = half_bits(w.y & 0xffffu, type), v[3] = half_bits(w.y >> 16, type);
+      const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+      uint32_t w[V / 2];
+      if constexpr (V == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(q);
+        w[0] = u.x, w[1] = u.y;
+      } else {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(q));
+      }
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        v[2 * j] = half_bits(w[j] & 0xffffu, type);
+        v[2 * j + 1] = half_bits(w[j] >> 16, type);
+      }
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    v[j] = j >= n ? 0.f : type == 2 ? static_cast<const float*>(p)[i + j * step]
-                                    : half_bits(static_cast<const uint16_t*>(p)[i + j * step], type);
+    for (int j = 0; j < V; ++j)
+      v[j] = j >= n ? 0.f : type == 2 ? static_cast<const float*>(p)[i + j * step]
+                                      : half_bits(static_cast<const uint16_t*>(p)[i + j * step], type);
+  }
 }
-template <bool VEC>
-__device__ __forceinline__ void store4(const float (&v)[4], void* p, int64_t i, int step, int n, int type) {
-  if (VEC) {
-    if (type == 2)
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-          make_uint2(pack_bits(v[0], v[1], type), pack_bits(v[2], v[3], type));
-    return;
-  }
+template <bool VEC, int V>
+__device__ __forceinline__ void store_columns(const float (&v)[V], void* p, int64_t i, int step, int n, int type) {
+  if constexpr (VEC) {
+    if (type == 2) {
+      float* f = static_cast<float*>(p) + i;
+      if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= n) continue;
-    if (type == 2) static_cast<float*>(p)[i + j * step] = v[j];
-    else static_cast<uint16_t*>(p)[i + j * step] = (uint16_t)(pack_bits(v[j], 0.f, type) & 0xffffu);
+        for (int h = 0; h < V; h += 8)
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(f + h), "f"(v[h]), "f"(v[h + 1]),
+                       "f"(v[h + 2]), "f"(v[h + 3]), "f"(v[h + 4]), "f"(v[h + 5]), "f"(v[h + 6]), "f"(v[h + 7])
+                       : "memory");
+      }
+    } else {
+      uint16_t* q = static_cast<uint16_t*>(p) + i;
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = pack_bits(v[2 * j], v[2 * j + 1], type);
+      if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+      } else {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (j >= n) continue;
+      if (type == 2) static_cast<float*>(p)[i + j * step] = v[j];
+      else static_cast<uint16_t*>(p)[i + j * step] = (uint16_t)(pack_bits(v[j], 0.f, type) & 0xffffu);
+    }
   }
 }
 
@@ -112,7 +154,7 @@ struct GemmParams {
   int C, KB;             // output columns (of y), stages of k
   int in, out;           // types of the operands, bias and pre; of y and residual
   int act, c_mn, r_mn;   // the activation; operands that are MN-major
-  int units_r, split, vec;
+  int units_r, units, split, vec;
   int give_up;           // test hook: the role of block 0 that gives up before its first wait
 };
 enum GemmRole { kGemmNone = 0, kGemmCopies, kGemmMmas, kGemmSums };
@@ -154,41 +196,52 @@ __device__ __forceinline__ void gemm_stage(uint32_t d, uint32_t ad, uint32_t as,
       : "memory");
 }
 
-// Four columns (c, c + step, ...) of output row `row`: z (and, gated, up) come
-// without the bias.
-template <bool VEC>
-__device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, int c, int step, float (&z)[4], float (&up)[4]) {
-  const int n = c >= p.C ? 0 : min(4, (p.C - c + step - 1) / step);
+// Columns c, c + step, ... (V of them) of output row `row`: z (and, gated, up)
+// come without the bias.
+template <bool VEC, int V>
+__device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, int c, int step, float (&z)[V], float (&up)[V]) {
+  const int n = c >= p.C ? 0 : min(V, (p.C - c + step - 1) / step);
   if (n <= 0) return;
   const bool gated = p.act == kActSwiglu;
-  float v[4];
+  float v[V];
   if (p.bias) {
-    load4<VEC>(v, p.bias, c, step, n, p.in);
+    load_columns<VEC>(v, p.bias, c, step, n, p.in);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] += v[j];
+    for (int j = 0; j < V; ++j) z[j] += v[j];
     if (gated) {
-      load4<VEC>(v, p.bias, (int64_t)p.C + c, step, n, p.in);
+      load_columns<VEC>(v, p.bias, (int64_t)p.C + c, step, n, p.in);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) up[j] += v[j];
+      for (int j = 0; j < V; ++j) up[j] += v[j];
     }
   }
   if (p.pre) {
-    store4<VEC>(z, p.pre, row * p.ldp + c, step, n, p.in);
-    if (gated) store4<VEC>(up, p.pre, row * p.ldp + p.C + c, step, n, p.in);
+    store_columns<VEC>(z, p.pre, row * p.ldp + c, step, n, p.in);
+    if (gated) store_columns<VEC>(up, p.pre, row * p.ldp + p.C + c, step, n, p.in);
   }
-  if (gated) {
+  switch (p.act) {
+    case kActNone: break;
+    case kActRelu:
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
-  } else {
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActRelu);
+      break;
+    case kActSilu:
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], p.act);
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActGelu);
+      break;
+    default:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
   }
   if (p.residual) {
-    load4<VEC>(v, p.residual, row * p.ldr + c, step, n, p.out);
+    load_columns<VEC>(v, p.residual, row * p.ldr + c, step, n, p.out);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] += v[j];
+    for (int j = 0; j < V; ++j) z[j] += v[j];
   }
-  store4<VEC>(z, p.y, row * p.ldy + c, step, n, p.out);
+  store_columns<VEC>(z, p.y, row * p.ldy + c, step, n, p.out);
 }
 
 // A unit: 128 columns of the output (gated: 64, with the gate's and the up
@@ -379,14 +432,293 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
     float z[4], up[4] = {0.f, 0.f, 0.f, 0.f};
     sums(z, q * 128 + c, step);
     if (gated) sums(up, q * 128 + 64 + c, step);
-    if (p.vec) gemm_finish<true>(p, r0 + q, c0 + c, 1, z, up);
-    else gemm_finish<false>(p, r0 + q, c0 + c, step, z, up);
+    if (p.vec) gemm_finish<true, 4>(p, r0 + q, c0 + c, 1, z, up);
+    else gemm_finish<false, 4>(p, r0 + q, c0 + c, step, z, up);
   }
   if (p.split > 1) {  // nobody leaves while its sums are read
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
+}
+
+// ---- long products: a pair of CTAs on 256 rows x 256 columns -----------------
+// Each CTA of the pair (a cluster of two) has 128 of the rows and half of the
+// columns' operand; one of them, the leader, issues cta_group::2 MMAs of 256 x
+// 256 x 16 over both, so that each operand byte in shared memory feeds twice the
+// products of a 128 x 256 tile. Persistent: the pairs take units in turn, and
+// two accumulators (all of tensor memory) let the epilogue of one unit run under
+// the MMAs of the next. Gated: the first CTA's half of the columns' operand is
+// the gate's rows of w, the second's the up product's, so that a unit is 128
+// columns and both products of a column sit in the same tensor memory lane.
+struct PairCfg {
+  static constexpr int NS = 6, EW = 8, NTHR = (EW + 4) * 32;
+  static constexpr int TileBytes = 128 * kMK * 2;  // an operand's part of a stage
+  static constexpr int Stage = 2 * TileBytes;
+  static constexpr int Pitch = 17;  // of the rows of 16 that a warp turns
+};
+struct PairSmem {
+  float turn[PairCfg::EW][2][32 * PairCfg::Pitch];
+  uint64_t full[PairCfg::NS], empty[PairCfg::NS], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int err;
+};
+constexpr size_t kPairBytes = (size_t)PairCfg::NS * PairCfg::Stage + sizeof(PairSmem);
+static_assert(kPairBytes <= 227 * 1024, "shared memory");
+
+// What a unit is: units go down eight row tiles before the next column tile, so
+// that the pairs at work share their operands in L2.
+struct PairUnit {
+  int r0, c0;
+};
+__device__ __forceinline__ PairUnit pair_unit(int u, const GemmParams& p, int width) {
+  const int units_c = p.units / p.units_r, band = u / (8 * units_c), in = u - band * 8 * units_c;
+  const int tall = min(8, p.units_r - 8 * band), c = in / tall;
+  return {256 * (8 * band + in - c * tall), width * c};
+}
+
+// A tile of this CTA, signalled at the leader's barrier.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %3, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(leader), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void pair_stage(uint32_t d, uint32_t ad, uint32_t as, uint32_t bd, uint32_t bs, uint32_t idesc,
+                                           uint32_t acc, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 l;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+      "setp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p0, %6, 0;\n\tsetp.eq.u32 pt, %3, %3;\n\t"
+      "mov.b64 a0, {%1, %8};\n\tmov.b64 b0, {%2, %8};\n\t"
+      "add.u32 l, %1, %4;\n\tmov.b64 a1, {l, %8};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a2, {l, %8};\n\t"
+      "add.u32 l, l, %4;\n\tmov.b64 a3, {l, %8};\n\t"
+      "add.u32 l, %2, %5;\n\tmov.b64 b1, {l, %8};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b2, {l, %8};\n\t"
+      "add.u32 l, l, %5;\n\tmov.b64 b3, {l, %8};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a0, b0, %3, p0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, pt;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, pt;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "r"(as), "r"(bs), "r"(acc), "r"(leader), "n"(kDescHi)
+      : "memory");
+}
+// The barrier at this place in both CTAs completes when the MMAs so far have.
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tsetp.ne.u32 e, %1, 0;\n\tmov.b16 m, 3;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+               "r"(leader)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+  using G = PairCfg;
+  constexpr int NS = G::NS, EW = G::EW;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sr = smem;                       // rows' operand: the 128-row operand of each CTA
+  uint8_t* sc = smem + NS * G::TileBytes;  // columns' operand
+  PairSmem* sm = reinterpret_cast<PairSmem*>(smem + NS * G::Stage);
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)uni(tid >> 5);
+  const int rank = blockIdx.x & 1;
+  if (tid == 32 * EW) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.c) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.r) : "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm->full[i], 1);
+      mbar_init(&sm->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->acc_full[i], 1);
+      mbar_init(&sm->acc_empty[i], 2 * EW);
+    }
+    sm->err = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();  // the kernel before this one is complete; tensor memory only from here on
+  if (warp == EW + 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_barrier();  // both CTAs' barriers are there
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm->tmem);
+  const bool gated = p.act == kActSwiglu;
+  const int width = gated ? 128 : 256;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // the test hook: a role of block 0 gives up, the pair's other waits are short
+  const int gives_up = blockIdx.x == 0 ? p.give_up : kGemmNone;
+  const uint32_t limit = first == 0 && p.give_up ? kTestWaitLimit : kWaitLimit;
+
+  if (warp == EW) {
+    // ---- copies, issued by one lane
+    const uint32_t leader = elect_one(), sr0 = uni(smem_u32(sr)), sc0 = uni(smem_u32(sc));
+    const uint32_t empty = uni(smem_u32(sm->empty)), full = uni(smem_u32(sm->full));
+    const uint32_t lead_full = uni(map_cta(full, 0));
+    int s = 0;
+    uint32_t phase = 1;  // the first round finds every stage free
+    bool ok = gives_up != kGemmCopies;
+    int issued = 0;
+    for (int u = first; u < p.units && ok; u += step) {
+      const PairUnit un = pair_unit(u, p, width);
+      const int rr = (int)uni(un.r0 + 128 * rank), cc = (int)uni(un.c0 + (rank ? (gated ? p.C : 128) : 0));
+      for (int kb = 0; kb < p.KB; ++kb) {
+        ok = bar_wait(empty + 8 * s, phase, limit);
+        if (!ok) break;
+        const uint32_t bar = lead_full + 8 * s, dr = sr0 + s * G::TileBytes, dc = sc0 + s * G::TileBytes;
+        if (rank == 0) expect_tx(full + 8 * s, 2 * G::Stage, leader);  // both CTAs' bytes
+        const int k = kb * kMK;
+        if (p.r_mn) {
+          pair_load(dr, &p.r, rr, k, bar, leader);
+          pair_load(dr + 8192, &p.r, rr + 64, k, bar, leader);
+        } else {
+          pair_load(dr, &p.r, k, rr, bar, leader);
+        }
+        if (p.c_mn) {
+          pair_load(dc, &p.c, cc, k, bar, leader);
+          pair_load(dc + 8192, &p.c, cc + 64, k, bar, leader);
+        } else {
+          pair_load(dc, &p.c, k, cc, bar, leader);
+        }
+        ++issued;
+        if (++s == NS) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) sm->err = 1;
+    // Copies in flight land before the pair leaves: the leader waits for both
+    // CTAs' (where its MMAs gave up and wait for none); where the leader's
+    // copies gave up, the second CTA's land while its wait runs out.
+    if (rank == 0)
+      for (int i = 0; i < NS; ++i)
+        if (i < issued) (void)bar_wait(full + 8 * i, ((issued - 1 - i) / NS) & 1, limit);
+  } else if (warp == EW + 1) {
+    if (rank == 0) {
+      // ---- MMAs, issued by one lane of the leader
+      const uint32_t leader = elect_one(), tm = uni(tmem);
+      const uint32_t a0 = uni(desc_lo(smem_u32(sr), p.r_mn)), b0 = uni(desc_lo(smem_u32(sc), p.c_mn));
+      const uint32_t as = uni(desc_step(p.r_mn)), bs = uni(desc_step(p.c_mn));
+      const uint32_t idesc = uni(gemm_idesc(p.in, 256, 256, p.r_mn, p.c_mn));
+      const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
+      const uint32_t acc_full = uni(smem_u32(sm->acc_full)), acc_empty = uni(smem_u32(sm->acc_empty));
+      bool ok = gives_up != kGemmMmas;
+      int s = 0;
+      uint32_t phase = 0, acc = 0, acc_phase = 1;  // the first round finds both accumulators free
+      int stages = 0, units = 0;
+      for (int u = first; u < p.units && ok; u += step) {
+        ok = bar_wait(acc_empty + 8 * acc, acc_phase, limit);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int kb = 0; kb < p.KB; ++kb) {
+          ok = bar_wait(full + 8 * s, phase, limit);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          pair_stage(tm + 256 * acc, a0 + (uint32_t)(s * (G::TileBytes >> 4)), as, b0 + (uint32_t)(s * (G::TileBytes >> 4)), bs, idesc,
+                     kb > 0, leader);
+          pair_commit(empty + 8 * s, leader);
+          ++stages;
+          if (++s == NS) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        pair_commit(acc_full + 8 * acc, leader);
+        ++units;
+        acc ^= 1;
+        acc_phase ^= acc ^ 1;
+      }
+      if (!ok) sm->err = 1;
+      // MMAs issued, and their arrivals, land before tensor memory is released
+      for (int i = 0; i < NS; ++i)
+        if (i < stages) (void)bar_wait(empty + 8 * i, ((stages - 1 - i) / NS) & 1, kWaitLimit);
+      for (int i = 0; i < 2; ++i)
+        if (i < units) (void)bar_wait(acc_full + 8 * i, ((units - 1 - i) / 2) & 1, kWaitLimit);
+    }
+  } else if (warp < EW) {
+    // ---- epilogue: warp w has tensor memory lanes 32 (w % 4) .. + 31, a row
+    // of the output each, and half w / 4 of the columns. A wait that runs out
+    // ends every later one of its warp and leaves NaN in what it still writes.
+    const int l0 = 32 * (warp & 3), half = warp >> 2, cols = width / 2;
+    const uint32_t acc_full = smem_u32(sm->acc_full), acc_empty = uni(map_cta(smem_u32(sm->acc_empty), 0));
+    float* turn = sm->turn[warp][0];
+    bool ok = gives_up != kGemmSums;
+    uint32_t acc = 0, acc_phase = 0;
+    for (int u = first; u < p.units; u += step) {
+      const PairUnit un = pair_unit(u, p, width);
+      ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t ta = tmem + ((uint32_t)l0 << 16) + 256 * acc + cols * half;
+      const int64_t r0 = (int64_t)un.r0 + 128 * rank + l0;
+      const int rows = (int)min((int64_t)32, p.R - r0), c0 = un.c0 + cols * half;
+#pragma unroll 1
+      for (int i = 0; i < cols; i += 16) {
+        uint32_t zr[16], ur[16];
+        float z[16], up[16];
+        if (ok) {
+          tmem_ld_rows(zr, ta + i);
+          if (gated) {
+            tmem_ld_rows(ur, ta + 128 + i);
+            tmem_wait(ur);
+          }
+          tmem_wait(zr);
+        }
+        if (i + 16 == cols && ok) {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          arrive_cluster(acc_empty + 8 * acc, lane == 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          z[j] = ok ? __uint_as_float(zr[j]) : __uint_as_float(0x7fffffffu);
+          up[j] = gated && ok ? __uint_as_float(ur[j]) : z[j];
+        }
+        const int c = c0 + i;
+        if (p.vec && c + 16 <= p.C) {
+          if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c, 1, z, up);
+          continue;
+        }
+        // any other rows: two rows of sixteen columns at a time
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          turn[lane * G::Pitch + j] = z[j];
+          if (gated) turn[(32 + lane) * G::Pitch + j] = up[j];
+        }
+        __syncwarp();
+        for (int r = lane >> 4; r < rows; r += 2) {
+          float a[1] = {turn[r * G::Pitch + (lane & 15)]}, b[1] = {gated ? turn[(32 + r) * G::Pitch + (lane & 15)] : 0.f};
+          gemm_finish<false, 1>(p, r0 + r, c + (lane & 15), 1, a, b);
+        }
+        __syncwarp();
+      }
+      if (!ok) sm->err = 1;
+      acc ^= 1;
+      acc_phase ^= acc ^ 1;
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_barrier();  // neither leaves, or frees its tensor memory, before the other is done
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (tid == 0 && *(volatile int*)&sm->err && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
+  if (warp == EW + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // 16-bit rows, `ld` elements apart: a K-major operand has `rows` rows of k
@@ -444,6 +776,14 @@ int vec4(const GemmArgs& a) {
          aligned(a.pre, a.pre ? a.ldp : 0, 8, 2) && aligned(a.bias, 0, 8, 2);
 }
 
+// Whether its whole groups of 16 columns start on 32-byte boundaries.
+int vec16(const GemmArgs& a) {
+  const int so = dtype_bytes(a.out);
+  return aligned(a.y, a.ldy, 32, so) && aligned(a.residual, a.residual ? a.ldr : 0, 32, so) &&
+         aligned(a.pre, a.pre ? a.ldp : 0, 32, 2) && aligned(a.bias, 0, 32, 2) &&
+         (a.act != kActSwiglu || !(a.pre || a.bias) || a.C % 16 == 0);
+}
+
 GemmParams params_of(const GemmArgs& a) {
   GemmParams p{};
   p.bias = a.bias;
@@ -484,6 +824,51 @@ const char* gemm_split(const GemmArgs& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = configure((const void*)gemm_split_kernel<NT>, gemm_smem_bytes<NT>(), configured);
   if (e == cudaSuccess) e = launch_cluster(gemm_split_kernel<NT>, units * p.split, G::NTHR, gemm_smem_bytes<NT>(), p.split, s, p);
+  return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
+}
+
+// Pairs of CTAs that the device runs at once (its SMs come in groups, some of
+// odd size), asked for once.
+int pairs_at_once(int sms) {
+  static std::atomic<int> known[64];
+  int device = 0;
+  (void)cudaGetDevice(&device);
+  int n = device < 64 ? known[device].load() : 0;
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+  cfg.blockDim = dim3(PairCfg::NTHR);
+  cfg.dynamicSmemBytes = kPairBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = sms / 2 > 0 ? sms / 2 : 1;
+  }
+  if (device < 64) known[device].store(n);
+  return n;
+}
+
+const char* gemm_pair(const GemmArgs& a, int sms, cudaStream_t s) {
+  GemmParams p = params_of(a);
+  const bool gated = a.act == kActSwiglu;
+  if (!map_16(&p.c, a.col, gated ? 2 * (int64_t)a.C : a.C, a.K, 128) || !map_16(&p.r, a.row, a.R, a.K, 128))
+    return "tensor map encoding failed";
+  const int64_t units_c = (a.C + (gated ? 127 : 255)) / (gated ? 128 : 256), units_r = (a.R + 255) / 256;
+  if (units_c * units_r > 0x3fffffff) return "too many tiles";
+  p.units_r = (int)units_r;
+  p.units = (int)(units_c * units_r);
+  p.vec = vec16(a);
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = configure((const void*)gemm_pair_kernel, kPairBytes, configured);
+  if (e != cudaSuccess) return cudaGetErrorString(e);
+  const int pairs = pairs_at_once(sms);
+  e = launch_cluster(gemm_pair_kernel, 2 * (int64_t)(p.units < pairs ? p.units : pairs), PairCfg::NTHR, kPairBytes, 2, s, p);
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
 
@@ -618,6 +1003,8 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
 }  // namespace
 
 const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
+  const int64_t wide = a.act == kActSwiglu ? 2 * (int64_t)a.C : a.C;
+  if (a.R > 1024 && wide > 1024) return gemm_pair(a, sms, s);
   // boxes of an MN-major operand are 64 wide
   if (a.R <= 16 && !a.row.mn) return gemm_split<16>(a, sms, s);
   if (a.R <= 32 && !a.row.mn) return gemm_split<32>(a, sms, s);
