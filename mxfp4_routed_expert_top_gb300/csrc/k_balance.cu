@@ -165,12 +165,39 @@ struct Entries {
   float2* sums;    // [entries]: rows counted, sum of l^2
 };
 
-template <typename T, bool VEC, int NV>
+// What a warp does with a row's logits: softmax(z) or softmax(log sigmoid(z))
+// in z; returns the squared logsumexp of the logits (0 where it has no part in
+// the loss).
+template <bool SIGMOID, int N>
+__device__ __forceinline__ float scores_row(float (&z)[N], bool squares) {
+  float l = 0.f;
+  if (SIGMOID) {
+    if (squares) {
+      float w[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = z[i];
+      l = softmax_row(w);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = log_sigmoid(z[i]);
+    (void)softmax_row(z);
+  } else {
+    l = softmax_row(z);
+  }
+  return squares ? l * l : 0.f;
+}
+
+// A warp a row, the next row's logits on their way meanwhile. The sums of the
+// probabilities go to a row of shared memory of the warp's own (in registers
+// they cost the warps that hide the loads).
+template <typename T, bool VEC, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const BalanceArgs p, const Entries out, int chunk_rows) {
-  extern __shared__ float shared[];  // [warps][E], then counts [E]
+  extern __shared__ __align__(16) float shared[];  // [warps][128 NV], then counts [E]
   __shared__ float2 warp_sums[kBalWarps];
-  int* count = reinterpret_cast<int*>(shared + kBalWarps * p.E);
+  constexpr int N = 4 * NV;
+  int* count = reinterpret_cast<int*>(shared + kBalWarps * 32 * N);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float4* mine = reinterpret_cast<float4*>(shared + warp * 32 * N) + lane;  // element i of lane l: [i / 4][l][i % 4]
   const Lanes<VEC, NV> at{lane, p.E};
   const int64_t first = (int64_t)blockIdx.x * chunk_rows, last = min(first + chunk_rows, p.T);
   pdl_wait();
@@ -181,47 +208,50 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
     span.end = min(span.end, last);
     if (span.begin >= span.end) continue;
     for (int e = threadIdx.x; e < p.E; e += kBalThreads) count[e] = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine[32 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
-    float sum[4 * NV], rows = 0.f, zz = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) sum[i] = 0.f;
+    float rows = 0.f, zz = 0.f;
+    // a row: its logits, its ids and whether it counts
+    float next[N];
+    int id = -1;
+    bool counts = false;
+    const auto fetch = [&](int64_t t) {
+      counts = t < span.end && !(p.mask && !p.mask[t]);
+      if (!counts) return;
+      at.load(next, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
+      id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+    };
+    fetch(span.begin + warp);
     for (int64_t t = span.begin + warp; t < span.end; t += kBalWarps) {
-      if (p.mask && !p.mask[t]) continue;
-      float z[4 * NV];
-      at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
-      if (lane < p.k) {
-        const int e = p.ids[t * p.k + lane];
-        if ((unsigned)e < (unsigned)p.E) atomicAdd(&count[e], 1);
+      const bool here = counts;
+      float z[N];
+      if (here) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = next[i];
+        if ((unsigned)id < (unsigned)p.E) atomicAdd(&count[id], 1);
       }
+      fetch(t + kBalWarps);
+      if (!here) continue;
       rows += 1.f;
-      if (p.sigmoid) {
-        if (p.z_coef != 0.f) {
-          float w[4 * NV];
+      zz += scores_row<SIGMOID>(z, p.z_coef != 0.f);
 #pragma unroll
-          for (int i = 0; i < 4 * NV; ++i) w[i] = z[i];
-          const float l = softmax_row(w);
-          zz = fmaf(l, l, zz);
-        }
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) z[i] = log_sigmoid(z[i]);
-        softmax_row(z);
-      } else {
-        const float l = softmax_row(z);
-        if (p.z_coef != 0.f) zz = fmaf(l, l, zz);
+      for (int i = 0; i < NV; ++i) {
+        float4 v = mine[32 * i];
+        v.x += z[4 * i], v.y += z[4 * i + 1], v.z += z[4 * i + 2], v.w += z[4 * i + 3];
+        mine[32 * i] = v;
       }
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) sum[i] += z[i];
     }
-#pragma unroll
-    for (int i = 0; i < 4 * NV; ++i)
-      if (at.col(i) < p.E) shared[warp * p.E + at.col(i)] = sum[i];
     if (lane == 0) warp_sums[warp] = make_float2(rows, zz);
     __syncthreads();
     const int64_t entry = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < p.E; e += kBalThreads) {
+      // column e is element i of lane l
+      const int l = VEC ? e / 4 % 32 : e % 32, i = VEC ? e / 128 * 4 + e % 4 : e / 32;
+      const float* from = shared + 128 * (i / 4) + 4 * l + i % 4;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) v += shared[w * p.E + e];
+      for (int w = 0; w < kBalWarps; ++w) v += from[w * 32 * N];
       out.probs[entry * p.E + e] = v;
       out.count[entry * p.E + e] = count[e];
     }
@@ -235,15 +265,16 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
 }
 
 // One cluster a sequence, 128 experts a CTA: the entries' sums in their order
-// (of eight interleaved parts), and the loss.
+// (of 32 interleaved parts, a warp each), and the loss.
 constexpr int kBalJoin = 1024;
 __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArgs p, const Entries in, int chunk_rows, int parts) {
-  __shared__ float probs[8][128];
-  __shared__ int count[8][128];
+  __shared__ float probs[32][128];
+  __shared__ int count[32][128];
   __shared__ float2 sums[32];
+  __shared__ float terms[4];
   __shared__ float loss;
-  const int e = threadIdx.x & 127, row = threadIdx.x >> 7;
-  const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, expert = 128 * part + e;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.x / parts, part = blockIdx.x - s * parts;
   pdl_wait();
   const Span span = sequence(p.offs, s, p.T);
   const bool some = span.begin < span.end;
@@ -251,43 +282,63 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
   if (p.status && p.offs && threadIdx.x == 0 && part == 0 &&
       (p.offs[s + 1] < p.offs[s] || p.offs[s] < 0 || p.offs[s + 1] > p.T))
     atomicOr(p.status, DEV_ERR_RANGE);
-  float v = 0.f;
-  int n = 0;
-  if (expert < p.E) {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  int n[4] = {0, 0, 0, 0};
+  if (p.E % 4 == 0) {
+    const int c = 128 * part + 4 * lane;
+    if (c < p.E) {
 #pragma unroll 4
-    for (int64_t i = first + row; i <= last; i += 8) {
-      v += in.probs[i * p.E + expert];
-      n += in.count[i * p.E + expert];
+      for (int64_t i = first + warp; i <= last; i += 32) {
+        const float4 a = *reinterpret_cast<const float4*>(in.probs + i * p.E + c);
+        const int4 b = *reinterpret_cast<const int4*>(in.count + i * p.E + c);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        n[0] += b.x, n[1] += b.y, n[2] += b.z, n[3] += b.w;
+      }
     }
+  } else {
+#pragma unroll 2
+    for (int64_t i = first + warp; i <= last; i += 32)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 128 * part + lane + 32 * j;
+        if (c < p.E) {
+          v[j] += in.probs[i * p.E + c];
+          n[j] += in.count[i * p.E + c];
+        }
+      }
   }
-  probs[row][e] = v;
-  count[row][e] = n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = p.E % 4 == 0 ? 4 * lane + j : lane + 32 * j;
+    probs[warp][e] = v[j];
+    count[warp][e] = n[j];
+  }
   // rows counted and l^2: every thread has some entries
   float2 t = make_float2(0.f, 0.f);
   for (int64_t i = first + threadIdx.x; i <= last; i += kBalJoin) t.x += in.sums[i].x, t.y += in.sums[i].y;
   t.x = warp_sum(t.x), t.y = warp_sum(t.y);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
+  if (lane == 0) sums[warp] = t;
   __syncthreads();
   if (threadIdx.x < 128) {
-    t = sums[threadIdx.x & 31];
+    const int e = threadIdx.x, expert = 128 * part + e;
+    t = sums[lane];
     t.x = warp_sum(t.x), t.y = warp_sum(t.y);
-    const float each = t.x > 0.f ? 1.f / t.x : 0.f;
-    v = 0.f, n = 0;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) v += probs[r][e], n += count[r][e];
-    const float mean = t.x > 0.f ? v / t.x : 0.f;
+    float all = 0.f;
+    int many = 0;
+#pragma unroll 8
+    for (int w = 0; w < 32; ++w) all += probs[w][e], many += count[w][e];
+    const float each = t.x > 0.f ? 1.f / t.x : 0.f, mean = t.x > 0.f ? all / t.x : 0.f;
     float term = 0.f;
     if (expert < p.E) {
-      p.counts[(int64_t)s * p.E + expert] = n;
+      p.counts[(int64_t)s * p.E + expert] = many;
       if (p.probs) p.probs[(int64_t)s * p.E + expert] = mean;
-      term = (float)n * ((float)p.E / (float)p.k) * each * mean;
+      term = (float)many * ((float)p.E / (float)p.k) * each * mean;
     }
     term = warp_sum(term);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) probs[threadIdx.x >> 5][0] = term;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (lane == 0) terms[warp] = term;
+    named_barrier_sync(1, 128);
     if (threadIdx.x == 0) {
-      loss = p.coef * (probs[0][0] + probs[1][0] + probs[2][0] + probs[3][0]) + (part == 0 ? p.z_coef * t.y * each : 0.f);
+      loss = p.coef * (terms[0] + terms[1] + terms[2] + terms[3]) + (part == 0 ? p.z_coef * t.y * each : 0.f);
       if (part == 0) p.tokens[s] = (int)t.x;
     }
   }
@@ -315,16 +366,27 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
 }
 
 // A warp a row, rows side by side in a chunk of its own, so that f stays in
-// registers over a sequence's rows.
-template <typename T, bool VEC, int NV>
+// registers over a sequence's rows. The routing weights' terms reach the lanes
+// that hold their experts through a row of shared memory that is zero between
+// rows (comparing every expert with every id took more instructions than the
+// rest).
+template <typename T, bool VEC, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
+  extern __shared__ __align__(16) float shared[];  // [warps][128 NV]
   constexpr int N = 4 * NV;
   const int lane = threadIdx.x & 31;
+  float* kept = shared + (threadIdx.x >> 5) * 32 * N;
+  float4* mine = reinterpret_cast<float4*>(kept) + lane;  // element i of lane l: [i / 4][l][i % 4]
   const Lanes<VEC, NV> at{lane, p.E};
   const int64_t warp = (int64_t)blockIdx.x * kBalWarps + (threadIdx.x >> 5);
   const int64_t first = warp * warp_rows, last = min(first + warp_rows, p.T);
   pdl_wait();
   if (first >= last) return;
+  if (p.weights) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine[32 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncwarp();
+  }
   int s = sequence_of(p.offs, p.S, first);
   Span span{0, 0};
   float f[N], aux = 0.f, zc = 0.f;
@@ -346,7 +408,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
     }
     if (t < span.begin || t >= span.end) continue;  // behind every sequence: left as it was
     T* out = static_cast<T*>(p.dlogits) + t * p.lddl;
-    float z[N], m[N];
+    float z[N];
     if (p.mask && !p.mask[t]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) z[i] = 0.f;
@@ -354,41 +416,82 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
       continue;
     }
     at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
-    float d[N];
-    if (p.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float x = z[i];
-        m[i] = 1.f / (1.f + expf(x));  // 1 - sigmoid
-        d[i] = log_sigmoid(x);
-      }
-      softmax_row(d);
-    }
-    const float l = !p.sigmoid || zc != 0.f ? softmax_row(z) : 0.f;
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) dot = fmaf(f[i], p.sigmoid ? d[i] : z[i], dot);
-    dot = warp_sum(dot);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float share = p.sigmoid ? d[i] * m[i] : z[i];
-      d[i] = aux * share * (f[i] - dot);
-      if (zc != 0.f) d[i] = fmaf(zc * l, z[i], d[i]);
-    }
+    int place = -1;  // of this lane's routing weight in `kept`
     if (p.weights) {
       const float w = lane < p.k ? p.weights[t * p.k + lane] : 0.f, dw = lane < p.k ? p.dweights[t * p.k + lane] : 0.f;
       const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
-      const bool kept = (unsigned)id < (unsigned)p.E;
-      const float mean = warp_sum(kept ? w * dw : 0.f), mine = kept ? w * (dw - mean) : 0.f;
-      for (int j = 0; j < p.k; ++j) {
-        const int e = __shfl_sync(0xffffffffu, id, j);
-        const float x = __shfl_sync(0xffffffffu, mine, j);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (at.col(i) == e) d[i] += p.sigmoid ? x * m[i] : x;
+      const bool there = (unsigned)id < (unsigned)p.E;
+      const float mean = warp_sum(there ? w * dw : 0.f);
+      float x = there ? w * (dw - mean) : 0.f;
+      // an expert that the row names again: its terms together, in order, in the first of its lanes
+      const uint32_t same = __match_any_sync(0xffffffffu, there ? id : -1 - lane);
+      if (__any_sync(0xffffffffu, same & (same - 1))) {
+        float all = 0.f;
+        for (int j = 0; j < p.k; ++j) {
+          const float y = __shfl_sync(0xffffffffu, x, j);
+          if (same >> j & 1) all += y;
+        }
+        x = all;
       }
+      if (there && lane == __ffs(same) - 1) {
+        place = VEC ? id : 128 * (id / 128) + 4 * (id % 32) + id / 32 % 4;
+        kept[place] = x;
+      }
+      __syncwarp();
     }
-    at.store(out, d);
+    float d[SIGMOID ? N : 1], dot = 0.f, l = 0.f;
+    if constexpr (SIGMOID) {
+      float m[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        m[i] = 1.f / (1.f + expf(z[i]));  // 1 - sigmoid
+        d[i] = log_sigmoid(z[i]);
+      }
+      (void)softmax_row(d);
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot = fmaf(f[i], d[i], dot);
+      dot = warp_sum(dot);
+      if (zc != 0.f) l = softmax_row(z);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.weights) {
+          const float4 w = mine[32 * i];
+          x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = 4 * i + j;
+          d[c] = m[c] * fmaf(aux * d[c], f[c] - dot, x[j]);
+          if (zc != 0.f) d[c] = fmaf(zc * l, z[c], d[c]);
+        }
+      }
+      at.store(out, d);
+    } else {
+      l = softmax_row(z);
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot = fmaf(f[i], z[i], dot);
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.weights) {
+          const float4 w = mine[32 * i];
+          x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = 4 * i + j;
+          z[c] = fmaf(z[c], fmaf(aux, f[c] - dot, zc * l), x[j]);
+        }
+      }
+      at.store(out, z);
+    }
+    if (p.weights) {
+      __syncwarp();
+      if (place >= 0) kept[place] = 0.f;
+      __syncwarp();
+    }
   }
 }
 
@@ -405,33 +508,39 @@ bool vec_rows(const void* p, int64_t ld, int E, int size) {
   return E % 4 == 0 && !(((uintptr_t)p | (uint64_t)(ld * size)) & (uint64_t)(4 * size - 1));
 }
 
-template <typename T, bool VEC>
+// NV parts of 128 experts: 1, 2, 4 or 8.
+template <typename T, bool VEC, bool SIGMOID>
 cudaError_t rows_nv(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
-  const size_t smem = (size_t)(kBalWarps + 1) * p.E * sizeof(float);  // 36 KB at most
+  const int nv = p.E <= 128 ? 1 : p.E <= 256 ? 2 : p.E <= 512 ? 4 : 8;
+  const size_t smem = (size_t)(kBalWarps * 128 * nv + p.E) * sizeof(float);  // 36 KB at most
   const dim3 g((unsigned)blocks), b(kBalThreads);
   const int c = (int)chunk;
-  if (p.E <= 128) return launch_after_previous(balance_rows_kernel<T, VEC, 1>, g, b, smem, s, p, out, c);
-  if (p.E <= 256) return launch_after_previous(balance_rows_kernel<T, VEC, 2>, g, b, smem, s, p, out, c);
-  if (p.E <= 512) return launch_after_previous(balance_rows_kernel<T, VEC, 4>, g, b, smem, s, p, out, c);
-  return launch_after_previous(balance_rows_kernel<T, VEC, 8>, g, b, smem, s, p, out, c);
+  if (nv == 1) return launch_after_previous(balance_rows_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, out, c);
+  if (nv == 2) return launch_after_previous(balance_rows_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, out, c);
+  if (nv == 4) return launch_after_previous(balance_rows_kernel<T, VEC, 4, SIGMOID>, g, b, smem, s, p, out, c);
+  return launch_after_previous(balance_rows_kernel<T, VEC, 8, SIGMOID>, g, b, smem, s, p, out, c);
 }
 template <typename T>
 cudaError_t rows_t(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
-  return vec_rows(p.logits, p.ldl, p.E, sizeof(T)) ? rows_nv<T, true>(p, out, chunk, blocks, s)
-                                                   : rows_nv<T, false>(p, out, chunk, blocks, s);
+  if (vec_rows(p.logits, p.ldl, p.E, sizeof(T)))
+    return p.sigmoid ? rows_nv<T, true, true>(p, out, chunk, blocks, s) : rows_nv<T, true, false>(p, out, chunk, blocks, s);
+  return p.sigmoid ? rows_nv<T, false, true>(p, out, chunk, blocks, s) : rows_nv<T, false, false>(p, out, chunk, blocks, s);
 }
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool SIGMOID>
 cudaError_t grad_nv(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
+  const int nv = p.E <= 128 ? 1 : p.E <= 256 ? 2 : p.E <= 512 ? 4 : 8;
+  const size_t smem = p.weights ? (size_t)kBalWarps * 128 * nv * sizeof(float) : 0;  // 32 KB at most
   const dim3 g((unsigned)blocks), b(kBalThreads);
-  if (p.E <= 128) return launch_after_previous(balance_grad_kernel<T, VEC, 1>, g, b, 0, s, p, rows);
-  if (p.E <= 256) return launch_after_previous(balance_grad_kernel<T, VEC, 2>, g, b, 0, s, p, rows);
-  if (p.E <= 512) return launch_after_previous(balance_grad_kernel<T, VEC, 4>, g, b, 0, s, p, rows);
-  return launch_after_previous(balance_grad_kernel<T, VEC, 8>, g, b, 0, s, p, rows);
+  if (nv == 1) return launch_after_previous(balance_grad_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, rows);
+  if (nv == 2) return launch_after_previous(balance_grad_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, rows);
+  if (nv == 4) return launch_after_previous(balance_grad_kernel<T, VEC, 4, SIGMOID>, g, b, smem, s, p, rows);
+  return launch_after_previous(balance_grad_kernel<T, VEC, 8, SIGMOID>, g, b, smem, s, p, rows);
 }
 template <typename T>
 cudaError_t grad_t(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
-  return vec_rows(p.logits, p.ldl, p.E, sizeof(T)) && vec_rows(p.dlogits, p.lddl, p.E, sizeof(T)) ? grad_nv<T, true>(p, rows, blocks, s)
-                                                                                               : grad_nv<T, false>(p, rows, blocks, s);
+  if (vec_rows(p.logits, p.ldl, p.E, sizeof(T)) && vec_rows(p.dlogits, p.lddl, p.E, sizeof(T)))
+    return p.sigmoid ? grad_nv<T, true, true>(p, rows, blocks, s) : grad_nv<T, true, false>(p, rows, blocks, s);
+  return p.sigmoid ? grad_nv<T, false, true>(p, rows, blocks, s) : grad_nv<T, false, false>(p, rows, blocks, s);
 }
 
 }  // namespace
@@ -441,9 +550,9 @@ size_t balance_workspace_bytes(int64_t T, int E, int64_t S) { return (size_t)ent
 cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace, cudaStream_t s) {
   const int64_t chunk = chunk_rows_of(p.T), blocks = (p.T + chunk - 1) / chunk, entries = blocks + p.S;
   Entries out;
-  out.sums = static_cast<float2*>(workspace);
-  out.probs = reinterpret_cast<float*>(out.sums + entries);
+  out.probs = static_cast<float*>(workspace);
   out.count = reinterpret_cast<int32_t*>(out.probs + entries * p.E);
+  out.sums = reinterpret_cast<float2*>(out.count + entries * p.E);
   cudaError_t e = dtype == 0   ? rows_t<__nv_bfloat16>(p, out, chunk, blocks, s)
                   : dtype == 1 ? rows_t<__half>(p, out, chunk, blocks, s)
                                : rows_t<float>(p, out, chunk, blocks, s);
@@ -467,7 +576,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
 
 cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
   // about as many warps as fit the GPU at once
-  const int64_t warps = (int64_t)sms * 3 * kBalWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t warps = (int64_t)sms * 2 * kBalWarps, rows = (p.T + warps - 1) / warps;
   const int64_t blocks = ((p.T + rows - 1) / rows + kBalWarps - 1) / kBalWarps;
   return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
          : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)

@@ -548,7 +548,7 @@ DF_MOE_API int df_moe_block_norm(int device, const void* u, int64_t ldu, int32_t
   a.gate_kind = gate_kind;
   a.scale = residual_scale;
   a.eps = eps;
-  return launched("block norm launch", dfm::launch_block_norm(a, dtype, weight_dtype, (cudaStream_t)stream));
+  return launched("block norm launch", dfm::launch_block_norm(a, dtype, weight_dtype, on.sms(), (cudaStream_t)stream));
 }
 
 DF_MOE_API size_t df_moe_block_norm_grad_workspace(int64_t T, int64_t H) {

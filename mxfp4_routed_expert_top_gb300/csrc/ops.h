@@ -134,7 +134,7 @@ struct BlockNormArgs {
   int H, post, gate_kind;
   float scale, eps;
 };
-cudaError_t launch_block_norm(const BlockNormArgs& p, int dtype, int wtype, cudaStream_t s);
+cudaError_t launch_block_norm(const BlockNormArgs& p, int dtype, int wtype, int sms, cudaStream_t s);
 
 struct BlockNormGradArgs {
   const void *dh, *dn, *u, *h, *post_w, *gate, *pre_w;
