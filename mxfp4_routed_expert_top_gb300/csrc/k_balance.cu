@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "internal.h"
@@ -25,8 +26,8 @@
 namespace dfm {
 namespace {
 
-constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
-constexpr int kBalBlocks = 456;  // chunks of rows at most: three blocks an SM
+constexpr int kBalThreads = 512, kBalWarps = kBalThreads / 32;
+constexpr int kBalBlocks = 152;  // chunks of rows at most: a block an SM, and few entries to join
 
 template <typename T>
 __device__ __forceinline__ float f32_of(T v);
@@ -109,31 +110,58 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// v becomes softmax(v); what it returns is logsumexp(v). A row of -inf alone
-// (nothing allowed) has neither: zeros, and 0. fmaxf drops a NaN, the sum
-// keeps it.
+// 2^x for x <= 0 or so, within 2 units of the last place; below 2^-126: 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// v becomes exp(v - l + log(scale)), l = logsumexp(v); `scale` is what the
+// values are still to be multiplied by (1 / their sum). exp(v - most) as a
+// power of two with one fused product: the rounding of most log2(e) is common to
+// the row and leaves with the sum. A row of -inf alone (nothing allowed) has
+// neither a softmax nor l: zeros, and 0. fmaxf drops a NaN, the sum keeps it.
 template <int N>
-__device__ __forceinline__ float softmax_row(float (&v)[N]) {
+__device__ __forceinline__ float softmax_row(float (&v)[N], float* scale) {
   float most = v[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) most = fmaxf(most, v[i]);
   most = warp_max(most);
-  const float base = most == -INFINITY ? 0.f : most;
+  const float base = most == -INFINITY ? 0.f : most * kLog2e;
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    v[i] = expf(v[i] - base);
+    v[i] = exp2_fast(fmaf(v[i], kLog2e, -base));
     sum += v[i];
   }
   sum = warp_sum(sum);
-  if (sum == 0.f) return 0.f;
-  const float inv = 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] *= inv;
-  return base + logf(sum);
+  *scale = sum == 0.f ? 0.f : 1.f / sum;
+  return sum == 0.f ? 0.f : kLn2 * (base + log2f(sum));
 }
-// log(1 / (1 + exp(-z))) without overflow; -inf stays.
-__device__ __forceinline__ float log_sigmoid(float z) { return fminf(z, 0.f) - log1pf(expf(-fabsf(z))); }
+// v becomes sigmoid(v) times a factor common to the row, m (if it is given)
+// 1 - sigmoid(v); `scale` is 1 over the sum. With M = min(most, 0) and e =
+// exp(M - v), sigmoid(v) exp(-M) = 1 / (exp(M) + e): scores that are all tiny
+// keep their ratios, and 1 - sigmoid(v) = e / (exp(M) + e).
+template <int N, bool REST>
+__device__ __forceinline__ void sigmoid_row(float (&v)[N], float* m, float* scale) {
+  float most = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) most = fmaxf(most, v[i]);
+  most = warp_max(most);
+  const float M = most == -INFINITY ? 0.f : fminf(most, 0.f) * kLog2e, low = exp2_fast(M);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float e = fminf(exp2_fast(fmaf(-v[i], kLog2e, M)), 1e37f), r = __fdividef(1.f, low + e);
+    if (REST) m[i] = v[i] != v[i] ? v[i] : e * r;
+    v[i] = v[i] == -INFINITY ? 0.f : v[i] != v[i] ? v[i] : r;  // fminf drops a NaN
+    sum += v[i];
+  }
+  sum = warp_sum(sum);
+  *scale = sum == 0.f ? 0.f : 1.f / sum;
+}
 
 struct Span {
   int64_t begin, end;
@@ -165,24 +193,21 @@ struct Entries {
   float2* sums;    // [entries]: rows counted, sum of l^2
 };
 
-// What a warp does with a row's logits: softmax(z) or softmax(log sigmoid(z))
-// in z; returns the squared logsumexp of the logits (0 where it has no part in
-// the loss).
+// A row's scores but for the factor `scale`, in z; returns the squared
+// logsumexp of the logits (0 where it has no part in the loss).
 template <bool SIGMOID, int N>
-__device__ __forceinline__ float scores_row(float (&z)[N], bool squares) {
+__device__ __forceinline__ float scores_row(float (&z)[N], float* scale, bool squares) {
   float l = 0.f;
   if (SIGMOID) {
     if (squares) {
       float w[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = z[i];
-      l = softmax_row(w);
+      l = softmax_row(w, scale);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = log_sigmoid(z[i]);
-    (void)softmax_row(z);
+    sigmoid_row<N, false>(z, nullptr, scale);
   } else {
-    l = softmax_row(z);
+    l = softmax_row(z, scale);
   }
   return squares ? l * l : 0.f;
 }
@@ -234,11 +259,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
       fetch(t + kBalWarps);
       if (!here) continue;
       rows += 1.f;
-      zz += scores_row<SIGMOID>(z, p.z_coef != 0.f);
+      float scale;
+      zz += scores_row<SIGMOID>(z, &scale, p.z_coef != 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float4 v = mine[32 * i];
-        v.x += z[4 * i], v.y += z[4 * i + 1], v.z += z[4 * i + 2], v.w += z[4 * i + 3];
+        v.x = fmaf(z[4 * i], scale, v.x), v.y = fmaf(z[4 * i + 1], scale, v.y);
+        v.z = fmaf(z[4 * i + 2], scale, v.z), v.w = fmaf(z[4 * i + 3], scale, v.w);
         mine[32 * i] = v;
       }
     }
@@ -365,20 +392,21 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
   }
 }
 
+constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
 // A warp a row, rows side by side in a chunk of its own, so that f stays in
 // registers over a sequence's rows. The routing weights' terms reach the lanes
 // that hold their experts through a row of shared memory that is zero between
 // rows (comparing every expert with every id took more instructions than the
 // rest).
 template <typename T, bool VEC, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
+__global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
   extern __shared__ __align__(16) float shared[];  // [warps][128 NV]
   constexpr int N = 4 * NV;
   const int lane = threadIdx.x & 31;
   float* kept = shared + (threadIdx.x >> 5) * 32 * N;
   float4* mine = reinterpret_cast<float4*>(kept) + lane;  // element i of lane l: [i / 4][l][i % 4]
   const Lanes<VEC, NV> at{lane, p.E};
-  const int64_t warp = (int64_t)blockIdx.x * kBalWarps + (threadIdx.x >> 5);
+  const int64_t warp = (int64_t)blockIdx.x * kBalGradWarps + (threadIdx.x >> 5);
   const int64_t first = warp * warp_rows, last = min(first + warp_rows, p.T);
   pdl_wait();
   if (first >= last) return;
@@ -439,19 +467,20 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
       }
       __syncwarp();
     }
-    float d[SIGMOID ? N : 1], dot = 0.f, l = 0.f;
+    float dot = 0.f, scale;
     if constexpr (SIGMOID) {
-      float m[N];
+      float d[N], m[N], soft = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        m[i] = 1.f / (1.f + expf(z[i]));  // 1 - sigmoid
-        d[i] = log_sigmoid(z[i]);
-      }
-      (void)softmax_row(d);
+      for (int i = 0; i < N; ++i) d[i] = z[i];
+      sigmoid_row<N, true>(d, m, &scale);
 #pragma unroll
       for (int i = 0; i < N; ++i) dot = fmaf(f[i], d[i], dot);
-      dot = warp_sum(dot);
-      if (zc != 0.f) l = softmax_row(z);
+      dot = warp_sum(dot) * scale;
+      if (zc != 0.f) {
+        const float l = softmax_row(z, &soft);
+        soft *= zc * l;
+      }
+      scale *= aux;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -462,16 +491,18 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 4 * i + j;
-          d[c] = m[c] * fmaf(aux * d[c], f[c] - dot, x[j]);
-          if (zc != 0.f) d[c] = fmaf(zc * l, z[c], d[c]);
+          d[c] = m[c] * fmaf(scale * d[c], f[c] - dot, x[j]);
+          if (zc != 0.f) d[c] = fmaf(soft, z[c], d[c]);
         }
       }
       at.store(out, d);
     } else {
-      l = softmax_row(z);
+      const float l = softmax_row(z, &scale);
 #pragma unroll
       for (int i = 0; i < N; ++i) dot = fmaf(f[i], z[i], dot);
-      dot = warp_sum(dot);
+      dot = warp_sum(dot) * scale;
+      const float rest = scale * (zc != 0.f ? zc * l : 0.f);
+      scale *= aux;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -482,7 +513,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const Balance
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 4 * i + j;
-          z[c] = fmaf(z[c], fmaf(aux, f[c] - dot, zc * l), x[j]);
+          z[c] = fmaf(z[c], fmaf(scale, f[c] - dot, rest), x[j]);
         }
       }
       at.store(out, z);
@@ -512,9 +543,20 @@ bool vec_rows(const void* p, int64_t ld, int E, int size) {
 template <typename T, bool VEC, bool SIGMOID>
 cudaError_t rows_nv(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
   const int nv = p.E <= 128 ? 1 : p.E <= 256 ? 2 : p.E <= 512 ? 4 : 8;
-  const size_t smem = (size_t)(kBalWarps * 128 * nv + p.E) * sizeof(float);  // 36 KB at most
+  const size_t smem = (size_t)(kBalWarps * 128 * nv + p.E) * sizeof(float);  // 68 KB at most
   const dim3 g((unsigned)blocks), b(kBalThreads);
   const int c = (int)chunk;
+  if (nv == 8) {
+    static std::atomic<uint64_t> configured{0};  // a bit a device
+    int device = 0;
+    (void)cudaGetDevice(&device);
+    if (device >= 64 || !(configured.load() >> device & 1)) {
+      const cudaError_t e = cudaFuncSetAttribute(balance_rows_kernel<T, VEC, 8, SIGMOID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)((kBalWarps * 1024 + kOpsMaxExperts) * sizeof(float)));
+      if (e != cudaSuccess) return e;
+      if (device < 64) configured.fetch_or(1ull << device);
+    }
+  }
   if (nv == 1) return launch_after_previous(balance_rows_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, out, c);
   if (nv == 2) return launch_after_previous(balance_rows_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, out, c);
   if (nv == 4) return launch_after_previous(balance_rows_kernel<T, VEC, 4, SIGMOID>, g, b, smem, s, p, out, c);
@@ -529,8 +571,8 @@ cudaError_t rows_t(const BalanceArgs& p, const Entries& out, int64_t chunk, int6
 template <typename T, bool VEC, bool SIGMOID>
 cudaError_t grad_nv(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
   const int nv = p.E <= 128 ? 1 : p.E <= 256 ? 2 : p.E <= 512 ? 4 : 8;
-  const size_t smem = p.weights ? (size_t)kBalWarps * 128 * nv * sizeof(float) : 0;  // 32 KB at most
-  const dim3 g((unsigned)blocks), b(kBalThreads);
+  const size_t smem = p.weights ? (size_t)kBalGradWarps * 128 * nv * sizeof(float) : 0;  // 32 KB at most
+  const dim3 g((unsigned)blocks), b(kBalGradThreads);
   if (nv == 1) return launch_after_previous(balance_grad_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, rows);
   if (nv == 2) return launch_after_previous(balance_grad_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, rows);
   if (nv == 4) return launch_after_previous(balance_grad_kernel<T, VEC, 4, SIGMOID>, g, b, smem, s, p, rows);
@@ -576,8 +618,8 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
 
 cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
   // about as many warps as fit the GPU at once
-  const int64_t warps = (int64_t)sms * 2 * kBalWarps, rows = (p.T + warps - 1) / warps;
-  const int64_t blocks = ((p.T + rows - 1) / rows + kBalWarps - 1) / kBalWarps;
+  const int64_t warps = (int64_t)sms * 2 * kBalGradWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t blocks = ((p.T + rows - 1) / rows + kBalGradWarps - 1) / kBalGradWarps;
   return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
          : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)
                       : grad_t<float>(p, rows, blocks, s);

@@ -42,24 +42,69 @@ template <>
 __device__ __forceinline__ float f32_of(__half v) { return __half2float(v); }
 
 template <typename T>
-__device__ __forceinline__ void load_eight(float* v, const T* p) {
+__device__ __forceinline__ void unpack_eight(float* v, const uint32_t (&u)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load_eight(float* v, const T* p, int i) {
+  p += i;
   if constexpr (sizeof(T) == 4) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
     const uint4 w = *reinterpret_cast<const uint4*>(p);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-      } else {
-        v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
-    }
+    unpack_eight<T>(v, u);
   }
 }
+// The same from shared memory, by its 32-bit address (generic addresses cost
+// two more instructions a load).
+template <typename T>
+struct InShared {
+  uint32_t at;
+};
+__device__ __forceinline__ void lds4(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+template <typename T>
+__device__ __forceinline__ void load_eight(float* v, InShared<T> p, int i) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+      lds4(w, p.at + 4 * (i + h));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[h + j] = __uint_as_float(w[j]);
+    }
+  } else {
+    lds4(w, p.at + 2 * i);
+    unpack_eight<T>(v, w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float load_one(InShared<T> p, int i) {
+  if constexpr (sizeof(T) == 4) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(p.at + 4 * i));
+    return f;
+  } else {
+    unsigned short w;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(p.at + 2 * i));
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(w));
+    else return __uint_as_float((uint32_t)w << 16);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float load_one(const T* p, int i) { return f32_of<T>(p[i]); }
+
 template <typename T>
 __device__ __forceinline__ void store_eight(T* p, const float* v) {
   if constexpr (sizeof(T) == 4) {
@@ -77,18 +122,19 @@ template <bool VEC>
 struct Row {
   int t, tpr, H;
   __device__ __forceinline__ int col(int i, int j) const { return VEC ? 8 * (t + tpr * i) + j : t + tpr * (8 * i + j); }
-  template <typename T>
-  __device__ __forceinline__ void load(float (&v)[8], const T* p, int i) const {
+  // from a const T* or InShared<T>
+  template <typename P>
+  __device__ __forceinline__ void load(float (&v)[8], P p, int i) const {
     if (VEC) {
       if (8 * (t + tpr * i) < H) {
-        load_eight(v, p + 8 * (t + tpr * i));
+        load_eight(v, p, 8 * (t + tpr * i));
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col(i, j) < H ? f32_of<T>(p[col(i, j)]) : 0.f;
+      for (int j = 0; j < 8; ++j) v[j] = col(i, j) < H ? load_one(p, col(i, j)) : 0.f;
     }
   }
   template <typename T>
@@ -108,60 +154,58 @@ struct Row {
 // half of its values and hands the other half over, so that lane l ends with
 // value l / 4 (nine shuffles, not forty). Alternating buffers: one barrier a
 // sum. The order of the additions is fixed.
-template <int N>
+template <int N, int WARPS>
 struct RowSum {
-  float (*buf)[N][32];  // [2], shared
+  static constexpr int S = WARPS == 32 ? 32 : 16;  // warps of a row at most
+  float (*buf)[N][S];                              // [2], shared; zero where the row has no warp
   int which = 0;
+  // before the first sum, and a barrier, by the whole block
+  __device__ __forceinline__ void init() const {
+    for (int i = threadIdx.x; i < 2 * N * S; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  }
   __device__ __forceinline__ void operator()(float (&s)[N], int tpr) {
     static_assert(N == 1 || N == 2 || N == 8, "");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
-    if constexpr (N == 8) {
+    constexpr int G = 32 / N;  // lanes that end with the same value
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-      for (int n = 4, o = 16; n; n >>= 1, o >>= 1)
+    for (int n = N / 2, o = 16; n; n >>= 1, o >>= 1)
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float keep = lane & o ? s[i + n] : s[i], give = lane & o ? s[i] : s[i + n];
-          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      for (int i = 0; i < n; ++i) {
+        const float keep = lane & o ? s[i + n] : s[i], give = lane & o ? s[i] : s[i + n];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    float mine = s[0];
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (tpr > 32) {
+      if (lane % G == 0) buf[which][lane / G][warp] = mine;
+      __syncthreads();
+      // the G lanes of a value add S / G of its warps each
+      mine = 0.f;
+      if constexpr (S > G) {
+#pragma unroll
+        for (int i = 0; i < S / G; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&buf[which][lane / G][S / G * (lane % G) + i]);
+          mine += (f.x + f.y) + (f.z + f.w);
         }
-      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
-      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-      float mine = s[0];
-      if (tpr > 32) {
-        if ((lane & 3) == 0) buf[which][lane >> 2][warp] = mine;
-        __syncthreads();
-        mine = 0.f;
-        for (int w = lane & 3; w < warps; w += 4) mine += buf[which][lane >> 2][w];
-        mine += __shfl_xor_sync(0xffffffffu, mine, 2);
-        mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+      } else {
+        mine = lane % G < S ? buf[which][lane / G][lane % G] : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, mine, 4 * i);
-    } else {
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-      if (tpr > 32) {
-        if (lane == 0)
-#pragma unroll
-          for (int i = 0; i < N; ++i) buf[which][i][warp] = s[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = lane < warps ? buf[which][i][lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-#pragma unroll
-          for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-      }
+      for (int o = G / 2; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, G * i);
     which ^= 1;
   }
 };
 
 // 1 / sqrt(mean + eps), of values that were scaled by `small` (and is then of
-// those too).
-__device__ __forceinline__ float rms_of(float sum, int H, float eps, float small) {
-  return __frsqrt_rn(sum / (float)H + eps * small * small);
+// those too). rsqrtf is within 2 units of the last place; one Newton step makes
+// that one.
+__device__ __forceinline__ float rms_of(float sum, float inv, float eps, float small) {
+  const float m = fmaf(sum, inv, eps * small * small), r = rsqrtf(m);
+  return r == 0.f ? r : fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r);  // 0: an infinite mean
 }
 
 // ---- rows, however they are held ----------------------------------------------
@@ -187,8 +231,8 @@ __device__ __forceinline__ void load_weights(float (&q)[NV][8], float (&v)[NV][8
 
 // sum v^2 over each of R rows, and of what factor the values are where that
 // overflows: 1 / sqrt(mean + eps) of the values themselves.
-template <int NV, int R>
-__device__ __forceinline__ void rms_rows(float (&rms)[R], const float (&v)[R][NV][8], RowSum<R>& sum, int tpr, int H, float eps) {
+template <int NV, int R, typename Sum>
+__device__ __forceinline__ void rms_rows(float (&rms)[R], const float (&v)[R][NV][8], Sum& sum, int tpr, float inv, float eps) {
   float s[R], small[R];
   bool over = false;
 #pragma unroll
@@ -218,16 +262,16 @@ __device__ __forceinline__ void rms_rows(float (&rms)[R], const float (&v)[R][NV
       if (!(s[r] < INFINITY)) s[r] = t[r], small[r] = kSmall;
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) rms[r] = rms_of(s[r], H, eps, small[r]) * small[r];
+  for (int r = 0; r < R; ++r) rms[r] = rms_of(s[r], inv, eps, small[r]) * small[r];
 }
 
 // R rows side by side (their sums share the barriers). in.u(r), in.r(r),
 // in.gate(r): where row r's arrays are; there[r]: whether it is one. `poison`
 // is 0, or NaN for every output. Every thread of the rows runs this.
-template <typename T, bool VEC, int NV, int R, typename In>
+template <typename T, bool VEC, int NV, int R, typename In, typename Sum>
 __device__ __forceinline__ void norm_rows(const BlockNormArgs& p, const Row<VEC>& at, const In& in, const int64_t (&row)[R],
-                                          const bool (&there)[R], RowSum<R>& sum, const float (&q)[NV][8], const float (&v)[NV][8],
-                                          float poison) {
+                                          const bool (&there)[R], Sum& sum, const float (&q)[NV][8], const float (&v)[NV][8],
+                                          float inv, float poison) {
   float h[R][NV][8], rms[R];
   if (p.u) {
 #pragma unroll
@@ -236,7 +280,7 @@ __device__ __forceinline__ void norm_rows(const BlockNormArgs& p, const Row<VEC>
       for (int i = 0; i < NV; ++i) at.load(h[r][i], in.u(r), i);
 #pragma unroll
     for (int r = 0; r < R; ++r) rms[r] = 1.f;
-    if (p.post) rms_rows<NV, R>(rms, h, sum, at.tpr, p.H, p.eps);
+    if (p.post) rms_rows<NV, R>(rms, h, sum, at.tpr, inv, p.eps);
     if (p.gate_kind == kGateToken)
 #pragma unroll
       for (int r = 0; r < R; ++r) rms[r] *= there[r] ? static_cast<const float*>(p.gate)[row[r]] : 0.f;
@@ -284,7 +328,7 @@ __device__ __forceinline__ void norm_rows(const BlockNormArgs& p, const Row<VEC>
         for (int i = 0; i < NV; ++i) at.store(static_cast<T*>(p.h) + row[r] * p.ldh, h[r][i], i);
   }
   if (!p.n) return;
-  rms_rows<NV, R>(rms, h, sum, at.tpr, p.H, p.eps);
+  rms_rows<NV, R>(rms, h, sum, at.tpr, inv, p.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r)
     if (there[r])
@@ -302,10 +346,10 @@ __device__ __forceinline__ void norm_rows(const BlockNormArgs& p, const Row<VEC>
 // the sum of G U and the gate's gradient post_w times the same sum. `sums_done`
 // runs behind the row's sums (whose barrier comes after the last read of an
 // earlier row). ok: false in any thread makes the row NaN.
-template <typename T, bool VEC, int NV, typename In, typename Done>
-__device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row<VEC>& at, const In& in, int64_t row, RowSum<8>& sum,
+template <typename T, bool VEC, int NV, typename In, typename Sum, typename Done>
+__device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row<VEC>& at, const In& in, int64_t row, Sum& sum,
                                          const float (&q)[NV][8], const float (&v)[NV][8], float (&dq)[NV][8], float (&dv)[NV][8],
-                                         bool ok, Done sums_done) {
+                                         float inv, bool ok, Done sums_done) {
   const bool full = p.gate_kind == kGateFull;
   float token = p.gate_kind == kGateToken ? static_cast<const float*>(p.gate)[row] : 1.f;
   float sh = 1.f, su = 1.f, s[8];
@@ -367,12 +411,12 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row<V
     if (!(s[1] < INFINITY)) su = kSmall;
   }
   // rms(h sh) = rh: H = h sh rh, rms(h) = sh rh; the same for u
-  float rh = p.dn ? rms_of(s[0], p.H, p.eps, sh) : 0.f, ru = p.post ? rms_of(s[1], p.H, p.eps, su) : 1.f, scale = p.scale;
+  float rh = p.dn ? rms_of(s[0], inv, p.eps, sh) : 0.f, ru = p.post ? rms_of(s[1], inv, p.eps, su) : 1.f, scale = p.scale;
   if (s[6] != 0.f) rh = ru = token = scale = __uint_as_float(0x7fffffffu);
-  const float inv = 1.f / (float)p.H, along = rh * s[2] * inv;
+  const float along = rh * s[2] * inv, turned = along * rh * s[5];
   rh *= sh;
   // the sum over the row of G q g u su, then of q g G U over H
-  const float gu = s[3] + rh * (s[4] - along * (rh / sh) * s[5]);
+  const float gu = s[3] + rh * (s[4] - turned);
   const float mean = ru * (token * gu) * inv;
   if (p.dgate && p.gate_kind == kGateToken && at.t == 0) static_cast<float*>(p.dgate)[row] = ru * gu;
   ru *= su;
@@ -475,32 +519,37 @@ struct GlobalGradRow {
 
 template <typename T, typename W, bool VEC, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_norm_kernel(const BlockNormArgs p, int tpr) {
-  __shared__ float buf[2][1][32];
+  __shared__ __align__(16) float buf[2][1][THREADS / 32 > 16 ? 32 : 16];
   const int rows = blockDim.x / tpr, g = threadIdx.x / tpr;
   const int64_t row[1] = {(int64_t)blockIdx.x * rows + g};
   const bool there[1] = {true};
   const Row<VEC> at{(int)threadIdx.x - g * tpr, tpr, p.H};
-  RowSum<1> sum{buf};
+  RowSum<1, (THREADS / 32 > 16 ? 32 : 16)> sum{buf};
+  sum.init();
+  __syncthreads();
   pdl_wait();
   if (row[0] >= p.T) return;  // a whole warp: rows == 1 where a row has more
   float q[NV][8], v[NV][8];
   load_weights<W, VEC, NV>(q, v, at, p.post_w, p.gate_kind == kGateChannel ? p.gate : nullptr, p.pre_w);
-  norm_rows<T, VEC, NV, 1>(p, at, GlobalRow<T>{p, row[0]}, row, there, sum, q, v, 0.f);
+  norm_rows<T, VEC, NV, 1>(p, at, GlobalRow<T>{p, row[0]}, row, there, sum, q, v, 1.f / (float)p.H, 0.f);
 }
 
 template <typename T, typename W, bool VEC, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_norm_grad_kernel(const BlockNormGradArgs p, int tpr, float* part, int workers) {
-  __shared__ float buf[2][8][32];
+  __shared__ __align__(16) float buf[2][8][THREADS / 32 > 16 ? 32 : 16];
   const int rows = blockDim.x / tpr, g = threadIdx.x / tpr;
   const int worker = blockIdx.x * rows + g;
   const Row<VEC> at{(int)threadIdx.x - g * tpr, tpr, p.H};
-  RowSum<8> sum{buf};
+  RowSum<8, (THREADS / 32 > 16 ? 32 : 16)> sum{buf};
+  sum.init();
+  __syncthreads();
   float dq[NV][8] = {}, dv[NV][8] = {}, q[NV][8], v[NV][8];
+  const float inv = 1.f / (float)p.H;
   pdl_wait();
   if (worker >= workers) return;  // a whole warp: rows == 1 where a row has more
   load_weights<W, VEC, NV>(q, v, at, p.post_w, p.gate_kind == kGateChannel ? p.gate : nullptr, p.pre_w);
   for (int64_t row = worker; row < p.T; row += workers)
-    grad_row<T, VEC, NV>(p, at, GlobalGradRow<T>{p, row}, row, sum, q, v, dq, dv, true, [] {});
+    grad_row<T, VEC, NV>(p, at, GlobalGradRow<T>{p, row}, row, sum, q, v, dq, dv, inv, true, [] {});
   put_columns<VEC, NV>(p, at, part, worker, workers, dq, dv);
 }
 
@@ -590,20 +639,19 @@ constexpr int kRingThreads = 512;  // 16 values a thread: rows of up to 8192
 // Where the arrays of the rows of a stage start.
 template <typename T, int R>
 struct RingRows {
-  const uint8_t* ring;
   uint32_t at[R][kArrays];
-  __device__ __forceinline__ const T* get(int r, int a) const { return reinterpret_cast<const T*>(ring + at[r][a]); }
-  __device__ __forceinline__ const T* u(int r) const { return get(r, 0); }
-  __device__ __forceinline__ const T* r(int r) const { return get(r, 1); }
-  __device__ __forceinline__ const T* gate(int r) const { return get(r, 2); }
+  __device__ __forceinline__ InShared<T> get(int r, int a) const { return {at[r][a]}; }
+  __device__ __forceinline__ InShared<T> u(int r) const { return get(r, 0); }
+  __device__ __forceinline__ InShared<T> r(int r) const { return get(r, 1); }
+  __device__ __forceinline__ InShared<T> gate(int r) const { return get(r, 2); }
 };
 template <typename T>
 struct RingGradRow : RingRows<T, 1> {
-  __device__ __forceinline__ const T* dh() const { return this->get(0, 0); }
-  __device__ __forceinline__ const T* dn() const { return this->get(0, 1); }
-  __device__ __forceinline__ const T* h() const { return this->get(0, 2); }
-  __device__ __forceinline__ const T* u() const { return this->get(0, 3); }
-  __device__ __forceinline__ const T* gate() const { return this->get(0, 4); }
+  __device__ __forceinline__ InShared<T> dh() const { return this->get(0, 0); }
+  __device__ __forceinline__ InShared<T> dn() const { return this->get(0, 1); }
+  __device__ __forceinline__ InShared<T> h() const { return this->get(0, 2); }
+  __device__ __forceinline__ InShared<T> u() const { return this->get(0, 3); }
+  __device__ __forceinline__ InShared<T> gate() const { return this->get(0, 4); }
 };
 
 // R rows a stage (two of 16 bits: their sums share two barriers).
@@ -612,9 +660,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
   constexpr int R = sizeof(T) == 2 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ RingSmem sm;
-  __shared__ float buf[2][R][32];
+  __shared__ __align__(16) float buf[2][R][16];
   const Row<VEC> at{(int)threadIdx.x, (int)blockDim.x, p.H};
-  RowSum<R> sum{buf};
+  RowSum<R, 16> sum{buf};
+  sum.init();
+  const float inv = 1.f / (float)p.H;
+  const uint32_t ring0 = smem_u32(ring);
   if (threadIdx.x == 0) {
     for (int i = 0; i < r.stages; ++i) mbar_init(&sm.full[i], 1);
     fence_barrier_init();
@@ -641,7 +692,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
     int64_t row[R];
     bool there[R];
     RingRows<T, R> in;
-    in.ring = ring;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       there[i] = first + i < p.T;
@@ -649,11 +699,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
       if (!VEC && there[i] && (row[i] == 0 || row[i] == p.T - 1)) ring_patch(r, ring, s * R + i, row[i]);
 #pragma unroll
       for (int a = 0, n = 0; a < 3; ++a) {
-        in.at[i][a] = ring_row<VEC>(r, s * R + (there[i] ? i : 0), a, n, row[i]);
+        in.at[i][a] = ring0 + ring_row<VEC>(r, s * R + (there[i] ? i : 0), a, n, row[i]);
         n += r.base[a] != nullptr;
       }
     }
-    norm_rows<T, VEC, 2, R>(p, at, in, row, there, sum, q, v, ok ? 0.f : __uint_as_float(0x7fffffffu));
+    norm_rows<T, VEC, 2, R>(p, at, in, row, there, sum, q, v, inv, ok ? 0.f : __uint_as_float(0x7fffffffu));
     before = s;
     if (++s == r.stages) {
       s = 0;
@@ -668,9 +718,12 @@ template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(const BlockNormGradArgs p, const RingArrays r, float* part) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ RingSmem sm;
-  __shared__ float buf[2][8][32];
+  __shared__ __align__(16) float buf[2][8][16];
   const Row<VEC> at{(int)threadIdx.x, (int)blockDim.x, p.H};
-  RowSum<8> sum{buf};
+  RowSum<8, 16> sum{buf};
+  sum.init();
+  const float inv = 1.f / (float)p.H;
+  const uint32_t ring0 = smem_u32(ring);
   if (threadIdx.x == 0) {
     for (int i = 0; i < r.stages; ++i) mbar_init(&sm.full[i], 1);
     fence_barrier_init();
@@ -692,13 +745,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
       ring_patch(r, ring, s, row);
     }
     RingGradRow<T> in;
-    in.ring = ring;
 #pragma unroll
     for (int a = 0, n = 0; a < kArrays; ++a) {
-      in.at[0][a] = ring_row<VEC>(r, s, a, n, row);
+      in.at[0][a] = ring0 + ring_row<VEC>(r, s, a, n, row);
       n += r.base[a] != nullptr;
     }
-    grad_row<T, VEC, 2>(p, at, in, row, sum, q, v, dq, dv, ok, [&] {
+    grad_row<T, VEC, 2>(p, at, in, row, sum, q, v, dq, dv, inv, ok, [&] {
       // behind the sums' barrier every thread is past the row before
       if (threadIdx.x == 0 && before >= 0 && ahead < p.T) {
         ring_fill<VEC, 1>(r, ring, &sm, before, ahead);
@@ -716,7 +768,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
   put_columns<VEC, 2>(p, at, part, blockIdx.x, gridDim.x, dq, dv);
 }
 
-// The workers' sums, in order of 32 interleaved parts. The first array's (G U)
+// The workers' sums, in order of 16 interleaved parts. The first array's (G U)
 // give two gradients, each times the other's factor.
 template <typename W>
 struct ColumnOuts {
@@ -724,22 +776,24 @@ struct ColumnOuts {
   const W *post_w, *gate;  // null: 1
   int first;               // which array has dn H
 };
+constexpr int kColThreads = 512;
 template <typename W>
-__global__ void __launch_bounds__(1024) norm_columns_kernel(const float* part, const ColumnOuts<W> o, int workers, int H) {
-  __shared__ float sums[32][33];
+__global__ void __launch_bounds__(kColThreads) norm_columns_kernel(const float* part, const ColumnOuts<W> o, int workers, int H) {
+  constexpr int WARPS = kColThreads / 32;
+  __shared__ float sums[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const float* in = part + (int64_t)blockIdx.y * workers * H;
   pdl_wait();
   float s = 0.f;
   if (c < H)
-#pragma unroll 4
-    for (int w = warp; w < workers; w += 32) s += in[(int64_t)w * H + c];
+#pragma unroll 10
+    for (int w = warp; w < workers; w += WARPS) s += in[(int64_t)w * H + c];
   sums[warp][lane] = s;
   __syncthreads();
   if (warp || c >= H) return;
   s = 0.f;
 #pragma unroll
-  for (int w = 0; w < 32; ++w) s += sums[w][lane];
+  for (int w = 0; w < WARPS; ++w) s += sums[w][lane];
   if ((int)blockIdx.y == o.first) {
     o.dpre_w[c] = s;
   } else {
@@ -880,7 +934,7 @@ cudaError_t grad_vec(const BlockNormGradArgs& p, float* part, int sms, cudaStrea
   o.first = o.dpost_w || o.dgate ? 1 : 0;
   const int arrays = o.first + (p.dpre_w ? 1 : 0);
   if (e == cudaSuccess && arrays)
-    e = launch_after_previous(norm_columns_kernel<W>, dim3((unsigned)((p.H + 31) / 32), arrays), dim3(1024), 0, s, (const float*)part, o, (int)workers, p.H);
+    e = launch_after_previous(norm_columns_kernel<W>, dim3((unsigned)((p.H + 31) / 32), arrays), dim3(kColThreads), 0, s, (const float*)part, o, (int)workers, p.H);
   return e;
 }
 template <typename T, typename W>
