@@ -145,6 +145,13 @@ struct BlockNormGradArgs {
   float scale, eps;
 };
 size_t block_norm_grad_workspace_bytes(int64_t T, int H);
+// of one type each
+cudaError_t block_norm_bf16(const BlockNormArgs& p, int wtype, int sms, cudaStream_t s);
+cudaError_t block_norm_f16(const BlockNormArgs& p, int wtype, int sms, cudaStream_t s);
+cudaError_t block_norm_f32(const BlockNormArgs& p, int wtype, int sms, cudaStream_t s);
+cudaError_t block_norm_grad_bf16(const BlockNormGradArgs& p, int wtype, float* part, int sms, cudaStream_t s);
+cudaError_t block_norm_grad_f16(const BlockNormGradArgs& p, int wtype, float* part, int sms, cudaStream_t s);
+cudaError_t block_norm_grad_f32(const BlockNormGradArgs& p, int wtype, float* part, int sms, cudaStream_t s);
 cudaError_t launch_block_norm_grad(const BlockNormGradArgs& p, int dtype, int wtype, void* workspace, int sms, cudaStream_t s);
 
 struct BalanceArgs {
