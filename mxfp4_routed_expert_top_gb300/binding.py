@@ -576,6 +576,25 @@ def _choice(kinds, name, v):
         raise DfMoeError(EINVAL, "%s must be one of %s, not %r" % (name, ", ".join(map(repr, kinds)), v)) from None
 
 
+def _some(*arrays):
+    """_place where arrays may be absent."""
+    try:  # the first a tensor, the others tensors on its device or absent
+        dev = arrays[0].get_device()
+        if dev >= 0:
+            out = [dev]
+            for a in arrays:
+                if a is None:
+                    out.append(None)
+                elif a.get_device() == dev:
+                    out.append(a.data_ptr())
+                else:
+                    return _place_any(arrays)
+            return out
+    except AttributeError:
+        pass
+    return _place_any(arrays)
+
+
 def _fits_64(sizes):
     """Whether no size (all of them or-ed) is cut by a 64-bit argument; negative
     ones are for the C call to refuse."""
@@ -597,7 +616,7 @@ def matmul(x, w, dtype, M, N, K, y, out_dtype, bias=None, act="none", residual=N
     """y = residual + act(x w' + bias) of 16-bit matrices (df_moe_matmul)."""
     if not _fits_64(M | N | K | ldx | ldw | ldy | ldr | ldp):
         _too_long()
-    dev, x, w, y, b, r, z, st = _place_any((x, w, y, bias, residual, pre, status))
+    dev, x, w, y, b, r, z, st = _some(x, w, y, bias, residual, pre, status)
     rc = _c.df_moe_matmul(dev, x, ldx, w, ldw, _dtype(dtype), M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y,
                           _dtype(out_dtype), ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -610,7 +629,7 @@ def matmul_grad(dy, x, w, dtype, M, N, K, dx=None, dw=None, dbias=None, grad_dty
     """Gradients of matmul's x, w and bias (df_moe_matmul_grad)."""
     if not _fits_64(M | N | K | lddy | ldx | ldw | lddx | lddw | ldp | lddz):
         _too_long()
-    dev, dy, x, w, dx, dw, db, z, dz, st = _place_any((dy, x, w, dx, dw, dbias, pre, dz, status))
+    dev, dy, x, w, dx, dw, db, z, dz, st = _some(dy, x, w, dx, dw, dbias, pre, dz, status)
     rc = _c.df_moe_matmul_grad(dev, dy, lddy, x, ldx, w, ldw, _dtype(dtype), M, N, K, _choice(_ACTS, "act", act), z,
                                ldp, dz, lddz, dx, lddx, dw, lddw, db, _dtype(grad_dtype), st,
                                _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
@@ -631,7 +650,7 @@ def block_norm(u, residual, dtype, T, H, h=None, n=None, post=False, post_weight
     """h = residual_scale residual + gate norm(u), n = norm(h) (df_moe_block_norm)."""
     if not _fits_64(T | H | ldu | ldr | ldg | ldh | ldn):
         _too_long()
-    dev, u, r, h, n, q, g, v = _place_any((u, residual, h, n, post_weight, gate, pre_weight))
+    dev, u, r, h, n, q, g, v = _some(u, residual, h, n, post_weight, gate, pre_weight)
     rc = _c.df_moe_block_norm(dev, u, ldu, 1 if post else 0, q, _choice(_GATES, "gate_kind", gate_kind), g, ldg, r, ldr,
                               residual_scale, v, eps, T, H, _dtype(dtype), _dtype(weight_dtype), h, ldh, n, ldn,
                               _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
@@ -654,8 +673,8 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
     """Gradients of block_norm (df_moe_block_norm_grad)."""
     if not _fits_64(T | H | lddh | lddn | ldu | ldh | ldg | lddu | lddr | lddg | workspace_bytes):
         _too_long()
-    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _place_any((
-        dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace))
+    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _some(
+        dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
     rc = _c.df_moe_block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q,
                                    _choice(_GATES, "gate_kind", gate_kind), g, ldg, residual_scale, v, eps, T, H,
                                    _dtype(dtype), _dtype(weight_dtype), du, lddu, dr, lddr, dq, dg, lddg, dv, ws,
@@ -680,8 +699,7 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
         _int32(E=E, k=k)
     if not _fits_64(T | S | ldl | workspace_bytes):
         _too_long()
-    dev, z, i, lo, c, t, ws, p, o, m, st = _place_any((logits, ids, loss, counts, tokens, workspace, probs, offs, mask,
-                                                       status))
+    dev, z, i, lo, c, t, ws, p, o, m, st = _some(logits, ids, loss, counts, tokens, workspace, probs, offs, mask, status)
     rc = _c.df_moe_balance_loss(dev, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
                                 z_coef, lo, c, t, p, ws, _workspace_bytes(workspace_bytes), st,
                                 _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
@@ -697,8 +715,7 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
         _int32(E=E, k=k)
     if not _fits_64(T | S | ldl | lddl):
         _too_long()
-    dev, g, z, i, c, t, d, o, m, w, dw = _place_any((dloss, logits, ids, counts, tokens, dlogits, offs, mask, weights,
-                                                     dweights))
+    dev, g, z, i, c, t, d, o, m, w, dw = _some(dloss, logits, ids, counts, tokens, dlogits, offs, mask, weights, dweights)
     rc = _c.df_moe_balance_loss_grad(dev, g, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score),
                                      coef, z_coef, c, t, w, dw, d, lddl,
                                      _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))

@@ -27,7 +27,7 @@ namespace dfm {
 namespace {
 
 constexpr int kBalThreads = 512, kBalWarps = kBalThreads / 32;
-constexpr int kBalBlocks = 152;  // chunks of rows at most: a block an SM, and few entries to join
+constexpr int kBalBlocks = 152;  // chunks of rows at most, of rows above 512: a block an SM, and few entries to join
 
 template <typename T>
 __device__ __forceinline__ float f32_of(T v);
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
   const Lanes<VEC, NV> at{lane, p.E};
   const int64_t first = (int64_t)blockIdx.x * chunk_rows, last = min(first + chunk_rows, p.T);
   pdl_wait();
+  pdl_launch_dependents();  // the join, which waits for the end of this
   for (int s = max(0, sequence_of(p.offs, p.S, first)); s < p.S; ++s) {
     Span span = sequence(p.offs, s, p.T);
     if (span.begin >= last) break;
@@ -242,8 +243,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
     int id = -1;
     bool counts = false;
     const auto fetch = [&](int64_t t) {
-      counts = t < span.end && !(p.mask && !p.mask[t]);
+      counts = t < span.end;
       if (!counts) return;
+      if (p.mask) counts = p.mask[t] != 0;  // its row is read all the same: one latency, not two
       at.load(next, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
       id = lane < p.k ? p.ids[t * p.k + lane] : -1;
     };
@@ -292,9 +294,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
 }
 
 // One cluster a sequence, 128 experts a CTA: the entries' sums in their order
-// (of 32 interleaved parts, a warp each), and the loss.
-constexpr int kBalJoin = 1024;
+// (interleaved over the warps, 32 of them or 8), and the loss.
+constexpr int kBalJoin = 1024, kBalJoinFew = 256;
 __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArgs p, const Entries in, int chunk_rows, int parts) {
+  const int warps = blockDim.x >> 5;
   __shared__ float probs[32][128];
   __shared__ int count[32][128];
   __shared__ float2 sums[32];
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
     const int c = 128 * part + 4 * lane;
     if (c < p.E) {
 #pragma unroll 4
-      for (int64_t i = first + warp; i <= last; i += 32) {
+      for (int64_t i = first + warp; i <= last; i += warps) {
         const float4 a = *reinterpret_cast<const float4*>(in.probs + i * p.E + c);
         const int4 b = *reinterpret_cast<const int4*>(in.count + i * p.E + c);
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
     }
   } else {
 #pragma unroll 2
-    for (int64_t i = first + warp; i <= last; i += 32)
+    for (int64_t i = first + warp; i <= last; i += warps)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = 128 * part + lane + 32 * j;
@@ -342,18 +345,18 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
   }
   // rows counted and l^2: every thread has some entries
   float2 t = make_float2(0.f, 0.f);
-  for (int64_t i = first + threadIdx.x; i <= last; i += kBalJoin) t.x += in.sums[i].x, t.y += in.sums[i].y;
+  for (int64_t i = first + threadIdx.x; i <= last; i += blockDim.x) t.x += in.sums[i].x, t.y += in.sums[i].y;
   t.x = warp_sum(t.x), t.y = warp_sum(t.y);
   if (lane == 0) sums[warp] = t;
   __syncthreads();
   if (threadIdx.x < 128) {
     const int e = threadIdx.x, expert = 128 * part + e;
-    t = sums[lane];
+    t = lane < warps ? sums[lane] : make_float2(0.f, 0.f);
     t.x = warp_sum(t.x), t.y = warp_sum(t.y);
     float all = 0.f;
     int many = 0;
 #pragma unroll 8
-    for (int w = 0; w < 32; ++w) all += probs[w][e], many += count[w][e];
+    for (int w = 0; w < warps; ++w) all += probs[w][e], many += count[w][e];
     const float each = t.x > 0.f ? 1.f / t.x : 0.f, mean = t.x > 0.f ? all / t.x : 0.f;
     float term = 0.f;
     if (expert < p.E) {
@@ -436,18 +439,23 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
     }
     if (t < span.begin || t >= span.end) continue;  // behind every sequence: left as it was
     T* out = static_cast<T*>(p.dlogits) + t * p.lddl;
-    float z[N];
-    if (p.mask && !p.mask[t]) {
+    float z[N], w = 0.f, dw = 0.f;
+    int id = -1;
+    const bool counts = !p.mask || p.mask[t];  // its row is read all the same: one latency, not two
+    at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
+    if (p.weights && lane < p.k) {
+      w = p.weights[t * p.k + lane];
+      dw = p.dweights[t * p.k + lane];
+      id = p.ids[t * p.k + lane];
+    }
+    if (!counts) {
 #pragma unroll
       for (int i = 0; i < N; ++i) z[i] = 0.f;
       at.store(out, z);
       continue;
     }
-    at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
     int place = -1;  // of this lane's routing weight in `kept`
     if (p.weights) {
-      const float w = lane < p.k ? p.weights[t * p.k + lane] : 0.f, dw = lane < p.k ? p.dweights[t * p.k + lane] : 0.f;
-      const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
       const bool there = (unsigned)id < (unsigned)p.E;
       const float mean = warp_sum(there ? w * dw : 0.f);
       float x = there ? w * (dw - mean) : 0.f;
@@ -526,12 +534,14 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
   }
 }
 
-int64_t chunk_rows_of(int64_t T) {
-  const int64_t rows = (T + kBalBlocks - 1) / kBalBlocks;
+// Rows of a block: short rows have few registers and small entries, so more
+// blocks share an SM.
+int64_t chunk_rows_of(int64_t T, int E) {
+  const int64_t blocks = kBalBlocks * (E <= 128 ? 3 : E <= 512 ? 2 : 1), rows = (T + blocks - 1) / blocks;
   return (rows + kBalWarps - 1) / kBalWarps * kBalWarps;
 }
-int64_t entries_of(int64_t T, int64_t S) {
-  const int64_t rows = chunk_rows_of(T);
+int64_t entries_of(int64_t T, int E, int64_t S) {
+  const int64_t rows = chunk_rows_of(T, E);
   return (T + rows - 1) / rows + S;
 }
 
@@ -587,10 +597,10 @@ cudaError_t grad_t(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaS
 
 }  // namespace
 
-size_t balance_workspace_bytes(int64_t T, int E, int64_t S) { return (size_t)entries_of(T, S) * (8 * (size_t)E + 8); }
+size_t balance_workspace_bytes(int64_t T, int E, int64_t S) { return (size_t)entries_of(T, E, S) * (8 * (size_t)E + 8); }
 
 cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace, cudaStream_t s) {
-  const int64_t chunk = chunk_rows_of(p.T), blocks = (p.T + chunk - 1) / chunk, entries = blocks + p.S;
+  const int64_t chunk = chunk_rows_of(p.T, p.E), blocks = (p.T + chunk - 1) / chunk, entries = blocks + p.S;
   Entries out;
   out.probs = static_cast<float*>(workspace);
   out.count = reinterpret_cast<int32_t*>(out.probs + entries * p.E);
@@ -602,7 +612,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
   const int parts = (p.E + 127) / 128;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.S * parts));
-  cfg.blockDim = dim3(kBalJoin);
+  cfg.blockDim = dim3(blocks > 64 * (int64_t)p.S ? kBalJoin : kBalJoinFew);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -618,7 +628,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
 
 cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
   // about as many warps as fit the GPU at once
-  const int64_t warps = (int64_t)sms * 2 * kBalGradWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t warps = (int64_t)sms * (p.E <= 128 ? 6 : p.E <= 512 ? 3 : 2) * kBalGradWarps, rows = (p.T + warps - 1) / warps;
   const int64_t blocks = ((p.T + rows - 1) / rows + kBalGradWarps - 1) / kBalGradWarps;
   return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
          : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)

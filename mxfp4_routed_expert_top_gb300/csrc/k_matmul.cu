@@ -880,7 +880,7 @@ struct ActGradParams {
   const void *dy, *pre;
   void *dz, *dbias;
   int64_t M, lddy, ldp, lddz;
-  int N, act, grad, vec, parts;
+  int N, act, grad, vec, parts, follows;
 };
 constexpr int kAgThreads = 256;
 
@@ -926,6 +926,8 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
 #pragma unroll
   for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.f;
   pdl_wait();
+  // a product of the same call, which waits for the end of this; nothing else may start early
+  if (p.follows) pdl_launch_dependents();
   const T* dy = static_cast<const T*>(p.dy) + c;
   const T* pre = static_cast<const T*>(p.pre) + c;
   T* dz = static_cast<T*>(p.dz) + c;
@@ -1025,6 +1027,7 @@ const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s) {
   p.N = a.N;
   p.act = a.act;
   p.grad = a.grad;
+  p.follows = a.follows;
   const bool some = a.act != kActNone;
   p.vec = a.N % 8 == 0 && aligned(a.dy, a.lddy, 16, 2) && (!some || (aligned(a.pre, a.ldp, 16, 2) && aligned(a.dz, a.lddz, 16, 2)));
   const int64_t strips = (a.N + 63) / 64, most = a.dbias ? 8 : 1 << 20;

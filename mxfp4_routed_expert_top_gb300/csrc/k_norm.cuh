@@ -461,6 +461,11 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row& 
 
 // The sums of a worker's rows, behind each other: part[array][worker][H].
 __device__ __forceinline__ bool wants_dq(const BlockNormGradArgs& p) { return p.dpost_w || (p.dgate && p.gate_kind == kGateChannel); }
+// The kernel that joins them, and only that, may start early (it waits for the
+// end of this one): what else may follow in the stream need not wait.
+__device__ __forceinline__ void let_columns_start(const BlockNormGradArgs& p) {
+  if (wants_dq(p) || p.dpre_w) pdl_launch_dependents();
+}
 template <int NV>
 __device__ __forceinline__ void put_columns(const BlockNormGradArgs& p, const Row& at, float* part, int worker, int workers,
                                             const Eight (&dq)[NV], const Eight (&dv)[NV]) {
@@ -524,6 +529,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_kernel(const BlockNor
   __syncthreads();
   const float inv = 1.f / (float)p.H;
   pdl_wait();
+  let_columns_start(p);
   if (worker >= workers) return;  // a whole warp: rows == 1 where a row has more
   Eight dq[NV], dv[NV], q[NV], v[NV];
 #pragma unroll
@@ -681,6 +687,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
   }
   __syncthreads();
   pdl_wait();
+  let_columns_start(p);
   int64_t ahead = blockIdx.x;
   for (int i = 0; i < r.stages && ahead < p.T; ++i, ahead += gridDim.x) ring.fill(i, ahead);
   Eight dq[2], dv[2], q[2], v[2];
@@ -714,12 +721,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
 }
 
 // ---- rows of any length and alignment --------------------------------------------
-// A block a row, value by value, in loops that stay small (unrolled over a
-// thread's values they did not fit the instruction cache, which took most of
-// the time). The second pass over a row finds it in L1 or L2. What a thread
-// keeps of a row (h) or over its rows (the column sums) is in shared memory, at
-// places that no other thread touches; longer rows' column sums in global.
+// A block a row, value by value, in loops that stay small (unrolled over all of
+// a thread's values they did not fit the instruction cache, which took most of
+// the time). Four values' loads go out together, before the first store, which
+// they could not pass. The second pass over a row finds it in L1 or L2. What a
+// thread keeps of a row (h) or over its rows (the column sums) is in shared
+// memory, at places that no other thread touches; longer rows' column sums in
+// global.
 constexpr int kOddThreads = 256, kOddUnroll = 4;
+
+// Values c, c + kOddThreads, ... (kOddUnroll of them) of a row that may be
+// absent (0, or `absent`).
+template <typename T>
+__device__ __forceinline__ void load_odd(float (&v)[kOddUnroll], const T* p, int c, int H, float absent = 0.f) {
+#pragma unroll
+  for (int i = 0; i < kOddUnroll; ++i) v[i] = p && c + i * kOddThreads < H ? f32_of<T>(p[c + i * kOddThreads]) : absent;
+}
+template <typename T>
+__device__ __forceinline__ void store_odd(T* p, const float (&v)[kOddUnroll], int c, int H) {
+#pragma unroll
+  for (int i = 0; i < kOddUnroll; ++i)
+    if (c + i * kOddThreads < H) p[c + i * kOddThreads] = T(v[i]);
+}
+#define DFM_ODD _Pragma("unroll") for (int i = 0; i < kOddUnroll; ++i)
+#define DFM_ODD_ROW _Pragma("unroll 1") for (int c = threadIdx.x; c < H; c += kOddUnroll * kOddThreads)
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* p, int64_t row, int64_t ld) {
+  return p ? static_cast<const T*>(p) + row * ld : nullptr;
+}
 
 template <typename T, typename W>
 __global__ void __launch_bounds__(kOddThreads) block_norm_odd_kernel(const BlockNormArgs p) {
@@ -730,21 +759,21 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_odd_kernel(const Block
   __syncthreads();
   pdl_wait();
   const int64_t row = blockIdx.x;
-  const T* u = static_cast<const T*>(p.u) + row * p.ldu;
-  const T* res = static_cast<const T*>(p.residual) + row * p.ldr;
-  const T* full = static_cast<const T*>(p.gate) + row * p.ldg;
-  const W *post_w = static_cast<const W*>(p.post_w), *pre_w = static_cast<const W*>(p.pre_w), *channel = static_cast<const W*>(p.gate);
-  const float inv = 1.f / (float)p.H;
-  float factor = 1.f;
-  if (p.u && p.post) {
+  const int H = p.H;
+  const T *u = row_of<T>(p.u, row, p.ldu), *res = row_of<T>(p.residual, row, p.ldr);
+  const T* full = p.gate_kind == kGateFull ? row_of<T>(p.gate, row, p.ldg) : nullptr;
+  const W *post_w = static_cast<const W*>(p.post_w), *pre_w = static_cast<const W*>(p.pre_w);
+  const W* channel = p.gate_kind == kGateChannel ? static_cast<const W*>(p.gate) : nullptr;
+  const float inv = 1.f / (float)H;
+  float factor = 1.f, x[kOddUnroll], y[kOddUnroll], w[kOddUnroll], g[kOddUnroll];
+  if (u && p.post) {
     float small = 1.f, s[1];
 #pragma unroll 1
     for (int again = 0;; ++again) {
       s[0] = 0.f;
-#pragma unroll kOddUnroll
-      for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
-        const float x = f32_of<T>(u[c]) * small;
-        s[0] = fmaf(x, x, s[0]);
+      DFM_ODD_ROW {
+        load_odd(x, u, c, H);
+        DFM_ODD s[0] = fmaf(x[i] * small, x[i] * small, s[0]);
       }
       sum(s, kOddThreads);
       if (again || s[0] < INFINITY) break;
@@ -754,34 +783,38 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_odd_kernel(const Block
   }
   if (p.gate_kind == kGateToken) factor *= static_cast<const float*>(p.gate)[row];
   float s[1] = {0.f}, small = 1.f;
-#pragma unroll kOddUnroll
-  for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
-    float h = 0.f;
-    if (p.u) {
-      h = f32_of<T>(u[c]) * factor;
-      if (post_w) h *= f32_of<W>(post_w[c]);
-      if (p.gate_kind == kGateChannel) h *= f32_of<W>(channel[c]);
-      if (p.gate_kind == kGateFull) h *= f32_of<T>(full[c]);
+  T* h = p.h ? static_cast<T*>(p.h) + row * p.ldh : nullptr;
+  DFM_ODD_ROW {
+    load_odd(x, u, c, H);
+    load_odd(y, res, c, H);
+    load_odd(w, post_w, c, H, 1.f);
+    load_odd(g, channel, c, H, 1.f);
+    if (full) load_odd(g, full, c, H);
+    DFM_ODD {
+      y[i] = fmaf(p.scale, y[i], u ? x[i] * factor * w[i] * g[i] : 0.f);
+      s[0] = fmaf(y[i], y[i], s[0]);
+      if (c + i * kOddThreads < H) kept[c + i * kOddThreads] = y[i];
     }
-    if (p.residual) h = p.u ? fmaf(p.scale, f32_of<T>(res[c]), h) : p.scale * f32_of<T>(res[c]);
-    if (p.h) (static_cast<T*>(p.h) + row * p.ldh)[c] = T(h);
-    kept[c] = h;
-    s[0] = fmaf(h, h, s[0]);
+    if (h) store_odd(h, y, c, H);
   }
   if (!p.n) return;
   sum(s, kOddThreads);
   if (!(s[0] < INFINITY)) {
     small = kSmall;
     s[0] = 0.f;
-    for (int c = threadIdx.x; c < p.H; c += kOddThreads) s[0] = fmaf(kept[c] * small, kept[c] * small, s[0]);
+    DFM_ODD_ROW {
+      load_odd(x, (const float*)kept, c, H);
+      DFM_ODD s[0] = fmaf(x[i] * small, x[i] * small, s[0]);
+    }
     sum(s, kOddThreads);
   }
   factor = rms_of(s[0], inv, p.eps, small) * small;
   T* n = static_cast<T*>(p.n) + row * p.ldn;
-#pragma unroll kOddUnroll
-  for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
-    const float h = kept[c] * factor;
-    n[c] = T(pre_w ? h * f32_of<W>(pre_w[c]) : h);
+  DFM_ODD_ROW {
+    load_odd(x, (const float*)kept, c, H);
+    load_odd(w, pre_w, c, H, 1.f);
+    DFM_ODD x[i] = x[i] * factor * w[i];
+    store_odd(n, x, c, H);
   }
 }
 
@@ -791,51 +824,50 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
   __shared__ __align__(16) float buf[2][8][16];
   RowSum<8, 16> sum{buf};
   sum.init();
-  const int64_t array = (int64_t)gridDim.x * p.H;
-  float* out_q = part + (int64_t)blockIdx.x * p.H;
-  float* out_v = out_q + (wants_dq(p) ? array : 0);
-  float *dq = in_shared ? kept : out_q, *dv = in_shared ? kept + p.H : out_v;
+  const int H = p.H;
   const bool want_q = wants_dq(p), want_v = p.dpre_w != nullptr;
+  float* out_q = part + (int64_t)blockIdx.x * H;
+  float* out_v = out_q + (want_q ? (int64_t)gridDim.x * H : 0);
+  float *dq = in_shared ? kept : out_q, *dv = in_shared ? kept + H : out_v;
   __syncthreads();
   pdl_wait();
-  for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
+  let_columns_start(p);
+  for (int c = threadIdx.x; c < H; c += kOddThreads) {
     if (want_q) dq[c] = 0.f;
     if (want_v) dv[c] = 0.f;
   }
-  const float inv = 1.f / (float)p.H;
-  const W *post_w = static_cast<const W*>(p.post_w), *pre_w = static_cast<const W*>(p.pre_w), *channel = static_cast<const W*>(p.gate);
-  const bool by_channel = p.gate_kind == kGateChannel, by_token = p.gate_kind == kGateToken, full = p.gate_kind == kGateFull;
+  const float inv = 1.f / (float)H;
+  const W *post_w = static_cast<const W*>(p.post_w), *pre_w = static_cast<const W*>(p.pre_w);
+  const W* channel = p.gate_kind == kGateChannel ? static_cast<const W*>(p.gate) : nullptr;
+  const bool by_token = p.gate_kind == kGateToken;
+  const void* gates = p.gate_kind == kGateFull ? p.gate : nullptr;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const T* dh = static_cast<const T*>(p.dh) + row * p.lddh;
-    const T* dn = static_cast<const T*>(p.dn) + row * p.lddn;
-    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
-    const T* u = static_cast<const T*>(p.u) + row * p.ldu;
-    const T* gate = static_cast<const T*>(p.gate) + row * p.ldg;
+    const T *dh = row_of<T>(p.dh, row, p.lddh), *dn = row_of<T>(p.dn, row, p.lddn), *u = row_of<T>(p.u, row, p.ldu);
+    const T *h = p.dn ? row_of<T>(p.h, row, p.ldh) : nullptr, *full = row_of<T>(gates, row, p.ldg);
     const float token = by_token ? static_cast<const float*>(p.gate)[row] : 1.f;
-    float sh = 1.f, su = 1.f, s[8];
+    float sh = 1.f, su = 1.f, s[8], a[kOddUnroll], b[kOddUnroll], x[kOddUnroll], y[kOddUnroll], q[kOddUnroll], g[kOddUnroll], v[kOddUnroll];
 #pragma unroll 1
     for (int again = 0;; ++again) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = 0.f;
-#pragma unroll kOddUnroll
-      for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
-        float y = 0.f, hs = 0.f;
-        if (p.dn) {
-          hs = f32_of<T>(h[c]) * sh;
-          y = f32_of<T>(dn[c]);
-          if (pre_w) y *= f32_of<W>(pre_w[c]);
-          s[0] = fmaf(hs, hs, s[0]);
-          s[2] = fmaf(hs, y, s[2]);
-        }
-        if (p.u) {
-          float x = f32_of<T>(u[c]) * su;
-          if (p.post) s[1] = fmaf(x, x, s[1]);
-          if (post_w) x *= f32_of<W>(post_w[c]);
-          if (by_channel) x *= f32_of<W>(channel[c]);
-          if (full) x *= f32_of<T>(gate[c]);
-          if (p.dh) s[3] = fmaf(x, f32_of<T>(dh[c]), s[3]);
-          s[4] = fmaf(x, y, s[4]);
-          s[5] = fmaf(x, hs, s[5]);
+      DFM_ODD_ROW {
+        load_odd(a, h, c, H);
+        load_odd(y, dn, c, H);
+        load_odd(x, u, c, H);
+        load_odd(b, dh, c, H);
+        load_odd(q, post_w, c, H, 1.f);
+        load_odd(v, pre_w, c, H, 1.f);
+        load_odd(g, channel, c, H, 1.f);
+        if (full) load_odd(g, full, c, H);
+        DFM_ODD {
+          a[i] *= sh, x[i] *= su, y[i] *= v[i];
+          s[0] = fmaf(a[i], a[i], s[0]);
+          if (p.post) s[1] = fmaf(x[i], x[i], s[1]);
+          s[2] = fmaf(a[i], y[i], s[2]);
+          x[i] *= q[i] * g[i];
+          s[3] = fmaf(x[i], b[i], s[3]);
+          s[4] = fmaf(x[i], y[i], s[4]);
+          s[5] = fmaf(x[i], a[i], s[5]);
         }
       }
       sum(s, kOddThreads);
@@ -845,28 +877,43 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
     }
     const RowFactors f = row_factors(s, sh, su, p.dn != nullptr, p.post != 0, token, inv, p.eps);
     if (by_token && p.dgate && threadIdx.x == 0) static_cast<float*>(p.dgate)[row] = f.dtoken;
-#pragma unroll kOddUnroll
-    for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
-      float G = p.dh ? f32_of<T>(dh[c]) : 0.f;
-      const float x = p.u ? f32_of<T>(u[c]) * f.ru : 0.f;
-      const float g = full ? f32_of<T>(gate[c]) : token;
-      if (p.dn) {
-        const float hat = f32_of<T>(h[c]) * f.rh, d = f32_of<T>(dn[c]);
-        if (want_v) dv[c] = fmaf(d, hat, dv[c]);
-        G = fmaf(f.rh, fmaf(-hat, f.along, pre_w ? d * f32_of<W>(pre_w[c]) : d), G);
+    T* dr = p.dresidual ? static_cast<T*>(p.dresidual) + row * p.lddr : nullptr;
+    T* du = p.du ? static_cast<T*>(p.du) + row * p.lddu : nullptr;
+    T* dg = gates && p.dgate ? static_cast<T*>(p.dgate) + row * p.lddg : nullptr;
+    DFM_ODD_ROW {
+      load_odd(a, h, c, H);
+      load_odd(y, dn, c, H);
+      load_odd(x, u, c, H);
+      load_odd(b, dh, c, H);
+      load_odd(q, post_w, c, H, 1.f);
+      load_odd(v, pre_w, c, H, 1.f);
+      load_odd(g, channel, c, H, 1.f);
+      DFM_ODD {
+        const int at = c + i * kOddThreads;
+        a[i] *= f.rh;
+        if (want_v && at < H) dv[at] = fmaf(y[i], a[i], dv[at]);
+        b[i] = fmaf(f.rh, fmaf(-a[i], f.along, y[i] * v[i]), b[i]);  // G
+        y[i] = p.scale * b[i];
       }
-      if (p.dresidual) (static_cast<T*>(p.dresidual) + row * p.lddr)[c] = T(p.scale * G);
-      if (!p.u) continue;
-      float q = post_w ? f32_of<W>(post_w[c]) : 1.f;
-      if (by_channel) q *= f32_of<W>(channel[c]);
-      if (full && p.dgate) (static_cast<T*>(p.dgate) + row * p.lddg)[c] = T(G * (x * q));
-      G *= g;
-      if (want_q) dq[c] = fmaf(G, x, dq[c]);
-      if (p.du) (static_cast<T*>(p.du) + row * p.lddu)[c] = T(p.post ? f.ru * fmaf(-x, f.mean, q * G) : q * G);
+      if (full) load_odd(v, full, c, H);  // (before the stores)
+      if (dr) store_odd(dr, y, c, H);
+      if (!u) continue;
+      DFM_ODD {
+        const int at = c + i * kOddThreads;
+        x[i] *= f.ru;
+        q[i] *= g[i];
+        y[i] = b[i] * (x[i] * q[i]);  // G a
+        b[i] *= full ? v[i] : token;
+        if (want_q && at < H) dq[at] = fmaf(b[i], x[i], dq[at]);
+        b[i] *= q[i];
+        if (p.post) b[i] = f.ru * fmaf(-x[i], f.mean, b[i]);
+      }
+      if (dg) store_odd(dg, y, c, H);
+      if (du) store_odd(du, b, c, H);
     }
   }
   if (!in_shared) return;
-  for (int c = threadIdx.x; c < p.H; c += kOddThreads) {
+  for (int c = threadIdx.x; c < H; c += kOddThreads) {
     if (want_q) out_q[c] = dq[c];
     if (want_v) out_v[c] = dv[c];
   }

@@ -469,6 +469,7 @@ DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, cons
     g.in = dtype;
     g.grad = grad_dtype;
     g.act = act;
+    g.follows = products;
     if ((rc = gemm_done("activation gradient", dfm::launch_act_grad(g, on.sms(), s)))) return rc;
   }
   dfm::GemmArgs a{};

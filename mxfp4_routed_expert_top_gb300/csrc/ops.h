@@ -119,6 +119,7 @@ struct ActGradArgs {
   void *dz, *dbias;  // dbias or null
   int64_t M, lddy, ldp, lddz;
   int N, in, grad, act;  // grad: type of dbias
+  bool follows;          // a product on dz comes next
 };
 const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s);
 
