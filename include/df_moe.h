@@ -637,6 +637,17 @@ DF_MOE_API int df_moe_balance_loss_grad(int device, const float* dloss, const vo
                                         const float* weights, const float* dweights, void* dlogits,
                                         int64_t lddl, void* stream);
 
+/* The same calls, with their arguments in order as 8-byte values (integers and
+ * addresses as int64, floats as doubles): for bindings that pay for every
+ * argument. An integer must fit the argument that it stands for. */
+#define DF_MOE_CALL_MATMUL 0
+#define DF_MOE_CALL_MATMUL_GRAD 1
+#define DF_MOE_CALL_BLOCK_NORM 2
+#define DF_MOE_CALL_BLOCK_NORM_GRAD 3
+#define DF_MOE_CALL_BALANCE_LOSS 4
+#define DF_MOE_CALL_BALANCE_LOSS_GRAD 5
+DF_MOE_API int df_moe_packed(int32_t call, const int64_t* args);
+
 #ifdef __cplusplus
 }
 #endif

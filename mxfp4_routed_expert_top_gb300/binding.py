@@ -7,6 +7,7 @@ There is no fallback: if the library is missing this module raises.
 """
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libdfmoe.so")
@@ -41,7 +42,7 @@ SYMBOLS = [
     "df_moe_unpermute_grad", "df_moe_fp8_quantize", "df_moe_fp8_matmul", "df_moe_test_fp8_give_up",
     "df_moe_matmul", "df_moe_matmul_grad", "df_moe_test_matmul_give_up", "df_moe_block_norm",
     "df_moe_block_norm_grad", "df_moe_block_norm_grad_workspace", "df_moe_balance_loss",
-    "df_moe_balance_loss_grad", "df_moe_balance_loss_workspace",
+    "df_moe_balance_loss_grad", "df_moe_balance_loss_workspace", "df_moe_packed",
 ]
 
 
@@ -129,25 +130,12 @@ def lib():
         L.df_moe_fp8_matmul.argtypes = [ci, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, i64, i64,
                                         i32, vp, i32, i64, vp, vp]
         L.df_moe_test_fp8_give_up.argtypes = [i32]
-        f32 = ctypes.c_float
-        L.df_moe_matmul.argtypes = [ci, vp, i64, vp, i64, i32, i64, i64, i64, vp, i32, vp, i64, vp, i64,
-                                    vp, i32, i64, vp, vp]
-        L.df_moe_matmul_grad.argtypes = [ci, vp, i64, vp, i64, vp, i64, i32, i64, i64, i64, i32, vp, i64,
-                                         vp, i64, vp, i64, vp, i64, vp, i32, vp, vp]
         L.df_moe_test_matmul_give_up.argtypes = [i32]
-        L.df_moe_block_norm.argtypes = [ci, vp, i64, i32, vp, i32, vp, i64, vp, i64, f32, vp, f32, i64, i64,
-                                        i32, i32, vp, i64, vp, i64, vp]
+        L.df_moe_packed.argtypes = [i32, ctypes.c_char_p]
         L.df_moe_block_norm_grad_workspace.argtypes = [i64, i64]
         L.df_moe_block_norm_grad_workspace.restype = sz
-        L.df_moe_block_norm_grad.argtypes = [ci, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, i64,
-                                             f32, vp, f32, i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, i64,
-                                             vp, vp, sz, vp]
         L.df_moe_balance_loss_workspace.argtypes = [i64, i32, i64]
         L.df_moe_balance_loss_workspace.restype = sz
-        L.df_moe_balance_loss.argtypes = [ci, vp, i32, i64, vp, i64, i32, i32, vp, i64, vp, i32, f32, f32,
-                                          vp, vp, vp, vp, vp, sz, vp, vp]
-        L.df_moe_balance_loss_grad.argtypes = [ci, vp, vp, i32, i64, vp, i64, i32, i32, vp, i64, vp, i32, f32,
-                                               f32, vp, vp, vp, vp, vp, i64, vp]
         for name in SYMBOLS:
             f = getattr(L, name)
             if f.restype is ctypes.c_int:  # default
@@ -569,6 +557,31 @@ def test_fp8_give_up(role):
 
 
 # ---- around the routed experts (no handle) -----------------------------------
+# These calls have twenty arguments and more, of which ctypes takes 0.1 us each:
+# they go as one block of 8-byte values (df_moe_packed). What a value cannot hold
+# does not pack.
+def _packer(call, layout):
+    pack = struct.Struct(layout).pack
+
+    def run(*args):
+        try:
+            block = pack(*args)
+        except struct.error:
+            raise DfMoeError(EINVAL, "an argument is not a number of 64 bits") from None
+        rc = _c.df_moe_packed(call, block)
+        if rc:
+            _failed(rc)
+    return run
+
+
+_matmul = _packer(0, "20q")
+_matmul_grad = _packer(1, "24q")
+_block_norm = _packer(2, "10qdqd9q")
+_block_norm_grad = _packer(3, "14qdqd15q")
+_balance_loss = _packer(4, "12q2d8q")
+_balance_loss_grad = _packer(5, "13q2d7q")
+
+
 def _choice(kinds, name, v):
     try:
         return kinds[v]
@@ -577,64 +590,47 @@ def _choice(kinds, name, v):
 
 
 def _some(*arrays):
-    """_place where arrays may be absent."""
+    """[device, address, ...] of arrays that may be absent (address 0)."""
     try:  # the first a tensor, the others tensors on its device or absent
         dev = arrays[0].get_device()
         if dev >= 0:
             out = [dev]
             for a in arrays:
                 if a is None:
-                    out.append(None)
+                    out.append(0)
                 elif a.get_device() == dev:
                     out.append(a.data_ptr())
                 else:
-                    return _place_any(arrays)
-            return out
+                    break
+            else:
+                return out
     except AttributeError:
         pass
-    return _place_any(arrays)
+    return [a or 0 for a in _place_any(arrays)]
 
 
-def _fits_64(sizes):
-    """Whether no size (all of them or-ed) is cut by a 64-bit argument; negative
-    ones are for the C call to refuse."""
-    return (sizes >> 63) in (0, -1)
-
-
-def _too_long():
-    raise DfMoeError(EINVAL, "a size does not fit 64 bits")
-
-
-def _workspace_bytes(n):
-    if n < 0:
-        raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    return n
+def _on(dev, stream):
+    """The stream of a call: `stream`, else torch's current one on the device."""
+    if stream is None and dev >= 0:
+        return _torch_stream(dev)
+    return _stream(stream) or 0
 
 
 def matmul(x, w, dtype, M, N, K, y, out_dtype, bias=None, act="none", residual=None, pre=None, ldx=0,
            ldw=0, ldy=0, ldr=0, ldp=0, status=None, stream=None):
     """y = residual + act(x w' + bias) of 16-bit matrices (df_moe_matmul)."""
-    if not _fits_64(M | N | K | ldx | ldw | ldy | ldr | ldp):
-        _too_long()
     dev, x, w, y, b, r, z, st = _some(x, w, y, bias, residual, pre, status)
-    rc = _c.df_moe_matmul(dev, x, ldx, w, ldw, _dtype(dtype), M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y,
-                          _dtype(out_dtype), ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    _matmul(dev, x, ldx, w, ldw, _dtype(dtype), M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y,
+            _dtype(out_dtype), ldy, st, _on(dev, stream))
 
 
 def matmul_grad(dy, x, w, dtype, M, N, K, dx=None, dw=None, dbias=None, grad_dtype="f32", act="none",
                 pre=None, dz=None, lddy=0, ldx=0, ldw=0, lddx=0, lddw=0, ldp=0, lddz=0, status=None,
                 stream=None):
     """Gradients of matmul's x, w and bias (df_moe_matmul_grad)."""
-    if not _fits_64(M | N | K | lddy | ldx | ldw | lddx | lddw | ldp | lddz):
-        _too_long()
     dev, dy, x, w, dx, dw, db, z, dz, st = _some(dy, x, w, dx, dw, dbias, pre, dz, status)
-    rc = _c.df_moe_matmul_grad(dev, dy, lddy, x, ldx, w, ldw, _dtype(dtype), M, N, K, _choice(_ACTS, "act", act), z,
-                               ldp, dz, lddz, dx, lddx, dw, lddw, db, _dtype(grad_dtype), st,
-                               _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    _matmul_grad(dev, dy, lddy, x, ldx, w, ldw, _dtype(dtype), M, N, K, _choice(_ACTS, "act", act), z, ldp, dz, lddz,
+                 dx, lddx, dw, lddw, db, _dtype(grad_dtype), st, _on(dev, stream))
 
 
 def test_matmul_give_up(role):
@@ -648,19 +644,14 @@ def block_norm(u, residual, dtype, T, H, h=None, n=None, post=False, post_weight
                gate_kind="none", residual_scale=1.0, pre_weight=None, weight_dtype="f32", eps=1e-6, ldu=0,
                ldr=0, ldg=0, ldh=0, ldn=0, stream=None):
     """h = residual_scale residual + gate norm(u), n = norm(h) (df_moe_block_norm)."""
-    if not _fits_64(T | H | ldu | ldr | ldg | ldh | ldn):
-        _too_long()
     dev, u, r, h, n, q, g, v = _some(u, residual, h, n, post_weight, gate, pre_weight)
-    rc = _c.df_moe_block_norm(dev, u, ldu, 1 if post else 0, q, _choice(_GATES, "gate_kind", gate_kind), g, ldg, r, ldr,
-                              residual_scale, v, eps, T, H, _dtype(dtype), _dtype(weight_dtype), h, ldh, n, ldn,
-                              _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    _block_norm(dev, u, ldu, 1 if post else 0, q, _choice(_GATES, "gate_kind", gate_kind), g, ldg, r, ldr,
+                residual_scale, v, eps, T, H, _dtype(dtype), _dtype(weight_dtype), h, ldh, n, ldn, _on(dev, stream))
 
 
 def block_norm_grad_workspace(T, H):
     """Bytes of workspace that block_norm_grad needs (df_moe_block_norm_grad_workspace)."""
-    if not _fits_64(T | H):
+    if (T | H) >> 63 not in (0, -1):
         return 0
     return _c.df_moe_block_norm_grad_workspace(T, H)
 
@@ -671,22 +662,18 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
                     workspace_bytes=0, lddh=0, lddn=0, ldu=0, ldh=0, ldg=0, lddu=0, lddr=0, lddg=0,
                     stream=None):
     """Gradients of block_norm (df_moe_block_norm_grad)."""
-    if not _fits_64(T | H | lddh | lddn | ldu | ldh | ldg | lddu | lddr | lddg | workspace_bytes):
-        _too_long()
     dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _some(
         dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
-    rc = _c.df_moe_block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q,
-                                   _choice(_GATES, "gate_kind", gate_kind), g, ldg, residual_scale, v, eps, T, H,
-                                   _dtype(dtype), _dtype(weight_dtype), du, lddu, dr, lddr, dq, dg, lddg, dv, ws,
-                                   _workspace_bytes(workspace_bytes),
-                                   _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    if workspace_bytes < 0:
+        raise DfMoeError(EINVAL, "workspace_bytes is negative")
+    _block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q,
+                     _choice(_GATES, "gate_kind", gate_kind), g, ldg, residual_scale, v, eps, T, H, _dtype(dtype),
+                     _dtype(weight_dtype), du, lddu, dr, lddr, dq, dg, lddg, dv, ws, workspace_bytes, _on(dev, stream))
 
 
 def balance_loss_workspace(T, E, S=1):
     """Bytes of workspace that balance_loss needs (df_moe_balance_loss_workspace)."""
-    if E > _INT32 or not _fits_64(T | S):
+    if E > _INT32 or (T | S) >> 63 not in (0, -1):
         return 0
     return _c.df_moe_balance_loss_workspace(T, E, S)
 
@@ -697,14 +684,11 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
     """The router's balance loss and every expert's count, a sequence (df_moe_balance_loss)."""
     if (E | k) > _INT32:
         _int32(E=E, k=k)
-    if not _fits_64(T | S | ldl | workspace_bytes):
-        _too_long()
+    if workspace_bytes < 0:
+        raise DfMoeError(EINVAL, "workspace_bytes is negative")
     dev, z, i, lo, c, t, ws, p, o, m, st = _some(logits, ids, loss, counts, tokens, workspace, probs, offs, mask, status)
-    rc = _c.df_moe_balance_loss(dev, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
-                                z_coef, lo, c, t, p, ws, _workspace_bytes(workspace_bytes), st,
-                                _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    _balance_loss(dev, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef, z_coef, lo,
+                  c, t, p, ws, workspace_bytes, st, _on(dev, stream))
 
 
 def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogits, offs=None, S=1,
@@ -713,11 +697,6 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
     """The gradient of the logits: the loss's and the routing weights' (df_moe_balance_loss_grad)."""
     if (E | k) > _INT32:
         _int32(E=E, k=k)
-    if not _fits_64(T | S | ldl | lddl):
-        _too_long()
     dev, g, z, i, c, t, d, o, m, w, dw = _some(dloss, logits, ids, counts, tokens, dlogits, offs, mask, weights, dweights)
-    rc = _c.df_moe_balance_loss_grad(dev, g, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score),
-                                     coef, z_coef, c, t, w, dw, d, lddl,
-                                     _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
-    if rc:
-        _failed(rc)
+    _balance_loss_grad(dev, g, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
+                       z_coef, c, t, w, dw, d, lddl, _on(dev, stream))

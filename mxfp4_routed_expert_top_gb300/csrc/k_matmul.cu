@@ -268,6 +268,62 @@ constexpr size_t gemm_smem_bytes() {
   return (size_t)GemmCfg<NT>::NS * (GemmCfg<NT>::CBytes + GemmCfg<NT>::RBytes) + sizeof(GemmSmem);
 }
 
+// The sums of SPLIT parts, [row][128] in shared memory of the cluster's CTAs:
+// four columns of a row a thread, 32 such items a warp and step, the CTAs in
+// turn.
+template <int SPLIT>
+__device__ __forceinline__ void split_epilogue(const GemmParams& p, const float* red, int part, int64_t r0, int rows, int c0, bool gated) {
+  constexpr int WARPS = GemmCfg<16>::NTHR / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quads = gated ? 16 : 32;
+  const int step = p.vec ? 1 : quads;
+  // the other CTAs' sums, by addresses that the compiler knows nothing of
+  // before the barrier (loads of asm that may be reordered among others)
+  uint32_t base[SPLIT];
+#pragma unroll
+  for (int q = 0; q < SPLIT; ++q)
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[q]) : "r"(smem_u32(red)), "r"(q) : "memory");
+  const auto sums = [&](float (&v)[4], int i) {
+    if constexpr (SPLIT == 1) {
+      if (p.vec) {
+        const float4 f = *reinterpret_cast<const float4*>(red + i);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = red[i + j * step];
+      }
+    } else {
+    float w[SPLIT][4];
+#pragma unroll
+    for (int q = 0; q < SPLIT; ++q) {
+      const uint32_t at = base[q] + 4 * i;
+      if (p.vec) {
+        asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[q][0]), "=f"(w[q][1]), "=f"(w[q][2]), "=f"(w[q][3]) : "r"(at));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(w[q][j]) : "r"(at + 4 * j * step));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = w[0][j];
+#pragma unroll
+      for (int q = 1; q < SPLIT; ++q) v[j] += w[q][j];
+    }
+    }
+  };
+#pragma unroll 2
+  for (int g = part * WARPS + warp; 32 * g < rows * quads; g += SPLIT * WARPS) {
+    const int item = 32 * g + lane, q = gated ? item >> 4 : item >> 5, l = item & (quads - 1);
+    if (q >= rows) continue;
+    const int c = p.vec ? 4 * l : l;
+    float z[4], up[4] = {0.f, 0.f, 0.f, 0.f};
+    sums(z, q * 128 + c);
+    if (gated) sums(up, q * 128 + 64 + c);
+    if (p.vec) gemm_finish<true, 4>(p, r0 + q, c0 + c, 1, z, up);
+    else gemm_finish<false, 4>(p, r0 + q, c0 + c, step, z, up);
+  }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(GemmCfg<NT>::NTHR, 2)
 gemm_split_kernel(const __grid_constant__ GemmParams p) {
@@ -381,13 +437,14 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
     if (!ok) sm->err = 1;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (ok) {
+      uint32_t v[2][16];
+      tmem_ld_rows(v[0], tmem + ((uint32_t)(32 * warp) << 16));
 #pragma unroll
       for (int i = 0; i < NT / 16; ++i) {
-        uint32_t v[16];
-        tmem_ld_rows(v, tmem + ((uint32_t)(32 * warp) << 16) + 16 * i);
-        tmem_wait(v);
+        tmem_wait(v[i & 1]);
+        if (i + 1 < NT / 16) tmem_ld_rows(v[(i + 1) & 1], tmem + ((uint32_t)(32 * warp) << 16) + 16 * (i + 1));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) red[(16 * i + j) * 128 + 32 * warp + lane] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) red[(16 * i + j) * 128 + 32 * warp + lane] = __uint_as_float(v[i & 1][j]);
       }
     }
   }
@@ -405,35 +462,13 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
-  // ---- epilogue: four columns of a row a thread, 32 such items a warp and
-  // step, the cluster's CTAs in turn
-  const int rows = (int)min((int64_t)NT, p.R - r0), quads = width / 4;
-  const uint32_t red0 = smem_u32(red);
-  const auto sums = [&](float (&v)[4], int i, int step) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = 0.f;
-    for (int q = 0; q < p.split; ++q) {
-      float w[4];
-      const uint32_t at = map_cta(red0 + 4 * i, q);
-      if (step == 1) {
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(at) : "memory");
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w[j]) : "r"(at + 4 * j * step) : "memory");
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += w[j];
-    }
-  };
-  for (int g = part * (G::NTHR / 32) + warp; 32 * g < rows * quads; g += p.split * (G::NTHR / 32)) {
-    const int item = 32 * g + lane, q = item / quads, l = item - q * quads;
-    if (q >= rows) continue;
-    const int step = p.vec ? 1 : quads, c = p.vec ? 4 * l : l;
-    float z[4], up[4] = {0.f, 0.f, 0.f, 0.f};
-    sums(z, q * 128 + c, step);
-    if (gated) sums(up, q * 128 + 64 + c, step);
-    if (p.vec) gemm_finish<true, 4>(p, r0 + q, c0 + c, 1, z, up);
-    else gemm_finish<false, 4>(p, r0 + q, c0 + c, step, z, up);
+  // ---- epilogue
+  const int rows = (int)min((int64_t)NT, p.R - r0);
+  switch (p.split) {
+    case 1: split_epilogue<1>(p, red, part, r0, rows, c0, gated); break;
+    case 2: split_epilogue<2>(p, red, part, r0, rows, c0, gated); break;
+    case 4: split_epilogue<4>(p, red, part, r0, rows, c0, gated); break;
+    default: split_epilogue<8>(p, red, part, r0, rows, c0, gated);
   }
   if (p.split > 1) {  // nobody leaves while its sums are read
     __syncwarp();
@@ -451,20 +486,26 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
 // the MMAs of the next. Gated: the first CTA's half of the columns' operand is
 // the gate's rows of w, the second's the up product's, so that a unit is 128
 // columns and both products of a column sit in the same tensor memory lane.
+// BN columns: 256, or 128 where those leave SMs without a unit.
+template <int BN>
 struct PairCfg {
-  static constexpr int NS = 6, EW = 8, NTHR = (EW + 4) * 32;
-  static constexpr int TileBytes = 128 * kMK * 2;  // an operand's part of a stage
-  static constexpr int Stage = 2 * TileBytes;
+  static constexpr int NS = BN == 256 ? 6 : 8, EW = 8, NTHR = (EW + 4) * 32;
+  static constexpr int RBytes = 128 * kMK * 2, CBytes = BN / 2 * kMK * 2;  // the operands' parts of a stage
+  static constexpr int Stage = RBytes + CBytes;
   static constexpr int Pitch = 17;  // of the rows of 16 that a warp turns
 };
+template <int BN>
 struct PairSmem {
-  float turn[PairCfg::EW][2][32 * PairCfg::Pitch];
-  uint64_t full[PairCfg::NS], empty[PairCfg::NS], acc_full[2], acc_empty[2];
+  using G = PairCfg<BN>;
+  float turn[G::EW][2][32 * G::Pitch];
+  uint64_t full[G::NS], empty[G::NS], acc_full[2], acc_empty[2];
   uint32_t tmem;
   int err;
 };
-constexpr size_t kPairBytes = (size_t)PairCfg::NS * PairCfg::Stage + sizeof(PairSmem);
-static_assert(kPairBytes <= 227 * 1024, "shared memory");
+template <int BN>
+constexpr size_t pair_bytes() {
+  return (size_t)PairCfg<BN>::NS * PairCfg<BN>::Stage + sizeof(PairSmem<BN>);
+}
 
 // What a unit is: units go down eight row tiles before the next column tile, so
 // that the pairs at work share their operands in L2.
@@ -522,13 +563,15 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
-  using G = PairCfg;
+template <int BN>
+__global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+  using G = PairCfg<BN>;
+  static_assert(pair_bytes<BN>() <= 227 * 1024, "shared memory");
   constexpr int NS = G::NS, EW = G::EW;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sr = smem;                       // rows' operand: the 128-row operand of each CTA
-  uint8_t* sc = smem + NS * G::TileBytes;  // columns' operand
-  PairSmem* sm = reinterpret_cast<PairSmem*>(smem + NS * G::Stage);
+  uint8_t* sc = smem + NS * G::RBytes;      // columns' operand
+  PairSmem<BN>* sm = reinterpret_cast<PairSmem<BN>*>(smem + NS * G::Stage);
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)uni(tid >> 5);
   const int rank = blockIdx.x & 1;
   if (tid == 32 * EW) {
@@ -549,7 +592,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
   }
   pdl_wait();  // the kernel before this one is complete; tensor memory only from here on
   if (warp == EW + 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(512u) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(2u * BN) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -558,7 +601,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sm->tmem);
   const bool gated = p.act == kActSwiglu;
-  const int width = gated ? 128 : 256;
+  const int width = gated ? BN / 2 : BN;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   // the test hook: a role of block 0 gives up, the pair's other waits are short
   const int gives_up = blockIdx.x == 0 ? p.give_up : kGemmNone;
@@ -575,11 +618,11 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
     int issued = 0;
     for (int u = first; u < p.units && ok; u += step) {
       const PairUnit un = pair_unit(u, p, width);
-      const int rr = (int)uni(un.r0 + 128 * rank), cc = (int)uni(un.c0 + (rank ? (gated ? p.C : 128) : 0));
+      const int rr = (int)uni(un.r0 + 128 * rank), cc = (int)uni(un.c0 + (rank ? (gated ? p.C : BN / 2) : 0));
       for (int kb = 0; kb < p.KB; ++kb) {
         ok = bar_wait(empty + 8 * s, phase, limit);
         if (!ok) break;
-        const uint32_t bar = lead_full + 8 * s, dr = sr0 + s * G::TileBytes, dc = sc0 + s * G::TileBytes;
+        const uint32_t bar = lead_full + 8 * s, dr = sr0 + s * G::RBytes, dc = sc0 + s * G::CBytes;
         if (rank == 0) expect_tx(full + 8 * s, 2 * G::Stage, leader);  // both CTAs' bytes
         const int k = kb * kMK;
         if (p.r_mn) {
@@ -590,7 +633,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
         }
         if (p.c_mn) {
           pair_load(dc, &p.c, cc, k, bar, leader);
-          pair_load(dc + 8192, &p.c, cc + 64, k, bar, leader);
+          if (BN == 256) pair_load(dc + 8192, &p.c, cc + 64, k, bar, leader);
         } else {
           pair_load(dc, &p.c, k, cc, bar, leader);
         }
@@ -614,7 +657,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
       const uint32_t leader = elect_one(), tm = uni(tmem);
       const uint32_t a0 = uni(desc_lo(smem_u32(sr), p.r_mn)), b0 = uni(desc_lo(smem_u32(sc), p.c_mn));
       const uint32_t as = uni(desc_step(p.r_mn)), bs = uni(desc_step(p.c_mn));
-      const uint32_t idesc = uni(gemm_idesc(p.in, 256, 256, p.r_mn, p.c_mn));
+      const uint32_t idesc = uni(gemm_idesc(p.in, 256, BN, p.r_mn, p.c_mn));
       const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
       const uint32_t acc_full = uni(smem_u32(sm->acc_full)), acc_empty = uni(smem_u32(sm->acc_empty));
       bool ok = gives_up != kGemmMmas;
@@ -629,7 +672,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
           ok = bar_wait(full + 8 * s, phase, limit);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          pair_stage(tm + 256 * acc, a0 + (uint32_t)(s * (G::TileBytes >> 4)), as, b0 + (uint32_t)(s * (G::TileBytes >> 4)), bs, idesc,
+          pair_stage(tm + BN * acc, a0 + (uint32_t)(s * (G::RBytes >> 4)), as, b0 + (uint32_t)(s * (G::CBytes >> 4)), bs, idesc,
                      kb > 0, leader);
           pair_commit(empty + 8 * s, leader);
           ++stages;
@@ -664,48 +707,56 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
       const PairUnit un = pair_unit(u, p, width);
       ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t ta = tmem + ((uint32_t)l0 << 16) + 256 * acc + cols * half;
+      const uint32_t ta = tmem + ((uint32_t)l0 << 16) + BN * acc + cols * half;
       const int64_t r0 = (int64_t)un.r0 + 128 * rank + l0;
       const int rows = (int)min((int64_t)32, p.R - r0), c0 = un.c0 + cols * half;
+      // 32 columns at a time: their loads run together
 #pragma unroll 1
-      for (int i = 0; i < cols; i += 16) {
-        uint32_t zr[16], ur[16];
-        float z[16], up[16];
+      for (int i = 0; i < cols; i += 32) {
+        uint32_t zr[2][16], ur[2][16];
         if (ok) {
-          tmem_ld_rows(zr, ta + i);
+          tmem_ld_rows(zr[0], ta + i);
+          tmem_ld_rows(zr[1], ta + i + 16);
           if (gated) {
-            tmem_ld_rows(ur, ta + 128 + i);
-            tmem_wait(ur);
+            tmem_ld_rows(ur[0], ta + BN / 2 + i);
+            tmem_ld_rows(ur[1], ta + BN / 2 + i + 16);
+            tmem_wait(ur[0]);
+            tmem_wait(ur[1]);
           }
-          tmem_wait(zr);
+          tmem_wait(zr[0]);
+          tmem_wait(zr[1]);
         }
-        if (i + 16 == cols && ok) {
+        if (i + 32 == cols && ok) {
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           arrive_cluster(acc_empty + 8 * acc, lane == 0);
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          z[j] = ok ? __uint_as_float(zr[j]) : __uint_as_float(0x7fffffffu);
-          up[j] = gated && ok ? __uint_as_float(ur[j]) : z[j];
-        }
-        const int c = c0 + i;
-        if (p.vec && c + 16 <= p.C) {
-          if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c, 1, z, up);
-          continue;
-        }
-        // any other rows: two rows of sixteen columns at a time
+        for (int h = 0; h < 2; ++h) {
+          float z[16], up[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          turn[lane * G::Pitch + j] = z[j];
-          if (gated) turn[(32 + lane) * G::Pitch + j] = up[j];
+          for (int j = 0; j < 16; ++j) {
+            z[j] = ok ? __uint_as_float(zr[h][j]) : __uint_as_float(0x7fffffffu);
+            up[j] = gated && ok ? __uint_as_float(ur[h][j]) : z[j];
+          }
+          const int c = c0 + i + 16 * h;
+          if (p.vec && c + 16 <= p.C) {
+            if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c, 1, z, up);
+            continue;
+          }
+          // any other rows: two rows of sixteen columns at a time
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            turn[lane * G::Pitch + j] = z[j];
+            if (gated) turn[(32 + lane) * G::Pitch + j] = up[j];
+          }
+          __syncwarp();
+          for (int r = lane >> 4; r < rows; r += 2) {
+            float a[1] = {turn[r * G::Pitch + (lane & 15)]}, b[1] = {gated ? turn[(32 + r) * G::Pitch + (lane & 15)] : 0.f};
+            gemm_finish<false, 1>(p, r0 + r, c + (lane & 15), 1, a, b);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        for (int r = lane >> 4; r < rows; r += 2) {
-          float a[1] = {turn[r * G::Pitch + (lane & 15)]}, b[1] = {gated ? turn[(32 + r) * G::Pitch + (lane & 15)] : 0.f};
-          gemm_finish<false, 1>(p, r0 + r, c + (lane & 15), 1, a, b);
-        }
-        __syncwarp();
       }
       if (!ok) sm->err = 1;
       acc ^= 1;
@@ -718,7 +769,7 @@ __global__ void __launch_bounds__(PairCfg::NTHR, 1) gemm_pair_kernel(const __gri
   cluster_barrier();  // neither leaves, or frees its tensor memory, before the other is done
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (tid == 0 && *(volatile int*)&sm->err && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
-  if (warp == EW + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  if (warp == EW + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * BN) : "memory");
 }
 
 // 16-bit rows, `ld` elements apart: a K-major operand has `rows` rows of k
@@ -829,6 +880,7 @@ const char* gemm_split(const GemmArgs& a, int sms, cudaStream_t s) {
 
 // Pairs of CTAs that the device runs at once (its SMs come in groups, some of
 // odd size), asked for once.
+template <int BN>
 int pairs_at_once(int sms) {
   static std::atomic<int> known[64];
   int device = 0;
@@ -837,8 +889,8 @@ int pairs_at_once(int sms) {
   if (n > 0) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
-  cfg.blockDim = dim3(PairCfg::NTHR);
-  cfg.dynamicSmemBytes = kPairBytes;
+  cfg.blockDim = dim3(PairCfg<BN>::NTHR);
+  cfg.dynamicSmemBytes = pair_bytes<BN>();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 2;
@@ -846,7 +898,7 @@ int pairs_at_once(int sms) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<BN>, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
     n = sms / 2 > 0 ? sms / 2 : 1;
   }
@@ -854,33 +906,37 @@ int pairs_at_once(int sms) {
   return n;
 }
 
+template <int BN>
 const char* gemm_pair(const GemmArgs& a, int sms, cudaStream_t s) {
   GemmParams p = params_of(a);
   const bool gated = a.act == kActSwiglu;
-  if (!map_16(&p.c, a.col, gated ? 2 * (int64_t)a.C : a.C, a.K, 128) || !map_16(&p.r, a.row, a.R, a.K, 128))
+  if (!map_16(&p.c, a.col, gated ? 2 * (int64_t)a.C : a.C, a.K, BN / 2) || !map_16(&p.r, a.row, a.R, a.K, 128))
     return "tensor map encoding failed";
-  const int64_t units_c = (a.C + (gated ? 127 : 255)) / (gated ? 128 : 256), units_r = (a.R + 255) / 256;
+  const int width = gated ? BN / 2 : BN;
+  const int64_t units_c = (a.C + width - 1) / width, units_r = (a.R + 255) / 256;
   if (units_c * units_r > 0x3fffffff) return "too many tiles";
   p.units_r = (int)units_r;
   p.units = (int)(units_c * units_r);
   p.vec = vec16(a);
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = configure((const void*)gemm_pair_kernel, kPairBytes, configured);
+  cudaError_t e = configure((const void*)gemm_pair_kernel<BN>, pair_bytes<BN>(), configured);
   if (e != cudaSuccess) return cudaGetErrorString(e);
-  const int pairs = pairs_at_once(sms);
-  e = launch_cluster(gemm_pair_kernel, 2 * (int64_t)(p.units < pairs ? p.units : pairs), PairCfg::NTHR, kPairBytes, 2, s, p);
+  const int pairs = pairs_at_once<BN>(sms);
+  e = launch_cluster(gemm_pair_kernel<BN>, 2 * (int64_t)(p.units < pairs ? p.units : pairs), PairCfg<BN>::NTHR, pair_bytes<BN>(), 2, s, p);
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
 
 // ---- gradient of the activation, and the bias's ---------------------------------
 // dz = act'(z) dy (gated: [dy u silu'(g) | dy silu(g)]) and its column sums.
-// A block has 64 columns and every parts-th 32 rows; the column sums of the
-// parts meet in the cluster's shared memory, in their order.
+// VEC: a thread has eight columns of a row, a block 64 columns and every
+// parts-th 32 rows; else a thread a column, a warp a row, a block 32 columns. A
+// few rows' loads go out together. The column sums of the parts meet in the
+// cluster's shared memory, in their order.
 struct ActGradParams {
   const void *dy, *pre;
   void *dz, *dbias;
   int64_t M, lddy, ldp, lddz;
-  int N, act, grad, vec, parts, follows;
+  int N, act, grad, parts, follows;
 };
 constexpr int kAgThreads = 256;
 
@@ -891,114 +947,101 @@ __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162floa
 template <>
 __device__ __forceinline__ float value(__half v) { return __half2float(v); }
 
-// Columns c, c + step, ...: n of eight; VEC: all eight side by side, 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(T (&v)[8], const T* p, int step, int n, bool vec) {
-  if (vec) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    memcpy(v, &w, 16);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < n ? p[j * step] : T(0.f);
-}
-template <typename T>
-__device__ __forceinline__ void store8(const float (&v)[8], T* p, int step, int n, bool vec) {
-  if (vec) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack16<T>(v[0], v[1]), pack16<T>(v[2], v[3]), pack16<T>(v[4], v[5]), pack16<T>(v[6], v[7]));
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) p[j * step] = T(v[j]);
-}
-
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParams p) {
-  __shared__ float sums[kAgThreads / 32][2][64];
-  __shared__ float total[2][64];
-  const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+  constexpr int E = VEC ? 8 : 1;               // columns a thread
+  constexpr int LANES = VEC ? 8 : 32;          // threads a row
+  constexpr int ROWS = kAgThreads / LANES;     // rows at a time
+  constexpr int COLS = E * LANES, U = VEC ? 2 : 8;  // columns a block, rows a thread loads together
+  __shared__ float sums[kAgThreads / 32][2][COLS];
+  __shared__ float total[2][COLS];
+  const int tid = threadIdx.x, tx = tid % LANES, ty = tid / LANES;
   const int strip = blockIdx.x / p.parts, part = blockIdx.x - strip * p.parts;
-  const int step = p.vec ? 1 : 8, c = 64 * strip + (p.vec ? 8 * tx : tx);
-  const int n = c >= p.N ? 0 : p.vec ? 8 : min(8, (p.N - c + 7) / 8);
-  const bool gated = p.act == kActSwiglu;
-  float s0[8], s1[8];
+  const int c = COLS * strip + E * tx;
+  const bool gated = p.act == kActSwiglu, some = p.act != kActNone;
+  float s0[E], s1[E];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.f;
+  for (int j = 0; j < E; ++j) s0[j] = s1[j] = 0.f;
   pdl_wait();
   // a product of the same call, which waits for the end of this; nothing else may start early
   if (p.follows) pdl_launch_dependents();
   const T* dy = static_cast<const T*>(p.dy) + c;
   const T* pre = static_cast<const T*>(p.pre) + c;
   T* dz = static_cast<T*>(p.dz) + c;
-  if (n > 0) {
-    for (int64_t r = 32 * (int64_t)part + ty; r < p.M; r += 32 * p.parts) {
-      T d[8], z[8], u[8];
-      load8(d, dy + r * p.lddy, step, n, p.vec);
-      if (p.act != kActNone) load8(z, pre + r * p.ldp, step, n, p.vec);
-      if (gated) load8(u, pre + r * p.ldp + p.N, step, n, p.vec);
-      float a[8], b[8];
+  struct alignas(2 * E) Part { T v[E]; };
+  const auto get = [](const T* q) { return *reinterpret_cast<const Part*>(q); };
+  if (c < p.N) {
+    for (int64_t r0 = (int64_t)ROWS * part + ty; r0 < p.M; r0 += (int64_t)U * ROWS * p.parts) {
+      Part d[U], z[U], u[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a[j] = value(d[j]);
-        if (gated) {
-          const float g = value(z[j]), sg = sigmoid_f(g);
-          b[j] = a[j] * (g * sg);
-          a[j] = a[j] * value(u[j]) * (sg * fmaf(g, 1.f - sg, 1.f));
-          s1[j] += b[j];
-        } else if (p.act != kActNone) {
-          a[j] *= act_slope(value(z[j]), p.act);
-        }
-        s0[j] += a[j];
+      for (int i = 0; i < U; ++i) {
+        const int64_t r = r0 + (int64_t)i * ROWS * p.parts;
+        if (r >= p.M) continue;
+        d[i] = get(dy + r * p.lddy);
+        if (some) z[i] = get(pre + r * p.ldp);
+        if (gated) u[i] = get(pre + r * p.ldp + p.N);
       }
-      if (p.act != kActNone) {
-        store8(a, dz + r * p.lddz, step, n, p.vec);
-        if (gated) store8(b, dz + r * p.lddz + p.N, step, n, p.vec);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t r = r0 + (int64_t)i * ROWS * p.parts;
+        if (r >= p.M) continue;
+        Part a, b;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          float x = value(d[i].v[j]);
+          if (gated) {
+            const float g = value(z[i].v[j]), sg = sigmoid_f(g), y = x * (g * sg);
+            x = x * value(u[i].v[j]) * (sg * fmaf(g, 1.f - sg, 1.f));
+            s1[j] += y;
+            b.v[j] = T(y);
+          } else if (some) {
+            x *= act_slope(value(z[i].v[j]), p.act);
+          }
+          s0[j] += x;
+          a.v[j] = T(x);
+        }
+        if (some) *reinterpret_cast<Part*>(dz + r * p.lddz) = a;
+        if (gated) *reinterpret_cast<Part*>(dz + r * p.lddz + p.N) = b;
       }
     }
   }
   if (!p.dbias) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < E; ++j) {
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
+    for (int o = LANES; o < 32; o <<= 1) {
       s0[j] += __shfl_xor_sync(0xffffffffu, s0[j], o);
       s1[j] += __shfl_xor_sync(0xffffffffu, s1[j], o);
     }
-    if ((tid & 31) < 8) {
-      const int at = p.vec ? 8 * tx + j : tx + 8 * j;
-      sums[tid >> 5][0][at] = s0[j];
-      sums[tid >> 5][1][at] = s1[j];
+    if ((tid & 31) < LANES) {
+      sums[tid >> 5][0][E * tx + j] = s0[j];
+      sums[tid >> 5][1][E * tx + j] = s1[j];
     }
   }
   __syncthreads();
-  if (tid < 128) {
+  if (tid < 2 * COLS) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAgThreads / 32; ++w) s += sums[w][tid >> 6][tid & 63];
-    total[tid >> 6][tid & 63] = s;
+    for (int w = 0; w < kAgThreads / 32; ++w) s += sums[w][tid / COLS][tid % COLS];
+    total[tid / COLS][tid % COLS] = s;
   }
   __syncthreads();
-  if (p.parts > 1) {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
-  const int col = 64 * strip + (tid & 63);
-  if (part == 0 && tid < (gated ? 128 : 64) && col < p.N) {
+  if (p.parts > 1) cluster_barrier();
+  const int col = COLS * strip + tid % COLS;
+  if (part == 0 && tid < (gated ? 2 * COLS : COLS) && col < p.N) {
     float s = 0.f;
     for (int q = 0; q < p.parts; ++q) {
       float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_cta(smem_u32(&total[tid >> 6][tid & 63]), q)) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_cta(smem_u32(&total[tid / COLS][tid % COLS]), q)) : "memory");
       s += v;
     }
-    const int at = (tid >> 6) * p.N + col;
+    const int at = tid / COLS * p.N + col;
     if (p.grad == 2) static_cast<float*>(p.dbias)[at] = s;
     else static_cast<T*>(p.dbias)[at] = T(s);
   }
   if (p.parts > 1) {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
   }
 }
 
@@ -1006,7 +1049,7 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
 
 const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
   const int64_t wide = a.act == kActSwiglu ? 2 * (int64_t)a.C : a.C;
-  if (a.R > 1024 && wide > 1024) return gemm_pair(a, sms, s);
+  if (a.R > 1024 && wide > 1024) return gemm_pair<256>(a, sms, s);
   // boxes of an MN-major operand are 64 wide
   if (a.R <= 16 && !a.row.mn) return gemm_split<16>(a, sms, s);
   if (a.R <= 32 && !a.row.mn) return gemm_split<32>(a, sms, s);
@@ -1029,14 +1072,16 @@ const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s) {
   p.grad = a.grad;
   p.follows = a.follows;
   const bool some = a.act != kActNone;
-  p.vec = a.N % 8 == 0 && aligned(a.dy, a.lddy, 16, 2) && (!some || (aligned(a.pre, a.ldp, 16, 2) && aligned(a.dz, a.lddz, 16, 2)));
-  const int64_t strips = (a.N + 63) / 64, most = a.dbias ? 8 : 1 << 20;
+  const bool vec = a.N % 8 == 0 && aligned(a.dy, a.lddy, 16, 2) && (!some || (aligned(a.pre, a.ldp, 16, 2) && aligned(a.dz, a.lddz, 16, 2)));
+  const int cols = vec ? 64 : 32, rows = 64;  // columns of a block, rows that it loads at once
+  const int64_t strips = (a.N + cols - 1) / cols, most = a.dbias ? 8 : 1 << 20;
   int64_t parts = 1;
-  while (2 * parts <= most && 64 * parts < a.M && strips * parts < 8 * sms) parts *= 2;
+  while (2 * parts <= most && rows * parts < a.M && strips * parts < 8 * sms) parts *= 2;
   p.parts = (int)parts;
   const int cluster = a.dbias ? p.parts : 1;
-  const cudaError_t e = a.in == 0 ? launch_cluster(act_grad_kernel<__nv_bfloat16>, strips * parts, kAgThreads, 0, cluster, s, p)
-                                  : launch_cluster(act_grad_kernel<__half>, strips * parts, kAgThreads, 0, cluster, s, p);
+  const auto launch = [&](auto kernel) { return launch_cluster(kernel, strips * parts, kAgThreads, 0, cluster, s, p); };
+  const cudaError_t e = a.in == 0 ? (vec ? launch(act_grad_kernel<__nv_bfloat16, true>) : launch(act_grad_kernel<__nv_bfloat16, false>))
+                                  : (vec ? launch(act_grad_kernel<__half, true>) : launch(act_grad_kernel<__half, false>));
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
 

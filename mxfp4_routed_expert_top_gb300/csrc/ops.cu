@@ -6,6 +6,9 @@
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
+#include <type_traits>
+#include <utility>
 
 #include "df_moe.h"
 #include "internal.h"
@@ -165,6 +168,30 @@ int check_rows(const char* name, const void* p, int64_t* ld, int64_t n, int size
   if (*ld < n) return fail(DF_MOE_EINVAL, "ld of %s is below the row's length", name);
   if (off(p, size)) return fail(DF_MOE_EINVAL, "%s is not aligned to its elements", name);
   return DF_MOE_OK;
+}
+
+// A call's arguments as 8-byte values, in order: a float as a double.
+template <typename A>
+A packed(const int64_t& v) {
+  if constexpr (std::is_pointer<A>::value) {
+    return reinterpret_cast<A>(static_cast<uintptr_t>(v));
+  } else if constexpr (std::is_same<A, float>::value) {
+    double d;
+    memcpy(&d, &v, sizeof d);
+    return (float)d;
+  } else {
+    return static_cast<A>(v);
+  }
+}
+template <typename... A, size_t... I>
+int call_packed(int (*f)(A...), const int64_t* args, std::index_sequence<I...>) {
+  int64_t v[sizeof...(A)];
+  memcpy(v, args, sizeof v);
+  return f(packed<A>(v[I])...);
+}
+template <typename... A>
+int call_packed(int (*f)(A...), const int64_t* args) {
+  return call_packed(f, args, std::index_sequence_for<A...>());
 }
 
 int check_balance(int dtype, int64_t T, int64_t E, int k, const int32_t* offs, int64_t S, int score, float coef, float z_coef) {
@@ -735,6 +762,18 @@ DF_MOE_API int df_moe_balance_loss_grad(int device, const float* dloss, const vo
   a.coef = coef;
   a.z_coef = z_coef;
   return launched("balance loss gradient launch", dfm::launch_balance_loss_grad(a, dtype, on.sms(), (cudaStream_t)stream));
+}
+
+DF_MOE_API int df_moe_packed(int32_t call, const int64_t* args) {
+  switch (call) {
+    case DF_MOE_CALL_MATMUL: return call_packed(df_moe_matmul, args);
+    case DF_MOE_CALL_MATMUL_GRAD: return call_packed(df_moe_matmul_grad, args);
+    case DF_MOE_CALL_BLOCK_NORM: return call_packed(df_moe_block_norm, args);
+    case DF_MOE_CALL_BLOCK_NORM_GRAD: return call_packed(df_moe_block_norm_grad, args);
+    case DF_MOE_CALL_BALANCE_LOSS: return call_packed(df_moe_balance_loss, args);
+    case DF_MOE_CALL_BALANCE_LOSS_GRAD: return call_packed(df_moe_balance_loss_grad, args);
+  }
+  return fail(DF_MOE_EINVAL, "unknown call %d", call);
 }
 
 }  // extern "C"

@@ -195,9 +195,11 @@ class OnDevice0:
 
 @pytest.mark.parametrize("name, kw", EVERY_CALL)
 def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name, kw):
+    """The stream is the last of the values that a call packs."""
+    import struct
     import torch
     binding, seen = dfm.binding, []
-    monkeypatch.setattr(binding._c, "df_moe_" + name, lambda *a: seen.append(a[-1]) or 0)
+    monkeypatch.setattr(binding._c, "df_moe_packed", lambda call, args: seen.append(struct.unpack("q", args[-8:])[0]) or 0)
     monkeypatch.setattr(binding, "_torch_stream", binding._find_torch_stream)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000 + dev)
     call = getattr(dfm, name)
@@ -205,4 +207,38 @@ def test_a_call_without_a_stream_runs_on_the_current_one(dfm, monkeypatch, name,
     call(**tensors)
     call(**kw)
     call(**dict(tensors, stream=0x77))
-    assert seen == [0x5000, None, 0x77]
+    assert seen == [0x5000, 0, 0x77]
+
+
+def test_packed_calls_are_the_calls(dfm):
+    """Every argument in its place: both ways give the same code and message."""
+    import ctypes
+    import struct
+    L = dfm.lib()
+    vp, i32, i64, f32, ci = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_int
+    kinds = {  # as the header has them
+        "matmul": [ci, vp, i64, vp, i64, i32, i64, i64, i64, vp, i32, vp, i64, vp, i64, vp, i32, i64, vp, vp],
+        "matmul_grad": [ci, vp, i64, vp, i64, vp, i64, i32, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i32, vp, vp],
+        "block_norm": [ci, vp, i64, i32, vp, i32, vp, i64, vp, i64, f32, vp, f32, i64, i64, i32, i32, vp, i64, vp, i64, vp],
+        "block_norm_grad": [ci, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, i64, f32, vp, f32, i64, i64, i32, i32, vp, i64,
+                            vp, i64, vp, vp, i64, vp, vp, ctypes.c_size_t, vp],
+        "balance_loss": [ci, vp, i32, i64, vp, i64, i32, i32, vp, i64, vp, i32, f32, f32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp],
+        "balance_loss_grad": [ci, vp, vp, i32, i64, vp, i64, i32, i32, vp, i64, vp, i32, f32, f32, vp, vp, vp, vp, vp, i64, vp],
+    }
+    values = {vp: (0, A, A + 1), i64: (0, 8, 64, -1, 1 << 40), i32: (0, 1, 2, 9), f32: (0.0, 1.0, 1e-6, float("nan")), ci: (0,),
+              ctypes.c_size_t: (0, 1 << 30)}
+    import random
+    rng = random.Random(0)
+    for call, (name, types) in enumerate(kinds.items()):
+        f = getattr(L, "df_moe_" + name)
+        f.argtypes = types
+        for _ in range(3000):
+            args = [rng.choice(values[t]) for t in types]
+            args[0] = 1 << 20  # no such device: nothing is launched
+            block = b"".join(struct.pack("d" if t is f32 else "q", v) for t, v in zip(types, args))
+            want = f(*args)
+            message = L.df_moe_last_error(None)
+            assert L.df_moe_packed(call, block) == want
+            if want:
+                assert L.df_moe_last_error(None) == message
+    assert L.df_moe_packed(6, b"") == -1 and L.df_moe_packed(-1, b"") == -1
