@@ -39,6 +39,18 @@ __device__ __forceinline__ uint32_t pack_bits(float lo, float hi, int type) {
   return type == 0 ? pack16<__nv_bfloat16>(lo, hi) : pack16<__half>(lo, hi);
 }
 
+template <typename Y>
+__device__ __forceinline__ Y from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
 // Columns i, i + step, ... of a row: n of V. VEC: all V, side by side and
 // aligned to them (32 bytes at most).
 template <bool VEC, int V>
@@ -154,7 +166,8 @@ struct GemmParams {
   int C, KB;             // output columns (of y), stages of k
   int in, out;           // types of the operands, bias and pre; of y and residual
   int act, c_mn, r_mn;   // the activation; operands that are MN-major
-  int units_r, units, split, vec;
+  int units_r, units, split;
+  int vec;               // the arrays are aligned to what a thread writes
   int give_up;           // test hook: the role of block 0 that gives up before its first wait
 };
 enum GemmRole { kGemmNone = 0, kGemmCopies, kGemmMmas, kGemmSums };
@@ -196,6 +209,28 @@ __device__ __forceinline__ void gemm_stage(uint32_t d, uint32_t ad, uint32_t as,
       : "memory");
 }
 
+template <int V>
+__device__ __forceinline__ void act_all(float (&z)[V], const float (&up)[V], int act) {
+  switch (act) {
+    case kActNone: break;
+    case kActRelu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActRelu);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActGelu);
+      break;
+    default:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
+  }
+}
+
 // Columns c, c + step, ... (V of them) of output row `row`: z (and, gated, up)
 // come without the bias.
 template <bool VEC, int V>
@@ -218,24 +253,7 @@ __device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, in
     store_columns<VEC>(z, p.pre, row * p.ldp + c, step, n, p.in);
     if (gated) store_columns<VEC>(up, p.pre, row * p.ldp + p.C + c, step, n, p.in);
   }
-  switch (p.act) {
-    case kActNone: break;
-    case kActRelu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActRelu);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActGelu);
-      break;
-    default:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
-  }
+  act_all(z, up, p.act);
   if (p.residual) {
     load_columns<VEC>(v, p.residual, row * p.ldr + c, step, n, p.out);
 #pragma unroll
@@ -252,7 +270,7 @@ __device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, in
 // columns because with few rows it is the weights, which stream.
 template <int NT>
 struct GemmCfg {
-  static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;  // stages
+  static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;  // stages
   static constexpr int CBytes = 128 * kMK * 2, RBytes = NT * kMK * 2;
   static constexpr uint32_t Cols = NT < 32 ? 32 : NT;
   static constexpr int NTHR = 256;
@@ -492,12 +510,11 @@ struct PairCfg {
   static constexpr int NS = BN == 256 ? 6 : 8, EW = 8, NTHR = (EW + 4) * 32;
   static constexpr int RBytes = 128 * kMK * 2, CBytes = BN / 2 * kMK * 2;  // the operands' parts of a stage
   static constexpr int Stage = RBytes + CBytes;
-  static constexpr int Pitch = 17;  // of the rows of 16 that a warp turns
 };
 template <int BN>
 struct PairSmem {
   using G = PairCfg<BN>;
-  float turn[G::EW][2][32 * G::Pitch];
+  float turn[G::EW][32 * 33];  // what a warp turns
   uint64_t full[G::NS], empty[G::NS], acc_full[2], acc_empty[2];
   uint32_t tmem;
   int err;
@@ -561,6 +578,69 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar, uint32_t leader) {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 32 rows x 32 columns of a warp, a row a lane, to rows of global memory that
+// nothing is known of: turned in shared memory ([32][33]), so that a store
+// covers a piece of one row. `rows`, `cols`: those there are.
+template <typename Y>
+__device__ __forceinline__ void put_rows(float* turn, const float (&v)[32], Y* to, int64_t ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) turn[33 * lane + j] = v[j];
+  __syncwarp();
+  if (lane < cols) {
+    to += lane;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, to += ld) *to = from_f32<Y>(turn[33 * r + lane]);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void put_rows(float* turn, const float (&v)[32], void* to, int64_t at, int64_t ld, int rows, int cols, int type) {
+  if (type == 0) put_rows(turn, v, static_cast<__nv_bfloat16*>(to) + at, ld, rows, cols);
+  else if (type == 1) put_rows(turn, v, static_cast<__half*>(to) + at, ld, rows, cols);
+  else put_rows(turn, v, static_cast<float*>(to) + at, ld, rows, cols);
+}
+// The other way: v += the rows' values.
+template <typename Y>
+__device__ __forceinline__ void add_rows(float* turn, float (&v)[32], const Y* from, int64_t ld, int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  if (lane < cols) {
+    from += lane;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, from += ld) turn[33 * r + lane] = to_f32(*from);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] += turn[33 * lane + j];
+  __syncwarp();
+}
+__device__ __forceinline__ void add_rows(float* turn, float (&v)[32], const void* from, int64_t at, int64_t ld, int rows, int cols, int type) {
+  if (type == 0) add_rows(turn, v, static_cast<const __nv_bfloat16*>(from) + at, ld, rows, cols);
+  else if (type == 1) add_rows(turn, v, static_cast<const __half*>(from) + at, ld, rows, cols);
+  else add_rows(turn, v, static_cast<const float*>(from) + at, ld, rows, cols);
+}
+__device__ __forceinline__ void add_bias(float (&v)[32], const void* bias, int c, int cols, int type) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < cols) v[j] += half_bits(static_cast<const uint16_t*>(bias)[c + j], type);
+}
+// gemm_finish of such a piece: z (and, gated, up) come without the bias.
+__device__ __forceinline__ void finish_rows(const GemmParams& p, float* turn, int64_t r0, int rows, int c, float (&z)[32], float (&up)[32]) {
+  const int cols = min(32, p.C - c);
+  if (rows <= 0 || cols <= 0) return;
+  const bool gated = p.act == kActSwiglu;
+  if (p.bias) {
+    add_bias(z, p.bias, c, cols, p.in);
+    if (gated) add_bias(up, p.bias, p.C + c, cols, p.in);
+  }
+  if (p.pre) {
+    put_rows(turn, z, p.pre, r0 * p.ldp + c, p.ldp, rows, cols, p.in);
+    if (gated) put_rows(turn, up, p.pre, r0 * p.ldp + p.C + c, p.ldp, rows, cols, p.in);
+  }
+  act_all(z, up, p.act);
+  if (p.residual) add_rows(turn, z, p.residual, r0 * p.ldr + c, p.ldr, rows, cols, p.out);
+  put_rows(turn, z, p.y, r0 * p.ldy + c, p.ldy, rows, cols, p.out);
 }
 
 template <int BN>
@@ -700,7 +780,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
     // ends every later one of its warp and leaves NaN in what it still writes.
     const int l0 = 32 * (warp & 3), half = warp >> 2, cols = width / 2;
     const uint32_t acc_full = smem_u32(sm->acc_full), acc_empty = uni(map_cta(smem_u32(sm->acc_empty), 0));
-    float* turn = sm->turn[warp][0];
+    float* turn = sm->turn[warp];
     bool ok = gives_up != kGemmSums;
     uint32_t acc = 0, acc_phase = 0;
     for (int u = first; u < p.units; u += step) {
@@ -713,7 +793,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
       // 32 columns at a time: their loads run together
 #pragma unroll 1
       for (int i = 0; i < cols; i += 32) {
-        uint32_t zr[2][16], ur[2][16];
+        uint32_t zr[2][16], ur[2][16] = {};
         if (ok) {
           tmem_ld_rows(zr[0], ta + i);
           tmem_ld_rows(zr[1], ta + i + 16);
@@ -731,31 +811,24 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
           __syncwarp();
           arrive_cluster(acc_empty + 8 * acc, lane == 0);
         }
+        const int c = c0 + i;
+        if (!ok) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float z[16], up[16];
+          for (int j = 0; j < 16; ++j) zr[0][j] = zr[1][j] = ur[0][j] = ur[1][j] = 0x7fffffffu;
+        }
+        if (p.vec && c + 32 <= p.C) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            z[j] = ok ? __uint_as_float(zr[h][j]) : __uint_as_float(0x7fffffffu);
-            up[j] = gated && ok ? __uint_as_float(ur[h][j]) : z[j];
-          }
-          const int c = c0 + i + 16 * h;
-          if (p.vec && c + 16 <= p.C) {
-            if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c, 1, z, up);
-            continue;
-          }
-          // any other rows: two rows of sixteen columns at a time
+          for (int h = 0; h < 2; ++h) {
+            float z[16], up[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            turn[lane * G::Pitch + j] = z[j];
-            if (gated) turn[(32 + lane) * G::Pitch + j] = up[j];
+            for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(zr[h][j]), up[j] = __uint_as_float(ur[h][j]);
+            if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c + 16 * h, 1, z, up);
           }
-          __syncwarp();
-          for (int r = lane >> 4; r < rows; r += 2) {
-            float a[1] = {turn[r * G::Pitch + (lane & 15)]}, b[1] = {gated ? turn[(32 + r) * G::Pitch + (lane & 15)] : 0.f};
-            gemm_finish<false, 1>(p, r0 + r, c + (lane & 15), 1, a, b);
-          }
-          __syncwarp();
+        } else {
+          float z[32], up[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(zr[j >> 4][j & 15]), up[j] = __uint_as_float(ur[j >> 4][j & 15]);
+          finish_rows(p, turn, r0, rows, c, z, up);
         }
       }
       if (!ok) sm->err = 1;
@@ -858,20 +931,32 @@ GemmParams params_of(const GemmArgs& a) {
   return p;
 }
 
+// Tiles of 128 columns (gated: 64) x NT rows.
+int64_t split_units(const GemmArgs& a, int NT) {
+  const int width = a.act == kActSwiglu ? 64 : 128;
+  return ((a.C + width - 1) / width) * ((a.R + NT - 1) / NT);
+}
+// In how many parts of k: as many as leave every one two blocks an SM to run on
+// and two stages.
+int split_of(const GemmArgs& a, int NT, int sms) {
+  const int64_t units = split_units(a, NT), KB = (a.K + kMK - 1) / kMK;
+  int split = 1;
+  while (split < 8 && 2 * split * units <= 2 * sms && 4 * split <= KB) split *= 2;
+  return split;
+}
+
 template <int NT>
-const char* gemm_split(const GemmArgs& a, int sms, cudaStream_t s) {
+const char* gemm_split(const GemmArgs& a, int split, cudaStream_t s) {
   using G = GemmCfg<NT>;
   static_assert(2 * (gemm_smem_bytes<NT>() + 1024) <= 228 * 1024, "two blocks an SM");
   GemmParams p = params_of(a);
   const bool gated = a.act == kActSwiglu;
   if (!map_16(&p.c, a.col, gated ? 2 * (int64_t)a.C : a.C, a.K, 64) || !map_16(&p.r, a.row, a.R, a.K, NT))
     return "tensor map encoding failed";
-  const int64_t units_c = (a.C + (gated ? 63 : 127)) / (gated ? 64 : 128), units_r = (a.R + NT - 1) / NT;
-  const int64_t units = units_c * units_r;
+  const int64_t units = split_units(a, NT);
   if (units > 0x3fffffff) return "too many tiles";
-  p.units_r = (int)units_r;
-  p.split = 1;
-  while (p.split < 8 && 2 * p.split * units <= 2 * sms && 2 * p.split <= p.KB) p.split *= 2;
+  p.units_r = (int)((a.R + NT - 1) / NT);
+  p.split = split;
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = configure((const void*)gemm_split_kernel<NT>, gemm_smem_bytes<NT>(), configured);
   if (e == cudaSuccess) e = launch_cluster(gemm_split_kernel<NT>, units * p.split, G::NTHR, gemm_smem_bytes<NT>(), p.split, s, p);
@@ -1047,14 +1132,40 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
 
 }  // namespace
 
+// Which form: up to 64 rows (of a K-major operand) the weights stream past
+// tiles of 16 or 32 rows. Above, the one that these times, in us and fitted to
+// measurements with 152 SMs, say is the fastest: a start and an end, and so
+// much a step of 64 of k, times the rounds that the tiles take. Measured (bf16,
+// inputs not in L2; tiles of 64 rows in parts of k | pairs of 128 | of 256
+// columns): 1024 x 1024 x 1024 9.3 | 9.2 | 12.3; 256 x 2048 x 7168 15.6 | 23.5 |
+// 38; 256 x 7168 x 2048 15.9 | 13.2 | 17.4; 1024 x 2048 x 7168 36.7 | 24.9 |
+// 38.0; 512 x 7168 x 7168 66 | 43.8 | 39.5; 4096 x 7168 x 1536 128 | 58.0 | 51.1.
+// Tiles of 32 rows for 64: 64 x 2048 x 7168 10.9 (one tile of 64 12.1), 64 x 7168
+// x 2048 10.6 (11.1).
 const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
-  const int64_t wide = a.act == kActSwiglu ? 2 * (int64_t)a.C : a.C;
-  if (a.R > 1024 && wide > 1024) return gemm_pair<256>(a, sms, s);
   // boxes of an MN-major operand are 64 wide
-  if (a.R <= 16 && !a.row.mn) return gemm_split<16>(a, sms, s);
-  if (a.R <= 32 && !a.row.mn) return gemm_split<32>(a, sms, s);
-  if (a.R <= 64) return gemm_split<64>(a, sms, s);
-  return gemm_split<128>(a, sms, s);
+  if (a.R <= 16 && !a.row.mn) return gemm_split<16>(a, split_of(a, 16, sms), s);
+  if (a.R <= 64 && !a.row.mn) return gemm_split<32>(a, split_of(a, 32, sms), s);
+  const double KB = (double)((a.K + kMK - 1) / kMK);
+  const auto rounds = [](double units, double slots) { return units <= slots ? 1. : (double)(int64_t)((units + slots - 1) / slots); };
+  // a pair's epilogue runs under the next unit's products, where those are long
+  // enough; one that turns its rows in shared memory takes the products' bandwidth
+  // there, and adds to them (3000 x 3001 x 3000 63 us by 128 columns, 48 by 256)
+  const bool whole = vec16(a);
+  const auto pair_time = [&](int bn, double step, double epilogue) {
+    const int width = a.act == kActSwiglu ? bn / 2 : bn;
+    const double units = (double)((a.C + width - 1) / width) * (double)((a.R + 255) / 256);
+    const double both = KB * step + epilogue, one = KB * step > epilogue ? KB * step : epilogue;
+    return 4.6 + (rounds(units, sms / 2) - 1) * (whole ? one : both) + both;
+  };
+  const int split = split_of(a, 64, sms);
+  const double blocks = (double)split_units(a, 64) * split;
+  double part_log = 0;
+  for (int q = split; q > 1; q /= 2) ++part_log;
+  const double by_64 = 4.2 + 0.5 * part_log + rounds(blocks, 2 * sms) * (2.6 + (KB + split - 1) / split * (blocks > sms ? 0.27 : 0.2));
+  const double by_128 = pair_time(128, 0.155, whole ? 2.2 : 4.5), by_256 = pair_time(256, 0.29, whole ? 3.4 : 5.4);
+  if (by_64 <= by_128 && by_64 <= by_256) return gemm_split<64>(a, split, s);
+  return by_128 < by_256 ? gemm_pair<128>(a, sms, s) : gemm_pair<256>(a, sms, s);
 }
 
 const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s) {
