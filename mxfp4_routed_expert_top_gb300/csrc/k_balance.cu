@@ -99,6 +99,7 @@ struct Lanes {
   }
 };
 
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -171,16 +172,21 @@ __device__ __forceinline__ Span sequence(const int32_t* offs, int s, int64_t T) 
   if (!offs) return {0, T};
   return {min(max((int64_t)offs[s], (int64_t)0), T), min(max((int64_t)offs[s + 1], (int64_t)0), T)};
 }
-// The last sequence that begins at or before `row` (-1: none).
+// The last sequence that begins at or before `row` (-1: none), looked for by a
+// whole warp: 32 places a step.
 __device__ __forceinline__ int sequence_of(const int32_t* offs, int S, int64_t row) {
   if (!offs) return 0;
-  int lo = -1, hi = S - 1;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (offs[mid] <= row) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = S;  // it is lo - 1, or among the n from lo
+  while (n > 0) {
+    const int stride = (n + 31) / 32, i = lane * stride;
+    const int before = __popc(__ballot_sync(0xffffffffu, i < n && offs[lo + min(i, n - 1)] <= row));
+    if (before == 0) break;
+    const int at = (before - 1) * stride;
+    lo += at + 1;
+    n = min(stride, n - at) - 1;
   }
-  return lo;
+  return lo - 1;
 }
 
 // A block has the rows of one chunk and leaves one entry for every sequence it
@@ -190,7 +196,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* offs, int S, int64_t r
 struct Entries {
   float* probs;    // [entries][E]
   int32_t* count;  // [entries][E]
-  float2* sums;    // [entries]: rows counted, sum of l^2
+  float2* sums;    // [entries]: rows counted (an int's bits), sum of l^2
 };
 
 // A row's scores but for the factor `scale`, in z; returns the squared
@@ -218,7 +224,8 @@ __device__ __forceinline__ float scores_row(float (&z)[N], float* scale, bool sq
 template <typename T, bool VEC, int NV, bool SIGMOID>
 __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const BalanceArgs p, const Entries out, int chunk_rows) {
   extern __shared__ __align__(16) float shared[];  // [warps][128 NV], then counts [E]
-  __shared__ float2 warp_sums[kBalWarps];
+  __shared__ int warp_rows[kBalWarps];
+  __shared__ float warp_zz[kBalWarps];
   constexpr int N = 4 * NV;
   int* count = reinterpret_cast<int*>(shared + kBalWarps * 32 * N);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -237,7 +244,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
 #pragma unroll
     for (int i = 0; i < NV; ++i) mine[32 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
-    float rows = 0.f, zz = 0.f;
+    int rows = 0;
+    float zz = 0.f;
     // a row: its logits, its ids and whether it counts
     float next[N];
     int id = -1;
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
       }
       fetch(t + kBalWarps);
       if (!here) continue;
-      rows += 1.f;
+      ++rows;
       float scale;
       zz += scores_row<SIGMOID>(z, &scale, p.z_coef != 0.f);
 #pragma unroll
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
         mine[32 * i] = v;
       }
     }
-    if (lane == 0) warp_sums[warp] = make_float2(rows, zz);
+    if (lane == 0) warp_rows[warp] = rows, warp_zz[warp] = zz;
     __syncthreads();
     const int64_t entry = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < p.E; e += kBalThreads) {
@@ -285,9 +293,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
       out.count[entry * p.E + e] = count[e];
     }
     if (threadIdx.x == 0) {
-      float2 v = make_float2(0.f, 0.f);
-      for (int w = 0; w < kBalWarps; ++w) v.x += warp_sums[w].x, v.y += warp_sums[w].y;
-      out.sums[entry] = v;
+      int n = 0;
+      float v = 0.f;
+      for (int w = 0; w < kBalWarps; ++w) n += warp_rows[w], v += warp_zz[w];
+      out.sums[entry] = make_float2(__int_as_float(n), v);
     }
     __syncthreads();
   }
@@ -300,7 +309,8 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
   const int warps = blockDim.x >> 5;
   __shared__ float probs[32][128];
   __shared__ int count[32][128];
-  __shared__ float2 sums[32];
+  __shared__ int warp_rows[32];
+  __shared__ float warp_zz[32];
   __shared__ float terms[4];
   __shared__ float loss;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -344,20 +354,20 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
     count[warp][e] = n[j];
   }
   // rows counted and l^2: every thread has some entries
-  float2 t = make_float2(0.f, 0.f);
-  for (int64_t i = first + threadIdx.x; i <= last; i += blockDim.x) t.x += in.sums[i].x, t.y += in.sums[i].y;
-  t.x = warp_sum(t.x), t.y = warp_sum(t.y);
-  if (lane == 0) sums[warp] = t;
+  int rows = 0;
+  float zz = 0.f;
+  for (int64_t i = first + threadIdx.x; i <= last; i += blockDim.x) rows += __float_as_int(in.sums[i].x), zz += in.sums[i].y;
+  rows = warp_sum(rows), zz = warp_sum(zz);
+  if (lane == 0) warp_rows[warp] = rows, warp_zz[warp] = zz;
   __syncthreads();
   if (threadIdx.x < 128) {
     const int e = threadIdx.x, expert = 128 * part + e;
-    t = lane < warps ? sums[lane] : make_float2(0.f, 0.f);
-    t.x = warp_sum(t.x), t.y = warp_sum(t.y);
+    rows = warp_sum(lane < warps ? warp_rows[lane] : 0), zz = warp_sum(lane < warps ? warp_zz[lane] : 0.f);
     float all = 0.f;
     int many = 0;
 #pragma unroll 8
     for (int w = 0; w < warps; ++w) all += probs[w][e], many += count[w][e];
-    const float each = t.x > 0.f ? 1.f / t.x : 0.f, mean = t.x > 0.f ? all / t.x : 0.f;
+    const float each = rows > 0 ? 1.f / (float)rows : 0.f, mean = rows > 0 ? all / (float)rows : 0.f;
     float term = 0.f;
     if (expert < p.E) {
       p.counts[(int64_t)s * p.E + expert] = many;
@@ -368,8 +378,8 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
     if (lane == 0) terms[warp] = term;
     named_barrier_sync(1, 128);
     if (threadIdx.x == 0) {
-      loss = p.coef * (terms[0] + terms[1] + terms[2] + terms[3]) + (part == 0 ? p.z_coef * t.y * each : 0.f);
-      if (part == 0) p.tokens[s] = (int)t.x;
+      loss = p.coef * (terms[0] + terms[1] + terms[2] + terms[3]) + (part == 0 ? p.z_coef * zz * each : 0.f);
+      if (part == 0) p.tokens[s] = rows;
     }
   }
   __syncthreads();
@@ -395,19 +405,32 @@ __global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalanceArg
   }
 }
 
+template <int NV>
+__device__ __forceinline__ float dot_row(const float4* f, const float (&v)[4 * NV]) {
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const float4 a = f[32 * i];
+    dot = fmaf(a.x, v[4 * i], fmaf(a.y, v[4 * i + 1], fmaf(a.z, v[4 * i + 2], fmaf(a.w, v[4 * i + 3], dot))));
+  }
+  return warp_sum(dot);
+}
+
 constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
-// A warp a row, rows side by side in a chunk of its own, so that f stays in
-// registers over a sequence's rows. The routing weights' terms reach the lanes
+// A warp a row, rows side by side in a chunk of its own, so that f is worked out
+// once a sequence (it stays in shared memory: in registers it cost a third of
+// the warps). The routing weights' terms reach the lanes
 // that hold their experts through a row of shared memory that is zero between
 // rows (comparing every expert with every id took more instructions than the
 // rest).
 template <typename T, bool VEC, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
-  extern __shared__ __align__(16) float shared[];  // [warps][128 NV]
+__global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : SIGMOID ? 2 : 3) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
+  extern __shared__ __align__(16) float shared[];  // [warps][128 NV] f, and with weights [warps][128 NV] their terms
   constexpr int N = 4 * NV;
   const int lane = threadIdx.x & 31;
-  float* kept = shared + (threadIdx.x >> 5) * 32 * N;
-  float4* mine = reinterpret_cast<float4*>(kept) + lane;  // element i of lane l: [i / 4][l][i % 4]
+  float* f_row = shared + (threadIdx.x >> 5) * 32 * N;
+  float* kept = f_row + kBalGradWarps * 32 * N;
+  float4 *f4 = reinterpret_cast<float4*>(f_row) + lane, *mine = reinterpret_cast<float4*>(kept) + lane;  // element i of lane l: [i / 4][l][i % 4]
   const Lanes<VEC, NV> at{lane, p.E};
   const int64_t warp = (int64_t)blockIdx.x * kBalGradWarps + (threadIdx.x >> 5);
   const int64_t first = warp * warp_rows, last = min(first + warp_rows, p.T);
@@ -418,36 +441,45 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
     for (int i = 0; i < NV; ++i) mine[32 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
   }
-  int s = sequence_of(p.offs, p.S, first);
+  int s = -2;  // not looked for yet
   Span span{0, 0};
-  float f[N], aux = 0.f, zc = 0.f;
-  bool fresh = true;
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = 0.f;
+  float aux = 0.f, zc = 0.f;
   for (int64_t t = first; t < last; ++t) {
-    while (s + 1 < p.S && p.offs && p.offs[s + 1] <= t) ++s, fresh = true;
-    if (s < 0) continue;
-    if (fresh) {
-      fresh = false;
-      span = sequence(p.offs, s, p.T);
-      const float n = (float)p.tokens[s], each = n > 0.f ? 1.f / n : 0.f, g = p.dloss[s];
-      aux = g * p.coef * each;
-      zc = 2.f * g * p.z_coef * each;
-      const float unit = (float)p.E / (float)p.k * each;
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = at.col(i) < p.E ? (float)p.counts[(int64_t)s * p.E + at.col(i)] * unit : 0.f;
-    }
-    if (t < span.begin || t >= span.end) continue;  // behind every sequence: left as it was
-    T* out = static_cast<T*>(p.dlogits) + t * p.lddl;
+    // the row first (one that turns out not to count is read all the same), so
+    // that its latency is not added to the sequence's
     float z[N], w = 0.f, dw = 0.f;
     int id = -1;
-    const bool counts = !p.mask || p.mask[t];  // its row is read all the same: one latency, not two
+    const bool counts = !p.mask || p.mask[t];
     at.load(z, static_cast<const T*>(p.logits) + t * p.ldl, -INFINITY);
     if (p.weights && lane < p.k) {
       w = p.weights[t * p.k + lane];
       dw = p.dweights[t * p.k + lane];
       id = p.ids[t * p.k + lane];
     }
+    bool fresh = s == -2;
+    if (fresh) s = sequence_of(p.offs, p.S, t);
+    while (s + 1 < p.S && p.offs && p.offs[s + 1] <= t) ++s, fresh = true;
+    if (s < 0) continue;
+    if (fresh) {
+      span = sequence(p.offs, s, p.T);
+      const float n = (float)p.tokens[s], each = n > 0.f ? 1.f / n : 0.f, g = p.dloss[s];
+      aux = g * p.coef * each;
+      zc = 2.f * g * p.z_coef * each;
+      const float unit = (float)p.E / (float)p.k * each;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = at.col(4 * i + j);
+          x[j] = c < p.E ? (float)p.counts[(int64_t)s * p.E + c] * unit : 0.f;
+        }
+        f4[32 * i] = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    if (t < span.begin || t >= span.end) continue;  // behind every sequence: left as it was
+    T* out = static_cast<T*>(p.dlogits) + t * p.lddl;
     if (!counts) {
 #pragma unroll
       for (int i = 0; i < N; ++i) z[i] = 0.f;
@@ -481,9 +513,7 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
 #pragma unroll
       for (int i = 0; i < N; ++i) d[i] = z[i];
       sigmoid_row<N, true>(d, m, &scale);
-#pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(f[i], d[i], dot);
-      dot = warp_sum(dot) * scale;
+      dot = dot_row<NV>(f4, d) * scale;
       if (zc != 0.f) {
         const float l = softmax_row(z, &soft);
         soft *= zc * l;
@@ -496,19 +526,19 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
           const float4 w = mine[32 * i];
           x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
         }
+        const float4 fi = f4[32 * i];
+        const float f[4] = {fi.x, fi.y, fi.z, fi.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 4 * i + j;
-          d[c] = m[c] * fmaf(scale * d[c], f[c] - dot, x[j]);
+          d[c] = m[c] * fmaf(scale * d[c], f[j] - dot, x[j]);
           if (zc != 0.f) d[c] = fmaf(soft, z[c], d[c]);
         }
       }
       at.store(out, d);
     } else {
       const float l = softmax_row(z, &scale);
-#pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(f[i], z[i], dot);
-      dot = warp_sum(dot) * scale;
+      dot = dot_row<NV>(f4, z) * scale;
       const float rest = scale * (zc != 0.f ? zc * l : 0.f);
       scale *= aux;
 #pragma unroll
@@ -518,10 +548,12 @@ __global__ void __launch_bounds__(kBalGradThreads, 2) balance_grad_kernel(const 
           const float4 w = mine[32 * i];
           x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
         }
+        const float4 fi = f4[32 * i];
+        const float f[4] = {fi.x, fi.y, fi.z, fi.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 4 * i + j;
-          z[c] = fmaf(z[c], fmaf(scale, f[c] - dot, rest), x[j]);
+          z[c] = fmaf(z[c], fmaf(scale, f[j] - dot, rest), x[j]);
         }
       }
       at.store(out, z);
@@ -549,6 +581,17 @@ bool vec_rows(const void* p, int64_t ld, int E, int size) {
   return E % 4 == 0 && !(((uintptr_t)p | (uint64_t)(ld * size)) & (uint64_t)(4 * size - 1));
 }
 
+// A kernel's dynamic shared memory, once a device.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int device = 0;
+  (void)cudaGetDevice(&device);
+  if (device < 64 && done.load() >> device & 1) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && device < 64) done.fetch_or(1ull << device);
+  return e;
+}
+
 // NV parts of 128 experts: 1, 2, 4 or 8.
 template <typename T, bool VEC, bool SIGMOID>
 cudaError_t rows_nv(const BalanceArgs& p, const Entries& out, int64_t chunk, int64_t blocks, cudaStream_t s) {
@@ -557,15 +600,9 @@ cudaError_t rows_nv(const BalanceArgs& p, const Entries& out, int64_t chunk, int
   const dim3 g((unsigned)blocks), b(kBalThreads);
   const int c = (int)chunk;
   if (nv == 8) {
-    static std::atomic<uint64_t> configured{0};  // a bit a device
-    int device = 0;
-    (void)cudaGetDevice(&device);
-    if (device >= 64 || !(configured.load() >> device & 1)) {
-      const cudaError_t e = cudaFuncSetAttribute(balance_rows_kernel<T, VEC, 8, SIGMOID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)((kBalWarps * 1024 + kOpsMaxExperts) * sizeof(float)));
-      if (e != cudaSuccess) return e;
-      if (device < 64) configured.fetch_or(1ull << device);
-    }
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(balance_rows_kernel<T, VEC, 8, SIGMOID>, (kBalWarps * 1024 + kOpsMaxExperts) * sizeof(float), done);
+    if (e != cudaSuccess) return e;
   }
   if (nv == 1) return launch_after_previous(balance_rows_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, out, c);
   if (nv == 2) return launch_after_previous(balance_rows_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, out, c);
@@ -581,8 +618,13 @@ cudaError_t rows_t(const BalanceArgs& p, const Entries& out, int64_t chunk, int6
 template <typename T, bool VEC, bool SIGMOID>
 cudaError_t grad_nv(const BalanceGradArgs& p, int64_t rows, int64_t blocks, cudaStream_t s) {
   const int nv = p.E <= 128 ? 1 : p.E <= 256 ? 2 : p.E <= 512 ? 4 : 8;
-  const size_t smem = p.weights ? (size_t)kBalGradWarps * 128 * nv * sizeof(float) : 0;  // 32 KB at most
+  const size_t smem = (p.weights ? 2 : 1) * (size_t)kBalGradWarps * 128 * nv * sizeof(float);  // 64 KB at most
   const dim3 g((unsigned)blocks), b(kBalGradThreads);
+  if (nv == 8) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(balance_grad_kernel<T, VEC, 8, SIGMOID>, 2 * kBalGradWarps * 1024 * sizeof(float), done);
+    if (e != cudaSuccess) return e;
+  }
   if (nv == 1) return launch_after_previous(balance_grad_kernel<T, VEC, 1, SIGMOID>, g, b, smem, s, p, rows);
   if (nv == 2) return launch_after_previous(balance_grad_kernel<T, VEC, 2, SIGMOID>, g, b, smem, s, p, rows);
   if (nv == 4) return launch_after_previous(balance_grad_kernel<T, VEC, 4, SIGMOID>, g, b, smem, s, p, rows);
@@ -628,7 +670,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
 
 cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
   // about as many warps as fit the GPU at once
-  const int64_t warps = (int64_t)sms * (p.E <= 128 ? 6 : p.E <= 512 ? 3 : 2) * kBalGradWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t warps = (int64_t)sms * (p.E <= 128 ? 6 : 3) * kBalGradWarps, rows = (p.T + warps - 1) / warps;
   const int64_t blocks = ((p.T + rows - 1) / rows + kBalGradWarps - 1) / kBalGradWarps;
   return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
          : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)

@@ -778,6 +778,42 @@ def test_balance_of_far_logits(dfm, score, shift):
     within(loss, want[0], 512 * U * want[0], "f32")
 
 
+def test_balance_counts_more_tokens_than_fp32_does(dfm):
+    T, E = 2 ** 24 + 3, 2
+    z = torch.zeros(T, E, device="cuda")
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ids[5] = 1
+    loss, probs = torch.empty(1, device="cuda"), torch.empty(1, E, device="cuda")
+    counts, tokens = torch.empty(1, E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    size = dfm.balance_loss_workspace(T, E)
+    dfm.balance_loss(z, "f32", T, E, ids, 1, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size, probs=probs)
+    assert tokens.item() == T and counts.tolist() == [[T - 1, 1]]
+    # halves: every partial sum is exact in fp32 but the last few
+    assert bool(((probs.double() - 0.5).abs() <= 64 * U).all()) and abs(loss.item() - 1.0) <= 128 * U
+
+
+@pytest.mark.parametrize("S", [1, 2, 31, 32, 33, 1023, 1025, 40000])
+def test_balance_finds_every_sequence(dfm, S):
+    """One token each, then two in the last: sequence s has expert s % E alone."""
+    E, T = 8, S + 1
+    of = torch.arange(T, device="cuda").clamp(max=S - 1)
+    ids = (of % E).to(torch.int32)[:, None].contiguous()
+    offs = torch.cat([torch.arange(S, device="cuda"), torch.tensor([T], device="cuda")]).to(torch.int32)
+    z = torch.zeros(T, E, device="cuda")
+    loss = torch.empty(S, device="cuda")
+    counts, tokens = torch.empty(S, E, dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda")
+    size = dfm.balance_loss_workspace(T, E, S)
+    dfm.balance_loss(z, "f32", T, E, ids, 1, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size, offs=offs, S=S)
+    want = torch.zeros(S, E, dtype=torch.int32, device="cuda").index_put_((of, of % E), torch.ones(T, dtype=torch.int32, device="cuda"),
+                                                                         accumulate=True)
+    assert torch.equal(counts, want) and torch.equal(tokens.long(), want.sum(1))
+    d = torch.empty_like(z)
+    dfm.balance_loss_grad(torch.ones(S, device="cuda"), z, "f32", T, E, None, 1, counts, tokens, d, offs=offs, S=S)
+    n = want.sum(1)[of][:, None].double()
+    f = torch.zeros(T, E, dtype=torch.float64, device="cuda").scatter_(1, (of % E)[:, None], float(E))
+    within(d, (f - 1) / E / n, 64 * U * (f + 1) / E / n, "f32")
+
+
 def test_balance_all_masked_and_no_rows(dfm):
     T, E, k, S = 30, 40, 2, 3
     for rows_there in (T, 0):
