@@ -19,6 +19,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "fastmath.cuh"
 #include "internal.h"
 #include "ops.h"
 #include "pipeline.cuh"
@@ -110,14 +111,6 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-
-// 2^x for x <= 0 or so, within 2 units of the last place; below 2^-126: 0.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // v becomes exp(v - l + log(scale)), l = logsumexp(v); `scale` is what the
 // values are still to be multiplied by (1 / their sum). exp(v - most) as a
@@ -424,7 +417,7 @@ constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
 // rows (comparing every expert with every id took more instructions than the
 // rest).
 template <typename T, bool VEC, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : SIGMOID ? 2 : 3) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
+__global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : 2) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
   extern __shared__ __align__(16) float shared[];  // [warps][128 NV] f, and with weights [warps][128 NV] their terms
   constexpr int N = 4 * NV;
   const int lane = threadIdx.x & 31;
@@ -670,7 +663,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& p, int dtype, void* workspace
 
 cudaError_t launch_balance_loss_grad(const BalanceGradArgs& p, int dtype, int sms, cudaStream_t s) {
   // about as many warps as fit the GPU at once
-  const int64_t warps = (int64_t)sms * (p.E <= 128 ? 6 : 3) * kBalGradWarps, rows = (p.T + warps - 1) / warps;
+  const int64_t warps = (int64_t)sms * (p.E <= 128 ? 6 : p.E <= 512 ? 3 : 2) * kBalGradWarps, rows = (p.T + warps - 1) / warps;
   const int64_t blocks = ((p.T + rows - 1) / rows + kBalGradWarps - 1) / kBalGradWarps;
   return dtype == 0   ? grad_t<__nv_bfloat16>(p, rows, blocks, s)
          : dtype == 1 ? grad_t<__half>(p, rows, blocks, s)

@@ -20,6 +20,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "fastmath.cuh"
 #include "internal.h"
 #include "ops.h"
 #include "pipeline.cuh"
@@ -132,26 +133,29 @@ __device__ __forceinline__ void store_columns(const float (&v)[V], void* p, int6
 }
 
 // ---- activations --------------------------------------------------------------
-// expf and normcdff keep the fp32 outputs' last bits; the quotient is within 2
-// units of the last place.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
     case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays
     case kActSilu: return z * sigmoid_f(z);
-    case kActGelu: return z * normcdff(z);
+    case kActGelu: {
+      float density;
+      return z * normal_cdf(z, &density);
+    }
     default: return z;
   }
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : z != z ? z : 0.f;
-    case kActSilu:
-    case kActSwiglu: {
+    case kActSilu: {
       const float s = sigmoid_f(z);
       return s * fmaf(z, 1.f - s, 1.f);
     }
-    case kActGelu: return fmaf(z * 0.3989422804f, expf(-0.5f * z * z), normcdff(z));
+    case kActGelu: {
+      float density;
+      const float cdf = normal_cdf(z, &density);
+      return fmaf(z * 0.398942280f, density, cdf);
+    }
     default: return 1.f;
   }
 }

@@ -5,8 +5,9 @@ Tolerances are a priori. U = 2^-24 is half a unit of fp32. A rounding to type t
 costs at most eps(t) / 2 of the value, and half the smallest subnormal below it.
 A sum in fp32 whose longest chain has n additions costs at most n U of the sum
 of the terms' magnitudes (2 n U where the tensor core may truncate instead of
-rounding). expf, logf, log1pf and normcdff are within 8 U, __fdividef within 4,
-of values that are not tiny.
+rounding). The library's exponentials, sigmoid and normal distribution function
+are within 128 U of values that are not tiny (an exponent's argument of size a is
+rounded: a U).
 """
 import math
 
