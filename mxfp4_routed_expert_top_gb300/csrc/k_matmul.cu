@@ -52,79 +52,37 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
-// Columns i, i + step, ... of a row: n of V. VEC: all V, side by side and
-// aligned to them (32 bytes at most).
-template <bool VEC, int V>
-__device__ __forceinline__ void load_columns(float (&v)[V], const void* p, int64_t i, int step, int n, int type) {
+// Columns i, i + step, ... of a row: n of four. VEC: all four, side by side and
+// aligned to them.
+template <bool VEC>
+__device__ __forceinline__ void load_columns(float (&v)[4], const void* p, int64_t i, int step, int n, int type) {
   if constexpr (VEC) {
-    static_assert(V == 4 || V == 16, "");
     if (type == 2) {
-      const float* f = static_cast<const float*>(p) + i;
-      if constexpr (V == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(f);
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-      } else {
-#pragma unroll
-        for (int h = 0; h < V; h += 8)
-          asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                       : "=f"(v[h]), "=f"(v[h + 1]), "=f"(v[h + 2]), "=f"(v[h + 3]), "=f"(v[h + 4]), "=f"(v[h + 5]),
-                         "=f"(v[h + 6]), "=f"(v[h + 7])
-                       : "l"(f + h));
-      }
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     } else {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-      uint32_t w[V / 2];
-      if constexpr (V == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q);
-        w[0] = u.x, w[1] = u.y;
-      } else {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(q));
-      }
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        v[2 * j] = half_bits(w[j] & 0xffffu, type);
-        v[2 * j + 1] = half_bits(w[j] >> 16, type);
-      }
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      v[0] = half_bits(w.x & 0xffffu, type), v[1] = half_bits(w.x >> 16, type);
+      v[2] = half_bits(w.y & 0xffffu, type), v[3] = half_bits(w.y >> 16, type);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < 4; ++j)
       v[j] = j >= n ? 0.f : type == 2 ? static_cast<const float*>(p)[i + j * step]
                                       : half_bits(static_cast<const uint16_t*>(p)[i + j * step], type);
   }
 }
-template <bool VEC, int V>
-__device__ __forceinline__ void store_columns(const float (&v)[V], void* p, int64_t i, int step, int n, int type) {
+template <bool VEC>
+__device__ __forceinline__ void store_columns(const float (&v)[4], void* p, int64_t i, int step, int n, int type) {
   if constexpr (VEC) {
-    if (type == 2) {
-      float* f = static_cast<float*>(p) + i;
-      if constexpr (V == 4) {
-        *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-#pragma unroll
-        for (int h = 0; h < V; h += 8)
-          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(f + h), "f"(v[h]), "f"(v[h + 1]),
-                       "f"(v[h + 2]), "f"(v[h + 3]), "f"(v[h + 4]), "f"(v[h + 5]), "f"(v[h + 6]), "f"(v[h + 7])
-                       : "memory");
-      }
-    } else {
-      uint16_t* q = static_cast<uint16_t*>(p) + i;
-      uint32_t w[V / 2];
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) w[j] = pack_bits(v[2 * j], v[2 * j + 1], type);
-      if constexpr (V == 4) {
-        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-      } else {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-      }
-    }
+    if (type == 2)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+          make_uint2(pack_bits(v[0], v[1], type), pack_bits(v[2], v[3], type));
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < 4; ++j) {
       if (j >= n) continue;
       if (type == 2) static_cast<float*>(p)[i + j * step] = v[j];
       else static_cast<uint16_t*>(p)[i + j * step] = (uint16_t)(pack_bits(v[j], 0.f, type) & 0xffffu);
@@ -132,31 +90,100 @@ __device__ __forceinline__ void store_columns(const float (&v)[V], void* p, int6
   }
 }
 
-// ---- activations --------------------------------------------------------------
-__device__ __forceinline__ float act_f(float z, int act) {
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays
-    case kActSilu: return z * sigmoid_f(z);
-    case kActGelu: {
-      float density;
-      return z * normal_cdf(z, &density);
+// Sixteen columns of a row, 32-byte aligned.
+__device__ __forceinline__ void load_sixteen(float (&v)[16], const void* p, int64_t i, int type) {
+  if (type == 2) {
+    const float* f = static_cast<const float*>(p) + i;
+#pragma unroll
+    for (int h = 0; h < 16; h += 8)
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[h]), "=f"(v[h + 1]), "=f"(v[h + 2]), "=f"(v[h + 3]), "=f"(v[h + 4]), "=f"(v[h + 5]),
+                     "=f"(v[h + 6]), "=f"(v[h + 7])
+                   : "l"(f + h));
+  } else {
+    uint32_t w[8];
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(static_cast<const uint16_t*>(p) + i));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[2 * j] = half_bits(w[j] & 0xffffu, type);
+      v[2 * j + 1] = half_bits(w[j] >> 16, type);
     }
-    default: return z;
   }
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
+__device__ __forceinline__ void store_sixteen(const float (&v)[16], void* p, int64_t i, int type) {
+  if (type == 2) {
+    float* f = static_cast<float*>(p) + i;
+#pragma unroll
+    for (int h = 0; h < 16; h += 8)
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(f + h), "f"(v[h]), "f"(v[h + 1]),
+                   "f"(v[h + 2]), "f"(v[h + 3]), "f"(v[h + 4]), "f"(v[h + 5]), "f"(v[h + 6]), "f"(v[h + 7])
+                   : "memory");
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bits(v[2 * j], v[2 * j + 1], type);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint16_t*>(p) + i), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  }
+}
+
+// ---- activations --------------------------------------------------------------
+__device__ __forceinline__ float relu_f(float z) { return z < 0.f ? 0.f : z; }  // NaN stays
+__device__ __forceinline__ void gelu_two(float& a, float& b) {
+  const Pair z = pair(a, b);
+  Pair density;
+  const float2 f = halves(mul2(z, normal_cdf(z, &density)));
+  a = f.x, b = f.y;
+}
+// z becomes act(z); V even but for one value.
+template <int V>
+__device__ __forceinline__ void act_all(float (&z)[V], const float (&up)[V], int act) {
   switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : z != z ? z : 0.f;
-    case kActSilu: {
-      const float s = sigmoid_f(z);
-      return s * fmaf(z, 1.f - s, 1.f);
-    }
-    case kActGelu: {
-      float density;
-      const float cdf = normal_cdf(z, &density);
-      return fmaf(z * 0.398942280f, density, cdf);
-    }
-    default: return 1.f;
+    case kActNone: break;
+    case kActRelu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = relu_f(z[j]);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] *= sigmoid_f(z[j]);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < V; j += 2) gelu_two(z[j], z[j + 1]);
+      break;
+    default:
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] *= sigmoid_f(z[j]) * up[j];
+  }
+}
+// s becomes act'(z).
+template <int V>
+__device__ __forceinline__ void slope_all(float (&s)[V], const float (&z)[V], int act) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = z[j] > 0.f ? 1.f : z[j] != z[j] ? z[j] : 0.f;
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const Pair x = pair(z[j], z[j + 1]);
+        Pair density;
+        const Pair cdf = normal_cdf(x, &density);
+        const float2 f = halves(fma2(mul2(x, both(0.398942280f)), density, cdf));
+        s[j] = f.x, s[j + 1] = f.y;
+      }
+      break;
+    default:  // silu, and the gate's of swiglu
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float g = sigmoid_f(z[j]);
+        s[j] = g * fmaf(z[j], 1.f - g, 1.f);
+      }
   }
 }
 
@@ -213,44 +240,22 @@ __device__ __forceinline__ void gemm_stage(uint32_t d, uint32_t ad, uint32_t as,
       : "memory");
 }
 
-template <int V>
-__device__ __forceinline__ void act_all(float (&z)[V], const float (&up)[V], int act) {
-  switch (act) {
-    case kActNone: break;
-    case kActRelu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActRelu);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActGelu);
-      break;
-    default:
-#pragma unroll
-      for (int j = 0; j < V; ++j) z[j] = act_f(z[j], kActSilu) * up[j];
-  }
-}
-
-// Columns c, c + step, ... (V of them) of output row `row`: z (and, gated, up)
+// Columns c, c + step, ... (four) of output row `row`: z (and, gated, up)
 // come without the bias.
-template <bool VEC, int V>
-__device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, int c, int step, float (&z)[V], float (&up)[V]) {
-  const int n = c >= p.C ? 0 : min(V, (p.C - c + step - 1) / step);
+template <bool VEC>
+__device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, int c, int step, float (&z)[4], float (&up)[4]) {
+  const int n = c >= p.C ? 0 : min(4, (p.C - c + step - 1) / step);
   if (n <= 0) return;
   const bool gated = p.act == kActSwiglu;
-  float v[V];
+  float v[4];
   if (p.bias) {
     load_columns<VEC>(v, p.bias, c, step, n, p.in);
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] += v[j];
+    for (int j = 0; j < 4; ++j) z[j] += v[j];
     if (gated) {
       load_columns<VEC>(v, p.bias, (int64_t)p.C + c, step, n, p.in);
 #pragma unroll
-      for (int j = 0; j < V; ++j) up[j] += v[j];
+      for (int j = 0; j < 4; ++j) up[j] += v[j];
     }
   }
   if (p.pre) {
@@ -261,7 +266,7 @@ __device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, in
   if (p.residual) {
     load_columns<VEC>(v, p.residual, row * p.ldr + c, step, n, p.out);
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] += v[j];
+    for (int j = 0; j < 4; ++j) z[j] += v[j];
   }
   store_columns<VEC>(z, p.y, row * p.ldy + c, step, n, p.out);
 }
@@ -341,8 +346,8 @@ __device__ __forceinline__ void split_epilogue(const GemmParams& p, const float*
     float z[4], up[4] = {0.f, 0.f, 0.f, 0.f};
     sums(z, q * 128 + c);
     if (gated) sums(up, q * 128 + 64 + c);
-    if (p.vec) gemm_finish<true, 4>(p, r0 + q, c0 + c, 1, z, up);
-    else gemm_finish<false, 4>(p, r0 + q, c0 + c, step, z, up);
+    if (p.vec) gemm_finish<true>(p, r0 + q, c0 + c, 1, z, up);
+    else gemm_finish<false>(p, r0 + q, c0 + c, step, z, up);
   }
 }
 
@@ -518,7 +523,7 @@ struct PairCfg {
 template <int BN>
 struct PairSmem {
   using G = PairCfg<BN>;
-  float turn[G::EW][32 * 33];  // what a warp turns
+  float turn[G::EW][32 * 32];  // what a warp turns
   uint64_t full[G::NS], empty[G::NS], acc_full[2], acc_empty[2];
   uint32_t tmem;
   int err;
@@ -585,18 +590,18 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // 32 rows x 32 columns of a warp, a row a lane, to rows of global memory that
-// nothing is known of: turned in shared memory ([32][33]), so that a store
-// covers a piece of one row. `rows`, `cols`: those there are.
+// nothing is known of: turned in shared memory (value (r, c) stands at 32 r + (c ^
+// r)), so that a store covers a piece of one row. `rows`, `cols`: those there are.
 template <typename Y>
 __device__ __forceinline__ void put_rows(float* turn, const float (&v)[32], Y* to, int64_t ld, int rows, int cols) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) turn[33 * lane + j] = v[j];
+  for (int j = 0; j < 32; ++j) turn[32 * lane + (j ^ lane)] = v[j];
   __syncwarp();
   if (lane < cols) {
     to += lane;
 #pragma unroll 8
-    for (int r = 0; r < rows; ++r, to += ld) *to = from_f32<Y>(turn[33 * r + lane]);
+    for (int r = 0; r < rows; ++r, to += ld) *to = from_f32<Y>(turn[32 * r + (lane ^ r)]);
   }
   __syncwarp();
 }
@@ -612,11 +617,11 @@ __device__ __forceinline__ void add_rows(float* turn, float (&v)[32], const Y* f
   if (lane < cols) {
     from += lane;
 #pragma unroll 8
-    for (int r = 0; r < rows; ++r, from += ld) turn[33 * r + lane] = to_f32(*from);
+    for (int r = 0; r < rows; ++r, from += ld) turn[32 * r + (lane ^ r)] = to_f32(*from);
   }
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] += turn[33 * lane + j];
+  for (int j = 0; j < 32; ++j) v[j] += turn[32 * lane + (j ^ lane)];
   __syncwarp();
 }
 __device__ __forceinline__ void add_rows(float* turn, float (&v)[32], const void* from, int64_t at, int64_t ld, int rows, int cols, int type) {
@@ -624,19 +629,19 @@ __device__ __forceinline__ void add_rows(float* turn, float (&v)[32], const void
   else if (type == 1) add_rows(turn, v, static_cast<const __half*>(from) + at, ld, rows, cols);
   else add_rows(turn, v, static_cast<const float*>(from) + at, ld, rows, cols);
 }
-__device__ __forceinline__ void add_bias(float (&v)[32], const void* bias, int c, int cols, int type) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < cols) v[j] += half_bits(static_cast<const uint16_t*>(bias)[c + j], type);
-}
-// gemm_finish of such a piece: z (and, gated, up) come without the bias.
-__device__ __forceinline__ void finish_rows(const GemmParams& p, float* turn, int64_t r0, int rows, int c, float (&z)[32], float (&up)[32]) {
+// The epilogue of such a piece: z (and, gated, up) come without the bias, of
+// which a lane has that of its column.
+__device__ __forceinline__ void finish_rows(const GemmParams& p, float* turn, int64_t r0, int rows, int c, float (&z)[32], float (&up)[32],
+                                            float bias, float bias_up) {
   const int cols = min(32, p.C - c);
-  if (rows <= 0 || cols <= 0) return;
+  if (rows <= 0 || cols <= 0) return;  // of the whole warp
   const bool gated = p.act == kActSwiglu;
   if (p.bias) {
-    add_bias(z, p.bias, c, cols, p.in);
-    if (gated) add_bias(up, p.bias, p.C + c, cols, p.in);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      z[j] += __shfl_sync(0xffffffffu, bias, j);
+      if (gated) up[j] += __shfl_sync(0xffffffffu, bias_up, j);
+    }
   }
   if (p.pre) {
     put_rows(turn, z, p.pre, r0 * p.ldp + c, p.ldp, rows, cols, p.in);
@@ -645,6 +650,30 @@ __device__ __forceinline__ void finish_rows(const GemmParams& p, float* turn, in
   act_all(z, up, p.act);
   if (p.residual) add_rows(turn, z, p.residual, r0 * p.ldr + c, p.ldr, rows, cols, p.out);
   put_rows(turn, z, p.y, r0 * p.ldy + c, p.ldy, rows, cols, p.out);
+}
+
+// Sixteen columns of a row whose arrays start them on 32-byte boundaries; the
+// bias is in them.
+__device__ __forceinline__ void finish_sixteen(const GemmParams& p, int64_t row, int c, float (&z)[16], float (&up)[16]) {
+  float v[16];
+  if (p.residual) load_sixteen(v, p.residual, row * p.ldr + c, p.out);  // on its way meanwhile
+  if (p.pre) {
+    store_sixteen(z, p.pre, row * p.ldp + c, p.in);
+    if (p.act == kActSwiglu) store_sixteen(up, p.pre, row * p.ldp + p.C + c, p.in);
+  }
+  act_all(z, up, p.act);
+  if (p.residual) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] += v[j];
+  }
+  store_sixteen(z, p.y, row * p.ldy + c, p.out);
+}
+// The epilogue has read its accumulator; the leader's MMAs may have it.
+__device__ __forceinline__ void pair_release(uint32_t bar, bool ok) {
+  if (!ok) return;
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  arrive_cluster(bar, (threadIdx.x & 31) == 0);
 }
 
 template <int BN>
@@ -691,6 +720,10 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
   const int gives_up = blockIdx.x == 0 ? p.give_up : kGemmNone;
   const uint32_t limit = first == 0 && p.give_up ? kTestWaitLimit : kWaitLimit;
 
+  // registers go from the warps that issue to those of the epilogue: 128 x 72 +
+  // 256 x 216 are the 384 x 168 of the launch
+  if (warp >= EW) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == EW) {
     // ---- copies, issued by one lane
     const uint32_t leader = elect_one(), sr0 = uni(smem_u32(sr)), sc0 = uni(smem_u32(sc));
@@ -778,7 +811,9 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
       for (int i = 0; i < 2; ++i)
         if (i < units) (void)bar_wait(acc_full + 8 * i, ((units - 1 - i) / 2) & 1, kWaitLimit);
     }
-  } else if (warp < EW) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- epilogue: warp w has tensor memory lanes 32 (w % 4) .. + 31, a row
     // of the output each, and half w / 4 of the columns. A wait that runs out
     // ends every later one of its warp and leaves NaN in what it still writes.
@@ -789,15 +824,60 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
     uint32_t acc = 0, acc_phase = 0;
     for (int u = first; u < p.units; u += step) {
       const PairUnit un = pair_unit(u, p, width);
-      ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t ta = tmem + ((uint32_t)l0 << 16) + BN * acc + cols * half;
       const int64_t r0 = (int64_t)un.r0 + 128 * rank + l0;
       const int rows = (int)min((int64_t)32, p.R - r0), c0 = un.c0 + cols * half;
-      // 32 columns at a time: their loads run together
+      // Sixteen columns at a time, in a loop that stays small: two warps a
+      // scheduler hide neither its loads from memory nor those of instructions
+      // (32 columns unrolled, with the bias read where it is used: 4096 x 19456 x 64
+      // with bias and relu 113 us, 80 so).
+      const int straight = p.vec ? max(0, min(cols, (p.C - c0) / 32 * 32)) : 0;
+      float bias[4], bias_up[2];  // of columns lane, lane + 32, ...
+      if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = lane + 32 * j;
+          if (c < cols && c0 + c < p.C) {
+            bias[j] = half_bits(static_cast<const uint16_t*>(p.bias)[c0 + c], p.in);
+            if (gated && j < 2) bias_up[j & 1] = half_bits(static_cast<const uint16_t*>(p.bias)[p.C + c0 + c], p.in);
+          }
+        }
+      }
+      ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-      for (int i = 0; i < cols; i += 32) {
+      for (int i = 0; i < straight; i += 16) {
+        uint32_t zr[16], ur[16];
+        float z[16], up[16];
+        if (ok) {
+          tmem_ld_rows(zr, ta + i);
+          if (gated) {
+            tmem_ld_rows(ur, ta + BN / 2 + i);
+            tmem_wait(ur);
+          }
+          tmem_wait(zr);
+        }
+        if (i + 16 == cols) pair_release(acc_empty + 8 * acc, ok);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          z[j] = ok ? __uint_as_float(zr[j]) : __uint_as_float(0x7fffffffu);
+          up[j] = gated && ok ? __uint_as_float(ur[j]) : z[j];
+        }
+        if (p.bias) {
+          const float b = i < 32 ? bias[0] : i < 64 ? bias[1] : i < 96 ? bias[2] : bias[3], bu = i < 32 ? bias_up[0] : bias_up[1];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            z[j] += __shfl_sync(0xffffffffu, b, (i & 16) + j);
+            if (gated) up[j] += __shfl_sync(0xffffffffu, bu, (i & 16) + j);
+          }
+        }
+        if (lane < rows) finish_sixteen(p, r0 + lane, c0 + i, z, up);
+      }
+      // any other rows and columns: 32 of each, turned
+#pragma unroll 1
+      for (int i = straight; i < cols; i += 32) {
         uint32_t zr[2][16], ur[2][16] = {};
+        float z[32], up[32];
         if (ok) {
           tmem_ld_rows(zr[0], ta + i);
           tmem_ld_rows(zr[1], ta + i + 16);
@@ -810,30 +890,14 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
           tmem_wait(zr[0]);
           tmem_wait(zr[1]);
         }
-        if (i + 32 == cols && ok) {
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          arrive_cluster(acc_empty + 8 * acc, lane == 0);
+        if (i + 32 == cols) pair_release(acc_empty + 8 * acc, ok);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          z[j] = ok ? __uint_as_float(zr[j >> 4][j & 15]) : __uint_as_float(0x7fffffffu);
+          up[j] = ok ? __uint_as_float(ur[j >> 4][j & 15]) : z[j];
         }
-        const int c = c0 + i;
-        if (!ok) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) zr[0][j] = zr[1][j] = ur[0][j] = ur[1][j] = 0x7fffffffu;
-        }
-        if (p.vec && c + 32 <= p.C) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float z[16], up[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(zr[h][j]), up[j] = __uint_as_float(ur[h][j]);
-            if (lane < rows) gemm_finish<true, 16>(p, r0 + lane, c + 16 * h, 1, z, up);
-          }
-        } else {
-          float z[32], up[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(zr[j >> 4][j & 15]), up[j] = __uint_as_float(ur[j >> 4][j & 15]);
-          finish_rows(p, turn, r0, rows, c, z, up);
-        }
+        const float b = i < 32 ? bias[0] : i < 64 ? bias[1] : i < 96 ? bias[2] : bias[3], bu = i < 32 ? bias_up[0] : bias_up[1];
+        finish_rows(p, turn, r0, rows, c0 + i, z, up, b, bu);
       }
       if (!ok) sm->err = 1;
       acc ^= 1;
@@ -1061,7 +1125,7 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
   const auto get = [](const T* q) { return *reinterpret_cast<const Part*>(q); };
   if (c < p.N) {
     for (int64_t r0 = (int64_t)ROWS * part + ty; r0 < p.M; r0 += (int64_t)U * ROWS * p.parts) {
-      Part d[U], z[U], u[U];
+      Part d[U] = {}, z[U] = {}, u[U] = {};
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int64_t r = r0 + (int64_t)i * ROWS * p.parts;
@@ -1069,6 +1133,12 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
         d[i] = get(dy + r * p.lddy);
         if (some) z[i] = get(pre + r * p.ldp);
         if (gated) u[i] = get(pre + r * p.ldp + p.N);
+      }
+      float g[U * E], slope[U * E];
+      if (some) {
+#pragma unroll
+        for (int i = 0; i < U * E; ++i) g[i] = value(z[i / E].v[i % E]);
+        slope_all(slope, g, p.act);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -1079,13 +1149,12 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
         for (int j = 0; j < E; ++j) {
           float x = value(d[i].v[j]);
           if (gated) {
-            const float g = value(z[i].v[j]), sg = sigmoid_f(g), y = x * (g * sg);
-            x = x * value(u[i].v[j]) * (sg * fmaf(g, 1.f - sg, 1.f));
+            const float y = x * (g[i * E + j] * sigmoid_f(g[i * E + j]));
+            x *= value(u[i].v[j]);
             s1[j] += y;
             b.v[j] = T(y);
-          } else if (some) {
-            x *= act_slope(value(z[i].v[j]), p.act);
           }
+          if (some) x *= slope[i * E + j];
           s0[j] += x;
           a.v[j] = T(x);
         }

@@ -29,6 +29,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "fastmath.cuh"
 #include "internal.h"
 #include "ops.h"
 #include "pipeline.cuh"
@@ -51,27 +52,6 @@ __device__ __forceinline__ float f32_of(__half v) { return __half2float(v); }
 // ---- eight values as four pairs ------------------------------------------------
 // One instruction does a pair (f32x2): the kernels' arithmetic takes half the
 // issue slots, which bound the gradient before.
-typedef unsigned long long Pair;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 halves(Pair p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 struct Eight {
   Pair v[4];
 };
