@@ -1,0 +1,8 @@
+// k_matmul_f16_f32.cu — the product (k_matmul.cuh) of fp16 matrices in fp32.
+#include "k_matmul.cuh"
+
+namespace dfm {
+
+const char* gemm_f16_f32(const GemmArgs& a, int sms, cudaStream_t s) { return gemm<1, 2>(a, sms, s); }
+
+}  // namespace dfm

@@ -113,6 +113,11 @@ struct GemmArgs {
   int give_up;
 };
 const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s);
+// of one pair of types each
+const char* gemm_bf16(const GemmArgs& a, int sms, cudaStream_t s);
+const char* gemm_bf16_f32(const GemmArgs& a, int sms, cudaStream_t s);
+const char* gemm_f16(const GemmArgs& a, int sms, cudaStream_t s);
+const char* gemm_f16_f32(const GemmArgs& a, int sms, cudaStream_t s);
 
 struct ActGradArgs {
   const void *dy, *pre;
