@@ -34,6 +34,15 @@ namespace {
 
 constexpr int kMK = 64;  // k of a stage: 128 bytes, the swizzle's row
 
+// Stages whose products add up in tensor memory, where an addition drops the
+// bits behind the last: a sum of K products comes out 1e-9 K too small (relative;
+// measured at random operands, K from 64 to 32768). Behind so many the sum goes
+// to registers and is added there, rounded to nearest: for an fp32 output 768 of
+// k (7e-7; 4096 x 2048 x 8192 9e-6 without), for a 16-bit one, which is rounded
+// by 2e-3 or 2e-4 itself, 8192.
+template <int OUT>
+constexpr int kChunk = OUT == 2 ? 12 : 128;
+
 // ---- elements of a type (0 bf16, 1 fp16, 2 fp32) -------------------------------
 // The kernels have IN and OUT as constants: branches on the type, and code for
 // the others between, slowed the epilogue by a third.
@@ -244,6 +253,15 @@ __device__ __forceinline__ void gemm_stage(uint32_t d, uint32_t ad, uint32_t as,
       : "memory");
 }
 
+// An accumulator has been read: into registers, once tcgen05.wait::ld is over, so
+// that no memory has to be released with the arrival (a release waits for the
+// warp's stores to global memory, 2000 cycles behind an epilogue).
+__device__ __forceinline__ void arrive_read(uint32_t bar, uint32_t leader) {
+  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+               "r"(leader)
+               : "memory");
+}
+
 // Columns c, c + step, ... (four) of output row `row`: z (and, gated, up)
 // come without the bias.
 template <bool VEC, int IN, int OUT>
@@ -285,12 +303,12 @@ template <int NT>
 struct GemmCfg {
   static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;  // stages
   static constexpr int CBytes = 128 * kMK * 2, RBytes = NT * kMK * 2;
-  static constexpr uint32_t Cols = NT < 32 ? 32 : NT;
+  static constexpr uint32_t Cols = 2 * NT;  // two accumulators, for sums of many chunks
   static constexpr int NTHR = 256;
   static_assert(NS * (CBytes + RBytes) >= 128 * NT * 4, "the sums fit the stages");
 };
 struct GemmSmem {
-  uint64_t full[8], empty[8], acc;
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
   uint32_t tmem;
   int err;
 };
@@ -374,7 +392,10 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
       mbar_init(&sm->full[i], 1);
       mbar_init(&sm->empty[i], 1);
     }
-    mbar_init(&sm->acc, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->acc_full[i], 1);
+      mbar_init(&sm->acc_empty[i], 4);
+    }
     sm->err = 0;
     fence_barrier_init();
   }
@@ -440,15 +461,23 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
     const uint32_t a0 = uni(desc_lo(smem_u32(sc), p.c_mn)), b0 = uni(desc_lo(smem_u32(sr), p.r_mn));
     const uint32_t as = uni(desc_step(p.c_mn)), bs = uni(desc_step(p.r_mn));
     const uint32_t idesc = uni(gemm_idesc(IN, 128, NT, p.c_mn, p.r_mn));
-    const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty)), acc = uni(smem_u32(&sm->acc));
+    const uint32_t full = uni(smem_u32(sm->full)), empty = uni(smem_u32(sm->empty));
+    const uint32_t acc_full = uni(smem_u32(sm->acc_full)), acc_empty = uni(smem_u32(sm->acc_empty));
     bool ok = gives_up != kGemmMmas;
-    int s = 0, kb = kb0;
+    int s = 0, kb = kb0, chunk = 0, in = 0;  // stages in the chunk
     uint32_t phase = 0;
-    for (; kb < kb1 && ok; ++kb) {
+    for (; kb < kb1 && ok; ++kb, ++in) {
+      if (in == kChunk<OUT>) {
+        mma_commit(acc_full + 8 * (chunk & 1), leader);
+        ++chunk, in = 0;
+        ok = bar_wait(acc_empty + 8 * (chunk & 1), (chunk >> 1 & 1) ^ 1, limit);  // the first two find theirs free
+        if (!ok) break;
+      }
       ok = bar_wait(full + 8 * s, phase, limit);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      gemm_stage(tm, a0 + (uint32_t)(s * (G::CBytes >> 4)), as, b0 + (uint32_t)(s * (G::RBytes >> 4)), bs, idesc, kb > kb0, leader);
+      gemm_stage(tm + NT * (chunk & 1), a0 + (uint32_t)(s * (G::CBytes >> 4)), as, b0 + (uint32_t)(s * (G::RBytes >> 4)), bs, idesc,
+                 in > 0, leader);
       mma_commit(empty + 8 * s, leader);
       if (++s == NS) {
         s = 0;
@@ -457,26 +486,45 @@ gemm_split_kernel(const __grid_constant__ GemmParams p) {
     }
     if (!ok) sm->err = 1;
     // MMAs issued, and their arrivals, land before tensor memory is released
-    mma_commit(acc, leader);
+    mma_commit(acc_full + 8 * (chunk & 1), leader);
     const int issued = kb - kb0;
     for (int i = 0; i < NS && i < issued; ++i) (void)bar_wait(empty + 8 * i, ((issued - 1 - i) / NS) & 1, kWaitLimit);
-    (void)bar_wait(acc, 0, kWaitLimit);
+    if (chunk > 0) (void)bar_wait(acc_full + 8 * (chunk - 1 & 1), chunk - 1 >> 1 & 1, kWaitLimit);
+    (void)bar_wait(acc_full + 8 * (chunk & 1), chunk >> 1 & 1, kWaitLimit);
   } else if (warp < 4) {
     // ---- sums to shared memory: lane = column
+    const int chunks = (kb1 - kb0 + kChunk<OUT> - 1) / kChunk<OUT>;
+    const uint32_t acc_full = smem_u32(sm->acc_full), acc_empty = smem_u32(sm->acc_empty);
     bool ok = gives_up != kGemmSums;
-    ok = ok && bar_wait(smem_u32(&sm->acc), 0, limit);
-    if (!ok) sm->err = 1;
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (ok) {
+    float sum[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sum[i] = 0.f;
+#pragma unroll 1
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      ok = ok && bar_wait(acc_full + 8 * (chunk & 1), chunk >> 1 & 1, limit);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t ta = tmem + ((uint32_t)(32 * warp) << 16) + NT * (chunk & 1);
       uint32_t v[2][16];
-      tmem_ld_rows(v[0], tmem + ((uint32_t)(32 * warp) << 16));
+      tmem_ld_rows(v[0], ta);
 #pragma unroll
       for (int i = 0; i < NT / 16; ++i) {
         tmem_wait(v[i & 1]);
-        if (i + 1 < NT / 16) tmem_ld_rows(v[(i + 1) & 1], tmem + ((uint32_t)(32 * warp) << 16) + 16 * (i + 1));
+        if (i + 1 < NT / 16) tmem_ld_rows(v[(i + 1) & 1], ta + 16 * (i + 1));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) red[(16 * i + j) * 128 + 32 * warp + lane] = __uint_as_float(v[i & 1][j]);
+        for (int j = 0; j < 16; ++j) sum[16 * i + j] += __uint_as_float(v[i & 1][j]);
       }
+      if (chunk + 1 < chunks) {
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        arrive_read(acc_empty + 8 * (chunk & 1), lane == 0);
+      }
+    }
+    if (!ok) {
+      sm->err = 1;
+    } else {  // no MMA reads the stages any more
+#pragma unroll
+      for (int i = 0; i < NT; ++i) red[i * 128 + 32 * warp + lane] = sum[i];
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -583,11 +631,6 @@ __device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t leader) {
       "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar, uint32_t leader) {
-  asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
-               "r"(leader)
-               : "memory");
-}
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -659,10 +702,10 @@ __device__ __forceinline__ void finish_rows(const GemmParams& p, float* turn, in
 
 // The epilogue has read its accumulator; the leader's MMAs may have it.
 __device__ __forceinline__ void pair_release(uint32_t bar, bool ok) {
-  if (!ok) return;
+  if (!ok || !bar) return;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
-  arrive_cluster(bar, (threadIdx.x & 31) == 0);
+  arrive_read(bar, (threadIdx.x & 31) == 0);
 }
 
 // What a warp has of a unit: 32 rows from r0 (`rows` of them there), columns c0
@@ -690,6 +733,7 @@ __device__ __forceinline__ void finish_straight(const GemmParams& p, const WarpT
   for (int i = 0; i < t.cols; i += 16) {
     uint32_t zr[16], ur[16];
     float z[16], up[gated ? 16 : 1], v[16];
+    __syncwarp();  // rows that are not there come back
     if (ok) {
       tmem_ld_rows(zr, t.ta + i);
       if (gated) tmem_ld_rows(ur, t.ta + up_at + i);
@@ -733,11 +777,55 @@ __device__ __forceinline__ void finish_straight(const GemmParams& p, const WarpT
   }
 }
 
-template <int BN, int IN, int OUT, bool VEC>
+// The BN / 2 columns of a warp in an accumulator, sixteen at a time: from ta on,
+// or (gated) half of them there and half among the up product's.
+template <int BN>
+__device__ __forceinline__ uint32_t sixteen_at(uint32_t ta, int i, bool gated) {
+  return ta + 16 * i + (gated && i >= BN / 64 ? BN / 2 - BN / 4 : 0);
+}
+// sum += the accumulator's.
+template <int BN>
+__device__ __forceinline__ void add_chunk(float (&sum)[BN / 2], uint32_t ta, bool gated) {
+  constexpr int G = BN == 128 ? 4 : 2;  // on their way together, as registers allow
+#pragma unroll
+  for (int i = 0; i < BN / 32; i += G) {
+    uint32_t v[G][16];
+#pragma unroll
+    for (int g = 0; g < G; ++g) tmem_ld_rows(v[g], sixteen_at<BN>(ta, i + g, gated));
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      tmem_wait(v[g]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[16 * (i + g) + j] += __uint_as_float(v[g][j]);
+    }
+  }
+}
+// The sums to the accumulator's place, where the epilogue finds them.
+template <int BN>
+__device__ __forceinline__ void put_sums(const float (&sum)[BN / 2], uint32_t ta, bool gated) {
+#pragma unroll
+  for (int i = 0; i < BN / 32; ++i) {
+    const float* v = sum + 16 * i;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            sixteen_at<BN>(ta, i, gated)),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// MANY: units of more than one chunk (a kernel of their own: the chunks' sums
+// cost the others registers).
+template <int BN, int IN, int OUT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   using G = PairCfg<BN>;
   static_assert(pair_bytes<BN>() <= 227 * 1024, "shared memory");
   constexpr int NS = G::NS, EW = G::EW;
+  // the sums' own place in tensor memory, behind the two accumulators, where it is large enough
+  constexpr bool SPARE = MANY && BN == 128;
+  constexpr uint32_t COLS = SPARE ? 4 * BN : 2 * BN;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sr = smem;                       // rows' operand: the 128-row operand of each CTA
   uint8_t* sc = smem + NS * G::RBytes;      // columns' operand
@@ -762,7 +850,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
   }
   pdl_wait();  // the kernel before this one is complete; tensor memory only from here on
   if (warp == EW + 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(2u * BN) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -837,17 +925,24 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
         bool ok = gives_up != kGemmMmas;
         int s = 0;
         uint32_t phase = 0, acc = 0, acc_phase = 1;  // the first round finds both accumulators free
-        int stages = 0, units = 0;
+        int stages = 0, chunks = 0;
         for (int u = first; u < p.units && ok; u += step) {
-          ok = bar_wait(acc_empty + 8 * acc, acc_phase, limit);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          for (int kb = 0; kb < p.KB; ++kb) {
+          for (int kb = 0, in = 0; kb < p.KB; ++kb, ++in) {
+            if (MANY && in == kChunk<OUT>) {
+              pair_commit(acc_full + 8 * acc, leader);
+              ++chunks, in = 0;
+              acc ^= 1;
+              acc_phase ^= acc ^ 1;
+            }
+            if (in == 0) {
+              ok = bar_wait(acc_empty + 8 * acc, acc_phase, limit);
+              if (!ok) break;
+            }
             ok = bar_wait(full + 8 * s, phase, limit);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             pair_stage(tm + BN * acc, a0 + (uint32_t)(s * (G::RBytes >> 4)), as, b0 + (uint32_t)(s * (G::CBytes >> 4)), bs, idesc,
-                       kb > 0, leader);
+                       in > 0, leader);
             pair_commit(empty + 8 * s, leader);
             ++stages;
             if (++s == NS) {
@@ -857,7 +952,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
           }
           if (!ok) break;
           pair_commit(acc_full + 8 * acc, leader);
-          ++units;
+          ++chunks;
           acc ^= 1;
           acc_phase ^= acc ^ 1;
         }
@@ -866,7 +961,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
         for (int i = 0; i < NS; ++i)
           if (i < stages) (void)bar_wait(empty + 8 * i, ((stages - 1 - i) / NS) & 1, kWaitLimit);
         for (int i = 0; i < 2; ++i)
-          if (i < units) (void)bar_wait(acc_full + 8 * i, ((units - 1 - i) / 2) & 1, kWaitLimit);
+          if (i < chunks) (void)bar_wait(acc_full + 8 * i, ((chunks - 1 - i) / 2) & 1, kWaitLimit);
       }
     }
   } else {
@@ -880,14 +975,32 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
     bool ok = gives_up != kGemmSums;
     uint32_t acc = 0, acc_phase = 0;
     for (int u = first; u < p.units; u += step) {
-      const PairUnit un = pair_unit(u, p, width);
+      const uint32_t ta = tmem + ((uint32_t)l0 << 16) + cols * half;
+      int unit = u;
+      if constexpr (MANY) {
+        float sum[BN / 2];
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) sum[j] = 0.f;
+#pragma unroll 1
+        for (int kb = kChunk<OUT>;; kb += kChunk<OUT>) {
+          ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          add_chunk<BN>(sum, ta + BN * acc, gated);
+          if (!SPARE && kb >= p.KB) break;
+          pair_release(acc_empty + 8 * acc, ok);
+          acc ^= 1;
+          acc_phase ^= acc ^ 1;
+          if (kb >= p.KB) break;
+        }
+        if (ok) put_sums<BN>(sum, ta + (SPARE ? 2 * BN : BN * acc), gated);
+        asm volatile("" : "+r"(unit));  // what follows is worked out behind the sums, not beside them
+      }
+      const PairUnit un = pair_unit(unit, p, width);
       WarpTile t;
-      t.ta = tmem + ((uint32_t)l0 << 16) + BN * acc + cols * half;
       t.r0 = (int64_t)un.r0 + 128 * rank + l0;
       t.rows = (int)min((int64_t)32, p.R - t.r0);
       t.c0 = un.c0 + cols * half;
       t.cols = cols;
-      t.release = acc_empty + 8 * acc;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = lane + 32 * j;
@@ -895,8 +1008,12 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
         t.bias[j] = there ? half_bits(static_cast<const uint16_t*>(p.bias)[t.c0 + c], IN) : 0.f;
         if (j < 2) t.bias_up[j & 1] = there && gated ? half_bits(static_cast<const uint16_t*>(p.bias)[p.C + t.c0 + c], IN) : 0.f;
       }
-      ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if constexpr (!MANY) {
+        ok = ok && bar_wait(acc_full + 8 * acc, acc_phase, limit);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      }
+      t.ta = ta + (SPARE ? 2 * BN : BN * acc);
+      t.release = SPARE ? 0 : acc_empty + 8 * acc;
       if constexpr (VEC) {
         switch (p.act) {
           case kActNone: finish_straight<IN, OUT, kActNone>(p, t, BN / 2, ok); break;
@@ -933,8 +1050,10 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
         }
       }
       if (!ok) sm->err = 1;
-      acc ^= 1;
-      acc_phase ^= acc ^ 1;
+      if (!SPARE) {
+        acc ^= 1;
+        acc_phase ^= acc ^ 1;
+      }
     }
   }
   __syncwarp();
@@ -943,7 +1062,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const _
   cluster_barrier();  // neither leaves, or frees its tensor memory, before the other is done
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (tid == 0 && *(volatile int*)&sm->err && p.status) atomicOr(p.status, DEV_ERR_TIMEOUT);
-  if (warp == EW + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * BN) : "memory");
+  if (warp == EW + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(COLS) : "memory");
 }
 
 // 16-bit rows, `ld` elements apart: a K-major operand has `rows` rows of k
@@ -1065,7 +1184,7 @@ const char* gemm_split(const GemmArgs& a, int split, cudaStream_t s) {
 
 // Pairs of CTAs that the device runs at once (its SMs come in groups, some of
 // odd size), asked for once.
-template <int BN, int IN, int OUT, bool VEC>
+template <int BN, int IN, int OUT, bool VEC, bool MANY>
 int pairs_at_once(int sms) {
   static std::atomic<int> known[64];
   int device = 0;
@@ -1083,7 +1202,7 @@ int pairs_at_once(int sms) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<BN, IN, OUT, VEC>, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<BN, IN, OUT, VEC, MANY>, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
     n = sms / 2 > 0 ? sms / 2 : 1;
   }
@@ -1091,7 +1210,7 @@ int pairs_at_once(int sms) {
   return n;
 }
 
-template <int BN, int IN, int OUT, bool VEC>
+template <int BN, int IN, int OUT, bool VEC, bool MANY>
 const char* gemm_pair_vec(const GemmArgs& a, int sms, cudaStream_t s) {
   GemmParams p = params_of(a);
   const bool gated = a.act == kActSwiglu;
@@ -1103,16 +1222,18 @@ const char* gemm_pair_vec(const GemmArgs& a, int sms, cudaStream_t s) {
   p.units_r = (int)units_r;
   p.units = (int)(units_c * units_r);
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = configure((const void*)gemm_pair_kernel<BN, IN, OUT, VEC>, pair_bytes<BN>(), configured);
+  cudaError_t e = configure((const void*)gemm_pair_kernel<BN, IN, OUT, VEC, MANY>, pair_bytes<BN>(), configured);
   if (e != cudaSuccess) return cudaGetErrorString(e);
-  const int pairs = pairs_at_once<BN, IN, OUT, VEC>(sms);
-  e = launch_cluster(gemm_pair_kernel<BN, IN, OUT, VEC>, 2 * (int64_t)(p.units < pairs ? p.units : pairs), PairCfg<BN>::NTHR, pair_bytes<BN>(), 2, s, p);
+  const int pairs = pairs_at_once<BN, IN, OUT, VEC, MANY>(sms);
+  e = launch_cluster(gemm_pair_kernel<BN, IN, OUT, VEC, MANY>, 2 * (int64_t)(p.units < pairs ? p.units : pairs), PairCfg<BN>::NTHR, pair_bytes<BN>(), 2, s, p);
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
 
 template <int BN, int IN, int OUT>
 const char* gemm_pair(const GemmArgs& a, int sms, cudaStream_t s) {
-  return vec16(a) ? gemm_pair_vec<BN, IN, OUT, true>(a, sms, s) : gemm_pair_vec<BN, IN, OUT, false>(a, sms, s);
+  if (a.K > kMK * kChunk<OUT>)
+    return vec16(a) ? gemm_pair_vec<BN, IN, OUT, true, true>(a, sms, s) : gemm_pair_vec<BN, IN, OUT, false, true>(a, sms, s);
+  return vec16(a) ? gemm_pair_vec<BN, IN, OUT, true, false>(a, sms, s) : gemm_pair_vec<BN, IN, OUT, false, false>(a, sms, s);
 }
 
 // Which form: up to 64 rows (of a K-major operand) the weights stream past
@@ -1136,18 +1257,23 @@ const char* gemm(const GemmArgs& a, int sms, cudaStream_t s) {
   // enough; one that turns its rows in shared memory takes the products' bandwidth
   // there, and adds to them (3000 x 3001 x 3000 63 us by 128 columns, 48 by 256)
   const bool whole = vec16(a);
+  // fp32 sums of many chunks: by 256 columns they go back to the accumulator they
+  // came from, and the epilogue holds up the next products; by 128 a chunk's
+  // change costs a little (by 128 | 256: 8192 x 7168 x 7168 493 | 479, 4096 x 7168 x
+  // 2048 83 | 99; in one chunk 469 | 440 and 80 | 71, with the sums short of bits)
+  const bool many = OUT == 2 && KB > kChunk<OUT>;
   const auto pair_time = [&](int bn, double step, double epilogue) {
     const int width = a.act == kActSwiglu ? bn / 2 : bn;
     const double units = (double)((a.C + width - 1) / width) * (double)((a.R + 255) / 256);
     const double both = KB * step + epilogue, one = KB * step > epilogue ? KB * step : epilogue;
-    return 4.6 + (rounds(units, sms / 2) - 1) * (whole ? one : both) + both;
+    return 4.6 + (rounds(units, sms / 2) - 1) * (whole && !(many && bn == 256) ? one : both) + both;
   };
   const int split = split_of(a, 64, sms);
   const double blocks = (double)split_units(a, 64) * split;
   double part_log = 0;
   for (int q = split; q > 1; q /= 2) ++part_log;
   const double by_64 = 4.2 + 0.5 * part_log + rounds(blocks, 2 * sms) * (2.6 + (KB + split - 1) / split * (blocks > sms ? 0.27 : 0.2));
-  const double by_128 = pair_time(128, 0.155, whole ? 2.2 : 4.5), by_256 = pair_time(256, 0.29, whole ? 3.4 : 5.4);
+  const double by_128 = pair_time(128, many ? 0.163 : 0.155, whole ? 2.2 : 4.5), by_256 = pair_time(256, 0.29, whole ? 3.4 : 5.4);
   if (by_64 <= by_128 && by_64 <= by_256) return gemm_split<64, IN, OUT>(a, split, s);
   return by_128 < by_256 ? gemm_pair<128, IN, OUT>(a, sms, s) : gemm_pair<256, IN, OUT>(a, sms, s);
 }

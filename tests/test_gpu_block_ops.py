@@ -208,6 +208,30 @@ def test_product_of_infinities_and_nan_stays_in_its_row(dfm, M):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("M, N, K, act", [(4, 64, 40000, "none"), (48, 128, 20000, "swiglu"), (100, 200, 33000, "none"), (2100, 1024, 9001, "none"),
+                                          (2100, 640, 9001, "swiglu"), (2100, 2050, 7000, "relu"), (5000, 2048, 1600, "none")])
+def test_product_sums_keep_their_bits(dfm, M, N, K, act):
+    """Of positive terms, so that no error cancels. An addition in tensor memory
+    may drop all behind the last bit (2 U): 48 of 16 products each make a part (some
+    8 bits of slack for the products of one, aligned to their largest: as much
+    again), and the parts are added with U each."""
+    g = gen(K)
+    x = torch.rand(M, -(-K // 8) * 8, generator=g, device="cuda").to(torch.bfloat16)
+    wide = 2 * N if act == "swiglu" else N
+    w = torch.rand(wide, -(-K // 8) * 8, generator=g, device="cuda").to(torch.bfloat16)
+    y, b = torch.empty(M, N, device="cuda"), None
+    if act == "swiglu":  # the gate: 0 but for one column of x, so that silu(1) times the up product's sum is left
+        w[:N] = 0
+        b = torch.zeros(wide, dtype=torch.bfloat16, device="cuda")
+        b[:N] = 1
+    dfm.matmul(x, w, "bf16", M, N, K, y, "f32", bias=b, act=act, ldx=x.stride(0), ldw=w.stride(0))
+    want = x[:, :K].double() @ w[wide - N:, :K].double().t()
+    if act == "swiglu":
+        want = want * torch.sigmoid(torch.tensor(1.0, device="cuda", dtype=torch.float64))
+    parts = -(-K // 768) + 8
+    assert bool(((y.double() - want).abs() <= (4 * 48 + parts + (128 if act == "swiglu" else 0)) * U * want).all())
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
 def test_activations_at_their_ends(dfm, act):
     """Large arguments of either sign: 0 or z, never NaN."""
@@ -759,6 +783,32 @@ def test_balance_strides(dfm, case, pad):
 @pytest.mark.parametrize("case", [BALANCE[3], BALANCE[4], BALANCE[5]], ids=lambda c: "-".join(map(str, c)))
 def test_balance_with_experts_that_are_not_allowed(dfm, case):
     check_balance(dfm, *case, closed=True)
+
+
+@pytest.mark.parametrize("T, E, k, dtype, drop", [
+    (2, 896, 32, "f32", 0.0), (17, 300, 5, "bf16", 0.3), (64, 1024, 8, "f32", 0.1), (127, 897, 16, "f16", 0.0), (128, 896, 16, "f32", 0.5),
+    (129, 896, 16, "f32", 0.1), (100, 128, 9, "bf16", 0.0), (129, 128, 9, "f32", 0.0), (200, 64, 32, "f32", 0.2), (257, 61, 12, "f16", 0.1),
+    (512, 32, 32, "f32", 0.1), (513, 20, 20, "bf16", 0.0), (40, 3, 32, "f32", 0.1), (40, 1, 32, "f32", 0.0), (5, 1024, 3, "f32", 1.0),
+])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_balance_of_few_rows(dfm, T, E, k, dtype, drop, score):
+    """Rows of one sequence that a cluster finishes, and just above; tokens that
+    name an expert many times, over several lots of a row's lanes."""
+    check_balance(dfm, T, E, k, dtype, score, 1, drop)
+
+
+@pytest.mark.parametrize("T, E", [(60, 20), (700, 100), (700, 900)])
+def test_balance_gradient_in_place(dfm, T, E):
+    g = gen(T + E)
+    z, ids = randn(T, E, g=g), torch.randint(0, E, (T, 4), generator=g, device="cuda", dtype=torch.int32)
+    loss, counts, tokens = torch.empty(1, device="cuda"), torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    size = dfm.balance_loss_workspace(T, E, 1)
+    kw = dict(coef=0.5, z_coef=0.01)
+    dfm.balance_loss(z, "f32", T, E, ids, 4, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size, **kw)
+    one, want = torch.ones(1, device="cuda"), torch.empty_like(z)
+    dfm.balance_loss_grad(one, z, "f32", T, E, ids, 4, counts, tokens, want, **kw)
+    dfm.balance_loss_grad(one, z, "f32", T, E, ids, 4, counts, tokens, z, **kw)
+    assert torch.equal(z, want)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
