@@ -369,6 +369,23 @@ def test_product_whose_wait_runs_out_says_so(dfm, M, N, K, role):
     assert torch.equal(y[good], again[good])
 
 
+@pytest.mark.parametrize("M, N, K, out", [(4, 256, 20000, "f32"), (300, 256, 20000, "f32"), (3000, 2304, 2500, "f32"), (3000, 2050, 2500, "f32"),
+                                          (3000, 512, 30000, "bf16")])
+@pytest.mark.parametrize("role", [1, 2, 3])
+def test_product_of_many_parts_whose_wait_runs_out_says_so(dfm, M, N, K, out, role):
+    g, _, x, w, _ = product_inputs(M, N, K, "bf16", "none", False, 9)
+    y, again = (torch.zeros(M, N, device="cuda", dtype=DT[out]) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dfm.test_matmul_give_up(role)
+    dfm.matmul(x, w, "bf16", M, N, K, y, out, status=status, ldx=x.stride(0), ldw=w.stride(0))
+    assert status.item() == 2 and bool(torch.isnan(y).any())
+    good = ~torch.isnan(y)
+    status.zero_()
+    dfm.matmul(x, w, "bf16", M, N, K, again, out, status=status, ldx=x.stride(0), ldw=w.stride(0))
+    assert status.item() == 0 and bool(torch.isfinite(again).all())
+    assert torch.equal(y[good], again[good])
+
+
 def test_product_rows_past_32_bits(dfm):
     """More than 2^31 elements of y, and of x."""
     M, N, K = 300_000, 8192, 8
