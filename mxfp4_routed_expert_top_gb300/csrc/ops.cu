@@ -502,6 +502,7 @@ DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, cons
   dfm::GemmArgs a{};
   a.in = dtype;
   a.status = status;
+  const int64_t columns = (K + 127) / 128;  // of tiles, of both
   const dfm::GemmOperand grad = {act ? dz : dy, act ? lddz : lddy, false};
   if (dx) {
     a.row = grad;
@@ -512,6 +513,8 @@ DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, cons
     a.out = dtype;
     a.y = dx;
     a.ldy = lddx;
+    a.order = dw ? dfm::kGemmFirst : dfm::kGemmAlone;
+    a.beside = dw ? ((wide + 63) / 64) * columns : 0;
     a.give_up = gemm_give_up_next;
     gemm_give_up_next = 0;
     if ((rc = gemm_done("gradient of x", dfm::launch_gemm(a, on.sms(), s)))) return rc;
@@ -526,6 +529,8 @@ DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, cons
     a.out = grad_dtype;
     a.y = dw;
     a.ldy = lddw;
+    a.order = dx ? dfm::kGemmSecond : dfm::kGemmAlone;
+    a.beside = dx ? ((M + 63) / 64) * columns : 0;
     a.give_up = gemm_give_up_next;
     gemm_give_up_next = 0;
     if ((rc = gemm_done("gradient of w", dfm::launch_gemm(a, on.sms(), s)))) return rc;

@@ -111,7 +111,12 @@ struct GemmArgs {
   int64_t ldr, ldp, ldy;
   uint32_t* status;
   int give_up;
+  // kGemmFirst: kGemmSecond comes next, of the same call, and does not need
+  // this one's output: it may run beside it.
+  int order;
+  int64_t beside;  // tiles of 64 x 128 of the other's output
 };
+enum { kGemmAlone = 0, kGemmFirst, kGemmSecond };
 const char* launch_gemm(const GemmArgs& a, int sms, cudaStream_t s);
 // of one pair of types each
 const char* gemm_bf16(const GemmArgs& a, int sms, cudaStream_t s);

@@ -323,6 +323,40 @@ def test_product_gradient_of_no_rows_is_zero(dfm):
     assert bool((dw == 0).all()) and bool((db == 0).all()) and unmarked(dw, 3.0)
 
 
+@pytest.mark.parametrize("M, N, K", [(9000, 64, 2048), (64, 5000, 2048), (700, 200, 2048)])
+def test_what_follows_a_product_gradient_finds_both(dfm, M, N, K):
+    """dx and dw run side by side; a kernel behind them reads either whole, also
+    from a graph."""
+    g, _, x, w, _ = product_inputs(M, N, K, "bf16", "none", False, 17)
+    dy = randn(M, N, g=g, dtype="bf16")
+    dx, n = (torch.zeros(M, K, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dw, m = (torch.zeros(N, K, device="cuda") for _ in range(2))  # fp32, as dw is by default
+
+    def run():
+        dx.zero_()
+        dw.zero_()
+        dfm.matmul_grad(dy, x, w, "bf16", M, N, K, dx=dx, dw=dw)
+        dfm.block_norm(None, dx, "bf16", M, K, n=n)
+        dfm.block_norm(None, dw, "f32", N, K, n=m)
+    dfm.matmul_grad(dy, x, w, "bf16", M, N, K, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    want = torch.empty_like(n), torch.empty_like(m)
+    dfm.block_norm(None, dx, "bf16", M, K, n=want[0])
+    dfm.block_norm(None, dw, "f32", N, K, n=want[1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        run()
+        assert torch.equal(n, want[0]) and torch.equal(m, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        n.zero_()
+        m.zero_()
+        graph.replay()
+        assert torch.equal(n, want[0]) and torch.equal(m, want[1])
+
+
 def test_product_gradient_against_differences(dfm):
     """<dx, d> is how the loss <dy, y> moves along d: central differences of the
     definition in 64 bits."""
