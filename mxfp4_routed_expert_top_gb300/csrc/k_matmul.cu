@@ -2,6 +2,8 @@
 // of the product's types; the product is in k_matmul.cuh, a file a pair of types.
 #include "k_matmul.cuh"
 
+#include <type_traits>
+
 namespace dfm {
 namespace {
 
@@ -9,13 +11,13 @@ namespace {
 // dz = act'(z) dy (gated: [dy u silu'(g) | dy silu(g)]) and its column sums.
 // VEC: a thread has eight columns of a row, a block 64 columns and every
 // parts-th 32 rows; else a thread a column, a warp a row, a block 32 columns. A
-// few rows' loads go out together. The column sums of the parts meet in the
+// few rows' loads go out together (kAgRows). The column sums of the parts meet in the
 // cluster's shared memory, in their order.
 struct ActGradParams {
   const void *dy, *pre;
   void *dz, *dbias;
   int64_t M, lddy, ldp, lddz;
-  int N, act, grad, parts, follows;
+  int N, grad, parts, follows;
 };
 constexpr int kAgThreads = 256;
 
@@ -26,18 +28,26 @@ __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162floa
 template <>
 __device__ __forceinline__ float value(__half v) { return __half2float(v); }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParams p) {
+// U: rows a thread loads together, as many as the registers of four blocks an SM
+// hold: HBM bounds it, and it is the bytes on their way that bring its rate
+// (4096 x 2048 swiglu 15.9 us, 5.3 TB/s; twice the rows spill, 26). A kernel an
+// activation: with all of them in one it had 128 registers and took 32 us;
+// 8192 x 7168 gelu with bias 90 (3.9 TB/s), 226 in one.
+template <bool VEC, int ACT>
+constexpr int kAgRows = !VEC || ACT == kActNone ? 8 : ACT == kActSwiglu ? 1 : 2;
+
+template <typename T, bool VEC, int ACT>
+__global__ void __launch_bounds__(kAgThreads, 4) act_grad_kernel(const ActGradParams p) {
   constexpr int E = VEC ? 8 : 1;               // columns a thread
   constexpr int LANES = VEC ? 8 : 32;          // threads a row
   constexpr int ROWS = kAgThreads / LANES;     // rows at a time
-  constexpr int COLS = E * LANES, U = VEC ? 2 : 8;  // columns a block, rows a thread loads together
+  constexpr int COLS = E * LANES, U = kAgRows<VEC, ACT>;  // columns a block
+  constexpr bool gated = ACT == kActSwiglu, some = ACT != kActNone;
   __shared__ float sums[kAgThreads / 32][2][COLS];
   __shared__ float total[2][COLS];
   const int tid = threadIdx.x, tx = tid % LANES, ty = tid / LANES;
   const int strip = blockIdx.x / p.parts, part = blockIdx.x - strip * p.parts;
   const int c = COLS * strip + E * tx;
-  const bool gated = p.act == kActSwiglu, some = p.act != kActNone;
   float s0[E], s1[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) s0[j] = s1[j] = 0.f;
@@ -50,6 +60,7 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
   struct alignas(2 * E) Part { T v[E]; };
   const auto get = [](const T* q) { return *reinterpret_cast<const Part*>(q); };
   if (c < p.N) {
+#pragma unroll 1
     for (int64_t r0 = (int64_t)ROWS * part + ty; r0 < p.M; r0 += (int64_t)U * ROWS * p.parts) {
       Part d[U] = {}, z[U] = {}, u[U] = {};
 #pragma unroll
@@ -60,27 +71,25 @@ __global__ void __launch_bounds__(kAgThreads) act_grad_kernel(const ActGradParam
         if (some) z[i] = get(pre + r * p.ldp);
         if (gated) u[i] = get(pre + r * p.ldp + p.N);
       }
-      float g[U * E], slope[U * E];
-      if (some) {
-#pragma unroll
-        for (int i = 0; i < U * E; ++i) g[i] = value(z[i / E].v[i % E]);
-        slope_all(slope, g, p.act);
-      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int64_t r = r0 + (int64_t)i * ROWS * p.parts;
-        if (r >= p.M) continue;
+        if (r >= p.M) break;
+        float g[E + E % 2], slope[E + E % 2];  // pairs
+#pragma unroll
+        for (int j = 0; j < E + E % 2; ++j) g[j] = some ? value(z[i].v[j % E]) : 0.f;
+        if (some) slope_all(slope, g, ACT);
         Part a, b;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           float x = value(d[i].v[j]);
           if (gated) {
-            const float y = x * (g[i * E + j] * sigmoid_f(g[i * E + j]));
+            const float y = x * (g[j] * sigmoid_f(g[j]));
             x *= value(u[i].v[j]);
             s1[j] += y;
             b.v[j] = T(y);
           }
-          if (some) x *= slope[i * E + j];
+          if (some) x *= slope[j];
           s0[j] += x;
           a.v[j] = T(x);
         }
@@ -147,20 +156,30 @@ const char* launch_act_grad(const ActGradArgs& a, int sms, cudaStream_t s) {
   p.ldp = a.ldp;
   p.lddz = a.lddz;
   p.N = a.N;
-  p.act = a.act;
   p.grad = a.grad;
   p.follows = a.follows;
   const bool some = a.act != kActNone;
   const bool vec = a.N % 8 == 0 && aligned(a.dy, a.lddy, 16, 2) && (!some || (aligned(a.pre, a.ldp, 16, 2) && aligned(a.dz, a.lddz, 16, 2)));
-  const int cols = vec ? 64 : 32, rows = 64;  // columns of a block, rows that it loads at once
+  const int cols = vec ? 64 : 32, rows = 64;  // columns of a block, rows that give it work
   const int64_t strips = (a.N + cols - 1) / cols, most = a.dbias ? 8 : 1 << 20;
   int64_t parts = 1;
   while (2 * parts <= most && rows * parts < a.M && strips * parts < 8 * sms) parts *= 2;
   p.parts = (int)parts;
   const int cluster = a.dbias ? p.parts : 1;
   const auto launch = [&](auto kernel) { return launch_cluster(kernel, strips * parts, kAgThreads, 0, cluster, s, p); };
-  const cudaError_t e = a.in == 0 ? (vec ? launch(act_grad_kernel<__nv_bfloat16, true>) : launch(act_grad_kernel<__nv_bfloat16, false>))
-                                  : (vec ? launch(act_grad_kernel<__half, true>) : launch(act_grad_kernel<__half, false>));
+  const auto by_act = [&](auto t, auto v) {
+    using T = decltype(t);
+    constexpr bool V = decltype(v)::value;
+    switch (a.act) {
+      case kActNone: return launch(act_grad_kernel<T, V, kActNone>);
+      case kActRelu: return launch(act_grad_kernel<T, V, kActRelu>);
+      case kActSilu: return launch(act_grad_kernel<T, V, kActSilu>);
+      case kActGelu: return launch(act_grad_kernel<T, V, kActGelu>);
+      default: return launch(act_grad_kernel<T, V, kActSwiglu>);
+    }
+  };
+  const auto by_rows = [&](auto t) { return vec ? by_act(t, std::true_type{}) : by_act(t, std::false_type{}); };
+  const cudaError_t e = a.in == 0 ? by_rows(__nv_bfloat16{}) : by_rows(__half{});
   return e == cudaSuccess ? nullptr : cudaGetErrorString(e);
 }
 
