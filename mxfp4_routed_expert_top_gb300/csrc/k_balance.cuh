@@ -148,7 +148,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Sum and maximum of a lane's values, in four chains.
+// Sum and maximum of a lane's values, in four chains. (Here and below one
+// instruction does a pair of values where it can: issue slots bound the long
+// rows as much as their latency.)
 template <int N>
 __device__ __forceinline__ float lane_max(const float (&v)[N]) {
   float m[4] = {v[0], v[1], v[2], v[3]};
@@ -158,10 +160,11 @@ __device__ __forceinline__ float lane_max(const float (&v)[N]) {
 }
 template <int N>
 __device__ __forceinline__ float lane_sum(const float (&v)[N]) {
-  float m[4] = {v[0], v[1], v[2], v[3]};
+  Pair a = pair(v[0], v[1]), b = pair(v[2], v[3]);
 #pragma unroll
-  for (int i = 4; i < N; ++i) m[i & 3] += v[i];
-  return (m[0] + m[1]) + (m[2] + m[3]);
+  for (int i = 4; i < N; i += 4) a = add2(a, pair(v[i], v[i + 1])), b = add2(b, pair(v[i + 2], v[i + 3]));
+  const float2 x = halves(a), y = halves(b);
+  return (x.x + x.y) + (y.x + y.y);
 }
 
 // v becomes exp(v - l + log(scale)), l = logsumexp(v); `scale` is what the
@@ -174,7 +177,10 @@ __device__ __forceinline__ float softmax_row(float (&v)[N], float* scale) {
   const float most = warp_max<L>(lane_max(v));
   const float base = most == -INFINITY ? 0.f : most * kLog2e;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = exp2_fast(fmaf(v[i], kLog2e, -base));
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = halves(fma2(pair(v[i], v[i + 1]), both(kLog2e), both(-base)));
+    v[i] = exp2_fast(x.x), v[i + 1] = exp2_fast(x.y);
+  }
   const float sum = warp_sum<L>(lane_sum(v));
   *scale = sum == 0.f ? 0.f : 1.f / sum;
   return sum == 0.f ? 0.f : kLn2 * (base + log2f(sum));
@@ -188,10 +194,17 @@ __device__ __forceinline__ void sigmoid_row(float (&v)[N], float* m, float* scal
   const float most = warp_max<L>(lane_max(v));
   const float M = most == -INFINITY ? 0.f : fminf(most, 0.f) * kLog2e, low = exp2_fast(M);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float e = fminf(exp2_fast(fmaf(-v[i], kLog2e, M)), 1e37f), r = __fdividef(1.f, low + e);
-    if (REST) m[i] = v[i] != v[i] ? v[i] : e * r;
-    v[i] = v[i] == -INFINITY ? 0.f : v[i] != v[i] ? v[i] : r;  // fminf drops a NaN
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = halves(fma2(pair(v[i], v[i + 1]), both(-kLog2e), both(M)));
+    const float e[2] = {fminf(exp2_fast(x.x), 1e37f), fminf(exp2_fast(x.y), 1e37f)};
+    const float2 sum = halves(add2(pair(e[0], e[1]), both(low)));
+    const float r[2] = {__fdividef(1.f, sum.x), __fdividef(1.f, sum.y)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float& z = v[i + j];
+      if (REST) m[i + j] = z != z ? z : e[j] * r[j];
+      z = z == -INFINITY ? 0.f : z != z ? z : r[j];  // fminf drops a NaN
+    }
   }
   const float sum = warp_sum<L>(lane_sum(v));
   *scale = sum == 0.f ? 0.f : 1.f / sum;
@@ -300,7 +313,7 @@ __device__ __forceinline__ void finish_alone(const BalanceArgs& p, float* sums, 
 // 16 us, with one a warp 21). The sums of the probabilities go to shared memory, a
 // place a lane and value (in registers they cost the warps that hide the loads).
 // With the join 16384 rows of 896 f32 take 20 us (3.0 TB/s: the exponentials and
-// the adds of a value bound it as much as its bytes), sigmoid 31.
+// the adds of a value bound it as much as its bytes), sigmoid 26.
 // alone: the blocks are one cluster, which finishes the call.
 template <typename T, bool VEC, int NV, int L, bool SIGMOID>
 __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const BalanceArgs p, const Entries out, int chunk_rows, int alone) {
@@ -361,10 +374,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
         zz += squares;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          float4 v = mine[32 * i];
-          v.x = fmaf(z[4 * i], scale, v.x), v.y = fmaf(z[4 * i + 1], scale, v.y);
-          v.z = fmaf(z[4 * i + 2], scale, v.z), v.w = fmaf(z[4 * i + 3], scale, v.w);
-          mine[32 * i] = v;
+          const float4 v = mine[32 * i];
+          const float2 a = halves(fma2(pair(z[4 * i], z[4 * i + 1]), both(scale), pair(v.x, v.y)));
+          const float2 b = halves(fma2(pair(z[4 * i + 2], z[4 * i + 3]), both(scale), pair(v.z, v.w)));
+          mine[32 * i] = make_float4(a.x, a.y, b.x, b.y);
         }
       }
     }
@@ -397,14 +410,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
 
 template <int L, int NV>
 __device__ __forceinline__ float dot_row(const float4* f, const float (&v)[4 * NV]) {
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  Pair d[2] = {both(0.f), both(0.f)};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const float4 a = f[32 * i];
-    d[0] = fmaf(a.x, v[4 * i], d[0]), d[1] = fmaf(a.y, v[4 * i + 1], d[1]);
-    d[2] = fmaf(a.z, v[4 * i + 2], d[2]), d[3] = fmaf(a.w, v[4 * i + 3], d[3]);
+    d[0] = fma2(pair(a.x, a.y), pair(v[4 * i], v[4 * i + 1]), d[0]);
+    d[1] = fma2(pair(a.z, a.w), pair(v[4 * i + 2], v[4 * i + 3]), d[1]);
   }
-  return warp_sum<L>((d[0] + d[1]) + (d[2] + d[3]));
+  const float2 x = halves(d[0]), y = halves(d[1]);
+  return warp_sum<L>((x.x + x.y) + (y.x + y.y));
 }
 
 constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
@@ -413,7 +427,7 @@ constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
 // third of the warps). The routing weights' terms reach the lanes that hold their
 // experts through rows of shared memory that are zero between (comparing every
 // expert with every id took more instructions than the rest). 16384 rows of 896
-// f32 26 us (4.5 TB/s), sigmoid 44; 65536 of 128 22 (33 with one row a warp).
+// f32 26 us (4.5 TB/s), sigmoid 43; 65536 of 128 22 (33 with one row a warp).
 template <typename T, bool VEC, int NV, int L, bool SIGMOID>
 __global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : 2) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
   extern __shared__ __align__(16) float shared[];  // [warps][NV][32 lanes][4] f, and with weights the same of their terms
@@ -553,11 +567,13 @@ __global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : 2) balance_grad_
         const float4 fi = f4[32 * i];
         const float f[4] = {fi.x, fi.y, fi.z, fi.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; j += 2) {
           const int c = 4 * i + j;
-          d[c] = m[c] * fmaf(scale * d[c], f[j] - dot, x[j]);
-          if (p.z_coef != 0.f) d[c] = fmaf(soft, z[c], d[c]);
-          z[c] = d[c];
+          const Pair t = fma2(mul2(both(scale), pair(d[c], d[c + 1])), add2(pair(f[j], f[j + 1]), both(-dot)), pair(x[j], x[j + 1]));
+          Pair r = mul2(pair(m[c], m[c + 1]), t);
+          if (p.z_coef != 0.f) r = fma2(both(soft), pair(z[c], z[c + 1]), r);
+          const float2 h = halves(r);
+          z[c] = h.x, z[c + 1] = h.y;
         }
       }
     } else {
@@ -572,9 +588,11 @@ __global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : 2) balance_grad_
         const float4 fi = f4[32 * i];
         const float f[4] = {fi.x, fi.y, fi.z, fi.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; j += 2) {
           const int c = 4 * i + j;
-          z[c] = fmaf(z[c], fmaf(scale, f[j] - dot, rest), x[j]);
+          const Pair t = fma2(both(scale), add2(pair(f[j], f[j + 1]), both(-dot)), both(rest));
+          const float2 r = halves(fma2(pair(z[c], z[c + 1]), t, pair(x[j], x[j + 1])));
+          z[c] = r.x, z[c + 1] = r.y;
         }
       }
     }
