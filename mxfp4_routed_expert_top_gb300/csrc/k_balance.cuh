@@ -219,20 +219,23 @@ __device__ __forceinline__ Span sequence(const int32_t* offs, int s, int64_t T) 
   return {min(max((int64_t)offs[s], (int64_t)0), T), min(max((int64_t)offs[s + 1], (int64_t)0), T)};
 }
 // The last sequence that begins at or before `row` (-1: none), looked for by a
-// whole warp: 32 places a step.
+// whole warp: 32 places a step, the last 128 in one.
 __device__ __forceinline__ int sequence_of(const int32_t* offs, int S, int64_t row) {
   if (!offs) return 0;
   const int lane = threadIdx.x & 31;
   int lo = 0, n = S;  // it is lo - 1, or among the n from lo
-  while (n > 0) {
+  while (n > 128) {
     const int stride = (n + 31) / 32, i = lane * stride;
     const int before = __popc(__ballot_sync(0xffffffffu, i < n && offs[lo + min(i, n - 1)] <= row));
-    if (before == 0) break;
+    if (before == 0) return lo - 1;
     const int at = (before - 1) * stride;
     lo += at + 1;
     n = min(stride, n - at) - 1;
   }
-  return lo - 1;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) before += lane + 32 * i < n && offs[lo + lane + 32 * i] <= row;
+  return lo + warp_sum(before) - 1;
 }
 
 // A row's scores but for the factor `scale`, in z; returns the squared
@@ -265,9 +268,9 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A call of one cluster: the blocks' sums and counts [E], rows and squares meet
-// in its shared memory, in the blocks' order, each block for a share of the
-// experts. `scratch`: a value a warp.
+// A call of one cluster: the blocks' sums and counts [E], rows and squares
+// (thread 0's) meet in its shared memory, in the blocks' order, each block for a
+// share of the experts. `scratch`: a value a warp.
 __device__ __forceinline__ void finish_alone(const BalanceArgs& p, float* sums, int* count, int rows, float zz, float* scratch) {
   __shared__ int block_rows;
   __shared__ float block_zz, block_term;
@@ -385,8 +388,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const Balance
     zz = warp_sum(at.lane == 0 ? zz : 0.f);
     if (lane == 0) warp_rows[warp] = rows, warp_zz[warp] = zz;
     __syncthreads();
-    rows = 0, zz = 0.f;
-    for (int w = 0; w < kBalWarps; ++w) rows += warp_rows[w], zz += warp_zz[w];
+    if (warp == 0) {  // thread 0 has them
+      rows = warp_sum(lane < kBalWarps ? warp_rows[lane] : 0);
+      zz = warp_sum(lane < kBalWarps ? warp_zz[lane] : 0.f);
+    }
     const int64_t entry = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < p.E; e += kBalThreads) {
       const float* from = shared + at.place(e);
