@@ -1265,11 +1265,11 @@ const char* gemm_pair(const GemmArgs& a, int sms, cudaStream_t s) {
 // measurements with 152 SMs, say is the fastest: a start and an end, and so
 // much a step of 64 of k, times the rounds that the tiles take. Measured (bf16,
 // inputs not in L2; tiles of 64 rows in parts of k | pairs of 128 | of 256
-// columns): 1024 x 1024 x 1024 9.3 | 9.2 | 12.3; 256 x 2048 x 7168 15.6 | 23.5 |
-// 38; 256 x 7168 x 2048 15.9 | 13.2 | 17.4; 1024 x 2048 x 7168 36.7 | 24.9 |
-// 38.0; 512 x 7168 x 7168 66 | 43.8 | 39.5; 4096 x 7168 x 1536 128 | 58.0 | 51.1.
-// Tiles of 32 rows for 64: 64 x 2048 x 7168 10.9 (one tile of 64 12.1), 64 x 7168
-// x 2048 10.6 (11.1).
+// columns): 1024 x 1024 x 1024 8.9 | 7.8 | 10.6; 256 x 2048 x 7168 15.8 | 22.7 |
+// 36; 256 x 7168 x 2048 15.6 | 12.5 | 16.0; 1024 x 2048 x 7168 36.0 | 23.9 |
+// 37.0; 512 x 7168 x 7168 66 | 42.8 | 38.6; 4096 x 7168 x 1536 124 | 57.6 | 50.9.
+// Tiles of 32 rows for 64: 64 x 2048 x 7168 11.1 (one tile of 64 12.3), 64 x 7168
+// x 2048 10.8 (11.3).
 template <int IN, int OUT>
 const char* gemm(const GemmArgs& a, int sms, cudaStream_t s) {
   // boxes of an MN-major operand are 64 wide
