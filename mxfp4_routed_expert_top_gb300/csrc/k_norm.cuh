@@ -17,10 +17,13 @@
 // registers over its rows and meet in a second kernel, in order. Sums are fp32.
 // A row whose squares overflow fp32 is summed again at 2^-70.
 //
-// Three forms, by the rows. Whole 16-byte pieces: from 1025 to 8192 values
-// through a ring of bulk copies (block_norm_ring_kernel), shorter and longer
+// Three forms, by the rows. Whole 16-byte pieces: from 513 to 8192 values
+// through a ring of bulk copies (block_norm_ring_kernel), shorter, longer and few
 // ones straight from memory. Any other rows: value by value, in loops that are
 // not unrolled (block_norm_odd_kernel). One file a type includes this one.
+// Measured, bf16 with a channel's gate, in us (norms straight | ring, gradients
+// straight | ring): 8192 x 7168 149 | 77 (6.1 TB/s), 384 | 141 (5.0 TB/s); 8192 x
+// 2048 39 | 27, 103 | 47; 8192 x 640 22 | 15, 44 | 32; 304 x 7168 8.5 | 6.3, 26 | 18.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -997,9 +1000,13 @@ cudaError_t norm_tw(const BlockNormArgs& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     return launch_after_previous(block_norm_odd_kernel<T, W>, dim3((unsigned)p.T), dim3(kOddThreads), 4 * (size_t)p.H, s, p);
   }
-  if (p.H > 1024 && p.H <= 16 * kRingThreads && p.T > 4 * sms) {
-    const Shape sh = shape_of(p.H, 16);
-    const int each = kRingThreads / sh.threads, rows = z == 2 ? 2 : 1;  // blocks an SM, rows a stage
+  const Shape sh16 = shape_of(p.H, 16);
+  const int each = kRingThreads / sh16.threads;  // blocks an SM of the ring
+  // rows that all start at once gain nothing from a ring (152 x 7168 4.7 us straight
+  // and 5.3, 304 8.5 and 6.3; 304 x 2048 4.4 and 4.7, 1000 8.0 and 6.2)
+  if (p.H > 512 && p.H <= 16 * kRingThreads && p.T > (int64_t)sms * each) {
+    const Shape sh = sh16;
+    const int rows = z == 2 ? 2 : 1;  // rows a stage
     RingArrays r{};
     r.T = p.T;
     r.bytes = p.H * z;
@@ -1064,7 +1071,9 @@ cudaError_t grad_rows(const BlockNormGradArgs& p, float* part, int64_t* workers,
     return launch_after_previous(block_norm_grad_odd_kernel<T, W>, dim3((unsigned)n), dim3(kOddThreads), in_shared ? 8 * (size_t)p.H : 0, s, p, part,
                                  in_shared);
   }
-  if (p.H > 1024 && p.H <= 16 * kRingThreads) {
+  // short rows: from some rows a worker on (304 x 1024 8.5 us straight and 9.7, 1000
+  // 19 and 14; longer ones always: 1 x 7168 12 and 8.1)
+  if (p.H > 512 && p.H <= 16 * kRingThreads && (p.H > 1024 || p.T > 4 * sms)) {
     const Shape sh = shape_of(p.H, 16);
     const int each = kRingThreads / sh.threads;  // blocks an SM
     RingArrays r{};

@@ -677,6 +677,17 @@ def test_norm_gradient_of_some(dfm, kind, kw):
     check_norm_grad(dfm, 333, 264, "bf16", "f32", True, kind, 1.0, **kw)
 
 
+@pytest.mark.parametrize("case", [
+    (170, 7168, "bf16", "f32", True, "channel", 1.0), (700, 2048, "f16", "f32", True, "full", 0.5), (1300, 1024, "bf16", "bf16", True, "token", 1.0),
+    (1500, 520, "bf16", "f32", False, "channel", 1.0), (1250, 520, "f32", "f32", True, "full", -1.0), (620, 768, "f32", "f32", True, "channel", 1.0),
+    (1217, 648, "f16", "f16", False, "none", 1.0),
+], ids=lambda c: "-".join(map(str, c)))
+def test_norms_through_the_ring(dfm, case):
+    """Rows of every length that it takes, a few more than start at once."""
+    check_norm(dfm, *case)
+    check_norm_grad(dfm, *case)
+
+
 def test_norm_gradient_in_place_and_without_rows(dfm):
     T, H, g = 50, 128, gen(0)
     dh, dn, u, h = (rows(T, H, g, "bf16") for _ in range(4))
