@@ -19,8 +19,8 @@ MXFP8_ACT = 8
 PLANES = 16
 KERNEL_KINDS = 18
 BF16, F16, F32, E4M3 = 0, 1, 2, 3
-_DTYPES = {"bf16": BF16, "f16": F16, "f32": F32, "e4m3": E4M3,
-           BF16: BF16, F16: F16, F32: F32, E4M3: E4M3}
+_TYPES = {"bf16": (BF16, 2), "f16": (F16, 2), "f32": (F32, 4), "e4m3": (E4M3, 1)}  # and the bytes of an element
+_TYPES.update({t[0]: t for t in _TYPES.values()})
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 _GATES = {"none": 0, "channel": 1, "token": 2, "full": 3}
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -409,36 +409,57 @@ def _find_torch_stream(dev):
 _torch_stream = _find_torch_stream  # from the first call on, torch's own
 
 
-def _dtype(d):
+def _find_tensor_calls(a):
+    global _get_device, _element_size, _data_ptr
+    import sys
+    torch = sys.modules.get("torch")
+    if torch:
+        _get_device, _element_size, _data_ptr = torch.Tensor.get_device, torch.Tensor.element_size, torch.Tensor.data_ptr
+    raise TypeError
+
+
+# Of a tensor (TypeError for what is none): torch's own from the second call on,
+# which cost less than methods that are looked up.
+_get_device = _element_size = _data_ptr = _find_tensor_calls
+
+
+def _type(d):
     try:
-        return _DTYPES[d]
+        return _TYPES[d]
     except (KeyError, TypeError):
         raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,))
 
 
-def _place(*arrays):
+def _place(names, sizes, *arrays):
     """[device, address, address, ...]: the one CUDA device that the torch
     tensors among the arrays lie on (-1, the current one, where there are only
-    raw addresses), and the arrays' addresses."""
-    try:  # all of them tensors on one device
-        out = [a.data_ptr() for a in arrays]
-        dev = arrays[0].get_device()
+    raw addresses), and the arrays' addresses (0 for one that is absent). The
+    tensors' elements have to be `sizes` bytes (0: any): the library goes by the
+    types that the call names, and would pass the end of a narrower array.
+    `names`: the arrays', for what is refused."""
+    try:  # all of them tensors on one device, or absent
+        dev = _get_device(arrays[0])
         if dev >= 0:
-            for a in arrays:
-                if a.get_device() != dev:
+            out = [dev]
+            for a, n in zip(arrays, sizes):
+                if a is None:
+                    out.append(0)
+                elif _get_device(a) == dev and (_element_size(a) == n or not n):
+                    out.append(_data_ptr(a))
+                else:
                     break
             else:
-                return [dev, *out]
-    except AttributeError:
+                return out
+    except TypeError:
         pass
-    return _place_any(arrays)
+    return _place_any(names, sizes, arrays)
 
 
-def _place_any(arrays):
+def _place_any(names, sizes, arrays):
     dev, out = -1, [-1]
-    for a in arrays:
+    for i, a in enumerate(arrays):
         if a is None or a.__class__ is int:
-            out.append(a)
+            out.append(a or 0)
             continue
         try:
             d, p = a.get_device(), a.data_ptr()
@@ -452,6 +473,11 @@ def _place_any(arrays):
             dev = d
         elif d < 0:
             raise DfMoeError(EINVAL, "every array must be in device memory")
+        size = getattr(a, "element_size", None)
+        if size and sizes[i] and size() != sizes[i]:
+            name = names.split()[i]
+            if name != "status" or size() < 4:  # of a wider one the first word is taken
+                raise DfMoeError(EINVAL, "%s has elements of %d bytes, not of the %d that the call takes" % (name, size(), sizes[i]))
         out.append(p)
     out[0] = dev
     return out
@@ -483,13 +509,15 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
         _int32(k=k, E=E, n_scales=n_scales)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
+    dtype, n = _type(dtype)
     if workspace is None and scales is None and rows_scales is None:
-        dev, i, x, r, o, q, s = _place(ids, x, rows, offs, pos, src)
+        dev, i, x, r, o, q, s = _place("ids x rows offs pos src", (4, n, n, 4, 4, 4), ids, x, rows, offs, pos, src)
         w = xs = rs = None
     else:
-        dev, i, x, r, o, q, s, w, xs, rs = _place_any((ids, x, rows, offs, pos, src, workspace, scales,
-                                                       rows_scales))
-    rc = _c.df_moe_permute(dev, i, T, k, E, x, _dtype(dtype), H, ldx, xs, n_scales, ld_scales, r,
+        dev, i, x, r, o, q, s, w, xs, rs = _place("ids x rows offs pos src workspace scales rows_scales",
+                                                  (4, n, n, 4, 4, 4, 0, 4, 4), ids, x, rows, offs, pos, src, workspace,
+                                                  scales, rows_scales)
+    rc = _c.df_moe_permute(dev, i, T, k, E, x, dtype, H, ldx, xs, n_scales, ld_scales, r,
                            ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -499,8 +527,9 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
     """Gradient of permute's x (df_moe_permute_grad)."""
     if k > _INT32:
         _int32(k=k)
-    dev, r, q, y = _place(drows, pos, dx)
-    rc = _c.df_moe_permute_grad(dev, r, _dtype(dtype), n_rows, ldr, q, T, k, H, y, ldx,
+    dtype, n = _type(dtype)
+    dev, r, q, y = _place("drows pos dx", (n, 4, n), drows, pos, dx)
+    rc = _c.df_moe_permute_grad(dev, r, dtype, n_rows, ldr, q, T, k, H, y, ldx,
                                 _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -510,8 +539,9 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
     """Weighted rows back to their tokens (df_moe_unpermute)."""
     if k > _INT32:
         _int32(k=k)
-    dev, r, q, w, y = _place(rows, pos, weights, y)
-    rc = _c.df_moe_unpermute(dev, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, y, ldy,
+    dtype, n = _type(dtype)
+    dev, r, q, w, y = _place("rows pos weights y", (n, 4, 4, n), rows, pos, weights, y)
+    rc = _c.df_moe_unpermute(dev, r, dtype, n_rows, ldr, q, w, T, k, H, y, ldy,
                              _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -522,8 +552,10 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
     if k > _INT32:
         _int32(k=k)
-    dev, g, r, q, w, dr, dw = _place(dy, rows, pos, weights, drows, dweights)
-    rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, _dtype(dtype), n_rows, ldr, q, w, T, k, H, dr,
+    dtype, n = _type(dtype)
+    dev, g, r, q, w, dr, dw = _place("dy rows pos weights drows dweights", (n, n, 4, 4, n, 4), dy, rows, pos, weights,
+                                     drows, dweights)
+    rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, dtype, n_rows, ldr, q, w, T, k, H, dr,
                                   lddr, dw, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -531,8 +563,9 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
-    dev, x, c, s = _place(x, codes, scales)
-    rc = _c.df_moe_fp8_quantize(dev, x, _dtype(dtype), M, K, ldx, c, ldc, s, lds, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+    dtype, n = _type(dtype)
+    dev, x, c, s = _place("x codes scales", (n, 1, 4), x, codes, scales)
+    rc = _c.df_moe_fp8_quantize(dev, x, dtype, M, K, ldx, c, ldc, s, lds, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -542,9 +575,10 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
     if G > _INT32:
         _int32(G=G)
-    dev, x, xs, w, ws, o, y, st = _place(x, xs, w, ws, offs, y, status)
+    dtype, n = _type(dtype)
+    dev, x, xs, w, ws, o, y, st = _place("x xs w ws offs y status", (1, 4, 1, 4, 4, n, 4), x, xs, w, ws, offs, y, status)
     rc = _c.df_moe_fp8_matmul(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
-                              1 if transposed else 0, y, _dtype(dtype), ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
+                              1 if transposed else 0, y, dtype, ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
 
@@ -589,48 +623,27 @@ def _choice(kinds, name, v):
         raise DfMoeError(EINVAL, "%s must be one of %s, not %r" % (name, ", ".join(map(repr, kinds)), v)) from None
 
 
-def _some(*arrays):
-    """[device, address, ...] of arrays that may be absent (address 0)."""
-    try:  # the first a tensor, the others tensors on its device or absent
-        dev = arrays[0].get_device()
-        if dev >= 0:
-            out = [dev]
-            for a in arrays:
-                if a is None:
-                    out.append(0)
-                elif a.get_device() == dev:
-                    out.append(a.data_ptr())
-                else:
-                    break
-            else:
-                return out
-    except AttributeError:
-        pass
-    return [a or 0 for a in _place_any(arrays)]
-
-
-def _on(dev, stream):
-    """The stream of a call: `stream`, else torch's current one on the device."""
-    if stream is None and dev >= 0:
-        return _torch_stream(dev)
-    return _stream(stream) or 0
-
-
 def matmul(x, w, dtype, M, N, K, y, out_dtype, bias=None, act="none", residual=None, pre=None, ldx=0,
            ldw=0, ldy=0, ldr=0, ldp=0, status=None, stream=None):
     """y = residual + act(x w' + bias) of 16-bit matrices (df_moe_matmul)."""
-    dev, x, w, y, b, r, z, st = _some(x, w, y, bias, residual, pre, status)
-    _matmul(dev, x, ldx, w, ldw, _dtype(dtype), M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y,
-            _dtype(out_dtype), ldy, st, _on(dev, stream))
+    dtype, n = _type(dtype)
+    out_dtype, o = _type(out_dtype)
+    dev, x, w, y, b, r, z, st = _place("x w y bias residual pre status", (n, n, o, n, o, n, 4), x, w, y, bias, residual, pre,
+                                       status)
+    _matmul(dev, x, ldx, w, ldw, dtype, M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y, out_dtype, ldy, st,
+            _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def matmul_grad(dy, x, w, dtype, M, N, K, dx=None, dw=None, dbias=None, grad_dtype="f32", act="none",
                 pre=None, dz=None, lddy=0, ldx=0, ldw=0, lddx=0, lddw=0, ldp=0, lddz=0, status=None,
                 stream=None):
     """Gradients of matmul's x, w and bias (df_moe_matmul_grad)."""
-    dev, dy, x, w, dx, dw, db, z, dz, st = _some(dy, x, w, dx, dw, dbias, pre, dz, status)
-    _matmul_grad(dev, dy, lddy, x, ldx, w, ldw, _dtype(dtype), M, N, K, _choice(_ACTS, "act", act), z, ldp, dz, lddz,
-                 dx, lddx, dw, lddw, db, _dtype(grad_dtype), st, _on(dev, stream))
+    dtype, n = _type(dtype)
+    grad_dtype, g = _type(grad_dtype)
+    dev, dy, x, w, dx, dw, db, z, dz, st = _place("dy x w dx dw dbias pre dz status", (n, n, n, n, g, g, n, n, 4), dy, x, w, dx,
+                                                  dw, dbias, pre, dz, status)
+    _matmul_grad(dev, dy, lddy, x, ldx, w, ldw, dtype, M, N, K, _choice(_ACTS, "act", act), z, ldp, dz, lddz,
+                 dx, lddx, dw, lddw, db, grad_dtype, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def test_matmul_give_up(role):
@@ -644,9 +657,13 @@ def block_norm(u, residual, dtype, T, H, h=None, n=None, post=False, post_weight
                gate_kind="none", residual_scale=1.0, pre_weight=None, weight_dtype="f32", eps=1e-6, ldu=0,
                ldr=0, ldg=0, ldh=0, ldn=0, stream=None):
     """h = residual_scale residual + gate norm(u), n = norm(h) (df_moe_block_norm)."""
-    dev, u, r, h, n, q, g, v = _some(u, residual, h, n, post_weight, gate, pre_weight)
-    _block_norm(dev, u, ldu, 1 if post else 0, q, _choice(_GATES, "gate_kind", gate_kind), g, ldg, r, ldr,
-                residual_scale, v, eps, T, H, _dtype(dtype), _dtype(weight_dtype), h, ldh, n, ldn, _on(dev, stream))
+    dtype, b = _type(dtype)
+    weight_dtype, w = _type(weight_dtype)
+    kind = _choice(_GATES, "gate_kind", gate_kind)
+    dev, u, r, h, n, q, g, v = _place("u residual h n post_weight gate pre_weight", (b, b, b, b, w, (0, w, 4, b)[kind], w), u,
+                                      residual, h, n, post_weight, gate, pre_weight)
+    _block_norm(dev, u, ldu, 1 if post else 0, q, kind, g, ldg, r, ldr, residual_scale, v, eps, T, H, dtype,
+                weight_dtype, h, ldh, n, ldn, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def block_norm_grad_workspace(T, H):
@@ -662,13 +679,17 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
                     workspace_bytes=0, lddh=0, lddn=0, ldu=0, ldh=0, ldg=0, lddu=0, lddr=0, lddg=0,
                     stream=None):
     """Gradients of block_norm (df_moe_block_norm_grad)."""
-    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _some(
+    dtype, b = _type(dtype)
+    weight_dtype, w = _type(weight_dtype)
+    kind = _choice(_GATES, "gate_kind", gate_kind)
+    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _place(
+        "dh dn u h du dresidual post_weight dpost_weight gate dgate pre_weight dpre_weight workspace",
+        (b, b, b, b, b, b, w, 4, (0, w, 4, b)[kind], (0, 4, 4, b)[kind], w, 4, 0),
         dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    _block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q,
-                     _choice(_GATES, "gate_kind", gate_kind), g, ldg, residual_scale, v, eps, T, H, _dtype(dtype),
-                     _dtype(weight_dtype), du, lddu, dr, lddr, dq, dg, lddg, dv, ws, workspace_bytes, _on(dev, stream))
+    _block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q, kind, g, ldg, residual_scale, v, eps, T, H,
+                     dtype, weight_dtype, du, lddu, dr, lddr, dq, dg, lddg, dv, ws, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def balance_loss_workspace(T, E, S=1):
@@ -686,9 +707,12 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
         _int32(E=E, k=k)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    dev, z, i, lo, c, t, ws, p, o, m, st = _some(logits, ids, loss, counts, tokens, workspace, probs, offs, mask, status)
-    _balance_loss(dev, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef, z_coef, lo,
-                  c, t, p, ws, workspace_bytes, st, _on(dev, stream))
+    dtype, n = _type(dtype)
+    dev, z, i, lo, c, t, ws, p, o, m, st = _place("logits ids loss counts tokens workspace probs offs mask status",
+                                                  (n, 4, 4, 4, 4, 0, 4, 4, 1, 4), logits, ids, loss, counts,
+                                                  tokens, workspace, probs, offs, mask, status)
+    _balance_loss(dev, z, dtype, ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef, z_coef, lo,
+                  c, t, p, ws, workspace_bytes, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogits, offs=None, S=1,
@@ -697,6 +721,9 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
     """The gradient of the logits: the loss's and the routing weights' (df_moe_balance_loss_grad)."""
     if (E | k) > _INT32:
         _int32(E=E, k=k)
-    dev, g, z, i, c, t, d, o, m, w, dw = _some(dloss, logits, ids, counts, tokens, dlogits, offs, mask, weights, dweights)
-    _balance_loss_grad(dev, g, z, _dtype(dtype), ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
-                       z_coef, c, t, w, dw, d, lddl, _on(dev, stream))
+    dtype, n = _type(dtype)
+    dev, g, z, i, c, t, d, o, m, w, dw = _place("dloss logits ids counts tokens dlogits offs mask weights dweights",
+                                                (4, n, 4, 4, 4, n, 4, 1, 4, 4), dloss, logits, ids, counts, tokens, dlogits,
+                                                offs, mask, weights, dweights)
+    _balance_loss_grad(dev, g, z, dtype, ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
+                       z_coef, c, t, w, dw, d, lddl, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)

@@ -242,3 +242,69 @@ def test_packed_calls_are_the_calls(dfm):
             if want:
                 assert L.df_moe_last_error(None) == message
     assert L.df_moe_packed(6, b"") == -1 and L.df_moe_packed(-1, b"") == -1
+
+
+class Elements(OnDevice0):
+    """The same with elements of a size."""
+
+    def __init__(self, size):
+        self.size = size
+
+    def element_size(self):
+        return self.size
+
+
+# The calls, and the bytes of an element of every array: 16-bit operands, fp32
+# where a call names no other type.
+ELEMENTS = [
+    ("matmul", MATMUL, dict(x=2, w=2, y=4, bias=2, residual=4, pre=2, status=4)),
+    ("matmul", dict(MATMUL, out_dtype="bf16"), dict(x=2, w=2, y=2, bias=2, residual=2, pre=2, status=4)),
+    ("matmul_grad", GRAD, dict(dy=2, x=2, w=2, dx=2, dw=4, dbias=4, pre=2, dz=2, status=4)),
+    ("matmul_grad", dict(GRAD, grad_dtype="bf16"), dict(dy=2, x=2, w=2, dx=2, dw=2, dbias=2, pre=2, dz=2, status=4)),
+    ("block_norm", NORM, dict(u=2, residual=2, h=2, n=2, post_weight=4, gate=4, pre_weight=4)),
+    ("block_norm", dict(NORM, weight_dtype="bf16"), dict(u=2, residual=2, h=2, n=2, post_weight=2, gate=2, pre_weight=2)),
+    ("block_norm", dict(NORM, gate_kind="token", weight_dtype="bf16"), dict(u=2, gate=4, pre_weight=2)),
+    ("block_norm", dict(NORM, gate_kind="full"), dict(u=2, gate=2, pre_weight=4)),
+    ("block_norm", dict(NORM, u=None), dict(residual=2, h=2, n=2, pre_weight=4)),
+    ("block_norm_grad", NORM_GRAD, dict(dh=2, dn=2, u=2, h=2, du=2, dresidual=2, post_weight=4, dpost_weight=4, gate=4, dgate=4,
+                                        pre_weight=4, dpre_weight=4)),
+    ("block_norm_grad", dict(NORM_GRAD, weight_dtype="bf16"), dict(post_weight=2, dpost_weight=4, gate=2, dgate=4, pre_weight=2,
+                                                                   dpre_weight=4)),
+    ("block_norm_grad", dict(NORM_GRAD, gate_kind="token"), dict(dh=2, gate=4, dgate=4)),
+    ("block_norm_grad", dict(NORM_GRAD, gate_kind="full"), dict(dh=2, gate=2, dgate=2)),
+    ("balance_loss", BALANCE, dict(logits=4, ids=4, loss=4, counts=4, tokens=4, probs=4, offs=4, mask=1, status=4)),
+    ("balance_loss", dict(BALANCE, dtype="f16"), dict(logits=2, ids=4)),
+    ("balance_loss_grad", BALANCE_GRAD, dict(dloss=4, logits=4, ids=4, counts=4, tokens=4, dlogits=4, offs=4, mask=1, weights=4,
+                                             dweights=4)),
+    ("balance_loss_grad", dict(BALANCE_GRAD, dtype="bf16"), dict(dloss=4, logits=2, dlogits=2)),
+]
+
+
+@pytest.mark.parametrize("name, kw, elements", ELEMENTS)
+@pytest.mark.parametrize("real", [False, True])
+def test_arrays_of_another_types_size_are_refused(dfm, monkeypatch, name, kw, elements, real):
+    """A named type wider than the tensor's, a default among them, would be read
+    and written past its end. A workspace's elements are not looked at."""
+    import torch
+    binding, seen = dfm.binding, []
+    monkeypatch.setattr(binding._c, "df_moe_packed", lambda call, args: seen.append(args) or 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000)
+    monkeypatch.setattr(binding, "_torch_stream", binding._find_torch_stream)
+    types = {1: torch.bool, 2: torch.bfloat16, 4: torch.float32, 8: torch.int64}
+    if real:  # torch's tensors, which stand for some on device 0
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+        monkeypatch.setattr(binding, "_get_device", lambda a: 0 if torch.is_tensor(a) else binding._find_tensor_calls(a))
+        monkeypatch.setattr(binding, "_element_size", torch.Tensor.element_size)
+        monkeypatch.setattr(binding, "_data_ptr", torch.Tensor.data_ptr)
+    make = (lambda n: torch.zeros(1, dtype=types[n])) if real else Elements
+    arrays = {key: make(n) for key, n in elements.items()}
+    rest = {key: None if key not in elements and key not in ("workspace",) and v == A else v for key, v in kw.items()}
+    if "workspace" in kw:
+        rest["workspace"] = make(1)
+    getattr(dfm, name)(**dict(rest, **arrays))
+    assert len(seen) == 1
+    for key, n in elements.items():
+        for other in {1, 2, 4, 8} - {n} - ({8} if key == "status" else set()):
+            refused(dfm, getattr(dfm, name), -1, "%s has elements of %d bytes" % (key, other),
+                    **dict(rest, **dict(arrays, **{key: make(other)})))
+    assert len(seen) == 1

@@ -235,3 +235,47 @@ def test_sizes_that_32_bits_would_cut_are_refused(dfm, name, kw):
 
 def test_permute_refuses_a_negative_workspace_size(dfm):
     refused(dfm, dfm.permute, -1, "workspace_bytes", **dict(PERMUTE, T=65537, k=1, workspace=A, workspace_bytes=-1))
+
+
+class Elements(OnDevice0):
+    """The same with elements of a size."""
+
+    def __init__(self, size):
+        self.size = size
+
+    def element_size(self):
+        return self.size
+
+
+# bytes of an element of every array of EVERY_CALL's calls
+ELEMENTS = {
+    "permute": dict(ids=4, x=2, rows=2, offs=4, pos=4, src=4, scales=4, rows_scales=4), "permute_grad": dict(drows=4, pos=4, dx=4),
+    "unpermute": dict(rows=4, pos=4, weights=4, y=4), "unpermute_grad": dict(dy=2, rows=2, pos=4, weights=4, drows=2, dweights=4),
+    "fp8_quantize": dict(x=2, codes=1, scales=4), "fp8_matmul": dict(x=1, xs=4, w=1, ws=4, offs=4, y=2, status=4),
+}
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL)
+@pytest.mark.parametrize("real", [False, True])
+def test_arrays_of_another_types_size_are_refused(dfm, monkeypatch, name, kw, real):
+    """A named type wider than the tensor's would be read and written past its end."""
+    import torch
+    binding, seen = dfm.binding, []
+    monkeypatch.setattr(binding._c, "df_moe_" + name, lambda *a: seen.append(a) or 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x5000)
+    monkeypatch.setattr(binding, "_torch_stream", binding._find_torch_stream)
+    types = {1: torch.uint8, 2: torch.bfloat16, 4: torch.float32, 8: torch.int64}
+    if real:  # torch's tensors, which stand for some on device 0
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+        monkeypatch.setattr(binding, "_get_device", lambda a: 0 if torch.is_tensor(a) else binding._find_tensor_calls(a))
+        monkeypatch.setattr(binding, "_element_size", torch.Tensor.element_size)
+        monkeypatch.setattr(binding, "_data_ptr", torch.Tensor.data_ptr)
+    make = (lambda n: torch.zeros(1, dtype=types[n])) if real else Elements
+    arrays = {key: make(n) for key, n in ELEMENTS[name].items()}
+    getattr(dfm, name)(**dict(kw, **arrays))
+    assert len(seen) == 1
+    for key, n in ELEMENTS[name].items():
+        for other in {1, 2, 4, 8} - {n} - ({8} if key == "status" else set()):
+            refused(dfm, getattr(dfm, name), -1, "%s has elements of %d bytes" % (key, other),
+                    **dict(kw, **dict(arrays, **{key: make(other)})))
+    assert len(seen) == 1
