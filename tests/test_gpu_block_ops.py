@@ -891,6 +891,31 @@ def test_balance_of_far_logits(dfm, score, shift):
     within(loss, want[0], 512 * U * want[0], "f32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E", [16, 300])
+def test_balance_of_scores_that_are_nothing_beside_the_largest(dfm, dtype, E):
+    """A sigmoid's score below 2^-126 of the largest is 0, and its logit's
+    gradient is the routing weight's alone."""
+    z = torch.full((1, E), -200.0, device="cuda")
+    z[0, :9] = torch.tensor([0.0, -50.0, -86.0, -89.0, -104.0, -1e3, -6e4, float("-inf"), 1.0])
+    z = z.to(DT[dtype])
+    ids = torch.tensor([[0, 1, 4, 7, 8]], dtype=torch.int32, device="cuda")
+    k = ids.shape[1]
+    loss, probs = torch.empty(1, device="cuda"), torch.empty(1, E, device="cuda")
+    counts, tokens = torch.empty(1, E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    size = dfm.balance_loss_workspace(1, E)
+    dfm.balance_loss(z, dtype, 1, E, ids, k, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size, probs=probs,
+                     score="sigmoid")
+    w, dw = torch.full((1, k), 1 / k, device="cuda"), torch.tensor([[1.0, -2.0, 3.0, 5.0, 7.0]], device="cuda")
+    dz = torch.empty_like(z)
+    dfm.balance_loss_grad(torch.ones(1, device="cuda"), z, dtype, 1, E, ids, k, counts, tokens, dz, weights=w, dweights=dw, score="sigmoid")
+    every = torch.ones(1, dtype=torch.bool, device="cuda")
+    want = balance64(z.double(), ids, k, E, [0, 1], every, "sigmoid", 1.0, 0.0, torch.ones(1, device="cuda"), w, dw)
+    # (an exponent of size 104 is rounded: 104 U)
+    assert bool(((probs.double() - want[3]).abs() <= 256 * U * want[3] + 2.0 ** -125).all())
+    within(dz, want[4], 512 * U * (want[4].abs() + want[3] * E) + 2.0 ** -120, dtype)
+
+
 def test_balance_counts_more_tokens_than_fp32_does(dfm):
     T, E = 2 ** 24 + 3, 2
     z = torch.zeros(T, E, device="cuda")
