@@ -168,22 +168,22 @@ __device__ __forceinline__ float lane_sum(const float (&v)[N]) {
 }
 
 // v becomes exp(v - l + log(scale)), l = logsumexp(v); `scale` is what the
-// values are still to be multiplied by (1 / their sum). exp(v - most) as a
-// power of two with one fused product: the rounding of most log2(e) is common to
-// the row and leaves with the sum. A row of -inf alone (nothing allowed) has
-// neither a softmax nor l: zeros, and 0. fmaxf drops a NaN, the sum keeps it.
+// values are still to be multiplied by (1 / their sum). The difference from the
+// largest comes before the factor log2(e): one product and sum would round most
+// log2(e), which is more than 1 off from 1e7 on and leaves fp32 near the end of
+// its range. A row of -inf alone (nothing allowed) has neither a softmax nor l:
+// zeros, and 0. fmaxf drops a NaN, the sum keeps it.
 template <int L, int N>
 __device__ __forceinline__ float softmax_row(float (&v)[N], float* scale) {
-  const float most = warp_max<L>(lane_max(v));
-  const float base = most == -INFINITY ? 0.f : most * kLog2e;
+  const float top = warp_max<L>(lane_max(v)), most = top == -INFINITY ? 0.f : top;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 x = halves(fma2(pair(v[i], v[i + 1]), both(kLog2e), both(-base)));
+    const float2 x = halves(mul2(add2(pair(v[i], v[i + 1]), both(-most)), both(kLog2e)));
     v[i] = exp2_fast(x.x), v[i + 1] = exp2_fast(x.y);
   }
   const float sum = warp_sum<L>(lane_sum(v));
   *scale = sum == 0.f ? 0.f : 1.f / sum;
-  return sum == 0.f ? 0.f : kLn2 * (base + log2f(sum));
+  return sum == 0.f ? 0.f : most + kLn2 * log2f(sum);
 }
 // v becomes sigmoid(v) times a factor common to the row, m (if it is given)
 // 1 - sigmoid(v); `scale` is 1 over the sum. With M = min(most, 0) and e =
@@ -194,10 +194,10 @@ template <int L, bool REST, int N>
 __device__ __forceinline__ void sigmoid_row(float (&v)[N], float* m, float* scale) {
   constexpr float kNone = 0x1p126f;
   const float most = warp_max<L>(lane_max(v));
-  const float M = most == -INFINITY ? 0.f : fminf(most, 0.f) * kLog2e, low = exp2_fast(M);
+  const float M = most == -INFINITY ? 0.f : fminf(most, 0.f), low = exp2_fast(M * kLog2e);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 x = halves(fma2(pair(v[i], v[i + 1]), both(-kLog2e), both(M)));
+    const float2 x = halves(mul2(add2(pair(v[i], v[i + 1]), both(-M)), both(-kLog2e)));
     const float e[2] = {fminf(exp2_fast(x.x), kNone), fminf(exp2_fast(x.y), kNone)};
     const float2 sum = halves(add2(pair(e[0], e[1]), both(low)));
     const float r[2] = {__fdividef(1.f, sum.x), __fdividef(1.f, sum.y)};

@@ -916,6 +916,93 @@ def test_balance_of_scores_that_are_nothing_beside_the_largest(dfm, dtype, E):
     within(dz, want[4], 512 * U * (want[4].abs() + want[3] * E) + 2.0 ** -120, dtype)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E", [6, 24, 61, 200, 896])
+def test_balance_of_logits_at_the_types_ends(dfm, score, dtype, E):
+    """The type's lowest value stands for an expert that is not allowed, the lowest
+    in the whole row for a token that no expert may have: uniform, by the
+    definition. Each row a sequence, then all of them one."""
+    g = gen(E)
+    low, high = torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max
+    z = randn(16, E, g=g)
+    z[0], z[1] = low, high
+    z[2, 1:] = low
+    z[3], z[3, E // 2] = low, high
+    z[4], z[4, 0] = float("-inf"), low
+    z[5], z[5, 1] = low, float("-inf")
+    z[6], z[7] = 0.7 * low, 0.7 * high  # about where a product with log2(e) leaves fp32
+    z[8], z[9] = 0.6 * low, 0.6 * high
+    z[10, ::2] = low
+    z[11] = low
+    z[11, -1] = 0.9 * low
+    z[12, ::3] = high
+    z[13], z[13, E - 1] = 0.9 * high, 0.8 * high
+    z[14, E // 3] = low
+    z = z.to(DT[dtype])
+    zd, T, k = z.double(), z.shape[0], 3
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    for S, at in ((T, list(range(T + 1))), (1, [0, T])):
+        offs = torch.tensor(at, dtype=torch.int32, device="cuda") if S > 1 else None
+        loss, probs = torch.empty(S, device="cuda"), torch.empty(S, E, device="cuda")
+        counts, tokens = torch.empty(S, E, dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda")
+        size = dfm.balance_loss_workspace(T, E, S)
+        kw = dict(offs=offs, S=S, score=score, coef=0.5)
+        dfm.balance_loss(z, dtype, T, E, ids, k, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size,
+                         probs=probs, **kw)
+        every = torch.ones(T, dtype=torch.bool, device="cuda")
+        want = balance64(zd, ids, k, E, at, every, score, 0.5, 0.0)
+        within(probs, want[3], 256 * U * want[3], dtype="f32")
+        f = want[1].double() * E / (k * torch.tensor(want[2], device="cuda")[:, None])
+        within(loss, want[0], 512 * U * 0.5 * (f * want[3]).sum(1), "f32")
+        # the gradient, without and with the squared logsumexp's part: terms of p (f + f p), l p and the routing weights'
+        dloss, w, dw = torch.ones(S, device="cuda"), torch.full((T, k), 1 / k, device="cuda"), randn(T, k, g=g)
+        for z_coef in (0.0, 1e-3):
+            dz = torch.empty_like(z)
+            dfm.balance_loss_grad(dloss, z, dtype, T, E, ids, k, counts, tokens, dz, weights=w, dweights=dw, z_coef=z_coef, **kw)
+            grad = balance64(zd, ids, k, E, at, every, score, 0.5, z_coef, dloss, w, dw)[4]
+            p = torch.softmax(torch.nn.functional.logsigmoid(zd) if score == "sigmoid" else zd, 1)
+            seq = torch.arange(T, device="cuda") if S > 1 else torch.zeros(T, dtype=torch.int64, device="cuda")
+            n = torch.tensor(want[2], device="cuda").double()[seq][:, None]
+            mag = 0.5 / n * p * (f[seq] + (f[seq] * p).sum(1, keepdim=True))
+            mag = mag + 2 * z_coef / n * torch.logsumexp(zd, 1, keepdim=True).abs() * torch.softmax(zd, 1)
+            kept = (w * (dw.abs() + (w * dw.abs()).sum(1, keepdim=True))).double()
+            mag = mag + torch.zeros_like(zd).scatter_add_(1, ids.long(), kept)
+            within(dz, grad, 512 * U * mag, dtype)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", [3e6, 1e8, 1e9, 1e10, 1e13, 1e30])
+def test_balance_of_logits_whose_spacing_is_wide(dfm, score, far):
+    """Rows about as far as their values lie apart: where an exponent's rounding is
+    more than the exponent."""
+    T, E, k = 40, 24, 2
+    g = gen(3)
+    step = max(1.0, 2.0 ** math.floor(math.log2(far) - 23))
+    z = torch.randint(-20, 3, (T, E), generator=g, device="cuda").double() * step
+    z = (z + torch.where(torch.arange(T, device="cuda") % 2 == 0, far, -far)[:, None]).float()
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    offs = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    loss, probs = torch.empty(T, device="cuda"), torch.empty(T, E, device="cuda")
+    counts, tokens = torch.empty(T, E, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int32, device="cuda")
+    size = dfm.balance_loss_workspace(T, E, T)
+    kw = dict(offs=offs, S=T, score=score)
+    dfm.balance_loss(z, "f32", T, E, ids, k, loss, counts, tokens, torch.empty(size, dtype=torch.uint8, device="cuda"), size, probs=probs,
+                     z_coef=1e-60 ** 0.5, **kw)
+    every, one = torch.ones(T, dtype=torch.bool, device="cuda"), torch.ones(T, device="cuda")
+    want = balance64(z.double(), ids, k, E, list(range(T + 1)), every, score, 1.0, 1e-60 ** 0.5, one)
+    within(probs, want[3], 256 * U * want[3], "f32")
+    if far < 1e18:  # where the square of the logarithm stays in fp32
+        within(loss, want[0], 512 * U * want[0], "f32")
+    dz = torch.empty_like(z)
+    dfm.balance_loss_grad(one, z, "f32", T, E, None, k, counts, tokens, dz, z_coef=1e-60 ** 0.5, **kw)
+    f = want[1].double() * E / k
+    # an exponential below 2^-126 is 0: as much of each f is missing (e^-88 = 6.1e-39 times f = 12 is 7.3e-38)
+    terms = f + (f * want[3]).sum(1, keepdim=True)
+    mag = want[3] * terms + 2e-30 * far * torch.softmax(z.double(), 1)
+    within(dz, want[4], 512 * U * mag + 2.0 ** -126 * terms, "f32")
+
+
 def test_balance_counts_more_tokens_than_fp32_does(dfm):
     T, E = 2 ** 24 + 3, 2
     z = torch.zeros(T, E, device="cuda")
