@@ -15,7 +15,8 @@
 // row needs are all linear in G's three terms, so one reduction gives them (h^2,
 // u^2, y h, and u q g times dh, y and h); its column sums stay in a block's
 // registers over its rows and meet in a second kernel, in order. Sums are fp32.
-// A row whose squares overflow fp32 is summed again at 2^-70.
+// A row whose squares overflow fp32 is summed again at 2^-70, a gradient row of
+// which any sum does with h and u at size 1.
 //
 // Three forms, by the rows. Whole 16-byte pieces: from 513 to 8192 values
 // through a ring of bulk copies (block_norm_ring_kernel), shorter, longer and few
@@ -342,7 +343,7 @@ struct RowFactors {
 __device__ __forceinline__ RowFactors row_factors(const float (&s)[8], float sh, float su, bool dn, bool post, float token, float inv,
                                                   float eps) {
   RowFactors f;
-  const float rh = dn ? rms_of(s[0], inv, eps, sh) : 0.f, ru = post ? rms_of(s[1], inv, eps, su) : 1.f;
+  const float rh = dn ? rms_of(s[0], inv, eps, sh) : 0.f, ru = post ? rms_of(s[1], inv, eps, su) : 1.f / su;
   f.along = rh * s[2] * inv;
   f.rh = rh * sh;
   const float gu = s[3] + f.rh * (s[4] - f.along * rh * s[5]);  // the sum of G q g u su, without a token's gate
@@ -350,6 +351,17 @@ __device__ __forceinline__ RowFactors row_factors(const float (&s)[8], float sh,
   f.mean = token * f.dtoken * inv;
   f.ru = ru * su;
   return f;
+}
+
+// Whether a row's six sums are all there (what comes of the last four is finite);
+// where one left fp32 or has no value, the scales with which h and u are summed
+// again: those that make a norm's rows of size 1, or kSmall where the squares do
+// not say.
+__device__ __forceinline__ bool summed(const float (&s)[8], const RowFactors& f, float& sh, float& su, bool post, float inv, float eps) {
+  if (s[0] + s[1] < INFINITY && fabsf(f.along) + fabsf(f.dtoken) < INFINITY) return true;
+  sh = s[0] < INFINITY ? sh * rms_of(s[0], inv, eps, sh) : kSmall;
+  su = post && s[1] < INFINITY ? su * rms_of(s[1], inv, eps, su) : kSmall;
+  return false;
 }
 
 // A row's gradients but the weights', whose terms are added to dq and dv:
@@ -368,6 +380,7 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row& 
   const bool has_u = MODE >= 0 || p.u, has_dh = MODE >= 0 || p.dh, has_dn = MODE >= 0 || p.dn;
   const float token = by_token ? static_cast<const float*>(p.gate)[row] : 1.f;
   float sh = 1.f, su = 1.f, s[8];
+  RowFactors f;
 #pragma unroll 1
   for (int again = 0;; ++again) {
     Pair c[6];
@@ -405,11 +418,9 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row& 
     }
     s[6] = ok ? 0.f : 1.f, s[7] = 0.f;
     sum(s, at.tpr);
-    if (again || (s[0] < INFINITY && s[1] < INFINITY)) break;
-    if (!(s[0] < INFINITY)) sh = kSmall;
-    if (!(s[1] < INFINITY)) su = kSmall;
+    f = row_factors(s, sh, su, has_dn, post, token, inv, p.eps);
+    if (again == 2 || summed(s, f, sh, su, post, inv, p.eps)) break;
   }
-  RowFactors f = row_factors(s, sh, su, has_dn, post, token, inv, p.eps);
   const bool bad = s[6] != 0.f;
   float scale = p.scale;
   if (bad) f.rh = f.ru = f.dtoken = scale = __uint_as_float(0x7fffffffu);
@@ -833,6 +844,7 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
     const T *dh = row_of<T>(p.dh, row, p.lddh), *dn = row_of<T>(p.dn, row, p.lddn), *u = row_of<T>(p.u, row, p.ldu);
     const T *h = p.dn ? row_of<T>(p.h, row, p.ldh) : nullptr, *full = row_of<T>(gates, row, p.ldg);
     const float token = by_token ? static_cast<const float*>(p.gate)[row] : 1.f;
+    RowFactors f;
     float sh = 1.f, su = 1.f, s[8], a[kOddUnroll], b[kOddUnroll], x[kOddUnroll], y[kOddUnroll], q[kOddUnroll], g[kOddUnroll], v[kOddUnroll];
 #pragma unroll 1
     for (int again = 0;; ++again) {
@@ -859,11 +871,9 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
         }
       }
       sum(s, kOddThreads);
-      if (again || (s[0] < INFINITY && s[1] < INFINITY)) break;
-      if (!(s[0] < INFINITY)) sh = kSmall;
-      if (!(s[1] < INFINITY)) su = kSmall;
+      f = row_factors(s, sh, su, p.dn != nullptr, p.post != 0, token, inv, p.eps);
+      if (again == 2 || summed(s, f, sh, su, p.post != 0, inv, p.eps)) break;
     }
-    const RowFactors f = row_factors(s, sh, su, p.dn != nullptr, p.post != 0, token, inv, p.eps);
     if (by_token && p.dgate && threadIdx.x == 0) static_cast<float*>(p.dgate)[row] = f.dtoken;
     T* dr = p.dresidual ? static_cast<T*>(p.dresidual) + row * p.lddr : nullptr;
     T* du = p.du ? static_cast<T*>(p.du) + row * p.lddu : nullptr;

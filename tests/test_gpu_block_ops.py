@@ -725,6 +725,41 @@ def test_norm_gradient_against_differences(dfm):
         assert abs((grad.double() * d).sum().item() - slope) <= 1e-5 * (grad.double().abs() * d.abs()).sum().item() + 1e-7
 
 
+@pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("H, T, dtype", [(64, 5, "f32"), (61, 5, "f32"), (64, 5, "bf16"), (2048, 400, "bf16"), (1024, 700, "f32"), (9000, 3, "bf16"),
+                                         (16384, 2, "f32")])
+def test_norm_gradient_whose_cross_sums_overflow(dfm, H, T, dtype, post, kind):
+    """u q g h and u q g y add up beyond fp32 where neither the squares of u nor h do."""
+    g = gen(H + T)
+
+    def most(size):  # values of one size and either sign
+        return (size * (0.5 + torch.rand(T, H, generator=g, device="cuda"))).to(DT[dtype])
+    big = 2.0 ** 63.5 / H ** 0.5  # squares that add up to a quarter of fp32's range and so
+    u, h = most(big / 1.5), most(big / 1.5)
+    dn, dh = most(0.1), most(1e-18)
+    u[-1], dn[-1], dh[-1] = u[-1] * 2.0 ** -30, dn[-1] * 1e28, dh[-1] * 1e3  # the sums with y alone
+    q = torch.full((H,), 3.0, device="cuda") if post else None
+    v = torch.full((H,), 2.0, device="cuda")
+    gate = {"none": None, "channel": torch.full((H,), 2.0, device="cuda"), "token": torch.full((T,), 2.0, device="cuda"),
+            "full": torch.full((T, H), 2.0, device="cuda").to(DT[dtype])}[kind]
+    out = dict(du=torch.empty_like(u), dresidual=torch.empty_like(u), dpre_weight=torch.empty(H, device="cuda"))
+    if post:
+        out["dpost_weight"] = torch.empty(H, device="cuda")
+    if kind != "none":
+        out["dgate"] = torch.empty_like(gate)
+    size = dfm.block_norm_grad_workspace(T, H)
+    dfm.block_norm_grad(dh, dn, u, h, dtype, T, H, post=post, post_weight=q, gate=gate, gate_kind=kind, pre_weight=v, eps=EPS,
+                        workspace=torch.empty(size, dtype=torch.uint8, device="cuda"), workspace_bytes=size, **out)
+    want = grad64(dh.double(), dn.double(), u.double(), h.double(), post, q, gate, kind, 1.0, v)
+    for key, o in out.items():
+        value, mag = want[key]
+        column = key in ("dpost_weight", "dpre_weight") or (key == "dgate" and kind == "channel")
+        kind_of = "f32" if column or (key == "dgate" and kind == "token") else dtype
+        assert bool((value.abs() < torch.finfo(DT[kind_of]).max).all()), key
+        within(o, value, (256 + (T + 64 if column else 0)) * U * mag, kind_of)
+
+
 # ---- balance ----------------------------------------------------------------
 def balance64(z, ids, k, E, offs, mask, score, coef, z_coef, dloss=None, weights=None, dweights=None):
     T, S = z.shape[0], len(offs) - 1
