@@ -574,7 +574,8 @@ DF_MOE_API size_t df_moe_block_norm_grad_workspace(int64_t T, int64_t H);
  * sum at h:
  *   dresidual = residual_scale G, du through gate and norm  [T][H] of dtype
  *   dpost_w, dpre_w  [H] fp32;  dgate: [H] fp32, [T] fp32 or [T][H] of dtype
- * each optional. workspace: df_moe_block_norm_grad_workspace bytes, 16-byte
+ * each optional. A row whose sums overflow fp32 is summed at other scales, as in
+ * the norm. workspace: df_moe_block_norm_grad_workspace bytes, 16-byte
  * aligned, for dpost_w, dpre_w and a channel's dgate (else NULL); not shared
  * by calls (or captured graphs) that may overlap. dresidual may be dh itself
  * or dn itself, with the same row distance, and du the other. */

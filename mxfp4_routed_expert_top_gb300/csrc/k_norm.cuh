@@ -15,8 +15,8 @@
 // row needs are all linear in G's three terms, so one reduction gives them (h^2,
 // u^2, y h, and u q g times dh, y and h); its column sums stay in a block's
 // registers over its rows and meet in a second kernel, in order. Sums are fp32.
-// A row whose squares overflow fp32 is summed again at 2^-70, a gradient row of
-// which any sum does with h and u at size 1.
+// A row whose squares (with eps) overflow fp32 is summed again at 2^-80, a gradient
+// row of which any sum does with h and u at size 1.
 //
 // Three forms, by the rows. Whole 16-byte pieces: from 513 to 8192 values
 // through a ring of bulk copies (block_norm_ring_kernel), shorter, longer and few
@@ -42,7 +42,9 @@
 namespace dfm {
 namespace {
 
-constexpr float kSmall = 0x1p-70f;  // of rows whose squares overflow
+// Of rows whose squares overflow: 32768 squares of 2^128 add up to 2^111, and what
+// counts beside a value of 2^56 (the least that overflows) stays normal.
+constexpr float kSmall = 0x1p-80f;
 
 template <typename T>
 __device__ __forceinline__ float f32_of(T v);
@@ -256,7 +258,7 @@ __device__ __forceinline__ void rms_rows(float (&rms)[R], const Eight (&v)[R][NV
   sum(s, tpr);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    over = over || !(s[r] < INFINITY);
+    over = over || !(s[r] + eps < INFINITY);
     rms[r] = rms_of(s[r], inv, eps, 1.f);
   }
   if (over) {
@@ -266,7 +268,7 @@ __device__ __forceinline__ void rms_rows(float (&rms)[R], const Eight (&v)[R][NV
     sum(t, tpr);
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (!(s[r] < INFINITY)) rms[r] = rms_of(t[r], inv, eps, kSmall) * kSmall;
+      if (!(s[r] + eps < INFINITY)) rms[r] = rms_of(t[r], inv, eps, kSmall) * kSmall;
   }
 }
 
@@ -358,9 +360,9 @@ __device__ __forceinline__ RowFactors row_factors(const float (&s)[8], float sh,
 // again: those that make a norm's rows of size 1, or kSmall where the squares do
 // not say.
 __device__ __forceinline__ bool summed(const float (&s)[8], const RowFactors& f, float& sh, float& su, bool post, float inv, float eps) {
-  if (s[0] + s[1] < INFINITY && fabsf(f.along) + fabsf(f.dtoken) < INFINITY) return true;
-  sh = s[0] < INFINITY ? sh * rms_of(s[0], inv, eps, sh) : kSmall;
-  su = post && s[1] < INFINITY ? su * rms_of(s[1], inv, eps, su) : kSmall;
+  if (s[0] + s[1] + eps < INFINITY && fabsf(f.along) + fabsf(f.dtoken) < INFINITY) return true;
+  sh = s[0] + eps < INFINITY ? sh * rms_of(s[0], inv, eps, sh) : kSmall;
+  su = post && s[1] + eps < INFINITY ? su * rms_of(s[1], inv, eps, su) : kSmall;
   return false;
 }
 
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_odd_kernel(const Block
         DFM_ODD s[0] = fmaf(x[i] * small, x[i] * small, s[0]);
       }
       sum(s, kOddThreads);
-      if (again || s[0] < INFINITY) break;
+      if (again || s[0] + p.eps < INFINITY) break;
       small = kSmall;
     }
     factor = rms_of(s[0], inv, p.eps, small) * small;
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_odd_kernel(const Block
   }
   if (!p.n) return;
   sum(s, kOddThreads);
-  if (!(s[0] < INFINITY)) {
+  if (!(s[0] + p.eps < INFINITY)) {
     small = kSmall;
     s[0] = 0.f;
     DFM_ODD_ROW {

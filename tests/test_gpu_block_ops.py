@@ -725,6 +725,42 @@ def test_norm_gradient_against_differences(dfm):
         assert abs((grad.double() * d).sum().item() - slope) <= 1e-5 * (grad.double().abs() * d.abs()).sum().item() + 1e-7
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H, T", [(1, 3), (48, 5), (1001, 5), (7168, 400), (8192, 3), (8192, 400), (32768, 3), (32767, 3)])
+def test_norm_of_rows_at_the_types_end(dfm, dtype, H, T):
+    """Rows whose squares overflow at any scale but a small one, and with an eps that
+    overflows beside them; both norms and their gradients."""
+    g = gen(H)
+    sign = torch.where(torch.rand(T, H, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x = sign * torch.finfo(DT[dtype]).max
+    x[1] *= torch.rand(H, generator=g, device="cuda")
+    x[2] = sign[2] * 1.3e38
+    x = x.to(DT[dtype])
+    for eps in (EPS, 3e38):
+        xd = x.double()
+        h, n = torch.empty_like(x), torch.empty_like(x)
+        if eps > 1:
+            x[0] = x[0] * 2.0 ** -65  # squares of 8e37, finite without eps where H is small
+            xd = x.double()
+        rms = torch.rsqrt((xd * xd).mean(1, keepdim=True) + eps)
+        dfm.block_norm(x, None, dtype, T, H, h, n, post=True, eps=eps)
+        want = xd * rms
+        # rms is below 2^-126 where x is largest, and loses three bits
+        within(h, want, 64 * U * want.abs(), dtype)
+        dfm.block_norm(None, x, dtype, T, H, n=n, eps=eps)
+        within(n, want, 64 * U * want.abs(), dtype)
+        # gradients a row, of both norms: dn large, so that the results are no subnormals
+        dn = (1e30 * torch.randn(T, H, generator=g, device="cuda")).to(DT[dtype])
+        dx, du = torch.empty_like(x), torch.empty_like(x)
+        hat, dd = want, dn.double()
+        grad = rms * (dd - hat * (dd * hat).mean(1, keepdim=True))
+        bound = rms * (128 + math.ceil(H / 256)) * U * (dd.abs() + hat.abs() * (dd * hat).abs().mean(1, keepdim=True))
+        dfm.block_norm_grad(None, dn, None, x, dtype, T, H, dresidual=dx, eps=eps)
+        within(dx, grad, bound, dtype)
+        dfm.block_norm_grad(dn, None, x, None, dtype, T, H, du=du, post=True, eps=eps)
+        within(du, grad, bound, dtype)
+
+
 @pytest.mark.parametrize("kind", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("H, T, dtype", [(64, 5, "f32"), (61, 5, "f32"), (64, 5, "bf16"), (2048, 400, "bf16"), (1024, 700, "f32"), (9000, 3, "bf16"),
