@@ -640,7 +640,8 @@ DF_MOE_API int df_moe_balance_loss_grad(int device, const float* dloss, const vo
 
 /* The same calls, with their arguments in order as 8-byte values (integers and
  * addresses as int64, floats as doubles): for bindings that pay for every
- * argument. An integer must fit the argument that it stands for. */
+ * argument. An integer that does not fit the argument that it stands for is
+ * refused (EINVAL). */
 #define DF_MOE_CALL_MATMUL 0
 #define DF_MOE_CALL_MATMUL_GRAD 1
 #define DF_MOE_CALL_BLOCK_NORM 2

@@ -384,7 +384,7 @@ def stream_read(buf, nbytes, sink, stream=None):
 # torch has current on the arrays' device (between other work of the same
 # program, and inside a capture); where all arrays are raw addresses, that is
 # the legacy default stream.
-_INT32 = 0x7fffffff  # larger: cut by the C call's 32-bit arguments, so refused here
+_INT32 = 0x7fffffff  # what lies further from 0 is cut by the C call's 32-bit arguments, so refused here
 
 
 class _Calls:
@@ -486,7 +486,7 @@ def _place_any(names, sizes, arrays):
 def _int32(**sizes):
     """Refuses what a 32-bit argument would cut."""
     for name, v in sizes.items():
-        if v > _INT32:
+        if not -_INT32 - 1 <= v <= _INT32:
             raise DfMoeError(EINVAL, "%s = %d does not fit 32 bits" % (name, v))
 
 
@@ -496,7 +496,7 @@ def _failed(rc):
 
 def permute_workspace(T, k, E):
     """Bytes of workspace that permute needs (df_moe_permute_workspace)."""
-    if (k | E) > _INT32:
+    if (k | E) >> 31:
         return 0
     return _c.df_moe_permute_workspace(T, k, E)
 
@@ -505,7 +505,7 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
             ldx=0, ldr=0, scales=None, n_scales=0, ld_scales=0, rows_scales=None, ld_rows_scales=0,
             stream=None):
     """Tokens sorted by expert (df_moe_permute): rows[pos[a]] = x[a // k]."""
-    if (k | E | n_scales) > _INT32:
+    if (k | E | n_scales) >> 31:
         _int32(k=k, E=E, n_scales=n_scales)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
@@ -525,7 +525,7 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
 
 def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=None):
     """Gradient of permute's x (df_moe_permute_grad)."""
-    if k > _INT32:
+    if k >> 31:
         _int32(k=k)
     dtype, n = _type(dtype)
     dev, r, q, y = _place("drows pos dx", (n, 4, n), drows, pos, dx)
@@ -537,7 +537,7 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
 
 def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, stream=None):
     """Weighted rows back to their tokens (df_moe_unpermute)."""
-    if k > _INT32:
+    if k >> 31:
         _int32(k=k)
     dtype, n = _type(dtype)
     dev, r, q, w, y = _place("rows pos weights y", (n, 4, 4, n), rows, pos, weights, y)
@@ -550,7 +550,7 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
 def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweights, lddy=0, ldr=0,
                    lddr=0, stream=None):
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
-    if k > _INT32:
+    if k >> 31:
         _int32(k=k)
     dtype, n = _type(dtype)
     dev, g, r, q, w, dr, dw = _place("dy rows pos weights drows dweights", (n, n, 4, 4, n, 4), dy, rows, pos, weights,
@@ -573,7 +573,7 @@ def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None
 def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0, ldxs=0, ldw=0,
                ldy=0, status=None, stream=None):
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
-    if G > _INT32:
+    if G >> 31:
         _int32(G=G)
     dtype, n = _type(dtype)
     dev, x, xs, w, ws, o, y, st = _place("x xs w ws offs y status", (1, 4, 1, 4, 4, n, 4), x, xs, w, ws, offs, y, status)
@@ -694,7 +694,7 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
 
 def balance_loss_workspace(T, E, S=1):
     """Bytes of workspace that balance_loss needs (df_moe_balance_loss_workspace)."""
-    if E > _INT32 or (T | S) >> 63 not in (0, -1):
+    if E >> 31 or (T | S) >> 63 not in (0, -1):
         return 0
     return _c.df_moe_balance_loss_workspace(T, E, S)
 
@@ -703,7 +703,7 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
                  probs=None, offs=None, S=1, mask=None, score="softmax", coef=1.0, z_coef=0.0, ldl=0,
                  status=None, stream=None):
     """The router's balance loss and every expert's count, a sequence (df_moe_balance_loss)."""
-    if (E | k) > _INT32:
+    if (E | k) >> 31:
         _int32(E=E, k=k)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
@@ -719,7 +719,7 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
                       mask=None, score="softmax", coef=1.0, z_coef=0.0, weights=None, dweights=None, ldl=0,
                       lddl=0, stream=None):
     """The gradient of the logits: the loss's and the routing weights' (df_moe_balance_loss_grad)."""
-    if (E | k) > _INT32:
+    if (E | k) >> 31:
         _int32(E=E, k=k)
     dtype, n = _type(dtype)
     dev, g, z, i, c, t, d, o, m, w, dw = _place("dloss logits ids counts tokens dlogits offs mask weights dweights",

@@ -183,10 +183,17 @@ A packed(const int64_t& v) {
     return static_cast<A>(v);
   }
 }
+// Whether an integer is its argument's: a cast cuts none off.
+template <typename A>
+bool fits(const int64_t& v) {
+  if constexpr (std::is_integral<A>::value) return static_cast<int64_t>(static_cast<A>(v)) == v && (std::is_signed<A>::value || v >= 0);
+  return true;
+}
 template <typename... A, size_t... I>
 int call_packed(int (*f)(A...), const int64_t* args, std::index_sequence<I...>) {
   int64_t v[sizeof...(A)];
   memcpy(v, args, sizeof v);
+  if (!(fits<A>(v[I]) && ...)) return fail(DF_MOE_EINVAL, "an integer does not fit the argument that it stands for");
   return f(packed<A>(v[I])...);
 }
 template <typename... A>

@@ -308,3 +308,30 @@ def test_arrays_of_another_types_size_are_refused(dfm, monkeypatch, name, kw, el
             refused(dfm, getattr(dfm, name), -1, "%s has elements of %d bytes" % (key, other),
                     **dict(rest, **dict(arrays, **{key: make(other)})))
     assert len(seen) == 1
+
+
+@pytest.mark.parametrize("v", [-(1 << 32) + 8, -(1 << 31) - 1, -(1 << 63)])
+def test_sizes_that_32_bits_would_cut_are_refused(dfm, v):
+    """-2^32 + 8 is not 8, and without rows neither."""
+    for T in (8, 0):
+        for key in ("E", "k"):
+            refused(dfm, dfm.balance_loss, -1, "32 bits", **dict(BALANCE, T=T, **{key: v}))
+            refused(dfm, dfm.balance_loss_grad, -1, "32 bits", **dict(BALANCE_GRAD, T=T, **{key: v}))
+    assert dfm.balance_loss_workspace(64, v, 1) == 0
+
+
+def test_packed_integers_that_do_not_fit_are_refused(dfm):
+    import struct
+    L = dfm.lib()
+    kinds = {0: "ipqpqiqqqpipqpqpiqpp", 1: "ipqpqpqiqqqipqpqpqpqpipp", 2: "ipqipipqpqfpfqqiipqpqp",
+             3: "ipqpqpqpqipipqfpfqqiipqpqppqppzp", 4: "ipiqpqiipqpiffpppppzpp", 5: "ippiqpqiipqpiffpppppqp"}
+    for call, types in kinds.items():
+        args = [0.0 if t == "f" else 0 for t in types]
+        args[0] = 1 << 20  # no such device
+        layout = "".join("d" if t == "f" else "q" for t in types)
+        for i, t in enumerate(types):
+            for v in ((1 << 31, 1 << 32, (1 << 32) + 2, -(1 << 32) + 2, -(1 << 31) - 1) if t == "i" else (-1, -(1 << 63)) if t == "z" else ()):
+                assert L.df_moe_packed(call, struct.pack(layout, *(args[:i] + [v] + args[i + 1:]))) == -1
+                assert b"does not fit" in L.df_moe_last_error(None), (call, i, v)
+        L.df_moe_packed(call, struct.pack(layout, *args))
+        assert b"does not fit" not in (L.df_moe_last_error(None) or b"")

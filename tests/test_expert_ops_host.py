@@ -279,3 +279,14 @@ def test_arrays_of_another_types_size_are_refused(dfm, monkeypatch, name, kw, re
             refused(dfm, getattr(dfm, name), -1, "%s has elements of %d bytes" % (key, other),
                     **dict(kw, **dict(arrays, **{key: make(other)})))
     assert len(seen) == 1
+
+
+@pytest.mark.parametrize("name, kw", EVERY_CALL[:4] + EVERY_CALL[5:])
+def test_negative_sizes_that_32_bits_would_cut_are_refused(dfm, name, kw):
+    """-2^32 + 2 is not 2."""
+    for size in ("k", "E", "n_scales", "G"):
+        if size in kw or (size == "n_scales" and name == "permute"):
+            for v in (-(1 << 32) + 2, -(1 << 31) - 1, -(1 << 64) + 2):
+                refused(dfm, getattr(dfm, name), -1, "32 bits", **dict(kw, **{size: v}))
+            refused(dfm, getattr(dfm, name), -1, "must", **dict(kw, **{size: -1}))
+    assert dfm.permute_workspace(70000, -(1 << 32) + 2, 8) == dfm.permute_workspace(70000, 2, -(1 << 32) + 8) == 0
