@@ -232,6 +232,45 @@ def test_product_sums_keep_their_bits(dfm, M, N, K, act):
     assert bool(((y.double() - want).abs() <= (4 * 48 + parts + (128 if act == "swiglu" else 0)) * U * want).all())
 
 
+@pytest.mark.parametrize("case", [
+    # M, N, K, dtype, out, act, bias, residual, pre: more than 8192 of k for 16-bit outputs, by tiles of 16, 32 and 64
+    # rows and by pairs of 128 and 256 columns, aligned and not, gated and not
+    (3, 130, 20000, "bf16", "bf16", "gelu", True, True, True), (40, 96, 9000, "f16", "f16", "swiglu", True, False, True),
+    (100, 130, 30000, "bf16", "bf16", "none", False, True, False), (300, 64, 70001, "f16", "f16", "silu", True, True, True),
+    (2100, 1024, 9001, "bf16", "bf16", "relu", True, True, True), (2100, 1026, 9001, "f16", "f16", "none", False, False, False),
+    (4200, 2304, 8200, "bf16", "bf16", "gelu", True, True, True), (4200, 2306, 8200, "f16", "f16", "none", True, True, True),
+    (2100, 640, 17000, "bf16", "bf16", "swiglu", True, True, True), (2100, 1281, 8200, "f16", "f16", "swiglu", False, False, True),
+    (4100, 2560, 8264, "bf16", "bf16", "swiglu", True, True, True),
+], ids=lambda c: "-".join(map(str, c)))
+def test_product_of_many_parts(dfm, case):
+    check_product(dfm, *case)
+
+
+@pytest.mark.parametrize("M, N, K, dtype, out, act", [(2100, 1024, 9001, "bf16", "bf16", "none"), (2100, 1026, 9001, "f16", "f16", "none"),
+                                                      (4200, 2304, 8200, "f16", "f16", "none"), (5, 64, 50000, "f16", "f16", "none"),
+                                                      (4200, 2306, 16500, "bf16", "bf16", "none"), (100, 40, 262144, "bf16", "f32", "none"),
+                                                      (2100, 1280, 20000, "f16", "f16", "swiglu")])
+def test_product_of_many_parts_of_positive_terms(dfm, M, N, K, dtype, out, act):
+    """No error cancels: 2 U an addition in tensor memory (parts of 8192, or 768, of k, 16
+    products at a time and some 8 bits of slack for their alignment: as much again), U a part."""
+    g = gen(K)
+    x = torch.rand(M, -(-K // 8) * 8, generator=g, device="cuda").to(DT[dtype])
+    wide = 2 * N if act == "swiglu" else N
+    w = (torch.rand(wide, -(-K // 8) * 8, generator=g, device="cuda") * 2.0 ** -4).to(DT[dtype])
+    y, b = torch.empty(M, N, device="cuda", dtype=DT[out]), None
+    if act == "swiglu":
+        w[:N] = 0
+        b = torch.zeros(wide, dtype=DT[dtype], device="cuda")
+        b[:N] = 1
+    dfm.matmul(x, w, dtype, M, N, K, y, out, bias=b, act=act, ldx=x.stride(0), ldw=w.stride(0))
+    want = x[:, :K].double() @ w[wide - N:, :K].double().t()
+    if act == "swiglu":
+        want = want * torch.sigmoid(torch.tensor(1.0, device="cuda", dtype=torch.float64))
+    chunk = 768 if out == "f32" else 8192
+    off = (4 * chunk // 16 + -(-K // chunk) + 8 + 128) * U
+    within(y, want, off * want, out)
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
 def test_activations_at_their_ends(dfm, act):
     """Large arguments of either sign: 0 or z, never NaN."""
@@ -307,6 +346,14 @@ def check_gradient(dfm, M, N, K, dtype, grad, act, wanted=("dx", "dw", "dbias"),
 
 @pytest.mark.parametrize("case", GRADS, ids=lambda c: "-".join(map(str, c)))
 def test_product_gradient(dfm, case):
+    check_gradient(dfm, *case)
+
+
+@pytest.mark.parametrize("case", [(9000, 130, 72, "bf16", "bf16", "none"), (20000, 64, 200, "f16", "f16", "gelu"), (9001, 1024, 1100, "bf16", "bf16", "none"),
+                                  (8500, 1030, 1101, "f16", "f16", "silu"), (9000, 2304, 2304, "bf16", "bf16", "none"), (8300, 300, 264, "bf16", "bf16", "swiglu")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_product_gradient_of_many_rows(dfm, case):
+    """dw's k is the rows: more than 8192 of them, in 16 bits."""
     check_gradient(dfm, *case)
 
 
