@@ -524,7 +524,9 @@ DF_MOE_API int df_moe_matmul(int device, const void* x, int64_t ldx, const void*
  *   x, w as in df_moe_matmul; x only for dw, w only for dx
  *   pre [M][W] z of dtype, and dz [M][W] of dtype (output, rounded: the products
  *       take it in 16 bits; 16-byte aligned, lddz a multiple of 8 where dx or dw
- *       is wanted): required with an activation, not touched without
+ *       is wanted): required with an activation, not touched without. dx and dw
+ *       then carry its rounding, an fp32 dw too, and an fp16 dz beyond 65504 is
+ *       infinite
  *   dx  [M][K] of dtype;  dw [W][K] and dbias [W] of grad_dtype: dtype or
  *       DF_MOE_F32. dbias sums dz before it is rounded. */
 DF_MOE_API int df_moe_matmul_grad(int device, const void* dy, int64_t lddy, const void* x, int64_t ldx,

@@ -318,7 +318,8 @@ __device__ __forceinline__ void finish_alone(const BalanceArgs& p, float* sums, 
 // 16 us, with one a warp 21). The sums of the probabilities go to shared memory, a
 // place a lane and value (in registers they cost the warps that hide the loads).
 // With the join 16384 rows of 896 f32 take 20 us (3.0 TB/s: the exponentials and
-// the adds of a value bound it as much as its bytes), sigmoid 26.
+// the adds of a value bound it as much as its bytes), sigmoid 26. Short rows off
+// vector boundaries spill 52 to 76 bytes a thread.
 // alone: the blocks are one cluster, which finishes the call.
 template <typename T, bool VEC, int NV, int L, bool SIGMOID>
 __global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const BalanceArgs p, const Entries out, int chunk_rows, int alone) {
@@ -434,7 +435,8 @@ constexpr int kBalGradThreads = 256, kBalGradWarps = kBalGradThreads / 32;
 // third of the warps). The routing weights' terms reach the lanes that hold their
 // experts through rows of shared memory that are zero between (comparing every
 // expert with every id took more instructions than the rest). 16384 rows of 896
-// f32 26 us (4.5 TB/s), sigmoid 43; 65536 of 128 22 (33 with one row a warp).
+// f32 26 us (4.5 TB/s), sigmoid 43 (a lane's three arrays of 32 values do not fit 128
+// registers: 156 bytes spill); 65536 of 128 22 (33 with one row a warp).
 template <typename T, bool VEC, int NV, int L, bool SIGMOID>
 __global__ void __launch_bounds__(kBalGradThreads, NV < 8 ? 1 : 2) balance_grad_kernel(const BalanceGradArgs p, int64_t warp_rows) {
   extern __shared__ __align__(16) float shared[];  // [warps][NV][32 lanes][4] f, and with weights the same of their terms

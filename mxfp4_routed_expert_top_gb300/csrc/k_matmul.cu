@@ -32,7 +32,8 @@ __device__ __forceinline__ float value(__half v) { return __half2float(v); }
 // hold: HBM bounds it, and it is the bytes on their way that bring its rate
 // (4096 x 2048 swiglu 15.9 us, 5.3 TB/s; twice the rows spill, 26). A kernel an
 // activation: with all of them in one it had 128 registers and took 32 us;
-// 8192 x 7168 gelu with bias 90 (3.9 TB/s), 226 in one.
+// 8192 x 7168 gelu with bias 90 (3.9 TB/s), 226 in one. Without an activation (the
+// bias alone, of bf16) 60 bytes of the eight rows spill.
 template <bool VEC, int ACT>
 constexpr int kAgRows = !VEC || ACT == kActNone ? 8 : ACT == kActSwiglu ? 1 : 2;
 

@@ -240,7 +240,11 @@ __device__ __forceinline__ uint32_t desc_step(int mn) { return mn ? 16 * 128 / 1
 // when its own blocks have what they need, which is when all that came before
 // the two is complete, and the second waits for the first only behind its own
 // work, so that what follows finds both complete (256 x 512 x 512 6.7 us, one behind
-// the other 11; 1024 x 1024 x 1024 10.3 and 16.3).
+// the other 11; 1024 x 1024 x 1024 10.3 and 16.3). That the second sees what came
+// before is inferred, not promised in so many words (visibility is promised to a grid
+// that waits): every block of the first has waited before it lets the second start,
+// so what the second reads (dz or dy, and x: nothing of the first's) is complete and
+// visible on the device by then, and it reads it by copies that do not pass L1.
 __device__ __forceinline__ void product_wait(const GemmParams& p) {
   if (p.order != kGemmSecond) pdl_wait();  // the kernel before this one is complete
 }
@@ -319,7 +323,8 @@ __device__ __forceinline__ void gemm_finish(const GemmParams& p, int64_t row, in
 // distributed shared memory in the order of the parts, where the epilogue
 // reads them along the rows. The 128-row operand is the one with the output's
 // columns because with few rows it is the weights, which stream: HBM and the start
-// bound it (1 x 7168 x 2048 6.9 us, 4.3 TB/s; 24 x 2048 x 7168 swiglu 15, 3.9 TB/s).
+// bound it (1 x 7168 x 2048 6.9 to 7.2 us, 4.1 to 4.3 TB/s; 24 x 2048 x 7168 swiglu 15,
+// 3.9 TB/s).
 template <int NT>
 struct GemmCfg {
   static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;  // stages
@@ -843,7 +848,8 @@ __device__ __forceinline__ void put_sums(const float (&sum)[BN / 2], uint32_t ta
 }
 
 // MANY: units of more than one chunk (a kernel of their own: the chunks' sums
-// cost the others registers).
+// cost the others registers). The vectors' epilogue spills some registers a unit: 52
+// to 124 bytes a thread, with MANY 176 to 612.
 template <int BN, int IN, int OUT, bool VEC, bool MANY>
 __global__ void __launch_bounds__(PairCfg<BN>::NTHR, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   using G = PairCfg<BN>;

@@ -23,7 +23,7 @@
 // ones straight from memory. Any other rows: value by value, in loops that are
 // not unrolled (block_norm_odd_kernel). One file a type includes this one.
 // Measured, bf16 with a channel's gate, in us (norms straight | ring, gradients
-// straight | ring): 8192 x 7168 149 | 77 (6.1 TB/s), 384 | 141 (5.0 TB/s); 8192 x
+// straight | ring): 8192 x 7168 149 | 77 (6.1 TB/s), 384 | 142 (5.0 TB/s); 8192 x
 // 2048 39 | 27, 103 | 47; 8192 x 640 22 | 15, 44 | 32; 304 x 7168 8.5 | 6.3, 26 | 18.
 #pragma once
 
@@ -178,8 +178,8 @@ struct RowSum {
 #pragma unroll
     for (int o = G / 2; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     // (Two branches for one and two values, one for eight: as the compiler
-    // schedules them the norms of 8192 x 7168 take 77 us (6.1 TB/s) and their gradient 141,
-    // the other way about 82 and 158.)
+    // schedules them the norms of 8192 x 7168 take 77 us (6.1 TB/s) and their gradient 142,
+    // the other way about 82 and 172.)
     if (N < 8 && tpr > 32 && lane % G == 0) buf[which][lane / G][warp] = mine;
     if (tpr > 32) {
       if (N == 8 && lane % G == 0) buf[which][lane / G][warp] = mine;
@@ -482,6 +482,9 @@ __device__ __forceinline__ void put_columns(const BlockNormGradArgs& p, const Ro
 }
 
 // ---- rows straight from global memory ------------------------------------------
+// Where a row takes a block of 1024 threads (64 registers each) these spill: the
+// gradient of few or wide rows up to 8192 336 bytes a thread, rows above 8192 728 to
+// 1608 and their gradient 1800 to 2780.
 template <typename T>
 struct GlobalRow {
   const BlockNormArgs& p;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_grad_ring_kernel(c
 // they could not pass. The second pass over a row finds it in L1 or L2. What a
 // thread keeps of a row (h) or over its rows (the column sums) is in shared
 // memory, at places that no other thread touches; longer rows' column sums in
-// global. Issue slots bound it (67%: a value a load): the gradient of 1023 x 2049
+// global. Issue slots bound it (66%: a value a load): the gradient of 1023 x 2049
 // fp32 21 us, 2.4 TB/s, 53 with the loops unrolled.
 constexpr int kOddThreads = 256, kOddUnroll = 4;
 
