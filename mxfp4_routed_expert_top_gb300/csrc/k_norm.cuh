@@ -16,7 +16,7 @@
 // u^2, y h, and u q g times dh, y and h); its column sums stay in a block's
 // registers over its rows and meet in a second kernel, in order. Sums are fp32.
 // A row whose squares (with eps) overflow fp32 is summed again at 2^-80, a gradient
-// row of which any sum does with h and u at size 1.
+// row of which any sum does with h and u at size 1 at most.
 //
 // Three forms, by the rows. Whole 16-byte pieces: from 513 to 8192 values
 // through a ring of bulk copies (block_norm_ring_kernel), shorter, longer and few
@@ -351,18 +351,19 @@ __device__ __forceinline__ RowFactors row_factors(const float (&s)[8], float sh,
   const float gu = s[3] + f.rh * (s[4] - f.along * rh * s[5]);  // the sum of G q g u su, without a token's gate
   f.dtoken = ru * gu;
   f.mean = token * f.dtoken * inv;
-  f.ru = ru * su;
+  f.ru = post ? ru * su : 1.f;
   return f;
 }
 
 // Whether a row's six sums are all there (what comes of the last four is finite);
 // where one left fp32 or has no value, the scales with which h and u are summed
-// again: those that make a norm's rows of size 1, or kSmall where the squares do
-// not say.
-__device__ __forceinline__ bool summed(const float (&s)[8], const RowFactors& f, float& sh, float& su, bool post, float inv, float eps) {
+// again: those that make larger rows of size 1, or kSmall where the squares do not
+// say. u^2 is summed from the second time on without a norm of u, too.
+__device__ __forceinline__ bool summed(const float (&s)[8], const RowFactors& f, float& sh, float& su, float inv, float eps) {
   if (s[0] + s[1] + eps < INFINITY && fabsf(f.along) + fabsf(f.dtoken) < INFINITY) return true;
-  sh = s[0] + eps < INFINITY ? sh * rms_of(s[0], inv, eps, sh) : kSmall;
-  su = post && s[1] + eps < INFINITY ? su * rms_of(s[1], inv, eps, su) : kSmall;
+  constexpr float kNone = 1e-30f;  // beside the squares of what is scaled
+  sh = s[0] < INFINITY ? fminf(1.f, sh * rms_of(s[0], inv, kNone, sh)) : kSmall;
+  su = s[1] < INFINITY ? fminf(1.f, su * rms_of(s[1], inv, kNone, su)) : kSmall;
   return false;
 }
 
@@ -401,7 +402,7 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row& 
       if (!has_u || !(post || by_token)) continue;
       Eight x = at.load(in.u(), i);
       if (again) x = mul(x, pair(su, su));
-      if (post) DFM_EIGHT c[1] = fma2(x.v[j], x.v[j], c[1]);
+      if (post || again) DFM_EIGHT c[1] = fma2(x.v[j], x.v[j], c[1]);
       x = mul(x, q[i]);
       if (full) x = mul(x, at.load(in.gate(), i));
       if (has_dh) {
@@ -421,7 +422,7 @@ __device__ __forceinline__ void grad_row(const BlockNormGradArgs& p, const Row& 
     s[6] = ok ? 0.f : 1.f, s[7] = 0.f;
     sum(s, at.tpr);
     f = row_factors(s, sh, su, has_dn, post, token, inv, p.eps);
-    if (again == 2 || summed(s, f, sh, su, post, inv, p.eps)) break;
+    if (again == 3 || summed(s, f, sh, su, inv, p.eps)) break;
   }
   const bool bad = s[6] != 0.f;
   float scale = p.scale;
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
         DFM_ODD {
           a[i] *= sh, x[i] *= su, y[i] *= v[i];
           s[0] = fmaf(a[i], a[i], s[0]);
-          if (p.post) s[1] = fmaf(x[i], x[i], s[1]);
+          if (p.post || again) s[1] = fmaf(x[i], x[i], s[1]);
           s[2] = fmaf(a[i], y[i], s[2]);
           x[i] *= q[i] * g[i];
           s[3] = fmaf(x[i], b[i], s[3]);
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(kOddThreads) block_norm_grad_odd_kernel(const 
       }
       sum(s, kOddThreads);
       f = row_factors(s, sh, su, p.dn != nullptr, p.post != 0, token, inv, p.eps);
-      if (again == 2 || summed(s, f, sh, su, p.post != 0, inv, p.eps)) break;
+      if (again == 3 || summed(s, f, sh, su, inv, p.eps)) break;
     }
     if (by_token && p.dgate && threadIdx.x == 0) static_cast<float*>(p.dgate)[row] = f.dtoken;
     T* dr = p.dresidual ? static_cast<T*>(p.dresidual) + row * p.lddr : nullptr;

@@ -843,6 +843,28 @@ def test_norm_gradient_whose_cross_sums_overflow(dfm, H, T, dtype, post, kind):
         within(o, value, (256 + (T + 64 if column else 0)) * U * mag, kind_of)
 
 
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("H, T, dtype", [(64, 6, "f32"), (61, 6, "f32"), (2048, 420, "bf16"), (1024, 700, "f32"), (9000, 6, "bf16")])
+def test_norm_gradient_of_rows_far_apart_in_size(dfm, H, T, dtype, post):
+    """h beyond fp32's root next to a small u, and the other way about: either is summed
+    at a scale of its own."""
+    g = gen(H)
+    size = torch.tensor([[1e-20, 1e30], [1e30, 1e-20], [1.0, 3e38], [3e38, 1.0], [1e-30, 1e19], [3e19, 3e19]], device="cuda")
+    size = size.repeat(-(-T // 6), 1)[:T]
+    lot = [(torch.randn(T, H, generator=g, device="cuda").clamp(-1, 1) * s).to(DT[dtype])
+           for s in (size[:, :1], size[:, 1:], torch.ones(T, 1, device="cuda"), 1e-15 * torch.ones(T, 1, device="cuda"))]
+    u, h, dn, dh = lot
+    q, gate = torch.full((H,), 1.5, device="cuda") if post else None, torch.full((T,), 0.5, device="cuda")
+    out = dict(du=torch.empty_like(u), dresidual=torch.empty_like(u), dgate=torch.empty(T, device="cuda"))
+    dfm.block_norm_grad(dh, dn, u, h, dtype, T, H, post=post, post_weight=q, gate=gate, gate_kind="token", eps=EPS, **out)
+    want = grad64(dh.double(), dn.double(), u.double(), h.double(), post, q, gate, "token", 1.0, None)
+    for key, o in out.items():
+        value, mag = want[key]
+        # not the gate's gradient of 61 terms of 3e38 times some 0.3 and more (6e39 of magnitudes, which no fp32 sum holds)
+        there = mag < torch.finfo(torch.float32).max
+        within(o[there], value[there], 256 * U * mag[there], "f32" if key == "dgate" else dtype)
+
+
 # ---- balance ----------------------------------------------------------------
 def balance64(z, ids, k, E, offs, mask, score, coef, z_coef, dloss=None, weights=None, dweights=None):
     T, S = z.shape[0], len(offs) - 1
