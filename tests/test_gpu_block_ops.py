@@ -271,6 +271,59 @@ def test_product_of_many_parts_of_positive_terms(dfm, M, N, K, dtype, out, act):
     within(y, want, off * want, out)
 
 
+def check_whole_product(dfm, M, N, K, dtype, out, act, bias, residual, pre):
+    """check_product with outputs whose rows lie behind each other: whole vectors."""
+    g, wide, x, w, b = product_inputs(M, N, K, dtype, act, bias, M + N + 2 * K)
+    r = randn(M, N, g=g, dtype=out) if residual else None
+    y, p = torch.full((M + 1, N), 3.0, device="cuda").to(DT[out]), torch.full((M + 1, wide), 3.0, device="cuda").to(DT[dtype])
+    dfm.matmul(x, w, dtype, M, N, K, y, out, bias=b, act=act, residual=r, pre=p if pre else None, ldx=x.stride(0), ldw=w.stride(0))
+    z = x.double() @ w.double().t()
+    bz = 2 * (K + 2) * U * (x.double().abs() @ w.double().abs().t())
+    if bias:
+        z = z + b.double()
+        bz = bz + U * z.abs()
+    if pre:
+        within(p[:M], z, bz, dtype)
+    want, bound = act64(z, act, N), act_bound(z, bz, act, N)
+    if residual:
+        want = want + r.double()
+        bound = bound + U * (want.abs() + bound)
+    within(y[:M], want, bound, out)
+    assert bool((y[M:] == 3).all()) and bool((p[M if pre else 0:] == 3).all())
+
+
+@pytest.mark.parametrize("out", ["in", "f32"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("M, N, K, dtype", [(5, 64, 200, "bf16"), (60, 72, 300, "f16"), (200, 96, 520, "bf16"), (2100, 1024, 520, "f16"),
+                                            (4100, 2048, 264, "bf16"), (2100, 2560, 1032, "f16")])
+def test_product_in_whole_vectors(dfm, M, N, K, dtype, act, out):
+    check_whole_product(dfm, M, N, K, dtype, dtype if out == "in" else out, act, True, True, True)
+
+
+@pytest.mark.parametrize("case", [
+    # by tiles of 16, 32 and 64 rows (parts of more than 8192 of k: eight of 8750), by pairs of 128 and 256 columns
+    (3, 128, 70000, "bf16", "bf16", "none", False, True, False), (40, 96, 70001, "f16", "f16", "swiglu", True, False, True),
+    (300, 64, 70000, "bf16", "bf16", "gelu", True, True, True), (2100, 1024, 9001, "f16", "f16", "gelu", True, True, True),
+    (1000, 2560, 8264, "bf16", "bf16", "relu", True, True, True), (1000, 2560, 16500, "f16", "f16", "none", False, False, False),
+    (2100, 640, 17000, "f16", "f16", "swiglu", True, True, True), (2100, 1280, 8264, "bf16", "bf16", "swiglu", False, True, False),
+], ids=lambda c: "-".join(map(str, c)))
+def test_product_of_many_parts_in_whole_vectors(dfm, case):
+    check_whole_product(dfm, *case)
+
+
+@pytest.mark.parametrize("M, N, K, dtype", [(70000, 64, 72, "bf16"), (70001, 61, 130, "f16"), (9000, 2304, 1024, "bf16"), (9001, 1000, 2560, "f16"),
+                                            (17000, 2048, 512, "f16")])
+def test_product_gradient_of_many_rows_in_16_bits(dfm, M, N, K, dtype):
+    """dw of 16 bits, in whole vectors where K is: parts of more than 8192 rows."""
+    g, _, x, _, _ = product_inputs(M, N, K, dtype, "none", False, M + N)
+    dy = rows(M, N, g, dtype, up8(N) - N, sigma=0.2)
+    dw = torch.full((N + 1, K), 3.0, device="cuda").to(DT[dtype])
+    dfm.matmul_grad(dy, x, None, dtype, M, N, K, dw=dw, grad_dtype=dtype, lddy=dy.stride(0), ldx=x.stride(0))
+    want, size = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    within(dw[:N], want, 2 * (M + 2) * U * size, dtype)
+    assert bool((dw[N:] == 3).all())
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
 def test_activations_at_their_ends(dfm, act):
     """Large arguments of either sign: 0 or z, never NaN."""
