@@ -423,9 +423,19 @@ def _find_tensor_calls(a):
 _get_device = _element_size = _data_ptr = _find_tensor_calls
 
 
-def _type(d):
+# By the type that a call names: its code, and the bytes of an element of each
+# array that it places.
+_PERMUTE = {a: (i, (4, n, n, 4, 4, 4), (4, n, n, 4, 4, 4, 0, 4, 4)) for a, (i, n) in _TYPES.items()}
+_PERMUTE_GRAD = {a: (i, (n, 4, n)) for a, (i, n) in _TYPES.items()}
+_UNPERMUTE = {a: (i, (n, 4, 4, n)) for a, (i, n) in _TYPES.items()}
+_UNPERMUTE_GRAD = {a: (i, (n, n, 4, 4, n, 4)) for a, (i, n) in _TYPES.items()}
+_FP8_QUANTIZE = {a: (i, (n, 1, 4)) for a, (i, n) in _TYPES.items()}
+_FP8_MATMUL = {a: (i, (1, 4, 1, 4, 4, n, 4)) for a, (i, n) in _TYPES.items()}
+
+
+def _of_type(table, d):
     try:
-        return _TYPES[d]
+        return table[d]
     except (KeyError, TypeError):
         raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,))
 
@@ -477,7 +487,8 @@ def _place_any(names, sizes, arrays):
         if size and sizes[i] and size() != sizes[i]:
             name = names.split()[i]
             if name != "status" or size() < 4:  # of a wider one the first word is taken
-                raise DfMoeError(EINVAL, "%s has elements of %d bytes, not of the %d that the call takes" % (name, size(), sizes[i]))
+                raise DfMoeError(EINVAL, "%s has elements of %d bytes, not of the %d that the call takes" %
+                                 (name, size(), sizes[i]))
         out.append(p)
     out[0] = dev
     return out
@@ -509,14 +520,13 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
         _int32(k=k, E=E, n_scales=n_scales)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    dtype, n = _type(dtype)
+    dtype, sizes, all_sizes = _of_type(_PERMUTE, dtype)
     if workspace is None and scales is None and rows_scales is None:
-        dev, i, x, r, o, q, s = _place("ids x rows offs pos src", (4, n, n, 4, 4, 4), ids, x, rows, offs, pos, src)
+        dev, i, x, r, o, q, s = _place("ids x rows offs pos src", sizes, ids, x, rows, offs, pos, src)
         w = xs = rs = None
     else:
-        dev, i, x, r, o, q, s, w, xs, rs = _place("ids x rows offs pos src workspace scales rows_scales",
-                                                  (4, n, n, 4, 4, 4, 0, 4, 4), ids, x, rows, offs, pos, src, workspace,
-                                                  scales, rows_scales)
+        dev, i, x, r, o, q, s, w, xs, rs = _place("ids x rows offs pos src workspace scales rows_scales", all_sizes, ids, x,
+                                                  rows, offs, pos, src, workspace, scales, rows_scales)
     rc = _c.df_moe_permute(dev, i, T, k, E, x, dtype, H, ldx, xs, n_scales, ld_scales, r,
                            ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -527,8 +537,8 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
     """Gradient of permute's x (df_moe_permute_grad)."""
     if k >> 31:
         _int32(k=k)
-    dtype, n = _type(dtype)
-    dev, r, q, y = _place("drows pos dx", (n, 4, n), drows, pos, dx)
+    dtype, sizes = _of_type(_PERMUTE_GRAD, dtype)
+    dev, r, q, y = _place("drows pos dx", sizes, drows, pos, dx)
     rc = _c.df_moe_permute_grad(dev, r, dtype, n_rows, ldr, q, T, k, H, y, ldx,
                                 _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -539,8 +549,8 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
     """Weighted rows back to their tokens (df_moe_unpermute)."""
     if k >> 31:
         _int32(k=k)
-    dtype, n = _type(dtype)
-    dev, r, q, w, y = _place("rows pos weights y", (n, 4, 4, n), rows, pos, weights, y)
+    dtype, sizes = _of_type(_UNPERMUTE, dtype)
+    dev, r, q, w, y = _place("rows pos weights y", sizes, rows, pos, weights, y)
     rc = _c.df_moe_unpermute(dev, r, dtype, n_rows, ldr, q, w, T, k, H, y, ldy,
                              _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -552,9 +562,8 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
     if k >> 31:
         _int32(k=k)
-    dtype, n = _type(dtype)
-    dev, g, r, q, w, dr, dw = _place("dy rows pos weights drows dweights", (n, n, 4, 4, n, 4), dy, rows, pos, weights,
-                                     drows, dweights)
+    dtype, sizes = _of_type(_UNPERMUTE_GRAD, dtype)
+    dev, g, r, q, w, dr, dw = _place("dy rows pos weights drows dweights", sizes, dy, rows, pos, weights, drows, dweights)
     rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, dtype, n_rows, ldr, q, w, T, k, H, dr,
                                   lddr, dw, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -563,8 +572,8 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
-    dtype, n = _type(dtype)
-    dev, x, c, s = _place("x codes scales", (n, 1, 4), x, codes, scales)
+    dtype, sizes = _of_type(_FP8_QUANTIZE, dtype)
+    dev, x, c, s = _place("x codes scales", sizes, x, codes, scales)
     rc = _c.df_moe_fp8_quantize(dev, x, dtype, M, K, ldx, c, ldc, s, lds, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -575,8 +584,8 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
     if G >> 31:
         _int32(G=G)
-    dtype, n = _type(dtype)
-    dev, x, xs, w, ws, o, y, st = _place("x xs w ws offs y status", (1, 4, 1, 4, 4, n, 4), x, xs, w, ws, offs, y, status)
+    dtype, sizes = _of_type(_FP8_MATMUL, dtype)
+    dev, x, xs, w, ws, o, y, st = _place("x xs w ws offs y status", sizes, x, xs, w, ws, offs, y, status)
     rc = _c.df_moe_fp8_matmul(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
                               1 if transposed else 0, y, dtype, ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -608,42 +617,57 @@ def _packer(call, layout):
     return run
 
 
-_matmul = _packer(0, "20q")
-_matmul_grad = _packer(1, "24q")
-_block_norm = _packer(2, "10qdqd9q")
-_block_norm_grad = _packer(3, "14qdqd15q")
-_balance_loss = _packer(4, "12q2d8q")
-_balance_loss_grad = _packer(5, "13q2d7q")
+_call_matmul = _packer(0, "20q")
+_call_matmul_grad = _packer(1, "24q")
+_call_block_norm = _packer(2, "10qdqd9q")
+_call_block_norm_grad = _packer(3, "14qdqd15q")
+_call_balance_loss = _packer(4, "12q2d8q")
+_call_balance_loss_grad = _packer(5, "13q2d7q")
 
 
-def _choice(kinds, name, v):
-    try:
-        return kinds[v]
-    except (KeyError, TypeError):
-        raise DfMoeError(EINVAL, "%s must be one of %s, not %r" % (name, ", ".join(map(repr, kinds)), v)) from None
+# By the names that a call gives: their codes, and the bytes of an element of each
+# array that it places.
+_PAIRS = [(a, i, n, b, j, o) for a, (i, n) in _TYPES.items() for b, (j, o) in _TYPES.items()]
+_MATMUL = {(a, b, c): (i, j, k, (n, n, o, n, o, n, 4)) for a, i, n, b, j, o in _PAIRS for c, k in _ACTS.items()}
+_MATMUL_GRAD = {(a, b, c): (i, j, k, (n, n, n, n, o, o, n, n, 4)) for a, i, n, b, j, o in _PAIRS for c, k in _ACTS.items()}
+_NORM = {(a, b, c): (i, j, k, (n, n, n, n, o, (0, o, 4, n)[k], o)) for a, i, n, b, j, o in _PAIRS for c, k in _GATES.items()}
+_NORM_GRAD = {(a, b, c): (i, j, k, (n, n, n, n, n, n, o, 4, (0, o, 4, n)[k], (0, 4, 4, n)[k], o, 4, 0))
+              for a, i, n, b, j, o in _PAIRS for c, k in _GATES.items()}
+_BALANCE = {(a, c): (i, k, (n, 4, 4, 4, 4, 0, 4, 4, 1, 4)) for a, (i, n) in _TYPES.items() for c, k in _SCORES.items()}
+_BALANCE_GRAD = {(a, c): (i, k, (4, n, 4, 4, 4, n, 4, 1, 4, 4)) for a, (i, n) in _TYPES.items() for c, k in _SCORES.items()}
+
+
+def _unknown(types, kinds, name, v):
+    """Names that are in no table."""
+    for t in types:
+        _of_type(_TYPES, t)
+    raise DfMoeError(EINVAL, "%s must be one of %s, not %r" % (name, ", ".join(map(repr, kinds)), v)) from None
 
 
 def matmul(x, w, dtype, M, N, K, y, out_dtype, bias=None, act="none", residual=None, pre=None, ldx=0,
            ldw=0, ldy=0, ldr=0, ldp=0, status=None, stream=None):
     """y = residual + act(x w' + bias) of 16-bit matrices (df_moe_matmul)."""
-    dtype, n = _type(dtype)
-    out_dtype, o = _type(out_dtype)
-    dev, x, w, y, b, r, z, st = _place("x w y bias residual pre status", (n, n, o, n, o, n, 4), x, w, y, bias, residual, pre,
-                                       status)
-    _matmul(dev, x, ldx, w, ldw, dtype, M, N, K, b, _choice(_ACTS, "act", act), r, ldr, z, ldp, y, out_dtype, ldy, st,
-            _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    try:
+        t, o, a, sizes = _MATMUL[dtype, out_dtype, act]
+    except (KeyError, TypeError):
+        _unknown((dtype, out_dtype), _ACTS, "act", act)
+    dev, x, w, y, b, r, z, st = _place("x w y bias residual pre status", sizes, x, w, y, bias, residual, pre, status)
+    _call_matmul(dev, x, ldx, w, ldw, t, M, N, K, b, a, r, ldr, z, ldp, y, o, ldy, st,
+                 _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def matmul_grad(dy, x, w, dtype, M, N, K, dx=None, dw=None, dbias=None, grad_dtype="f32", act="none",
                 pre=None, dz=None, lddy=0, ldx=0, ldw=0, lddx=0, lddw=0, ldp=0, lddz=0, status=None,
                 stream=None):
     """Gradients of matmul's x, w and bias (df_moe_matmul_grad)."""
-    dtype, n = _type(dtype)
-    grad_dtype, g = _type(grad_dtype)
-    dev, dy, x, w, dx, dw, db, z, dz, st = _place("dy x w dx dw dbias pre dz status", (n, n, n, n, g, g, n, n, 4), dy, x, w, dx,
-                                                  dw, dbias, pre, dz, status)
-    _matmul_grad(dev, dy, lddy, x, ldx, w, ldw, dtype, M, N, K, _choice(_ACTS, "act", act), z, ldp, dz, lddz,
-                 dx, lddx, dw, lddw, db, grad_dtype, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    try:
+        t, g, a, sizes = _MATMUL_GRAD[dtype, grad_dtype, act]
+    except (KeyError, TypeError):
+        _unknown((dtype, grad_dtype), _ACTS, "act", act)
+    dev, dy, x, w, dx, dw, db, z, dz, st = _place("dy x w dx dw dbias pre dz status", sizes, dy, x, w, dx, dw, dbias, pre, dz,
+                                                  status)
+    _call_matmul_grad(dev, dy, lddy, x, ldx, w, ldw, t, M, N, K, a, z, ldp, dz, lddz, dx, lddx, dw, lddw, db, g, st,
+                      _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def test_matmul_give_up(role):
@@ -657,13 +681,14 @@ def block_norm(u, residual, dtype, T, H, h=None, n=None, post=False, post_weight
                gate_kind="none", residual_scale=1.0, pre_weight=None, weight_dtype="f32", eps=1e-6, ldu=0,
                ldr=0, ldg=0, ldh=0, ldn=0, stream=None):
     """h = residual_scale residual + gate norm(u), n = norm(h) (df_moe_block_norm)."""
-    dtype, b = _type(dtype)
-    weight_dtype, w = _type(weight_dtype)
-    kind = _choice(_GATES, "gate_kind", gate_kind)
-    dev, u, r, h, n, q, g, v = _place("u residual h n post_weight gate pre_weight", (b, b, b, b, w, (0, w, 4, b)[kind], w), u,
-                                      residual, h, n, post_weight, gate, pre_weight)
-    _block_norm(dev, u, ldu, 1 if post else 0, q, kind, g, ldg, r, ldr, residual_scale, v, eps, T, H, dtype,
-                weight_dtype, h, ldh, n, ldn, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    try:
+        t, w, kind, sizes = _NORM[dtype, weight_dtype, gate_kind]
+    except (KeyError, TypeError):
+        _unknown((dtype, weight_dtype), _GATES, "gate_kind", gate_kind)
+    dev, u, r, h, n, q, g, v = _place("u residual h n post_weight gate pre_weight", sizes, u, residual, h, n, post_weight, gate,
+                                      pre_weight)
+    _call_block_norm(dev, u, ldu, 1 if post else 0, q, kind, g, ldg, r, ldr, residual_scale, v, eps, T, H, t, w, h, ldh, n, ldn,
+                     _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def block_norm_grad_workspace(T, H):
@@ -679,17 +704,18 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
                     workspace_bytes=0, lddh=0, lddn=0, ldu=0, ldh=0, ldg=0, lddu=0, lddr=0, lddg=0,
                     stream=None):
     """Gradients of block_norm (df_moe_block_norm_grad)."""
-    dtype, b = _type(dtype)
-    weight_dtype, w = _type(weight_dtype)
-    kind = _choice(_GATES, "gate_kind", gate_kind)
+    try:
+        t, w, kind, sizes = _NORM_GRAD[dtype, weight_dtype, gate_kind]
+    except (KeyError, TypeError):
+        _unknown((dtype, weight_dtype), _GATES, "gate_kind", gate_kind)
     dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _place(
         "dh dn u h du dresidual post_weight dpost_weight gate dgate pre_weight dpre_weight workspace",
-        (b, b, b, b, b, b, w, 4, (0, w, 4, b)[kind], (0, 4, 4, b)[kind], w, 4, 0),
-        dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
+        sizes, dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    _block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q, kind, g, ldg, residual_scale, v, eps, T, H,
-                     dtype, weight_dtype, du, lddu, dr, lddr, dq, dg, lddg, dv, ws, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    _call_block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q, kind, g, ldg, residual_scale, v, eps, T, H,
+                          t, w, du, lddu, dr, lddr, dq, dg, lddg, dv, ws, workspace_bytes,
+                          _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def balance_loss_workspace(T, E, S=1):
@@ -707,12 +733,14 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
         _int32(E=E, k=k)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    dtype, n = _type(dtype)
-    dev, z, i, lo, c, t, ws, p, o, m, st = _place("logits ids loss counts tokens workspace probs offs mask status",
-                                                  (n, 4, 4, 4, 4, 0, 4, 4, 1, 4), logits, ids, loss, counts,
-                                                  tokens, workspace, probs, offs, mask, status)
-    _balance_loss(dev, z, dtype, ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef, z_coef, lo,
-                  c, t, p, ws, workspace_bytes, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    try:
+        kind, sc, sizes = _BALANCE[dtype, score]
+    except (KeyError, TypeError):
+        _unknown((dtype,), _SCORES, "score", score)
+    dev, z, i, lo, c, t, ws, p, o, m, st = _place("logits ids loss counts tokens workspace probs offs mask status", sizes, logits,
+                                                  ids, loss, counts, tokens, workspace, probs, offs, mask, status)
+    _call_balance_loss(dev, z, kind, ldl, i, T, E, k, o, S, m, sc, coef, z_coef, lo, c, t, p, ws, workspace_bytes, st,
+                       _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
 
 def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogits, offs=None, S=1,
@@ -721,9 +749,11 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
     """The gradient of the logits: the loss's and the routing weights' (df_moe_balance_loss_grad)."""
     if (E | k) >> 31:
         _int32(E=E, k=k)
-    dtype, n = _type(dtype)
-    dev, g, z, i, c, t, d, o, m, w, dw = _place("dloss logits ids counts tokens dlogits offs mask weights dweights",
-                                                (4, n, 4, 4, 4, n, 4, 1, 4, 4), dloss, logits, ids, counts, tokens, dlogits,
-                                                offs, mask, weights, dweights)
-    _balance_loss_grad(dev, g, z, dtype, ldl, i, T, E, k, o, S, m, _choice(_SCORES, "score", score), coef,
-                       z_coef, c, t, w, dw, d, lddl, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
+    try:
+        kind, sc, sizes = _BALANCE_GRAD[dtype, score]
+    except (KeyError, TypeError):
+        _unknown((dtype,), _SCORES, "score", score)
+    dev, g, z, i, c, t, d, o, m, w, dw = _place("dloss logits ids counts tokens dlogits offs mask weights dweights", sizes, dloss,
+                                                logits, ids, counts, tokens, dlogits, offs, mask, weights, dweights)
+    _call_balance_loss_grad(dev, g, z, kind, ldl, i, T, E, k, o, S, m, sc, coef, z_coef, c, t, w, dw, d, lddl,
+                            _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
