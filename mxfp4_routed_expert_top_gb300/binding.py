@@ -423,46 +423,44 @@ def _find_tensor_calls(a):
 _get_device = _element_size = _data_ptr = _find_tensor_calls
 
 
-# By the type that a call names: its code, and the bytes of an element of each
-# array that it places.
-_PERMUTE = {a: (i, (4, n, n, 4, 4, 4), (4, n, n, 4, 4, 4, 0, 4, 4)) for a, (i, n) in _TYPES.items()}
-_PERMUTE_GRAD = {a: (i, (n, 4, n)) for a, (i, n) in _TYPES.items()}
-_UNPERMUTE = {a: (i, (n, 4, 4, n)) for a, (i, n) in _TYPES.items()}
-_UNPERMUTE_GRAD = {a: (i, (n, n, 4, 4, n, 4)) for a, (i, n) in _TYPES.items()}
-_FP8_QUANTIZE = {a: (i, (n, 1, 4)) for a, (i, n) in _TYPES.items()}
-_FP8_MATMUL = {a: (i, (1, 4, 1, 4, 4, n, 4)) for a, (i, n) in _TYPES.items()}
-
-
-def _of_type(table, d):
+def _type(d):
     try:
-        return table[d]
+        return _TYPES[d]
     except (KeyError, TypeError):
-        raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,))
+        raise DfMoeError(EINVAL, "dtype must be one of 'bf16', 'f16', 'f32', 'e4m3', not %r" % (d,)) from None
 
 
-def _place(names, sizes, *arrays):
-    """[device, address, address, ...]: the one CUDA device that the torch
-    tensors among the arrays lie on (-1, the current one, where there are only
-    raw addresses), and the arrays' addresses (0 for one that is absent). The
-    tensors' elements have to be `sizes` bytes (0: any): the library goes by the
-    types that the call names, and would pass the end of a narrower array.
-    `names`: the arrays', for what is refused."""
+def _placer(layout, lead=None):
+    """place(array, ..., size=0, other=0, gate_size=0, dgate_size=0) -> (device, address, ...):
+    the one CUDA device that the torch tensors among the arrays lie on (-1, the
+    current one, where there are only raw addresses), and the arrays' addresses (0
+    for one that is absent). `layout`: the arrays' names, each with the bytes of an
+    element, which a tensor's have to be (0: any): the library goes by the types
+    that the call names, and would pass the end of a narrower array. `lead`: the
+    array that the device is asked of first, where it is not the first.
+
+    The function is written out here, without a loop, since a decode step's calls
+    take microseconds: with a loop it cost 0.3 us more (seven arrays)."""
+    names, sizes = zip(*(word.split(":") for word in layout.split()))
+    checks = ["dev >= 0"]
+    for a, n in zip(names, sizes):
+        wide = {"0": "True", "gate_size": "(not gate_size or _element_size(gate) == gate_size)",
+                "dgate_size": "(not dgate_size or _element_size(dgate) == dgate_size)"}.get(n, "_element_size(%s) == %s" % (a, n))
+        checks.append(wide if a == names[0] and not lead else "(%s is None or _get_device(%s) == dev and %s)" % (a, a, wide))
+    scope = {}
+    exec("""
+def place(%s, size=0, other=0, gate_size=0, dgate_size=0):
     try:  # all of them tensors on one device, or absent
-        dev = _get_device(arrays[0])
-        if dev >= 0:
-            out = [dev]
-            for a, n in zip(arrays, sizes):
-                if a is None:
-                    out.append(0)
-                elif _get_device(a) == dev and (_element_size(a) == n or not n):
-                    out.append(_data_ptr(a))
-                else:
-                    break
-            else:
-                return out
+        dev = _get_device(%s)
+        if %s:
+            return dev, %s
     except TypeError:
         pass
-    return _place_any(names, sizes, arrays)
+    return _place_any(%r, (%s,), (%s,))
+""" % (", ".join(names), lead or names[0], " and ".join(checks),
+       ", ".join("0 if %s is None else _data_ptr(%s)" % (a, a) for a in names), names, ", ".join(sizes), ", ".join(names)),
+         globals(), scope)
+    return scope["place"]
 
 
 def _place_any(names, sizes, arrays):
@@ -485,10 +483,9 @@ def _place_any(names, sizes, arrays):
             raise DfMoeError(EINVAL, "every array must be in device memory")
         size = getattr(a, "element_size", None)
         if size and sizes[i] and size() != sizes[i]:
-            name = names.split()[i]
-            if name != "status" or size() < 4:  # of a wider one the first word is taken
+            if names[i] != "status" or size() < 4:  # of a wider one the first word is taken
                 raise DfMoeError(EINVAL, "%s has elements of %d bytes, not of the %d that the call takes" %
-                                 (name, size(), sizes[i]))
+                                 (names[i], size(), sizes[i]))
         out.append(p)
     out[0] = dev
     return out
@@ -503,6 +500,15 @@ def _int32(**sizes):
 
 def _failed(rc):
     raise DfMoeError(rc, lib().df_moe_last_error(None).decode())
+
+
+_place_permute = _placer("ids:4 x:size rows:size offs:4 pos:4 src:4")
+_place_permute_all = _placer("ids:4 x:size rows:size offs:4 pos:4 src:4 workspace:0 scales:4 rows_scales:4")
+_place_permute_grad = _placer("drows:size pos:4 dx:size")
+_place_unpermute = _placer("rows:size pos:4 weights:4 y:size")
+_place_unpermute_grad = _placer("dy:size rows:size pos:4 weights:4 drows:size dweights:4")
+_place_fp8_quantize = _placer("x:size codes:1 scales:4")
+_place_fp8_matmul = _placer("x:1 xs:4 w:1 ws:4 offs:4 y:size status:4")
 
 
 def permute_workspace(T, k, E):
@@ -520,13 +526,12 @@ def permute(ids, T, k, E, x, dtype, H, rows, offs, pos, src, workspace=None, wor
         _int32(k=k, E=E, n_scales=n_scales)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
-    dtype, sizes, all_sizes = _of_type(_PERMUTE, dtype)
+    dtype, n = _type(dtype)
     if workspace is None and scales is None and rows_scales is None:
-        dev, i, x, r, o, q, s = _place("ids x rows offs pos src", sizes, ids, x, rows, offs, pos, src)
+        dev, i, x, r, o, q, s = _place_permute(ids, x, rows, offs, pos, src, n)
         w = xs = rs = None
     else:
-        dev, i, x, r, o, q, s, w, xs, rs = _place("ids x rows offs pos src workspace scales rows_scales", all_sizes, ids, x,
-                                                  rows, offs, pos, src, workspace, scales, rows_scales)
+        dev, i, x, r, o, q, s, w, xs, rs = _place_permute_all(ids, x, rows, offs, pos, src, workspace, scales, rows_scales, n)
     rc = _c.df_moe_permute(dev, i, T, k, E, x, dtype, H, ldx, xs, n_scales, ld_scales, r,
                            ldr, rs, ld_rows_scales, o, q, s, w, workspace_bytes, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -537,8 +542,8 @@ def permute_grad(drows, dtype, n_rows, pos, T, k, H, dx, ldr=0, ldx=0, stream=No
     """Gradient of permute's x (df_moe_permute_grad)."""
     if k >> 31:
         _int32(k=k)
-    dtype, sizes = _of_type(_PERMUTE_GRAD, dtype)
-    dev, r, q, y = _place("drows pos dx", sizes, drows, pos, dx)
+    dtype, n = _type(dtype)
+    dev, r, q, y = _place_permute_grad(drows, pos, dx, n)
     rc = _c.df_moe_permute_grad(dev, r, dtype, n_rows, ldr, q, T, k, H, y, ldx,
                                 _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -549,8 +554,8 @@ def unpermute(rows, dtype, n_rows, pos, weights, T, k, H, y, ldr=0, ldy=0, strea
     """Weighted rows back to their tokens (df_moe_unpermute)."""
     if k >> 31:
         _int32(k=k)
-    dtype, sizes = _of_type(_UNPERMUTE, dtype)
-    dev, r, q, w, y = _place("rows pos weights y", sizes, rows, pos, weights, y)
+    dtype, n = _type(dtype)
+    dev, r, q, w, y = _place_unpermute(rows, pos, weights, y, n)
     rc = _c.df_moe_unpermute(dev, r, dtype, n_rows, ldr, q, w, T, k, H, y, ldy,
                              _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -562,8 +567,8 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
     """Gradients of unpermute's rows and weights (df_moe_unpermute_grad)."""
     if k >> 31:
         _int32(k=k)
-    dtype, sizes = _of_type(_UNPERMUTE_GRAD, dtype)
-    dev, g, r, q, w, dr, dw = _place("dy rows pos weights drows dweights", sizes, dy, rows, pos, weights, drows, dweights)
+    dtype, n = _type(dtype)
+    dev, g, r, q, w, dr, dw = _place_unpermute_grad(dy, rows, pos, weights, drows, dweights, n)
     rc = _c.df_moe_unpermute_grad(dev, g, lddy, r, dtype, n_rows, ldr, q, w, T, k, H, dr,
                                   lddr, dw, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -572,8 +577,8 @@ def unpermute_grad(dy, rows, dtype, n_rows, pos, weights, T, k, H, drows, dweigh
 
 def fp8_quantize(x, dtype, M, K, codes, scales, ldx=0, ldc=0, lds=0, stream=None):
     """Rows as e4m3 codes with one fp32 scale per 128 (df_moe_fp8_quantize)."""
-    dtype, sizes = _of_type(_FP8_QUANTIZE, dtype)
-    dev, x, c, s = _place("x codes scales", sizes, x, codes, scales)
+    dtype, n = _type(dtype)
+    dev, x, c, s = _place_fp8_quantize(x, codes, scales, n)
     rc = _c.df_moe_fp8_quantize(dev, x, dtype, M, K, ldx, c, ldc, s, lds, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
         _failed(rc)
@@ -584,8 +589,8 @@ def fp8_matmul(x, xs, w, ws, offs, G, M, N, K, y, dtype, transposed=False, ldx=0
     """e4m3 rows times their group's e4m3 weights (df_moe_fp8_matmul)."""
     if G >> 31:
         _int32(G=G)
-    dtype, sizes = _of_type(_FP8_MATMUL, dtype)
-    dev, x, xs, w, ws, o, y, st = _place("x xs w ws offs y status", sizes, x, xs, w, ws, offs, y, status)
+    dtype, n = _type(dtype)
+    dev, x, xs, w, ws, o, y, st = _place_fp8_matmul(x, xs, w, ws, offs, y, status, n)
     rc = _c.df_moe_fp8_matmul(dev, x, ldx, xs, ldxs, w, ldw, ws, o, G, M, N, K,
                               1 if transposed else 0, y, dtype, ldy, st, _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream))
     if rc:
@@ -625,22 +630,27 @@ _call_balance_loss = _packer(4, "12q2d8q")
 _call_balance_loss_grad = _packer(5, "13q2d7q")
 
 
-# By the names that a call gives: their codes, and the bytes of an element of each
-# array that it places.
+_place_matmul = _placer("x:size w:size y:other bias:size residual:other pre:size status:4")
+_place_matmul_grad = _placer("dy:size x:size w:size dx:size dw:other dbias:other pre:size dz:size status:4")
+_place_norm = _placer("u:size residual:size h:size n:size post_weight:other gate:gate_size pre_weight:other",
+                      "residual if u is None else u")
+_place_norm_grad = _placer("dh:size dn:size u:size h:size du:size dresidual:size post_weight:other dpost_weight:4 gate:gate_size "
+                           "dgate:dgate_size pre_weight:other dpre_weight:4 workspace:0", "dn if dh is None else dh")
+_place_balance = _placer("logits:size ids:4 loss:4 counts:4 tokens:4 workspace:0 probs:4 offs:4 mask:1 status:4")
+_place_balance_grad = _placer("dloss:4 logits:size ids:4 counts:4 tokens:4 dlogits:size offs:4 mask:1 weights:4 dweights:4")
+
+# By the names that a call gives: their codes, and the bytes of an element of the
+# arrays of those types (of gates and their gradients by the kind of gate, too).
 _PAIRS = [(a, i, n, b, j, o) for a, (i, n) in _TYPES.items() for b, (j, o) in _TYPES.items()]
-_MATMUL = {(a, b, c): (i, j, k, (n, n, o, n, o, n, 4)) for a, i, n, b, j, o in _PAIRS for c, k in _ACTS.items()}
-_MATMUL_GRAD = {(a, b, c): (i, j, k, (n, n, n, n, o, o, n, n, 4)) for a, i, n, b, j, o in _PAIRS for c, k in _ACTS.items()}
-_NORM = {(a, b, c): (i, j, k, (n, n, n, n, o, (0, o, 4, n)[k], o)) for a, i, n, b, j, o in _PAIRS for c, k in _GATES.items()}
-_NORM_GRAD = {(a, b, c): (i, j, k, (n, n, n, n, n, n, o, 4, (0, o, 4, n)[k], (0, 4, 4, n)[k], o, 4, 0))
-              for a, i, n, b, j, o in _PAIRS for c, k in _GATES.items()}
-_BALANCE = {(a, c): (i, k, (n, 4, 4, 4, 4, 0, 4, 4, 1, 4)) for a, (i, n) in _TYPES.items() for c, k in _SCORES.items()}
-_BALANCE_GRAD = {(a, c): (i, k, (4, n, 4, 4, 4, n, 4, 1, 4, 4)) for a, (i, n) in _TYPES.items() for c, k in _SCORES.items()}
+_PRODUCT = {(a, b, c): (i, j, k, n, o) for a, i, n, b, j, o in _PAIRS for c, k in _ACTS.items()}
+_NORM = {(a, b, c): (i, j, k, n, o, (0, o, 4, n)[k], (0, 4, 4, n)[k]) for a, i, n, b, j, o in _PAIRS for c, k in _GATES.items()}
+_BALANCE = {(a, c): (i, k, n) for a, (i, n) in _TYPES.items() for c, k in _SCORES.items()}
 
 
 def _unknown(types, kinds, name, v):
     """Names that are in no table."""
     for t in types:
-        _of_type(_TYPES, t)
+        _type(t)
     raise DfMoeError(EINVAL, "%s must be one of %s, not %r" % (name, ", ".join(map(repr, kinds)), v)) from None
 
 
@@ -648,10 +658,10 @@ def matmul(x, w, dtype, M, N, K, y, out_dtype, bias=None, act="none", residual=N
            ldw=0, ldy=0, ldr=0, ldp=0, status=None, stream=None):
     """y = residual + act(x w' + bias) of 16-bit matrices (df_moe_matmul)."""
     try:
-        t, o, a, sizes = _MATMUL[dtype, out_dtype, act]
+        t, o, a, size, other = _PRODUCT[dtype, out_dtype, act]
     except (KeyError, TypeError):
         _unknown((dtype, out_dtype), _ACTS, "act", act)
-    dev, x, w, y, b, r, z, st = _place("x w y bias residual pre status", sizes, x, w, y, bias, residual, pre, status)
+    dev, x, w, y, b, r, z, st = _place_matmul(x, w, y, bias, residual, pre, status, size, other)
     _call_matmul(dev, x, ldx, w, ldw, t, M, N, K, b, a, r, ldr, z, ldp, y, o, ldy, st,
                  _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
@@ -661,11 +671,10 @@ def matmul_grad(dy, x, w, dtype, M, N, K, dx=None, dw=None, dbias=None, grad_dty
                 stream=None):
     """Gradients of matmul's x, w and bias (df_moe_matmul_grad)."""
     try:
-        t, g, a, sizes = _MATMUL_GRAD[dtype, grad_dtype, act]
+        t, g, a, size, other = _PRODUCT[dtype, grad_dtype, act]
     except (KeyError, TypeError):
         _unknown((dtype, grad_dtype), _ACTS, "act", act)
-    dev, dy, x, w, dx, dw, db, z, dz, st = _place("dy x w dx dw dbias pre dz status", sizes, dy, x, w, dx, dw, dbias, pre, dz,
-                                                  status)
+    dev, dy, x, w, dx, dw, db, z, dz, st = _place_matmul_grad(dy, x, w, dx, dw, dbias, pre, dz, status, size, other)
     _call_matmul_grad(dev, dy, lddy, x, ldx, w, ldw, t, M, N, K, a, z, ldp, dz, lddz, dx, lddx, dw, lddw, db, g, st,
                       _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
@@ -682,11 +691,10 @@ def block_norm(u, residual, dtype, T, H, h=None, n=None, post=False, post_weight
                ldr=0, ldg=0, ldh=0, ldn=0, stream=None):
     """h = residual_scale residual + gate norm(u), n = norm(h) (df_moe_block_norm)."""
     try:
-        t, w, kind, sizes = _NORM[dtype, weight_dtype, gate_kind]
+        t, w, kind, size, other, gate_size, _ = _NORM[dtype, weight_dtype, gate_kind]
     except (KeyError, TypeError):
         _unknown((dtype, weight_dtype), _GATES, "gate_kind", gate_kind)
-    dev, u, r, h, n, q, g, v = _place("u residual h n post_weight gate pre_weight", sizes, u, residual, h, n, post_weight, gate,
-                                      pre_weight)
+    dev, u, r, h, n, q, g, v = _place_norm(u, residual, h, n, post_weight, gate, pre_weight, size, other, gate_size)
     _call_block_norm(dev, u, ldu, 1 if post else 0, q, kind, g, ldg, r, ldr, residual_scale, v, eps, T, H, t, w, h, ldh, n, ldn,
                      _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
@@ -705,12 +713,12 @@ def block_norm_grad(dh, dn, u, h, dtype, T, H, du=None, dresidual=None, post=Fal
                     stream=None):
     """Gradients of block_norm (df_moe_block_norm_grad)."""
     try:
-        t, w, kind, sizes = _NORM_GRAD[dtype, weight_dtype, gate_kind]
+        t, w, kind, size, other, gate_size, dgate_size = _NORM[dtype, weight_dtype, gate_kind]
     except (KeyError, TypeError):
         _unknown((dtype, weight_dtype), _GATES, "gate_kind", gate_kind)
-    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _place(
-        "dh dn u h du dresidual post_weight dpost_weight gate dgate pre_weight dpre_weight workspace",
-        sizes, dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace)
+    dev, dh, dn, u, h, du, dr, q, dq, g, dg, v, dv, ws = _place_norm_grad(
+        dh, dn, u, h, du, dresidual, post_weight, dpost_weight, gate, dgate, pre_weight, dpre_weight, workspace, size, other,
+        gate_size, dgate_size)
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
     _call_block_norm_grad(dev, dh, lddh, dn, lddn, u, ldu, h, ldh, 1 if post else 0, q, kind, g, ldg, residual_scale, v, eps, T, H,
@@ -734,11 +742,11 @@ def balance_loss(logits, dtype, T, E, ids, k, loss, counts, tokens, workspace=No
     if workspace_bytes < 0:
         raise DfMoeError(EINVAL, "workspace_bytes is negative")
     try:
-        kind, sc, sizes = _BALANCE[dtype, score]
+        kind, sc, size = _BALANCE[dtype, score]
     except (KeyError, TypeError):
         _unknown((dtype,), _SCORES, "score", score)
-    dev, z, i, lo, c, t, ws, p, o, m, st = _place("logits ids loss counts tokens workspace probs offs mask status", sizes, logits,
-                                                  ids, loss, counts, tokens, workspace, probs, offs, mask, status)
+    dev, z, i, lo, c, t, ws, p, o, m, st = _place_balance(logits, ids, loss, counts, tokens, workspace, probs, offs, mask,
+                                                          status, size)
     _call_balance_loss(dev, z, kind, ldl, i, T, E, k, o, S, m, sc, coef, z_coef, lo, c, t, p, ws, workspace_bytes, st,
                        _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)
 
@@ -750,10 +758,10 @@ def balance_loss_grad(dloss, logits, dtype, T, E, ids, k, counts, tokens, dlogit
     if (E | k) >> 31:
         _int32(E=E, k=k)
     try:
-        kind, sc, sizes = _BALANCE_GRAD[dtype, score]
+        kind, sc, size = _BALANCE[dtype, score]
     except (KeyError, TypeError):
         _unknown((dtype,), _SCORES, "score", score)
-    dev, g, z, i, c, t, d, o, m, w, dw = _place("dloss logits ids counts tokens dlogits offs mask weights dweights", sizes, dloss,
-                                                logits, ids, counts, tokens, dlogits, offs, mask, weights, dweights)
+    dev, g, z, i, c, t, d, o, m, w, dw = _place_balance_grad(dloss, logits, ids, counts, tokens, dlogits, offs, mask, weights,
+                                                             dweights, size)
     _call_balance_loss_grad(dev, g, z, kind, ldl, i, T, E, k, o, S, m, sc, coef, z_coef, c, t, w, dw, d, lddl,
                             _torch_stream(dev) if stream is None and dev >= 0 else _stream(stream) or 0)

@@ -483,9 +483,9 @@ __device__ __forceinline__ void put_columns(const BlockNormGradArgs& p, const Ro
 }
 
 // ---- rows straight from global memory ------------------------------------------
-// Where a row takes a block of 1024 threads (64 registers each) these spill: the
+// Where a row takes a block of 1024 threads (64 registers each at most) these spill: the
 // gradient of few or wide rows up to 8192 336 bytes a thread, rows above 8192 728 to
-// 1608 and their gradient 1800 to 2780.
+// 1608 and their gradient 1800 to 2790.
 template <typename T>
 struct GlobalRow {
   const BlockNormArgs& p;
