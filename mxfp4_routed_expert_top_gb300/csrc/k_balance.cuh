@@ -192,20 +192,19 @@ __device__ __forceinline__ float softmax_row(float (&v)[N], float* scale) {
 // the last that has a quotient, a score is 0 beside the largest, as -inf's is.
 template <int L, bool REST, int N>
 __device__ __forceinline__ void sigmoid_row(float (&v)[N], float* m, float* scale) {
-  constexpr float kNone = 0x1p126f;
   const float most = warp_max<L>(lane_max(v));
   const float M = most == -INFINITY ? 0.f : fminf(most, 0.f), low = exp2_fast(M * kLog2e);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float2 x = halves(mul2(add2(pair(v[i], v[i + 1]), both(-M)), both(-kLog2e)));
-    const float e[2] = {fminf(exp2_fast(x.x), kNone), fminf(exp2_fast(x.y), kNone)};
+    const float e[2] = {fminf(exp2_fast(x.x), 0x1p126f), fminf(exp2_fast(x.y), 0x1p126f)};
     const float2 sum = halves(add2(pair(e[0], e[1]), both(low)));
     const float r[2] = {__fdividef(1.f, sum.x), __fdividef(1.f, sum.y)};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float& z = v[i + j];
       if (REST) m[i + j] = z != z ? z : e[j] * r[j];
-      z = z != z ? z : e[j] == kNone ? 0.f : r[j];  // fminf drops a NaN
+      z = (j ? x.y : x.x) >= 126.f ? 0.f : z != z ? z : r[j];  // fminf drops a NaN
     }
   }
   const float sum = warp_sum<L>(lane_sum(v));
